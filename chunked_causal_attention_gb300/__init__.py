@@ -10,25 +10,31 @@ from __future__ import annotations
 
 from typing import Optional, Sequence
 
-from ._lib import (AttnError, EXPORTS, PASS_BWD, PASS_BWD_CHUNK, PASS_FWD, PLAN_FLOPS, PLAN_FLOPS_RESPLIT_EDGES,
+from ._lib import (AttnError, EXPORTS, KV4_ATTEND, KV4_ATTEND_MASS, KV4_ROWS, PASS_BWD, PASS_BWD_CHUNK, PASS_FWD,
+                   PASS_MASS, PLAN_FLOPS, PLAN_FLOPS_RESPLIT_EDGES,
                    PLAN_UNIFORM, attn_bwd, attn_bwd_chunk, attn_bwd_dq, attn_bwd_prep, attn_bwd_tiles, attn_fwd,
-                   attn_fwd_merge, attn_fwd_noalloc, attn_fwd_tiles, attn_noalloc_status, attn_plan,
+                   attn_fwd_merge, attn_fwd_noalloc, attn_fwd_tiles, attn_key_mass, attn_kv4_attend, attn_kv4_cache,
+                   attn_kv4_evict, attn_kv4_load, attn_kv4_store, attn_kv4_workspace_size, attn_noalloc_status, attn_plan,
                    attn_plan_infinipipe, attn_plan_multiplex, attn_plan_varlen, attn_shape, attn_status,
                    attn_workspace_size, lib, make_shape, shape_of, strerror, version,
                    kernel_launches)
+from .kv4 import KV4Cache, kv4_attention, kv4_cache, kv4_evict, kv4_load, kv4_store, kv4_workspace
 
 __all__ = ["AttnError", "EXPORTS", "PLAN_UNIFORM", "PLAN_FLOPS", "PLAN_FLOPS_RESPLIT_EDGES", "attn_plan",
            "attn_plan_varlen", "attn_plan_infinipipe", "attn_plan_multiplex", "attn_workspace_size", "attn_fwd", "attn_fwd_tiles", "attn_fwd_merge", "attn_bwd",
            "attn_bwd_prep", "attn_bwd_tiles", "attn_bwd_dq", "attn_bwd_chunk", "attn_fwd_noalloc",
            "attn_noalloc_status", "attn_status", "attn_shape",
            "make_shape", "shape_of", "workspace", "forward", "backward", "forward_streamed", "backward_streamed",
-           "PASS_FWD", "PASS_BWD", "PASS_BWD_CHUNK", "plan_infinipipe", "lib", "strerror", "version",
+           "PASS_FWD", "PASS_BWD", "PASS_BWD_CHUNK", "PASS_MASS", "plan_infinipipe",
+           "attn_key_mass", "attn_kv4_cache", "attn_kv4_workspace_size", "attn_kv4_store", "attn_kv4_load",
+           "attn_kv4_attend", "attn_kv4_evict", "KV4_ROWS", "KV4_ATTEND", "KV4_ATTEND_MASS", "KV4Cache", "kv4_cache",
+           "kv4_workspace", "kv4_store", "kv4_load", "kv4_attention", "kv4_evict", "key_mass", "key_mass_workspace", "lib", "strerror", "version",
            "kernel_launches"]
 
 
 def workspace(shape: attn_shape, chunks: Sequence, pass_: int, device="cuda", per_chunk: bool = False):
     """A uint8 device buffer of the size the library asks for (pass 0 forward,
-    1 backward, 2 chunk-streamed backward), with its 256-byte status header
+    1 backward, 2 chunk-streamed backward, 3 key mass), with its 256-byte status header
     zeroed. per_chunk: ``chunks`` is a list of calls (each a chunk or a list
     of chunks) and the buffer fits any one of them."""
     import torch
@@ -106,6 +112,28 @@ def backward_streamed(q, k, v, o, lse, dout, chunks: Sequence, scale: Optional[f
     for c in reversed(calls):
         attn_bwd_chunk(q, k, v, o, lse, dout, c, shape, dq, dk, dv, dk_acc, dv_acc, ws, stream)
     return dq, dk, dv, dk_acc, dv_acc
+
+
+def key_mass_workspace(q, k, chunks: Sequence, packed: bool = False):
+    """A workspace for key_mass on these chunks, for callers that keep one."""
+    return workspace(shape_of(q, None, packed, k), chunks, PASS_MASS, q.device)
+
+
+def key_mass(q, k, lse, chunks: Sequence, scale: Optional[float] = None, packed: bool = False, mass_in=None,
+             mass_out=None, ws=None, stream=None):
+    """The attention weight that each key received, fp32 [B, Hkv, T]: the sum
+    over the chunks' query rows and over the query heads of its key/value head,
+    from q, k and the forward's lse. mass_in (optional) is added; mass_out may be
+    given, also the same tensor as mass_in, to accumulate call by call. Chunks
+    over the last rows alone give the weights as those rows see them."""
+    import torch
+    shape = shape_of(q, scale, packed, k)
+    if mass_out is None:
+        mass_out = torch.empty((shape.B, shape.Hkv or shape.H, shape.T), dtype=torch.float32, device=q.device)
+    if ws is None:
+        ws = workspace(shape, chunks, PASS_MASS, q.device)
+    attn_key_mass(q, k, lse, chunks, shape, mass_in, mass_out, ws, stream)
+    return mass_out
 
 
 def plan_infinipipe(seq_lens: Sequence[int], K: int, token_cap: int, cost=None):

@@ -27,13 +27,20 @@ PLAN_FLOPS_RESPLIT_EDGES = 2
 # Every symbol include/attn.h declares.
 EXPORTS = ("attn_plan", "attn_plan_varlen", "attn_plan_multiplex", "attn_plan_infinipipe", "attn_workspace_size", "attn_fwd", "attn_fwd_tiles",
            "attn_fwd_merge", "attn_bwd", "attn_bwd_prep", "attn_bwd_tiles", "attn_bwd_dq",
-           "attn_bwd_chunk", "attn_fwd_noalloc", "attn_noalloc_status", "attn_status", "attn_strerror",
+           "attn_bwd_chunk", "attn_key_mass", "attn_kv4_workspace_size", "attn_kv4_store", "attn_kv4_load",
+           "attn_kv4_attend", "attn_kv4_evict", "attn_fwd_noalloc", "attn_noalloc_status", "attn_status", "attn_strerror",
            "attn_version", "attn_kernel_launches")
 
 # attn_workspace_size passes
 PASS_FWD = 0
 PASS_BWD = 1
 PASS_BWD_CHUNK = 2
+PASS_MASS = 3
+
+# attn_kv4_workspace_size ops
+KV4_ROWS = 0
+KV4_ATTEND = 1
+KV4_ATTEND_MASS = 2
 
 # Size of the library-held scratch area of attn_fwd_noalloc (ATTN_NOALLOC_SCRATCH_BYTES).
 NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -57,6 +64,13 @@ class attn_shape(ctypes.Structure):
                 ("Hkv", ctypes.c_int64), ("sb_kv", ctypes.c_int64), ("st_kv", ctypes.c_int64), ("sh_kv", ctypes.c_int64)]
 
 
+class attn_kv4_cache(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("Hkv", ctypes.c_int64), ("cap", ctypes.c_int64), ("D", ctypes.c_int64),
+                ("sb", ctypes.c_int64), ("sh", ctypes.c_int64),
+                ("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
+
+
 _lib: Optional[ctypes.CDLL] = None
 
 _VP = ctypes.c_void_p
@@ -64,6 +78,8 @@ _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
 _CP = ctypes.POINTER(attn_chunk)
 _SP = ctypes.POINTER(attn_shape)
+_KP = ctypes.POINTER(attn_kv4_cache)
+_SZ = ctypes.c_size_t
 _SIG = {
     "attn_plan": ([_I64, _I32, _I32, _CP, _I32, ctypes.POINTER(_I32)], ctypes.c_int),
     "attn_plan_varlen": ([ctypes.POINTER(_I64), _I32, _I32, _I32, _CP, _I32, ctypes.POINTER(_I32)], ctypes.c_int),
@@ -83,6 +99,12 @@ _SIG = {
     "attn_bwd_dq": ([_CP, _I32, _SP, _VP, _VP, ctypes.c_size_t, _VP], ctypes.c_int),
     "attn_bwd_chunk": ([_VP, _VP, _VP, _VP, _VP, _VP, _CP, _I32, _SP, _VP, _VP, _VP, _VP, _VP, _VP, ctypes.c_size_t,
                         _VP], ctypes.c_int),
+    "attn_key_mass": ([_VP, _VP, _VP, _CP, _I32, _SP, _VP, _VP, _VP, _SZ, _VP], ctypes.c_int),
+    "attn_kv4_workspace_size": ([_KP, _SP, _I32, ctypes.POINTER(_SZ)], ctypes.c_int),
+    "attn_kv4_store": ([_VP, _VP, _SP, _KP, _VP, _VP, _VP, _SZ, _VP], ctypes.c_int),
+    "attn_kv4_load": ([_KP, _VP, _VP, _SP, _VP, _VP, _VP, _SZ, _VP], ctypes.c_int),
+    "attn_kv4_attend": ([_VP, _SP, _KP, _VP, _VP, _VP, _VP, _VP, _I64, _VP, _SZ, _VP], ctypes.c_int),
+    "attn_kv4_evict": ([_KP, _VP, _VP, _I64, _I32, _I32, _KP, _VP, _VP, _I64, _VP, _VP, _SZ, _VP], ctypes.c_int),
     "attn_fwd_noalloc": ([_VP, _VP, _VP, _CP, _I32, _SP, _VP, _VP, _VP], ctypes.c_int),
     "attn_noalloc_status": ([_VP], ctypes.c_int),
     "attn_status": ([_VP, _VP], ctypes.c_int),
@@ -346,6 +368,138 @@ def attn_bwd_chunk(q, k, v, o, lse, dout, chunks, shape, dq, dk, dv, dk_acc, dv_
                                                   ctypes.byref(shape), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dk_acc),
                                                   _ptr(dv_acc), _ptr(ws), ws.numel() * ws.element_size(),
                                                   _stream(stream)))
+
+
+def attn_key_mass(q, k, lse, chunks, shape, mass_in, mass_out, ws, stream=None) -> None:
+    """Attention weight of each key over the chunks' rows (see include/attn.h)."""
+    _expect("attn_key_mass", shape, "q", q)
+    _expect("attn_key_mass", shape, "kv", k)
+    _expect("attn_key_mass", shape, "lse", lse)
+    _same_device("attn_key_mass", q, k, lse, mass_in, mass_out, ws)
+    Hkv = shape.Hkv if shape.Hkv > 0 else shape.H
+    _expect_flat("attn_key_mass", "float32", shape.B * Hkv * shape.T, mass_in, mass_out)
+    arr, n = chunk_array(chunks)
+    with _on(q):
+        _check("attn_key_mass", lib().attn_key_mass(_ptr(q), _ptr(k), _ptr(lse), arr, n, ctypes.byref(shape),
+                                                    _ptr(mass_in), _ptr(mass_out), _ptr(ws),
+                                                    ws.numel() * ws.element_size(), _stream_of(stream, q)))
+
+
+# ------------------------------------------------------------------ 4-bit cache
+
+class _Stay:
+    """A context that changes nothing."""
+    def __enter__(self):
+        pass
+
+    def __exit__(self, *_):
+        pass
+
+
+_STAY = _Stay()
+
+
+def _on(t):
+    """t's device as the current one for a call: the library launches on the current device."""
+    import torch
+    i = t.device.index
+    return _STAY if i is None or torch.cuda.current_device() == i else torch.cuda.device(i)
+
+
+def _stream_of(stream, t) -> Optional[int]:
+    """The given stream, or the current one of t's device."""
+    if stream is None:
+        import torch
+        return torch.cuda.current_stream(t.device).cuda_stream
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _same_device(fn: str, first, *others) -> None:
+    """All tensors (None passes) on the device of the first, a GPU."""
+    dev = first.device
+    if dev.type != "cuda":
+        raise AttnError(fn, ATTN_E_INVAL)
+    for t in others:
+        if t is not None and t.device != dev:
+            raise AttnError(fn, ATTN_E_INVAL)
+
+
+def _expect_flat(fn: str, dtype: str, numel: int, *tensors) -> None:
+    """Contiguous tensors (None passes) of `numel` elements of a dtype."""
+    import torch
+    for t in tensors:
+        if t is not None and not (t.dtype == getattr(torch, dtype) and t.numel() == numel and t.is_contiguous()):
+            raise AttnError(fn, ATTN_E_INVAL)
+
+
+def attn_kv4_workspace_size(cache: attn_kv4_cache, shape: Optional[attn_shape], op: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check("attn_kv4_workspace_size", lib().attn_kv4_workspace_size(
+        ctypes.byref(cache), None if shape is None else ctypes.byref(shape), op, ctypes.byref(out)))
+    return out.value
+
+
+def _kv4_rows_args(fn: str, k, v, shape, cache, pos, cu_seqlens, ws) -> None:
+    _same_device(fn, k, v, pos, cu_seqlens, ws)
+    _expect(fn, shape, "q", k, v)
+    _expect_flat(fn, "int32", cache.B, pos)
+    _expect_flat(fn, "int32", cache.B + 1, cu_seqlens)
+
+
+def attn_kv4_store(k, v, shape, cache: attn_kv4_cache, pos, cu_seqlens, ws, stream=None) -> None:
+    _kv4_rows_args("attn_kv4_store", k, v, shape, cache, pos, cu_seqlens, ws)
+    with _on(k):
+        _check("attn_kv4_store", lib().attn_kv4_store(
+            k.data_ptr(), v.data_ptr(), ctypes.byref(shape), ctypes.byref(cache), _ptr(pos), _ptr(cu_seqlens),
+            _ptr(ws), ws.numel() * ws.element_size(), _stream_of(stream, k)))
+
+
+def attn_kv4_load(cache: attn_kv4_cache, pos, cu_seqlens, shape, k, v, ws, stream=None) -> None:
+    _kv4_rows_args("attn_kv4_load", k, v, shape, cache, pos, cu_seqlens, ws)
+    with _on(k):
+        _check("attn_kv4_load", lib().attn_kv4_load(
+            ctypes.byref(cache), _ptr(pos), _ptr(cu_seqlens), ctypes.byref(shape), k.data_ptr(), v.data_ptr(),
+            _ptr(ws), ws.numel() * ws.element_size(), _stream_of(stream, k)))
+
+
+def _mass_ld(fn: str, cache: attn_kv4_cache, *tensors) -> int:
+    """Row length of contiguous fp32 [B, Hkv, ld] tensors (None passes), one for all."""
+    import torch
+    ld = 0
+    for t in tensors:
+        if t is None:
+            continue
+        if not (t.dtype == torch.float32 and t.dim() == 3 and t.is_contiguous() and t.shape[0] == cache.B
+                and t.shape[1] == cache.Hkv and ld in (0, t.shape[2])):
+            raise AttnError(fn, ATTN_E_INVAL)
+        ld = t.shape[2]
+    return ld
+
+
+def attn_kv4_attend(q, shape, cache: attn_kv4_cache, lens, o, lse, mass_in, mass_out, ws, stream=None) -> None:
+    fn = "attn_kv4_attend"
+    _same_device(fn, q, lens, o, lse, mass_in, mass_out, ws)
+    _expect(fn, shape, "q", q, o)
+    _expect(fn, shape, "lse", lse)
+    _expect_flat(fn, "int32", cache.B, lens)
+    ld = _mass_ld(fn, cache, mass_in, mass_out)
+    with _on(q):
+        _check(fn, lib().attn_kv4_attend(q.data_ptr(), ctypes.byref(shape), ctypes.byref(cache), _ptr(lens),
+                                         o.data_ptr(), lse.data_ptr(), _ptr(mass_in), _ptr(mass_out), ld, _ptr(ws),
+                                         ws.numel() * ws.element_size(), _stream_of(stream, q)))
+
+
+def attn_kv4_evict(src: attn_kv4_cache, lens, mass, keep: int, recent: int, dst: attn_kv4_cache, lens_out, mass_out,
+                   slots, ws, stream=None) -> None:
+    fn = "attn_kv4_evict"
+    _same_device(fn, lens, mass, lens_out, mass_out, slots, ws)
+    _expect_flat(fn, "int32", src.B, lens, lens_out)
+    _expect_flat(fn, "int32", src.B * src.Hkv * keep, slots)
+    ld, ld_out = _mass_ld(fn, src, mass), _mass_ld(fn, src, mass_out)
+    with _on(lens):
+        _check(fn, lib().attn_kv4_evict(ctypes.byref(src), _ptr(lens), _ptr(mass), ld, keep, recent,
+                                        ctypes.byref(dst), _ptr(lens_out), _ptr(mass_out), ld_out, _ptr(slots),
+                                        _ptr(ws), ws.numel() * ws.element_size(), _stream_of(stream, lens)))
 
 
 def attn_fwd_noalloc(q, k, v, chunks, shape, o, lse, stream=None) -> None:

@@ -7,6 +7,7 @@
 #include <vector>
 
 #include "attn_internal.h"
+#include "kv4.h"
 
 using namespace attn;
 
@@ -231,6 +232,9 @@ int check_chunks_stream(const attn_chunk* c, int32_t n, int32_t T) {
 
 std::atomic<uint64_t> attn::g_kernel_launches{0};
 
+int attn::shape_geom(const attn_shape* s, Geom* g) { return check_shape(s, g); }
+int attn::chunks_fwd_status(const attn_chunk* c, int32_t n, int32_t T) { return check_chunks_fwd(c, n, T); }
+
 void attn::wait_settings(uint64_t* wait_ns, int32_t* stall) {
     *wait_ns = 4000000000ull;
     *stall = 0;
@@ -437,6 +441,9 @@ int attn_workspace_size(const attn_shape* shape, const attn_chunk* chunks, int32
         BwdLayout L;
         bwd_chunk_layout(g, chunks, n, L);
         *bytes = L.bytes;
+    } else if (pass == 3) {
+        if ((st = check_chunks_fwd(chunks, n, g.T))) return st;
+        *bytes = key_mass_bytes(g, chunks, n);
     } else {
         return ATTN_E_INVAL;
     }

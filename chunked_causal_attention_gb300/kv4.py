@@ -1,0 +1,134 @@
+"""Key/value cache held in 4 bits: what a program does with the resident K and V
+once a prompt's chunks have run. Rows are stored as e2m1 codes with one e4m3
+scale for 16 dims (include/attn.h has the format), new tokens attend to them,
+and a cache is cut to a budget by the attention weight that its slots received.
+
+    cache = cca.kv4_cache(B, Hkv, cap, D)
+    cca.kv4_store(cache, k, v, pos)                      # a prompt's rows, or one row a sequence
+    o, lse = cca.kv4_attention(q, cache, lens, mass_in=mass, mass_out=mass)
+    lens2, slots = cca.kv4_evict(cache, lens, mass, keep, recent, smaller, mass2)
+
+pos and lens are int32 tensors on the GPU, so the calls can be captured into a
+graph and replayed. Torch provides memory and streams only.
+"""
+from __future__ import annotations
+
+from typing import Optional
+
+from . import _lib
+from ._lib import ATTN_E_INVAL, AttnError
+
+
+class KV4Cache:
+    """A 4-bit cache in four uint8 tensors: codes [B, Hkv, cap, D / 2] and scales
+    [B, Hkv, cap, ceil(D / 16)] of the keys and of the values, possibly views of
+    larger ones (some sequences, heads or slots) as long as rows are contiguous.
+    k_scale and v_scale are powers of two that every value is multiplied by;
+    choose them so that the largest magnitude is below 2688 times the scale."""
+
+    def __init__(self, k_codes, k_scales, v_codes, v_scales, D: int, k_scale: float = 1.0, v_scale: float = 1.0):
+        import torch
+        arrays = (k_codes, k_scales, v_codes, v_scales)
+        if k_codes.dim() != 4 or D < 8 or D % 8:
+            raise AttnError("KV4Cache", ATTN_E_INVAL)
+        B, Hkv, cap, _ = k_codes.shape
+        strides = set()
+        for t, n in zip(arrays, (D // 2, -(-D // 16)) * 2):
+            if (t.dtype != torch.uint8 or tuple(t.shape) != (B, Hkv, cap, n) or t.device != k_codes.device
+                    or (n > 1 and t.stride(3) != 1) or (cap > 1 and t.stride(2) != n)):
+                raise AttnError("KV4Cache", ATTN_E_INVAL)
+            sh = t.stride(1) if Hkv > 1 else cap * n
+            sb = t.stride(0) if B > 1 else Hkv * sh
+            if sh % n or sb % n:
+                raise AttnError("KV4Cache", ATTN_E_INVAL)
+            strides.add((sb // n, sh // n))
+        if len(strides) != 1:
+            raise AttnError("KV4Cache", ATTN_E_INVAL)
+        (sb, sh), = strides
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales = arrays
+        self.B, self.Hkv, self.cap, self.D = B, Hkv, cap, D
+        self.k_scale, self.v_scale = float(k_scale), float(v_scale)
+        self.device = k_codes.device
+        self.desc = _lib.attn_kv4_cache(B, Hkv, cap, D, sb, sh, *(t.data_ptr() for t in arrays), self.k_scale,
+                                        self.v_scale)
+        _lib.attn_kv4_workspace_size(self.desc, None, _lib.KV4_ROWS)      # the library's own checks
+
+    def _for(self, fn: str, t) -> None:
+        if t.device != self.device:
+            raise AttnError(fn, ATTN_E_INVAL)
+
+
+def kv4_cache(B: int, Hkv: int, cap: int, D: int, device="cuda", k_scale: float = 1.0, v_scale: float = 1.0) -> KV4Cache:
+    """An empty cache of cap slots (a multiple of 16)."""
+    import torch
+    codes = [torch.zeros((B, Hkv, cap, n), dtype=torch.uint8, device=device) for n in (D // 2, -(-D // 16)) * 2]
+    return KV4Cache(*codes, D=D, k_scale=k_scale, v_scale=v_scale)
+
+
+def kv4_workspace(cache: KV4Cache, q=None, mass: bool = False):
+    """A workspace for the calls on this cache, status header zeroed: for storing,
+    loading and evicting, and with q also for attention of queries of its shape
+    (with mass: accumulating weights). _lib.attn_status reads its errors."""
+    import torch
+    n = _lib.attn_kv4_workspace_size(cache.desc, None, _lib.KV4_ROWS) if q is None else \
+        _lib.attn_kv4_workspace_size(cache.desc, _lib.shape_of(q), _lib.KV4_ATTEND_MASS if mass else _lib.KV4_ATTEND)
+    ws = torch.empty(n, dtype=torch.uint8, device=cache.device)
+    ws[:256].zero_()
+    return ws
+
+
+def kv4_store(cache: KV4Cache, k, v, pos, cu_seqlens=None, ws=None, stream=None) -> None:
+    """Store rows: k, v bf16 [B, Hkv, T, D], row t of sequence b in slot pos[b] + t;
+    with cu_seqlens (int32 [B + 1]) packed [T, Hkv, D], each sequence's tokens from pos[b] on."""
+    cache._for("kv4_store", k)
+    if ws is None:
+        ws = kv4_workspace(cache)
+    _lib.attn_kv4_store(k, v, _lib.shape_of(k, 1.0, cu_seqlens is not None), cache.desc, pos, cu_seqlens, ws, stream)
+
+
+def kv4_load(cache: KV4Cache, pos, T: int, cu_seqlens=None, k=None, v=None, ws=None, stream=None):
+    """The values of T rows from slot pos[b] on, bf16 [B, Hkv, T, D]; with cu_seqlens
+    packed [T, Hkv, D]. k and v may be given (rows outside the cache stay as they were)."""
+    import torch
+    if k is None or v is None:
+        shape = (T, cache.Hkv, cache.D) if cu_seqlens is not None else (cache.B, cache.Hkv, T, cache.D)
+        k = torch.empty(shape, dtype=torch.bfloat16, device=cache.device) if k is None else k
+        v = torch.empty(shape, dtype=torch.bfloat16, device=cache.device) if v is None else v
+    cache._for("kv4_load", k)
+    if ws is None:
+        ws = kv4_workspace(cache)
+    _lib.attn_kv4_load(cache.desc, pos, cu_seqlens, _lib.shape_of(k, 1.0, cu_seqlens is not None), k, v, ws, stream)
+    return k, v
+
+
+def kv4_attention(q, cache: KV4Cache, lens, scale: Optional[float] = None, mass_in=None, mass_out=None, ws=None,
+                  stream=None):
+    """(o, lse) of the newest T tokens of each sequence, q bf16 [B, H, T, D], over the
+    lens[b] slots in use (their own included). mass_out fp32 [B, Hkv, n]: each slot's
+    weight over the call's rows is added to mass_in (None: zeros; may be mass_out)."""
+    import torch
+    cache._for("kv4_attention", q)
+    shape = _lib.shape_of(q, scale)
+    o = torch.empty_strided(q.shape, q.stride(), dtype=q.dtype, device=q.device)
+    lse = torch.empty((shape.B, shape.H, shape.T), dtype=torch.float32, device=q.device)
+    if ws is None:
+        ws = kv4_workspace(cache, q, mass_out is not None)
+    _lib.attn_kv4_attend(q, shape, cache.desc, lens, o, lse, mass_in, mass_out, ws, stream)
+    return o, lse
+
+
+def kv4_evict(cache: KV4Cache, lens, mass, keep: int, recent: int, out: KV4Cache, mass_out=None, lens_out=None,
+              ws=None, stream=None):
+    """Cut each sequence to at most keep slots, per key/value head: its last `recent`
+    and those with the highest mass, moved to the front of `out` in their order.
+    Returns (lens_out, slots): int32 [B] and the source slots int32 [B, Hkv, keep]."""
+    import torch
+    cache._for("kv4_evict", lens)
+    out._for("kv4_evict", lens)
+    slots = torch.empty((cache.B, cache.Hkv, max(int(keep), 0)), dtype=torch.int32, device=lens.device)
+    if lens_out is None:
+        lens_out = torch.empty_like(lens)
+    if ws is None:
+        ws = kv4_workspace(cache)
+    _lib.attn_kv4_evict(cache.desc, lens, mass, keep, recent, out.desc, lens_out, mass_out, slots, ws, stream)
+    return lens_out, slots

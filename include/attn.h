@@ -181,8 +181,8 @@ int attn_plan_infinipipe(const int64_t* seq_lens, int32_t nseq, int32_t K, int64
                          int32_t* call_off, int32_t call_cap, int32_t* n_calls);
 
 /* Workspace bytes for pass 0 (forward: attn_fwd and its stages), pass 1
- * (backward: attn_bwd and its stages) or pass 2 (attn_bwd_chunk on exactly
- * these chunks) of this shape and chunk table.
+ * (backward: attn_bwd and its stages), pass 2 (attn_bwd_chunk on exactly
+ * these chunks) or pass 3 (attn_key_mass) of this shape and chunk table.
  * Validates like the compute calls. */
 int attn_workspace_size(const attn_shape* shape, const attn_chunk* chunks, int32_t n,
                         int32_t pass, size_t* bytes);
@@ -279,6 +279,129 @@ int attn_bwd_dq(const attn_chunk* chunks, int32_t n, const attn_shape* shape,
 int attn_bwd_chunk(const void* q, const void* k, const void* v, const void* o, const float* lse,
                    const void* dout, const attn_chunk* chunks, int32_t n, const attn_shape* shape,
                    void* dq, void* dk, void* dv, float* dk_acc, float* dv_acc,
+                   void* ws, size_t ws_bytes, void* stream);
+
+/* ---- attention weight of each key --------------------------------------- */
+
+/* The attention weight that each key received, summed over the query rows of
+ * the chunks and over the query heads of its key/value head:
+ *   mass_out[b][hk][j] = mass_in[b][hk][j]
+ *       + sum_{h of hk} sum_{t in chunks, ctx_begin <= j <= t} exp(scale * q_t . k_j - LSE_t)
+ * from the forward's q, k and lse (no V, no O). Chunks as attn_fwd (kv_split is
+ * validated and ignored): all of a prompt's chunks give the weights of the whole
+ * prompt, one chunk holding the last rows the weights as those rows see them, and
+ * a caller that runs chunk by chunk accumulates with mass_in = mass_out. Rows
+ * outside every chunk contribute nothing; every entry j in [0, T) of mass_out is
+ * written. A row whose lse is -inf contributes nothing. Sums are fp32 in a fixed
+ * order: the result does not change from run to run.
+ * mass_in, mass_out: fp32 [B][Hkv][T] contiguous, 16-byte aligned; mass_in may be
+ * NULL (zeros) or equal mass_out, and must not overlap it otherwise. Workspace:
+ * attn_workspace_size(pass 3) for the same chunks. Errors as attn_fwd. */
+int attn_key_mass(const void* q, const void* k, const float* lse, const attn_chunk* chunks, int32_t n,
+                  const attn_shape* shape, const float* mass_in, float* mass_out,
+                  void* ws, size_t ws_bytes, void* stream);
+
+/* ---- key/value cache held in 4 bits -------------------------------------- */
+
+/* A cache of cap slots for each of B sequences and Hkv key/value heads. The row
+ * of slot t of head h of sequence b is row r = b*sb + h*sh + t of four arrays in
+ * device memory:
+ *   k_codes, v_codes    r * D/2 bytes on: D codes e2m1 (sign, two exponent bits,
+ *                       one fraction bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6), two a
+ *                       byte, the even dim in the low four bits
+ *   k_scales, v_scales  r * ceil(D/16) bytes on: one e4m3 scale for each 16
+ *                       consecutive dims (the last block may have 8)
+ * A value is code * block scale * k_scale (or v_scale). k_scale and v_scale are
+ * powers of two in [2^-64, 2^64], so every value has at most six significant bits
+ * and is exact in bf16. A block that held a NaN or an infinity has scale NaN.
+ * D: a multiple of 8 from 8 to 256. cap, sb and sh: multiples of 16; sb and sh
+ * (in slots) allow a view of some sequences, heads or slots of a larger cache.
+ * The arrays are 16-byte aligned. */
+typedef struct {
+    int64_t B, Hkv, cap, D;
+    int64_t sb, sh;
+    void *k_codes, *k_scales, *v_codes, *v_scales;
+    float k_scale, v_scale;
+} attn_kv4_cache;
+
+/* Conventions of the attn_kv4_* calls
+ *   - pos, lens and cu_seqlens are device arrays of int32, read when the call
+ *     runs: a captured graph replays with whatever they hold then.
+ *   - ws: at least attn_kv4_workspace_size() bytes, 256-byte aligned. Its first
+ *     256 bytes are zeroed by the caller once, before its first use. The calls
+ *     only ever set the status word there and attn_status() reads and clears it
+ *     (ATTN_E_BOUNDS: a slot, length or offset outside the cache), so that a
+ *     decode loop needs one look at the end. Calls that may overlap on the GPU
+ *     take different workspaces.
+ *   - Every call may be captured into a graph, and allocates nothing. */
+
+/* Workspace bytes of one attn_kv4_* call: op ATTN_KV4_ROWS (attn_kv4_store,
+ * attn_kv4_load, attn_kv4_evict; shape may be NULL), ATTN_KV4_ATTEND
+ * (attn_kv4_attend without mass_out; shape is the queries') or
+ * ATTN_KV4_ATTEND_MASS (with). A workspace that is large enough for one may
+ * serve the others. */
+#define ATTN_KV4_ROWS         0
+#define ATTN_KV4_ATTEND       1
+#define ATTN_KV4_ATTEND_MASS  2
+int attn_kv4_workspace_size(const attn_kv4_cache* cache, const attn_shape* shape, int32_t op, size_t* bytes);
+
+/* Store rows of K and V. Dense (cu_seqlens NULL): shape B = cache B, H = cache
+ * Hkv, T rows each; row t of sequence b goes to slot pos[b] + t. Packed
+ * (cu_seqlens: B + 1 offsets): shape B = 1, T tokens in all, and token
+ * cu_seqlens[b] + t goes to slot pos[b] + t of sequence b. k and v are bf16 with
+ * the shape's (query) strides. For each block of 16 dims, with ts the tensor scale:
+ *   s = e4m3(max|x| / (6 ts)),  code = e2m1(x / (s ts))
+ * both to nearest even, saturating at 448 and 6; s = 0 gives code 0 (with the
+ * sign of x). A row whose slot is outside [0, cap), and a token of no sequence,
+ * is skipped (ATTN_E_BOUNDS). Errors: ATTN_E_INVAL (NULL pointers, sizes that
+ * do not fit each other, 2^31 rows or more, a tensor scale that is not a power
+ * of two in range, D of cache and shape differ), ATTN_E_ALIGN, ATTN_E_UNSUPPORTED,
+ * ATTN_E_WORKSPACE, ATTN_E_CUDA. */
+int attn_kv4_store(const void* k, const void* v, const attn_shape* shape, const attn_kv4_cache* cache,
+                   const int32_t* pos, const int32_t* cu_seqlens, void* ws, size_t ws_bytes, void* stream);
+
+/* The reverse of attn_kv4_store: the rows' values in bf16 (exact unless a value
+ * leaves bf16's range). Rows that attn_kv4_store would skip are left as they were
+ * (ATTN_E_BOUNDS). Errors as attn_kv4_store. */
+int attn_kv4_load(const attn_kv4_cache* cache, const int32_t* pos, const int32_t* cu_seqlens,
+                  const attn_shape* shape, void* k, void* v, void* ws, size_t ws_bytes, void* stream);
+
+/* Attention of the newest T tokens of each sequence over its cache (their own
+ * rows stored before the call). q, o: bf16 with the shape's (query) strides,
+ * shape B = cache B, H a multiple of cache Hkv (query head h reads key/value head
+ * h / (H / Hkv); the shape's own Hkv fields are ignored), T = 1 for single-token
+ * decoding, D = cache D. With n = lens[b] slots in use, query i sees
+ * the slots j <= n - T + i:
+ *   LSE_i = ln sum_j exp(scale * q_i . k_j),  O_i = sum_j exp(scale * q_i . k_j - LSE_i) v_j
+ * A query that sees no slot (n - T + i < 0; n = 0) has O = 0 and LSE = -inf.
+ * lse: fp32 [B][H][T] contiguous. mass_out (or NULL): the weight of each slot over
+ * the call's queries and the heads of its key/value head is added,
+ *   mass_out[b][hk][j] = mass_in[b][hk][j] + sum exp(scale * q_i . k_j - LSE_i)  for j < n,
+ * with rows of mass_ld fp32 (mass_in NULL: zeros; it may equal mass_out and must
+ * not overlap it otherwise); entries j >= n are left as they were. A length outside
+ * [0, cap] (with mass_out: or above mass_ld) is reported (ATTN_E_BOUNDS) and taken
+ * as the nearest in range. The products are made in fp16 with fp32 sums: cache
+ * values and queries (scaled by a power of two) are exact there, softmax weights
+ * are rounded to 11 bits. Errors as attn_kv4_store. */
+int attn_kv4_attend(const void* q, const attn_shape* shape, const attn_kv4_cache* cache, const int32_t* lens,
+                    void* o, float* lse, const float* mass_in, float* mass_out, int64_t mass_ld,
+                    void* ws, size_t ws_bytes, void* stream);
+
+/* Cut every sequence to at most `keep` slots: of the n = lens[b] slots in use, the
+ * last min(recent, keep) and those of the others with the highest mass (ties: the
+ * lowest slot; NaN counts as the highest), m = min(n, keep) in all, move to slots
+ * 0..m-1 of dst in their order, chosen for each key/value head on its own.
+ *   lens_out[b] = m;  slots[b][h][i] = the source slot of row i, -1 for m <= i < keep
+ *   mass_out[b][h][i] = mass[b][h][slots[b][h][i]]   (mass_out may be NULL)
+ * Rows m and on of dst and mass_out are left as they were. mass: rows of mass_ld
+ * fp32; mass_out: rows of mass_out_ld >= keep; slots: int32 [B][Hkv][keep]
+ * contiguous. src and dst have the same B, Hkv, D and tensor scales, dst.cap >= keep >= 1,
+ * 0 <= recent; src and dst, and mass and mass_out, must not overlap, and lens_out
+ * may equal lens. Lengths out of range as in attn_kv4_attend. Errors as
+ * attn_kv4_store. */
+int attn_kv4_evict(const attn_kv4_cache* src, const int32_t* lens, const float* mass, int64_t mass_ld,
+                   int32_t keep, int32_t recent, const attn_kv4_cache* dst, int32_t* lens_out,
+                   float* mass_out, int64_t mass_out_ld, int32_t* slots,
                    void* ws, size_t ws_bytes, void* stream);
 
 /* ---- forward without a caller-provided workspace ----------------------- */

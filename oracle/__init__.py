@@ -13,6 +13,8 @@ attention  the plain definition of causal softmax attention in float64 with an
            explicit score matrix, its analytic backward, sampled-row forms for
            long sequences, and the chunk-by-chunk method with the log-sum-exp
            merge that the chunked schedule is built on.
+kv4        the 4-bit key/value cache: its rounding, attention over it, the
+           attention weight of keys, eviction by that weight.
 
 Every function states the passage it follows. Parity is pinned by the
 ``-m "not gpu"`` tests in ``tests/test_oracle_*.py`` against brute force,
