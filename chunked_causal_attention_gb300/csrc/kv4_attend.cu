@@ -1,127 +1,811 @@
-// Attention of the newest tokens over the 4-bit cache: the simple form. One
-// block per query row, four warps over its keys with a running maximum and sum,
-// lanes over dims; the slots' weights by a second pass over the keys.
+// Attention of the newest tokens over the 4-bit cache.
+//
+//   s_rj = scale q_r . k_j,   O_r = sum_j 2^(s2_rj - m_r) v_j / l_r,   s2 = s log2 e
+//
+// A row of the call is one query of one head; the G = H / Hkv heads that share a
+// key/value head and the T new tokens make R = G T rows that read the same slots.
+// For few rows the call is bound by the bytes of the cache (0.5625 B a value), so
+// every byte is read once, by bulk copies into shared memory, and R rows share it.
+//
+// Split. The work is the list of 64-slot tiles of all units (sequence, key/value
+// head, group of 8 NT rows). Each block takes an equal stretch of that list, found
+// on the device from lens: no block idles whatever the lengths are, and the host
+// need not know them. A unit that lies in one block is finished there; the partials
+// (O, m, l) of a unit cut between blocks go to the workspace and merge_kernel joins
+// them in block order, so results do not depend on timing.
+//
+// Warps. Each of a block's four warps takes 16 slots of every tile, with its own
+// ring of bulk copies, running maximum and accumulators, and meets the others only
+// at a unit's end.
+//
+// Products. With few rows the matrix product's M side is the cache's: S^T = K Q^T
+// (16 slots x 8 rows) and O^T = V^T P^T (16 dims x 8 rows), mma m16n8k16 in fp16.
+// A value code * scale has at most 6 significant bits, so cvt.rn.f16x2.e2m1x2 and
+// one multiplication give it exactly in fp16. Queries are multiplied by a power of
+// two that brings the row's largest to [2^14, 2^15): their 8 bits are exact in fp16
+// down to 2^-28 of the largest. Which dim stands where in a product is free as long
+// as both sides agree, so each lane reads whole words of codes: for K lane c of a
+// quad holds a quarter of the row's words, for V^T lane g of the eight row groups
+// holds an eighth, and two slots' words are interleaved by two logical operations
+// into bytes that convert to (slot a, slot b) pairs.
+//
+// Softmax weights are rounded to fp16 too, after a factor 2^11 and with a running
+// maximum that may lag by up to 2^4: weights stay below 2^15, and those under 2^-35
+// of the row's largest are flushed (1M of them would be 2^-15 of the sum). l is
+// summed in fp32, one partial sum a lane.
+#include <algorithm>
+
 #include "kv4_device.cuh"
+#include "tc_common.cuh"
 
 namespace attn {
 namespace {
 
 using namespace kv4;
 
-__device__ __forceinline__ float warp_sum(float x) {
-#pragma unroll
-    for (int m = 16; m > 0; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
-    return x;
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kSlots = 16;                 // slots of a warp's slice
+constexpr int kTileSlots = kWarps * kSlots;
+constexpr float kLag = 4.f;                // how far (log2) a score may pass the running maximum
+constexpr float kUp = 11.f;                // weights are held times 2^kUp
+constexpr int kMaxGrid = 1024;
+
+// What the launch derives from the shapes.
+struct Split {
+    int32_t R, RT;        // rows of a key/value head; units they make
+    int32_t pitch;        // fp32 scores kept of each slot (mass), a row group
+    int64_t slot_floats;  // floats of a partial: 8 NT rows of D, then m and l of each
+    float* lse2;          // [B H T] log2 of the rows' sums (mass)
+    float* scores;        // [unit][cap][pitch]
+    uint64_t wait_ns;
+    int32_t stall;
+};
+
+template <int DT, int NT>
+struct Layout {
+    static constexpr int STAGES = DT == 256 ? 3 : 4;
+    static constexpr int CODES = kSlots * DT / 2, SCALES = kSlots * DT / 16;
+    static constexpr int STAGE = 2 * (CODES + SCALES);
+    static constexpr int RING = kWarps * STAGES * STAGE;
+    static constexpr int ROWS = 8 * NT;
+    static constexpr int O_PITCH = DT + 8;
+    static constexpr int O_OFF = RING;
+    static constexpr int Q_OFF = O_OFF + ROWS * O_PITCH * 4;
+    static constexpr int Q_BYTES = NT == 1 ? 0 : NT * (DT / 16) * 32 * 8;
+    static constexpr int QS_OFF = Q_OFF + Q_BYTES;                  // score factor of each row
+    static constexpr int ML_OFF = QS_OFF + ROWS * 4;               // m then l of each warp and row
+    static constexpr int BAR_OFF = ML_OFF + 2 * kWarps * ROWS * 4;
+    static constexpr int MISC_OFF = BAR_OFF + kWarps * STAGES * 8;
+    static constexpr int BYTES = MISC_OFF + 64;
+};
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+                 : "memory");
 }
 
-// This lane's 8 dims of a cached row.
-__device__ __forceinline__ void row8(const uint8_t* codes, const uint8_t* scales, float ts, int lane, bool on,
-                                     float (&x)[8]) {
-    const uint32_t c = on ? *reinterpret_cast<const uint32_t*>(codes + lane * 4) : 0u;
-    const uint32_t s = on ? scales[lane >> 1] : 0u;
-    const float d = __half2float(__low2half(as_half2(scales_f16x2(s)))) * ts;
-    const uint32_t f[4] = {codes_f16x2<0>(c), codes_f16x2<1>(c), codes_f16x2<2>(c), codes_f16x2<3>(c)};
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// 8x8 transpose of 16-bit elements across the warp.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// The bits of a where m is set, of b elsewhere.
+__device__ __forceinline__ uint32_t pick(uint32_t m, uint32_t a, uint32_t b) { return (a & m) | (b & ~m); }
+
+// Slots in use of sequence b.
+__device__ __forceinline__ int32_t slots_of(const Kv4AttendArgs& a, int32_t b) {
+    const int64_t most = a.mass_out && a.mass_ld < a.c.cap ? a.mass_ld : a.c.cap;
+    return length_of(a.lens, b, (int32_t)most, a.status);
+}
+
+__device__ __forceinline__ int32_t tiles_of(int32_t n) { return (n + kTileSlots - 1) / kTileSlots; }
+
+// First tile of block c when `total` tiles are dealt to `blocks` blocks.
+__device__ __forceinline__ int64_t first_tile(int64_t c, int64_t total, int32_t blocks) { return c * total / blocks; }
+
+// Block-wide sums over the sequences of their tiles: of all, and of those before sequence `upto`.
+template <int THREADS>
+__device__ __forceinline__ void sum_tiles(const Kv4AttendArgs& a, int32_t upto, int64_t& total, int64_t& before,
+                                          int64_t* scratch) {
+    int64_t all = 0, some = 0;
+    for (int b = threadIdx.x; b < a.c.B; b += THREADS) {
+        const int32_t t = tiles_of(slots_of(a, b));
+        all += t;
+        if (b < upto) some += t;
+    }
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) {
+        all += __shfl_xor_sync(0xffffffffu, all, m);
+        some += __shfl_xor_sync(0xffffffffu, some, m);
+    }
+    if ((threadIdx.x & 31) == 0) {
+        scratch[2 * (threadIdx.x >> 5)] = all;
+        scratch[2 * (threadIdx.x >> 5) + 1] = some;
+    }
+    __syncthreads();
+    total = before = 0;
+    for (int w = 0; w < THREADS / 32; ++w) {
+        total += scratch[2 * w];
+        before += scratch[2 * w + 1];
+    }
+    __syncthreads();
+}
+
+// A place in the tile list.
+struct Cursor {
+    int32_t b, v, t;      // sequence, unit of the sequence, tile of the unit
+    int32_t n, nt;        // the sequence's slots in use and tiles
+    __device__ __forceinline__ void next(const Kv4AttendArgs& a, int32_t units) {
+        if (++t < nt) return;
+        t = 0;
+        if (++v < units) return;
+        v = 0;
+        nt = 0;
+        while (nt == 0 && ++b < a.c.B) {
+            n = slots_of(a, b);
+            nt = tiles_of(n);
+        }
+    }
+};
+
+// The words (8 codes each) of a row that a lane holds for the K product: word i of lane c of the quad.
+template <int DT>
+__device__ __forceinline__ int k_word(int c, int i) {
+    return DT == 256 ? (i & 4) * 4 + 4 * c + (i & 3) : (DT / 32) * c + i;
+}
+
+template <int DT, int NT, bool EXACT, bool MASS>
+__global__ void __launch_bounds__(kThreads, NT == 1 && DT <= 128 ? 4 : 2)
+    split_kernel(const Kv4AttendArgs a, const Split sp) {
+    using L = Layout<DT, NT>;
+    constexpr int KW = DT / 32;            // K words a lane and row
+    constexpr int KB = DT / 64;            // K scales a lane and row
+    constexpr int VB = DT / 16;            // V bytes a lane and slot = 16-dim steps of O^T
+    extern __shared__ __align__(128) uint8_t sm[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int g = lane >> 2, c = lane & 3;
+    const int cb = EXACT ? DT / 2 : a.c.cb, nb = EXACT ? DT / 16 : a.c.nb, D = EXACT ? DT : a.c.D;
+    const int G = a.g.H / a.c.Hkv, units = a.c.Hkv * sp.RT;
+    float* sO = reinterpret_cast<float*>(sm + L::O_OFF);
+    uint2* sQ = reinterpret_cast<uint2*>(sm + L::Q_OFF);
+    float* sQS = reinterpret_cast<float*>(sm + L::QS_OFF);
+    float* sM = reinterpret_cast<float*>(sm + L::ML_OFF);
+    float* sL = sM + kWarps * L::ROWS;
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::MISC_OFF);
+    int64_t* scratch = reinterpret_cast<int64_t*>(sm + L::O_OFF);
+    const uint32_t ring = smem_u32(sm) + warp * L::STAGES * L::STAGE;
+    const uint8_t* ring_p = sm + warp * L::STAGES * L::STAGE;
+    const uint32_t bar = smem_u32(sm) + L::BAR_OFF + warp * L::STAGES * 8;
+
+    if (lane == 0)
+        for (int s = 0; s < L::STAGES; ++s) tc::mbar_init(bar + 8 * s, 1);
+    if (tid == 0) *abort_flag = 0;
+    tc::fence_barrier_init();
+
+    // ---- this block's stretch of the tile list
+    int64_t total, before;
+    sum_tiles<kThreads>(a, 0, total, before, scratch);
+    total *= units;
+    const int32_t blocks = (int32_t)min((int64_t)a.grid, total);
+    if ((int32_t)blockIdx.x >= blocks) return;
+    const int64_t t0 = first_tile(blockIdx.x, total, blocks), t1 = first_tile(blockIdx.x + 1, total, blocks);
+    Cursor cur{0, 0, 0, 0, 0};
+    {
+        int64_t left = t0;
+        cur.n = slots_of(a, 0);
+        cur.nt = tiles_of(cur.n);
+        while (left >= (int64_t)cur.nt * units) {       // t0 < total: ends at a sequence with tiles
+            left -= (int64_t)cur.nt * units;
+            ++cur.b;
+            cur.n = slots_of(a, cur.b);
+            cur.nt = tiles_of(cur.n);
+        }
+        cur.v = (int32_t)(left / cur.nt);
+        cur.t = (int32_t)(left - (int64_t)cur.v * cur.nt);
+    }
+
+    // ---- bulk copies of this warp's slices, in list order
+    Cursor ahead = cur;
+    int64_t to_fetch = t1 - t0;
+    uint32_t fetched = 0, used = 0;
+    bool ok = true;
+    auto fetch = [&]() {
+        if (to_fetch <= 0) return;
+        --to_fetch;
+        const int32_t k0 = ahead.t * kTileSlots + warp * kSlots;
+        if (k0 < ahead.n && ok) {
+            if (lane == 0 && !sp.stall) {
+                const int64_t row = (int64_t)ahead.b * a.c.sb + (int64_t)(ahead.v / sp.RT) * a.c.sh + k0;
+                const uint32_t s = fetched % L::STAGES, dst = ring + s * L::STAGE, f = bar + 8 * s;
+                const uint32_t nc = kSlots * cb, ns = kSlots * nb;
+                tc::mbar_expect_tx(f, 2 * (nc + ns));
+                bulk_load(dst, a.c.kc + row * cb, nc, f);
+                bulk_load(dst + 2 * L::CODES, a.c.ks + row * nb, ns, f);
+                bulk_load(dst + L::CODES, a.c.vc + row * cb, nc, f);
+                bulk_load(dst + 2 * L::CODES + L::SCALES, a.c.vs + row * nb, ns, f);
+            }
+            ++fetched;
+        }
+        if (to_fetch > 0) ahead.next(a, units);
+    };
+#pragma unroll
+    for (int s = 0; s < L::STAGES; ++s) fetch();
+
+    // slot of a 16-row fragment row: neighbours in a different half of a bank line for K's and V's reads
+    const int slot_lo = g ^ ((g >> 1) & 1);
+    int vrow[4];                                        // the fragment's columns 2c, 2c+1, 2c+8, 2c+9
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float2 y = __half22float2(as_half2(f[i]));
-        x[2 * i] = y.x * d;
-        x[2 * i + 1] = y.y * d;
+        const int r = 2 * c + (i & 1);
+        vrow[i] = (r ^ ((r >> 1) & 1)) + (i & 2) * 4;
     }
-}
 
-__device__ __forceinline__ void query8(const Kv4AttendArgs& a, int b, int h, int i, int lane, bool on, float (&q)[8]) {
-    const __nv_bfloat16* p = reinterpret_cast<const __nv_bfloat16*>(a.q) + (int64_t)b * a.g.sb + (int64_t)h * a.g.sh +
-                             (int64_t)i * a.g.st;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) q[j] = on ? __bfloat162float(p[lane * 8 + j]) : 0.f;
-}
+    uint32_t qf[NT == 1 ? DT / 16 : 1][2];
+    float qs[NT][2], m[NT][2], l[NT][2];
+    int32_t lim[NT][2];                                 // slots [0, lim) seen
+    int32_t lim_min = 0;                                // by every row
+    float o[NT][VB][4];
+    bool fresh = true;
 
-__global__ void __launch_bounds__(128) attend_rows(const Kv4AttendArgs a) {
-    const int r = blockIdx.x;                       // (b, h, i)
-    const int i = r % a.g.T, h = r / a.g.T % a.g.H, b = r / a.g.T / a.g.H;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const bool on = lane * 8 < a.c.D;
-    const int hk = h / (a.g.H / a.g.Hkv);
-    const int64_t most = a.mass_out && a.mass_ld < a.c.cap ? a.mass_ld : a.c.cap;
-    const int n = length_of(a.lens, b, (int32_t)most, a.status);
-    const int seen = n - a.g.T + i + 1;             // slots [0, seen)
-    float q[8], o[8] = {}, m = -INFINITY, l = 0.f;
-    query8(a, b, h, i, lane, on, q);
-    const int64_t row0 = (int64_t)b * a.c.sb + (int64_t)hk * a.c.sh;
-    for (int j = warp; j < seen; j += 4) {
-        float x[8];
-        row8(a.c.kc + (row0 + j) * a.c.cb, a.c.ks + (row0 + j) * a.c.nb, a.c.k_scale, lane, on, x);
-        float s = 0.f;
+    for (int64_t it = t0; it < t1; ++it) {
+        const int32_t hk = cur.v / sp.RT, rt = cur.v - hk * sp.RT;
+        if (fresh) {
+            // ---- a unit begins: its queries
+            fresh = false;
+            __syncthreads();                            // the last unit's sO, sQ, sQS are read
+            const int rows = min(L::ROWS, sp.R - rt * L::ROWS);
+#pragma unroll 1
+            for (int n = 0; n < NT; ++n) {
+                if (NT > 1 && (n & (kWarps - 1)) != warp) continue;
+                const int r = rt * L::ROWS + 8 * n + g;
+                const bool on = 8 * n + g < rows;
+                const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q) + (int64_t)cur.b * a.g.sb +
+                                         (int64_t)(hk * G + r % G) * a.g.sh + (int64_t)(r / G) * a.g.st;
+                uint32_t w[KW][4];
+                uint32_t top = 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s = fmaf(q[e], x[e], s);
-        s = warp_sum(s) * a.g.scale;
-        const float mn = s > m ? s : m;
-        const float w = expf(m - mn), p = expf(s - mn);
-        row8(a.c.vc + (row0 + j) * a.c.cb, a.c.vs + (row0 + j) * a.c.nb, a.c.v_scale, lane, on, x);
+                for (int i = 0; i < KW; ++i) {
+                    const int kw = k_word<DT>(c, i);
+                    uint4 x = make_uint4(0, 0, 0, 0);
+                    if (on && 8 * kw < D) x = *reinterpret_cast<const uint4*>(q + 8 * kw);
+                    w[i][0] = x.x; w[i][1] = x.y; w[i][2] = x.z; w[i][3] = x.w;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = fmaf(o[e], w, p * x[e]);
-        l = fmaf(l, w, p);
-        m = mn;
-    }
-    __shared__ float so[4][256], sm[4], sl[4];
+                    for (int j = 0; j < 4; ++j) top = max(top, max(w[i][j] & 0x7FFFu, (w[i][j] >> 16) & 0x7FFFu));
+                }
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                // 2^(14 - e), e the largest's exponent; 1 for a row of zeros or with a value that is not finite
+                int up = 14 - ((int)(top >> 7) - 127);
+                up = min(up, 120);
+                if (top == 0 || top >= 0x7F80u) up = 0;
+                const float f = __int_as_float((127 + up) << 23);
+                if (c == 0 && (NT > 1 || warp == 0))
+                    sQS[8 * n + g] = a.g.scale * kLog2e * __int_as_float((127 - up) << 23) * a.c.k_scale;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) so[warp][lane * 8 + e] = o[e];
-    if (lane == 0) { sm[warp] = m; sl[warp] = l; }
-    __syncthreads();
-    float top = -INFINITY;
-    for (int w = 0; w < 4; ++w) top = sl[w] != 0.f && !(sm[w] <= top) ? sm[w] : top;
-    float total = 0.f, f[4];
-    for (int w = 0; w < 4; ++w) {
-        f[w] = sl[w] != 0.f ? expf(sm[w] - top) : 0.f;
-        total += f[w] * sl[w];
-    }
-    const bool none = seen <= 0;
-    __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.o) + (int64_t)b * a.g.sb + (int64_t)h * a.g.sh +
-                         (int64_t)i * a.g.st;
-    for (int d = threadIdx.x; d < a.c.D; d += 128) {
-        float y = 0.f;
-        for (int w = 0; w < 4; ++w) y += sl[w] != 0.f ? f[w] * so[w][d] : 0.f;
-        out[d] = __float2bfloat16(none ? 0.f : y / total);
-    }
-    if (threadIdx.x == 0) a.lse[r] = none ? -INFINITY : top + logf(total);
-}
-
-// One warp per slot: its weight over the rows of its key/value head.
-__global__ void __launch_bounds__(256) attend_mass(const Kv4AttendArgs a) {
-    const int lane = threadIdx.x & 31;
-    const int j = blockIdx.x * 8 + (threadIdx.x >> 5), bh = blockIdx.y;
-    const int b = bh / a.c.Hkv, hk = bh % a.c.Hkv, G = a.g.H / a.c.Hkv;
-    const int n = length_of(a.lens, b, (int32_t)min((int64_t)a.c.cap, a.mass_ld), a.status);
-    if (j >= n) return;
-    const bool on = lane * 8 < a.c.D;
-    const int64_t row = (int64_t)b * a.c.sb + (int64_t)hk * a.c.sh + j;
-    float x[8], w = 0.f;
-    row8(a.c.kc + row * a.c.cb, a.c.ks + row * a.c.nb, a.c.k_scale, lane, on, x);
-    for (int h = hk * G; h < hk * G + G; ++h)
-        for (int i = 0; i < a.g.T; ++i) {
-            if (j > n - a.g.T + i) continue;
-            float q[8], s = 0.f;
-            query8(a, b, h, i, lane, on, q);
+                for (int i = 0; i < KW; ++i)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s = fmaf(q[e], x[e], s);
-            s = warp_sum(s) * a.g.scale;
-            w += expf(s - a.lse[((int64_t)b * a.g.H + h) * a.g.T + i]);
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t p[2];
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const uint32_t x = w[i][2 * half + j];
+                            p[j] = as_u32(__floats2half2_rn(__uint_as_float(x << 16) * f,
+                                                            __uint_as_float(x & 0xFFFF0000u) * f));
+                        }
+                        if constexpr (NT == 1) {
+                            qf[2 * i + half][0] = p[0];
+                            qf[2 * i + half][1] = p[1];
+                        } else {
+                            sQ[(n * (DT / 16) + 2 * i + half) * 32 + lane] = make_uint2(p[0], p[1]);
+                        }
+                    }
+            }
+            __syncthreads();
+            lim_min = cur.n - a.g.T + 1 + (rt * L::ROWS) / G;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int r = 8 * n + 2 * c + j;
+                    qs[n][j] = sQS[r];
+                    lim[n][j] = r < rows ? cur.n - a.g.T + 1 + (rt * L::ROWS + r) / G : 0;
+                    m[n][j] = -INFINITY;
+                    l[n][j] = 0.f;
+                }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < VB; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) o[n][i][j] = 0.f;
         }
-    if (lane == 0) {
-        const int64_t at = (int64_t)bh * a.mass_ld + j;
-        a.mass_out[at] = (a.mass_in ? a.mass_in[at] : 0.f) + w;
+
+        const int32_t k0 = cur.t * kTileSlots + warp * kSlots;
+        if (k0 < cur.n) {
+            const uint32_t st = used % L::STAGES;
+            if (ok) ok = tc::mbar_wait_warp(bar + 8 * st, (used / L::STAGES) & 1, abort_flag, a.status, sp.wait_ns);
+            if (ok) {
+                ++used;
+                const uint8_t* kc = ring_p + st * L::STAGE;
+                const uint8_t* vc = kc + L::CODES;
+                const uint8_t* ks = kc + 2 * L::CODES;
+                const uint8_t* vs = ks + L::SCALES;
+                const bool masked = k0 + kSlots > lim_min;
+
+                // ---- S^T = K Q^T
+                uint32_t kw[2][KW];
+                uint32_t ksc[2][KB];                    // scale of each block, in both halves
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int r = slot_lo + 8 * h;
+                    if constexpr (EXACT) {
+                        if constexpr (DT == 64) {
+                            const uint2 x = *reinterpret_cast<const uint2*>(kc + r * 32 + 8 * c);
+                            kw[h][0] = x.x; kw[h][1] = x.y;
+                            const uint32_t y = scales_f16x2(ks[r * 4 + c]);
+                            ksc[h][0] = __byte_perm(y, 0, 0x1010);
+                        } else {
+#pragma unroll
+                            for (int p = 0; p < DT / 128; ++p) {
+                                const uint4 x = *reinterpret_cast<const uint4*>(kc + r * (DT / 2) + 64 * p + 16 * c);
+                                kw[h][4 * p] = x.x; kw[h][4 * p + 1] = x.y; kw[h][4 * p + 2] = x.z; kw[h][4 * p + 3] = x.w;
+                                const uint32_t y = scales_f16x2(
+                                    *reinterpret_cast<const uint16_t*>(ks + r * (DT / 16) + 8 * p + 2 * c));
+                                ksc[h][2 * p] = __byte_perm(y, 0, 0x1010);
+                                ksc[h][2 * p + 1] = __byte_perm(y, 0, 0x3232);
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < KW; ++i) {
+                            const int wd = k_word<DT>(c, i);
+                            kw[h][i] = 8 * wd < D ? *reinterpret_cast<const uint32_t*>(kc + r * cb + 4 * wd) : 0u;
+                            if (!(i & 1))
+                                ksc[h][i / 2] = __byte_perm(scales_f16x2(8 * wd < D ? ks[r * nb + wd / 2] : 0), 0, 0x1010);
+                        }
+                    }
+                }
+                float s[NT][4];
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) s[n][j] = 0.f;
+#pragma unroll
+                for (int i = 0; i < KW; ++i) {
+                    const __half2 s0 = as_half2(ksc[0][i / 2]), s1 = as_half2(ksc[1][i / 2]);
+                    const uint32_t x0 = kw[0][i], x1 = kw[1][i];
+                    const uint32_t a0[4] = {as_u32(__hmul2(as_half2(codes_f16x2<0>(x0)), s0)),
+                                            as_u32(__hmul2(as_half2(codes_f16x2<0>(x1)), s1)),
+                                            as_u32(__hmul2(as_half2(codes_f16x2<1>(x0)), s0)),
+                                            as_u32(__hmul2(as_half2(codes_f16x2<1>(x1)), s1))};
+                    const uint32_t a1[4] = {as_u32(__hmul2(as_half2(codes_f16x2<2>(x0)), s0)),
+                                            as_u32(__hmul2(as_half2(codes_f16x2<2>(x1)), s1)),
+                                            as_u32(__hmul2(as_half2(codes_f16x2<3>(x0)), s0)),
+                                            as_u32(__hmul2(as_half2(codes_f16x2<3>(x1)), s1))};
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        if constexpr (NT == 1) {
+                            mma16816(s[n], a0, qf[2 * i][0], qf[2 * i][1]);
+                            mma16816(s[n], a1, qf[2 * i + 1][0], qf[2 * i + 1][1]);
+                        } else {
+                            const uint2 b0 = sQ[(n * (DT / 16) + 2 * i) * 32 + lane];
+                            const uint2 b1 = sQ[(n * (DT / 16) + 2 * i + 1) * 32 + lane];
+                            mma16816(s[n], a0, b0.x, b0.y);
+                            mma16816(s[n], a1, b1.x, b1.y);
+                        }
+                    }
+                }
+
+                // ---- weights
+                const int ka = k0 + slot_lo;            // this lane's slots: ka, ka + 8
+                bool over = false;
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float x = s[n][j] * qs[n][j & 1];
+                        if (masked && ka + (j & 2) * 4 >= lim[n][j & 1]) x = -INFINITY;
+                        s[n][j] = x;
+                        over |= x > m[n][j & 1] + kLag;
+                    }
+                if constexpr (MASS) {
+                    float* dst = sp.scores + ((int64_t)(cur.b * units + cur.v) * a.c.cap + ka) * sp.pitch + 2 * c;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        if (8 * n + 2 * c < sp.pitch) {
+                            if (ka < cur.n) *reinterpret_cast<float2*>(dst + 8 * n) = make_float2(s[n][0], s[n][1]);
+                            if (ka + 8 < cur.n)
+                                *reinterpret_cast<float2*>(dst + 8 * n + (int64_t)8 * sp.pitch) = make_float2(s[n][2], s[n][3]);
+                        }
+                }
+                if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            float x = fmaxf(s[n][j], s[n][j + 2]);
+                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                            x = fmaxf(x, m[n][j]);
+                            const float f = x == m[n][j] ? 1.f : ex2(m[n][j] - x);
+                            m[n][j] = x;
+                            l[n][j] *= f;
+#pragma unroll
+                            for (int i = 0; i < VB; ++i) {
+                                o[n][i][j] *= f;
+                                o[n][i][j + 2] *= f;
+                            }
+                        }
+                }
+                uint32_t p[NT][2];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const float b0 = m[n][0] == -INFINITY ? 0.f : m[n][0] - kUp;
+                    const float b1 = m[n][1] == -INFINITY ? 0.f : m[n][1] - kUp;
+                    const float p0 = ex2(s[n][0] - b0), p1 = ex2(s[n][1] - b1);
+                    const float p2 = ex2(s[n][2] - b0), p3 = ex2(s[n][3] - b1);
+                    l[n][0] += p0 + p2;
+                    l[n][1] += p1 + p3;
+                    p[n][0] = transpose8(as_u32(__floats2half2_rn(p0, p1)));
+                    p[n][1] = transpose8(as_u32(__floats2half2_rn(p2, p3)));
+                }
+
+                // ---- O^T += V^T P^T
+                constexpr int VW = VB >= 4 ? VB / 4 : 1;    // words a lane and slot
+                uint32_t vw[4][VW];
+                uint32_t vsc[2][DT == 256 ? 2 : 1];         // scales of slot pairs
+                uint32_t vraw[4][DT == 256 ? 2 : 1];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if constexpr (EXACT) {
+                        const uint8_t* p8 = vc + vrow[i] * (DT / 2) + VB * g;
+                        if constexpr (DT == 64) vw[i][0] = *reinterpret_cast<const uint32_t*>(p8);
+                        if constexpr (DT == 128) {
+                            const uint2 x = *reinterpret_cast<const uint2*>(p8);
+                            vw[i][0] = x.x; vw[i][1] = x.y;
+                        }
+                        if constexpr (DT == 256) {
+                            const uint4 x = *reinterpret_cast<const uint4*>(p8);
+                            vw[i][0] = x.x; vw[i][1] = x.y; vw[i][2] = x.z; vw[i][3] = x.w;
+                        }
+                        if constexpr (DT == 256) {
+                            const uint32_t y = *reinterpret_cast<const uint16_t*>(vs + vrow[i] * 16 + 2 * g);
+                            vraw[i][0] = y & 0xFF;
+                            vraw[i][1] = y >> 8;
+                        } else {
+                            vraw[i][0] = vs[vrow[i] * (DT / 16) + (DT == 64 ? g >> 1 : g)];
+                        }
+                    } else {
+#pragma unroll
+                        for (int w = 0; w < VW; ++w) {
+                            const int wd = VW * g + w;
+                            vw[i][w] = 8 * wd < D ? *reinterpret_cast<const uint32_t*>(vc + vrow[i] * cb + 4 * wd) : 0u;
+                            if (w % 2 == 0) vraw[i][w / 2] = 8 * wd < D ? vs[vrow[i] * nb + wd / 2] : 0u;
+                        }
+                    }
+                }
+                bool nan = false;
+                if (masked) {
+                    // slots behind the last one hold anything: scale 0. NaN scales of slots that some
+                    // rows do not see are kept out of the product and given to the rows that do
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int y = 0; y < (DT == 256 ? 2 : 1); ++y) {
+                            if (k0 + vrow[i] >= cur.n) vraw[i][y] = 0;
+                            if ((vraw[i][y] & 0x7F) == 0x7F) {
+                                nan = true;
+                                vraw[i][y] = 0;
+                            }
+                        }
+                }
+#pragma unroll
+                for (int y = 0; y < (DT == 256 ? 2 : 1); ++y) {
+                    vsc[0][y] = scales_f16x2(vraw[0][y] | vraw[1][y] << 8);
+                    vsc[1][y] = scales_f16x2(vraw[2][y] | vraw[3][y] << 8);
+                }
+#pragma unroll
+                for (int w = 0; w < VW; ++w) {
+                    constexpr uint32_t M = 0x0F0F0F0Fu;
+                    const uint32_t lo0 = pick(M, vw[0][w], vw[1][w] << 4), hi0 = pick(M, vw[0][w] >> 4, vw[1][w]);
+                    const uint32_t lo1 = pick(M, vw[2][w], vw[3][w] << 4), hi1 = pick(M, vw[2][w] >> 4, vw[3][w]);
+                    const __half2 s0 = as_half2(vsc[0][w / 2]), s1 = as_half2(vsc[1][w / 2]);
+                    auto step = [&](int i, uint32_t l0, uint32_t h0, uint32_t l1, uint32_t h1) {
+                        const uint32_t av[4] = {as_u32(__hmul2(as_half2(l0), s0)), as_u32(__hmul2(as_half2(h0), s0)),
+                                                as_u32(__hmul2(as_half2(l1), s1)), as_u32(__hmul2(as_half2(h1), s1))};
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) mma16816(o[n][4 * w + i], av, p[n][0], p[n][1]);
+                    };
+                    step(0, codes_f16x2<0>(lo0), codes_f16x2<0>(hi0), codes_f16x2<0>(lo1), codes_f16x2<0>(hi1));
+                    step(1, codes_f16x2<1>(lo0), codes_f16x2<1>(hi0), codes_f16x2<1>(lo1), codes_f16x2<1>(hi1));
+                    step(2, codes_f16x2<2>(lo0), codes_f16x2<2>(hi0), codes_f16x2<2>(lo1), codes_f16x2<2>(hi1));
+                    step(3, codes_f16x2<3>(lo0), codes_f16x2<3>(hi0), codes_f16x2<3>(lo1), codes_f16x2<3>(hi1));
+                }
+                if (masked && __any_sync(0xffffffffu, nan)) {
+                    for (int k = 0; k < kSlots; ++k)
+#pragma unroll
+                        for (int w = 0; w < VW; ++w) {
+                            const int wd = VW * g + w;
+                            if (8 * wd >= D || k0 + k >= cur.n || (vs[k * nb + wd / 2] & 0x7F) != 0x7F) continue;
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i)
+                                        if (k0 + k < lim[n][j & 1]) o[n][4 * w + i][j] = __int_as_float(0x7FC00000);
+                        }
+                }
+            }
+            __syncwarp();                               // the slice is read: its stage may be filled again
+        }
+        fetch();
+
+        if (cur.t == cur.nt - 1 || it == t1 - 1) {
+            // ---- the unit, or this block's share of it, ends: join the warps
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    float x = l[n][j];
+                    x += __shfl_xor_sync(0xffffffffu, x, 4);
+                    x += __shfl_xor_sync(0xffffffffu, x, 8);
+                    x += __shfl_xor_sync(0xffffffffu, x, 16);
+                    if (g == 0) {
+                        sM[warp * L::ROWS + 8 * n + 2 * c + j] = m[n][j];
+                        sL[warp * L::ROWS + 8 * n + 2 * c + j] = x;
+                    }
+                }
+            __syncthreads();
+            float f[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int r = 8 * n + 2 * c + j;
+                    float top = sM[r];
+                    for (int w = 1; w < kWarps; ++w) top = fmaxf(top, sM[w * L::ROWS + r]);
+                    f[n][j] = m[n][j] == -INFINITY ? 0.f : ex2(m[n][j] - top);
+                }
+            for (int w = 0; w < kWarps; ++w) {
+                if (warp == w) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            float2* dst = reinterpret_cast<float2*>(sO + (8 * n + 2 * c + j) * L::O_PITCH + 2 * VB * g);
+#pragma unroll
+                            for (int i = 0; i < VB; ++i) {
+                                float2 x = make_float2(o[n][i][j] * f[n][j], o[n][i][j + 2] * f[n][j]);
+                                if (w) x = make_float2(x.x + dst[i].x, x.y + dst[i].y);
+                                dst[i] = x;
+                            }
+                        }
+                }
+                __syncthreads();
+            }
+            const int rows = min(L::ROWS, sp.R - rt * L::ROWS);
+            const bool begins = it - cur.t >= t0, ends = cur.t == cur.nt - 1;
+            float* part = a.parts + (2 * (int64_t)blockIdx.x + (begins ? 1 : 0)) * sp.slot_floats;
+            for (int r = warp; r < rows; r += kWarps) {
+                float top = sM[r], sum = 0.f;
+                for (int w = 1; w < kWarps; ++w) top = fmaxf(top, sM[w * L::ROWS + r]);
+                for (int w = 0; w < kWarps; ++w) {
+                    const float mw = sM[w * L::ROWS + r];
+                    sum += sL[w * L::ROWS + r] * (mw == -INFINITY ? 0.f : ex2(mw - top));
+                }
+                if (begins && ends) {
+                    const int rr = rt * L::ROWS + r, h = hk * G + rr % G, i = rr / G;
+                    const bool none = cur.n - a.g.T + 1 + i <= 0;
+                    const float inv = none ? 0.f : a.c.v_scale / sum;
+                    __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(a.o) + (int64_t)cur.b * a.g.sb +
+                                         (int64_t)h * a.g.sh + (int64_t)i * a.g.st;
+                    for (int d = 2 * lane; d < D; d += 64)
+                        *reinterpret_cast<uint32_t*>(dst + d) = pack_bf16(sO[r * L::O_PITCH + d] * inv, sO[r * L::O_PITCH + d + 1] * inv);
+                    if (lane == 0) {
+                        const float l2 = none ? -INFINITY : top - kUp + lg2(sum);
+                        const int64_t at = ((int64_t)cur.b * a.g.H + h) * a.g.T + i;
+                        a.lse[at] = l2 * kLn2;
+                        if (MASS) sp.lse2[at] = l2;
+                    }
+                } else {
+                    for (int d = 2 * lane; d < D; d += 64)
+                        *reinterpret_cast<float2*>(part + (int64_t)r * D + d) =
+                            *reinterpret_cast<const float2*>(sO + r * L::O_PITCH + d);
+                    if (lane == 0) {
+                        part[(int64_t)L::ROWS * D + r] = top;
+                        part[(int64_t)L::ROWS * D + L::ROWS + r] = sum;
+                    }
+                }
+            }
+            fresh = true;
+        }
+        if (it + 1 < t1) cur.next(a, units);
     }
+    // a wait gave up: this warp's copies in flight end (bounded) before the block does
+    for (; used < fetched; ++used) {
+        const uint64_t begin = tc::globaltimer();
+        while (!tc::mbar_try_wait(bar + 8 * (used % L::STAGES), (used / L::STAGES) & 1) &&
+               tc::globaltimer() - begin < sp.wait_ns) {
+        }
+    }
+}
+
+// Rows of units that no block finished: the partials of the blocks that share the
+// unit, in block order; and the rows of empty sequences. One block per (unit, row).
+constexpr int kMergeThreads = 128;
+__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Kv4AttendArgs a, const Split sp, int32_t unit_rows) {
+    __shared__ int64_t scratch[2 * kMergeThreads / 32];
+    __shared__ float weight[kMaxGrid], red[kMergeThreads / 32];
+    const int tid = threadIdx.x, G = a.g.H / a.c.Hkv, units = a.c.Hkv * sp.RT;
+    const int u = blockIdx.x / unit_rows, r = blockIdx.x - u * unit_rows;
+    const int b = u / units, v = u - b * units, hk = v / sp.RT, rt = v - hk * sp.RT;
+    const int rr = rt * unit_rows + r;
+    if (rr >= sp.R) return;
+    const int h = hk * G + rr % G, i = rr / G, D = a.c.D;
+    const int64_t at = ((int64_t)b * a.g.H + h) * a.g.T + i;
+    __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(a.o) + (int64_t)b * a.g.sb + (int64_t)h * a.g.sh +
+                         (int64_t)i * a.g.st;
+    const int32_t n = slots_of(a, b);
+    int64_t total, before;
+    sum_tiles<kMergeThreads>(a, b, total, before, scratch);
+    total *= units;
+    const bool none = n - a.g.T + 1 + i <= 0;
+    if (none) {
+        for (int d = tid; d < D; d += kMergeThreads) dst[d] = __float2bfloat16(0.f);
+        if (tid == 0) {
+            a.lse[at] = -INFINITY;
+            if (sp.lse2) sp.lse2[at] = -INFINITY;
+        }
+        return;
+    }
+    const int32_t blocks = (int32_t)min((int64_t)a.grid, total);
+    const int64_t first = before * units + (int64_t)v * tiles_of(n), last = first + tiles_of(n) - 1;
+    const int c0 = (int)(((first + 1) * blocks - 1) / total), c1 = (int)(((last + 1) * blocks - 1) / total);
+    if (c0 == c1) return;                               // finished by its block
+    // block c0 holds the unit's begin: there the partial is the block's second
+    auto slot = [&](int c) { return a.parts + (2 * (int64_t)c + (c == c0 ? 1 : 0)) * sp.slot_floats; };
+    const int64_t off_m = (int64_t)unit_rows * D + r, off_l = off_m + unit_rows;
+    auto block_max = [&](float x) {
+#pragma unroll
+        for (int m = 16; m > 0; m >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, m));
+        __syncthreads();
+        if ((tid & 31) == 0) red[tid >> 5] = x;
+        __syncthreads();
+        return fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+    };
+    float top = -INFINITY;
+    for (int c = c0 + tid; c <= c1; c += kMergeThreads) top = fmaxf(top, slot(c)[off_m]);
+    top = block_max(top);
+    float sum = 0.f;
+    for (int c = c0 + tid; c <= c1; c += kMergeThreads) {
+        const float mc = slot(c)[off_m];
+        const float w = mc == -INFINITY ? 0.f : ex2(mc - top);
+        weight[c - c0] = w;
+        sum += w * slot(c)[off_l];
+    }
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+    __syncthreads();
+    if ((tid & 31) == 0) red[tid >> 5] = sum;
+    __syncthreads();
+    sum = (red[0] + red[1]) + (red[2] + red[3]);
+    const float inv = a.c.v_scale / sum;
+    for (int d = tid; d < D; d += kMergeThreads) {
+        float y = 0.f;
+#pragma unroll 4
+        for (int c = c0; c <= c1; ++c) y = fmaf(weight[c - c0], slot(c)[(int64_t)r * D + d], y);
+        dst[d] = __float2bfloat16(y * inv);
+    }
+    if (tid == 0) {
+        const float l2 = top - kUp + lg2(sum);
+        a.lse[at] = l2 * kLn2;
+        if (sp.lse2) sp.lse2[at] = l2;
+    }
+}
+
+// mass_out = mass_in + sum over the rows of 2^(s2 - lse2), from the scores that the split kernel kept.
+__global__ void __launch_bounds__(256) mass_kernel(const Kv4AttendArgs a, const Split sp, int32_t unit_rows) {
+    const int chunks = (a.c.cap + 255) / 256;
+    const int bh = blockIdx.x / chunks, b = bh / a.c.Hkv, hk = bh - b * a.c.Hkv, G = a.g.H / a.c.Hkv;
+    const int32_t n = slots_of(a, b);
+    const int j = (blockIdx.x - bh * chunks) * 256 + threadIdx.x;
+    if (j >= n) return;
+    float w = 0.f;
+    for (int rt = 0; rt < sp.RT; ++rt) {
+        const float* s = sp.scores + ((int64_t)((int64_t)bh * sp.RT + rt) * a.c.cap + j) * sp.pitch;
+        const int rows = min(unit_rows, sp.R - rt * unit_rows);
+        for (int r = 0; r < rows; ++r) {
+            const int rr = rt * unit_rows + r;
+            const float l2 = sp.lse2[((int64_t)b * a.g.H + hk * G + rr % G) * a.g.T + rr / G];
+            w += l2 == -INFINITY ? 0.f : ex2(s[r] - l2);
+        }
+    }
+    const int64_t at = (int64_t)bh * a.mass_ld + j;
+    a.mass_out[at] = (a.mass_in ? a.mass_in[at] : 0.f) + w;
+}
+
+int row_tiles(int D, int64_t R) { return R <= 8 ? 1 : (R <= 16 || D > 128) ? 2 : 4; }
+
+int blocks_per_sm(int D, int nt) { return nt == 1 && D <= 128 ? 4 : 2; }
+
+struct Plan {
+    int nt, grid;
+    Split sp;
+    int64_t parts, lse2, scores;      // floats
+};
+
+Plan plan_of(const Kv4Geom& c, const Geom& g, bool mass) {
+    Plan p;
+    const int64_t R = (int64_t)(g.H / c.Hkv) * g.T;
+    p.nt = row_tiles(c.D, R);
+    p.sp.R = (int32_t)R;
+    p.sp.RT = (int32_t)((R + 8 * p.nt - 1) / (8 * p.nt));
+    p.sp.pitch = R <= 2 ? 2 : R <= 4 ? 4 : 8 * p.nt;
+    p.sp.slot_floats = (int64_t)8 * p.nt * (c.D + 2);
+    const int64_t units = (int64_t)c.B * c.Hkv * p.sp.RT;
+    const int64_t tiles = units * ((c.cap + kTileSlots - 1) / kTileSlots);
+    p.grid = (int)std::min<int64_t>(std::min(device_sm_count() * blocks_per_sm(c.D, p.nt), kMaxGrid), tiles);
+    p.parts = 2 * (int64_t)p.grid * p.sp.slot_floats;
+    p.lse2 = mass ? ((int64_t)g.B * g.H * g.T + 63) / 64 * 64 : 0;
+    p.scores = mass ? units * c.cap * p.sp.pitch : 0;
+    return p;
+}
+
+template <int DT, int NT, bool EXACT, bool MASS>
+cudaError_t launch_split(const Kv4AttendArgs& a, const Plan& p, cudaStream_t s) {
+    constexpr int bytes = Layout<DT, NT>::BYTES;
+    cudaError_t e = cudaFuncSetAttribute(split_kernel<DT, NT, EXACT, MASS>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    split_kernel<DT, NT, EXACT, MASS><<<p.grid, kThreads, bytes, s>>>(a, p.sp);
+    return counted(cudaGetLastError());
+}
+
+template <int DT, int NT>
+cudaError_t launch_dims(const Kv4AttendArgs& a, const Plan& p, cudaStream_t s) {
+    if (a.c.D == DT) return a.mass_out ? launch_split<DT, NT, true, true>(a, p, s) : launch_split<DT, NT, true, false>(a, p, s);
+    return a.mass_out ? launch_split<DT, NT, false, true>(a, p, s) : launch_split<DT, NT, false, false>(a, p, s);
 }
 
 }  // namespace
 
-size_t kv4_attend_bytes(const Kv4Geom&, const Geom&, bool) { return 0; }
+size_t kv4_attend_bytes(const Kv4Geom& c, const Geom& g, bool mass) {
+    const Plan p = plan_of(c, g, mass);
+    return (size_t)(p.parts + p.lse2 + p.scores) * 4;
+}
 
-cudaError_t launch_kv4_attend(const Kv4AttendArgs& a, cudaStream_t s) {
-    attend_rows<<<a.g.B * a.g.H * a.g.T, 128, 0, s>>>(a);
-    cudaError_t e = counted(cudaGetLastError());
+cudaError_t launch_kv4_attend(const Kv4AttendArgs& args, cudaStream_t s) {
+    Kv4AttendArgs a = args;
+    Plan p = plan_of(a.c, a.g, a.mass_out != nullptr);
+    a.grid = p.grid;
+    p.sp.lse2 = a.mass_out ? a.parts + p.parts : nullptr;
+    p.sp.scores = a.mass_out ? a.parts + p.parts + p.lse2 : nullptr;
+    wait_settings(&p.sp.wait_ns, &p.sp.stall);
+    cudaError_t e;
+    if (a.c.D <= 64)
+        e = p.nt == 1 ? launch_dims<64, 1>(a, p, s) : p.nt == 2 ? launch_dims<64, 2>(a, p, s) : launch_dims<64, 4>(a, p, s);
+    else if (a.c.D <= 128)
+        e = p.nt == 1 ? launch_dims<128, 1>(a, p, s) : p.nt == 2 ? launch_dims<128, 2>(a, p, s) : launch_dims<128, 4>(a, p, s);
+    else
+        e = p.nt == 1 ? launch_dims<256, 1>(a, p, s) : launch_dims<256, 2>(a, p, s);
+    if (e != cudaSuccess) return e;
+    const int unit_rows = 8 * p.nt;
+    const int64_t rows = (int64_t)a.c.B * a.c.Hkv * p.sp.RT * unit_rows;
+    merge_kernel<<<(unsigned)rows, kMergeThreads, 0, s>>>(a, p.sp, unit_rows);
+    e = counted(cudaGetLastError());
     if (e != cudaSuccess || !a.mass_out) return e;
-    attend_mass<<<dim3((a.c.cap + 7) / 8, a.c.B * a.c.Hkv), 256, 0, s>>>(a);
+    mass_kernel<<<(unsigned)((int64_t)((a.c.cap + 255) / 256) * a.c.B * a.c.Hkv), 256, 0, s>>>(a, p.sp, unit_rows);
     return counted(cudaGetLastError());
 }
 

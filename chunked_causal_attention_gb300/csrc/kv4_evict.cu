@@ -99,12 +99,13 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const Kv4EvictArgs a) 
 
 // One warp per kept row: its codes, scales and mass. Block (0, 0) writes the lengths.
 __global__ void __launch_bounds__(256) move_kernel(const Kv4EvictArgs a) {
-    const int bh = blockIdx.y, b = bh / a.src.Hkv, h = bh % a.src.Hkv, lane = threadIdx.x & 31;
-    if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) {
+    const int chunks = (a.keep + 7) / 8, bh = blockIdx.x / chunks, chunk = blockIdx.x - bh * chunks;
+    const int b = bh / a.src.Hkv, h = bh % a.src.Hkv, lane = threadIdx.x & 31;
+    if (chunk == 0 && h == 0 && threadIdx.x == 0) {
         const int n = min(max(a.lens[b], 0), (int)min((int64_t)a.src.cap, a.mass_ld));
         a.lens_out[b] = min(n, a.keep);
     }
-    const int i = blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int i = chunk * 8 + (threadIdx.x >> 5);
     if (i >= a.keep) return;
     const int j = a.slots[(int64_t)bh * a.keep + i];
     if (j < 0 || j >= a.src.cap) return;
@@ -128,7 +129,7 @@ cudaError_t launch_kv4_evict(const Kv4EvictArgs& a, cudaStream_t s) {
     choose_kernel<<<BH, kThreads, 0, s>>>(a);
     cudaError_t e = counted(cudaGetLastError());
     if (e != cudaSuccess) return e;
-    move_kernel<<<dim3((a.keep + 7) / 8, BH), 256, 0, s>>>(a);
+    move_kernel<<<(unsigned)((int64_t)((a.keep + 7) / 8) * BH), 256, 0, s>>>(a);
     return counted(cudaGetLastError());
 }
 
