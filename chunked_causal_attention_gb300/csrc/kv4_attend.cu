@@ -7,14 +7,14 @@
 // For few rows the call is bound by the bytes of the cache (0.5625 B a value), so
 // every byte is read once, by bulk copies into shared memory, and R rows share it.
 //
-// Split. The work is the list of 64-slot tiles of all units (sequence, key/value
+// Split. The work is the list of 64- or 128-slot tiles of all units (sequence, key/value
 // head, group of 8 NT rows). Each block takes an equal stretch of that list, found
 // on the device from lens: no block idles whatever the lengths are, and the host
 // need not know them. A unit that lies in one block is finished there; the partials
 // (O, m, l) of a unit cut between blocks go to the workspace and merge_kernel joins
 // them in block order, so results do not depend on timing.
 //
-// Warps. Each of a block's four warps takes 16 slots of every tile, with its own
+// Warps. Each of a block's four warps takes 16 or 32 slots of every tile, with its own
 // ring of bulk copies, running maximum and accumulators, and meets the others only
 // at a unit's end.
 //
@@ -45,8 +45,7 @@ using namespace kv4;
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kSlots = 16;                 // slots of a warp's slice
-constexpr int kTileSlots = kWarps * kSlots;
+constexpr int kSlots = 16;                 // slots of a fragment; a warp's slice is one or two of them
 constexpr float kLag = 4.f;                // how far (log2) a score may pass the running maximum
 constexpr float kUp = 11.f;                // weights are held times 2^kUp
 constexpr int kMaxGrid = 1024;
@@ -62,10 +61,17 @@ struct Split {
     int32_t stall;
 };
 
+__host__ __device__ constexpr int blocks_per_sm(int dt, int nt) { return nt == 1 && dt <= 128 ? 4 : 2; }
+
+// Fragments of 16 slots in a warp's slice: two where the registers of a second one are there.
+__host__ __device__ constexpr int fragments(int dt, int nt) { return nt == 1 && dt <= 128 ? 2 : 1; }
+__host__ __device__ constexpr int tile_slots(int dt, int nt) { return kWarps * kSlots * fragments(dt, nt); }
+
 template <int DT, int NT>
 struct Layout {
-    static constexpr int STAGES = DT == 256 ? 3 : 4;
-    static constexpr int CODES = kSlots * DT / 2, SCALES = kSlots * DT / 16;
+    static constexpr int KS = fragments(DT, NT), SLOTS = kSlots * KS, TILE = tile_slots(DT, NT);
+    static constexpr int STAGES = KS == 2 ? 2 : DT == 256 ? 3 : 4;
+    static constexpr int CODES = SLOTS * DT / 2, SCALES = SLOTS * DT / 16;
     static constexpr int STAGE = 2 * (CODES + SCALES);
     static constexpr int RING = kWarps * STAGES * STAGE;
     static constexpr int ROWS = 8 * NT;
@@ -99,6 +105,13 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     return y;
 }
 
+// Programmatic dependent launch: a kernel launched with it may start while the one
+// before it in the stream runs, and waits here until that one has ended and its
+// writes are visible.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+// Let the next kernel of the stream be launched.
+__device__ __forceinline__ void grid_go() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
+
 // The bits of a where m is set, of b elsewhere.
 __device__ __forceinline__ uint32_t pick(uint32_t m, uint32_t a, uint32_t b) { return (a & m) | (b & ~m); }
 
@@ -108,18 +121,19 @@ __device__ __forceinline__ int32_t slots_of(const Kv4AttendArgs& a, int32_t b) {
     return length_of(a.lens, b, (int32_t)most, a.status);
 }
 
-__device__ __forceinline__ int32_t tiles_of(int32_t n) { return (n + kTileSlots - 1) / kTileSlots; }
+template <int TILE>
+__device__ __forceinline__ int32_t tiles_of(int32_t n) { return (n + TILE - 1) / TILE; }
 
 // First tile of block c when `total` tiles are dealt to `blocks` blocks.
 __device__ __forceinline__ int64_t first_tile(int64_t c, int64_t total, int32_t blocks) { return c * total / blocks; }
 
 // Block-wide sums over the sequences of their tiles: of all, and of those before sequence `upto`.
-template <int THREADS>
+template <int THREADS, int TILE>
 __device__ __forceinline__ void sum_tiles(const Kv4AttendArgs& a, int32_t upto, int64_t& total, int64_t& before,
                                           int64_t* scratch) {
     int64_t all = 0, some = 0;
     for (int b = threadIdx.x; b < a.c.B; b += THREADS) {
-        const int32_t t = tiles_of(slots_of(a, b));
+        const int32_t t = tiles_of<TILE>(slots_of(a, b));
         all += t;
         if (b < upto) some += t;
     }
@@ -145,16 +159,19 @@ __device__ __forceinline__ void sum_tiles(const Kv4AttendArgs& a, int32_t upto, 
 struct Cursor {
     int32_t b, v, t;      // sequence, unit of the sequence, tile of the unit
     int32_t n, nt;        // the sequence's slots in use and tiles
-    __device__ __forceinline__ void next(const Kv4AttendArgs& a, int32_t units) {
-        if (++t < nt) return;
+    // The next tile; true if it is another unit's.
+    template <int TILE>
+    __device__ __forceinline__ bool next(const Kv4AttendArgs& a, int32_t units) {
+        if (++t < nt) return false;
         t = 0;
-        if (++v < units) return;
+        if (++v < units) return true;
         v = 0;
         nt = 0;
         while (nt == 0 && ++b < a.c.B) {
             n = slots_of(a, b);
-            nt = tiles_of(n);
+            nt = tiles_of<TILE>(n);
         }
+        return true;
     }
 };
 
@@ -165,12 +182,14 @@ __device__ __forceinline__ int k_word(int c, int i) {
 }
 
 template <int DT, int NT, bool EXACT, bool MASS>
-__global__ void __launch_bounds__(kThreads, NT == 1 && DT <= 128 ? 4 : 2)
-    split_kernel(const Kv4AttendArgs a, const Split sp) {
+__global__ void __launch_bounds__(kThreads, blocks_per_sm(DT, NT)) split_kernel(const Kv4AttendArgs a, const Split sp) {
     using L = Layout<DT, NT>;
+    constexpr int KS = L::KS;
     constexpr int KW = DT / 32;            // K words a lane and row
     constexpr int KB = DT / 64;            // K scales a lane and row
     constexpr int VB = DT / 16;            // V bytes a lane and slot = 16-dim steps of O^T
+    constexpr int VW = VB / 4;             // V words a lane and slot
+    constexpr int VS = DT == 256 ? 2 : 1;  // V scales a lane and slot
     extern __shared__ __align__(128) uint8_t sm[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, c = lane & 3;
@@ -192,23 +211,26 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && DT <= 128 ? 4 : 2)
     if (tid == 0) *abort_flag = 0;
     tc::fence_barrier_init();
 
+    grid_go();
+
     // ---- this block's stretch of the tile list
     int64_t total, before;
-    sum_tiles<kThreads>(a, 0, total, before, scratch);
+    sum_tiles<kThreads, L::TILE>(a, 0, total, before, scratch);
     total *= units;
     const int32_t blocks = (int32_t)min((int64_t)a.grid, total);
     if ((int32_t)blockIdx.x >= blocks) return;
-    const int64_t t0 = first_tile(blockIdx.x, total, blocks), t1 = first_tile(blockIdx.x + 1, total, blocks);
+    const int64_t t0 = first_tile(blockIdx.x, total, blocks);
+    const int32_t n_tiles = (int32_t)(first_tile(blockIdx.x + 1, total, blocks) - t0);
     Cursor cur{0, 0, 0, 0, 0};
     {
         int64_t left = t0;
         cur.n = slots_of(a, 0);
-        cur.nt = tiles_of(cur.n);
+        cur.nt = tiles_of<L::TILE>(cur.n);
         while (left >= (int64_t)cur.nt * units) {       // t0 < total: ends at a sequence with tiles
             left -= (int64_t)cur.nt * units;
             ++cur.b;
             cur.n = slots_of(a, cur.b);
-            cur.nt = tiles_of(cur.n);
+            cur.nt = tiles_of<L::TILE>(cur.n);
         }
         cur.v = (int32_t)(left / cur.nt);
         cur.t = (int32_t)(left - (int64_t)cur.v * cur.nt);
@@ -216,18 +238,23 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && DT <= 128 ? 4 : 2)
 
     // ---- bulk copies of this warp's slices, in list order
     Cursor ahead = cur;
-    int64_t to_fetch = t1 - t0;
-    uint32_t fetched = 0, used = 0;
+    int64_t ahead_row = 0;                              // cache row of slot 0 of the unit ahead
+    auto unit_row = [&]() { ahead_row = (int64_t)ahead.b * a.c.sb + (int64_t)(ahead.v / sp.RT) * a.c.sh; };
+    unit_row();
+    int32_t to_fetch = n_tiles;
+    uint32_t fetched = 0, fetch_stage = 0, used = 0, use_stage = 0, use_parity = 0;
     bool ok = true;
     auto fetch = [&]() {
         if (to_fetch <= 0) return;
         --to_fetch;
-        const int32_t k0 = ahead.t * kTileSlots + warp * kSlots;
+        const int32_t k0 = ahead.t * L::TILE + warp * L::SLOTS;
         if (k0 < ahead.n && ok) {
             if (lane == 0 && !sp.stall) {
-                const int64_t row = (int64_t)ahead.b * a.c.sb + (int64_t)(ahead.v / sp.RT) * a.c.sh + k0;
-                const uint32_t s = fetched % L::STAGES, dst = ring + s * L::STAGE, f = bar + 8 * s;
-                const uint32_t nc = kSlots * cb, ns = kSlots * nb;
+                const int64_t row = ahead_row + k0;
+                const uint32_t dst = ring + fetch_stage * L::STAGE, f = bar + 8 * fetch_stage;
+                // whole slices, but no further than the 16 slots that hold the last one (the capacity is a multiple of 16)
+                const uint32_t slots = KS == 1 ? kSlots : min(L::SLOTS, (ahead.n - k0 + kSlots - 1) & ~(kSlots - 1));
+                const uint32_t nc = slots * cb, ns = slots * nb;
                 tc::mbar_expect_tx(f, 2 * (nc + ns));
                 bulk_load(dst, a.c.kc + row * cb, nc, f);
                 bulk_load(dst + 2 * L::CODES, a.c.ks + row * nb, ns, f);
@@ -235,33 +262,33 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && DT <= 128 ? 4 : 2)
                 bulk_load(dst + 2 * L::CODES + L::SCALES, a.c.vs + row * nb, ns, f);
             }
             ++fetched;
+            fetch_stage = fetch_stage + 1 == L::STAGES ? 0 : fetch_stage + 1;
         }
-        if (to_fetch > 0) ahead.next(a, units);
+        if (to_fetch > 0 && ahead.next<L::TILE>(a, units)) unit_row();
     };
 #pragma unroll
     for (int s = 0; s < L::STAGES; ++s) fetch();
 
     // slot of a 16-row fragment row: neighbours in a different half of a bank line for K's and V's reads
     const int slot_lo = g ^ ((g >> 1) & 1);
-    int vrow[4];                                        // the fragment's columns 2c, 2c+1, 2c+8, 2c+9
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = 2 * c + (i & 1);
-        vrow[i] = (r ^ ((r >> 1) & 1)) + (i & 2) * 4;
-    }
+    // the fragment's columns 2c, 2c+1 (and 8 further): the same permutation
+    const int v_even = (2 * c) ^ (c & 1), v_odd = (2 * c + 1) ^ (c & 1);
 
     uint32_t qf[NT == 1 ? DT / 16 : 1][2];
-    float qs[NT][2], m[NT][2], l[NT][2];
+    float qs[NT][2], l[NT][2];
+    float up[NT][2];                                    // kUp - m, m the running maximum
     int32_t lim[NT][2];                                 // slots [0, lim) seen
     int32_t lim_min = 0;                                // by every row
+    int32_t hk = 0, rt = 0;
     float o[NT][VB][4];
     bool fresh = true;
 
-    for (int64_t it = t0; it < t1; ++it) {
-        const int32_t hk = cur.v / sp.RT, rt = cur.v - hk * sp.RT;
+    for (int32_t it = 0; it < n_tiles; ++it) {
         if (fresh) {
             // ---- a unit begins: its queries
             fresh = false;
+            hk = cur.v / sp.RT;
+            rt = cur.v - hk * sp.RT;
             __syncthreads();                            // the last unit's sO, sQ, sQS are read
             const int rows = min(L::ROWS, sp.R - rt * L::ROWS);
 #pragma unroll 1
@@ -285,12 +312,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && DT <= 128 ? 4 : 2)
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
                 // 2^(14 - e), e the largest's exponent; 1 for a row of zeros or with a value that is not finite
-                int up = 14 - ((int)(top >> 7) - 127);
-                up = min(up, 120);
-                if (top == 0 || top >= 0x7F80u) up = 0;
-                const float f = __int_as_float((127 + up) << 23);
+                int lift = 14 - ((int)(top >> 7) - 127);
+                lift = min(lift, 120);
+                if (top == 0 || top >= 0x7F80u) lift = 0;
+                const float f = __int_as_float((127 + lift) << 23);
                 if (c == 0 && (NT > 1 || warp == 0))
-                    sQS[8 * n + g] = a.g.scale * kLog2e * __int_as_float((127 - up) << 23) * a.c.k_scale;
+                    sQS[8 * n + g] = a.g.scale * kLog2e * __int_as_float((127 - lift) << 23) * a.c.k_scale;
 #pragma unroll
                 for (int i = 0; i < KW; ++i)
 #pragma unroll
@@ -319,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && DT <= 128 ? 4 : 2)
                     const int r = 8 * n + 2 * c + j;
                     qs[n][j] = sQS[r];
                     lim[n][j] = r < rows ? cur.n - a.g.T + 1 + (rt * L::ROWS + r) / G : 0;
-                    m[n][j] = -INFINITY;
+                    up[n][j] = INFINITY;
                     l[n][j] = 0.f;
                 }
 #pragma unroll
@@ -330,229 +357,283 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && DT <= 128 ? 4 : 2)
                     for (int j = 0; j < 4; ++j) o[n][i][j] = 0.f;
         }
 
-        const int32_t k0 = cur.t * kTileSlots + warp * kSlots;
+        const int32_t k0 = cur.t * L::TILE + warp * L::SLOTS;
         if (k0 < cur.n) {
-            const uint32_t st = used % L::STAGES;
-            if (ok) ok = tc::mbar_wait_warp(bar + 8 * st, (used / L::STAGES) & 1, abort_flag, a.status, sp.wait_ns);
+            if (ok) ok = tc::mbar_wait_warp(bar + 8 * use_stage, use_parity, abort_flag, a.status, sp.wait_ns);
             if (ok) {
+                const uint8_t* stage = ring_p + use_stage * L::STAGE;
+                const bool masked = k0 + L::SLOTS > lim_min;
                 ++used;
-                const uint8_t* kc = ring_p + st * L::STAGE;
-                const uint8_t* vc = kc + L::CODES;
-                const uint8_t* ks = kc + 2 * L::CODES;
-                const uint8_t* vs = ks + L::SCALES;
-                const bool masked = k0 + kSlots > lim_min;
+                if (++use_stage == L::STAGES) {
+                    use_stage = 0;
+                    use_parity ^= 1;
+                }
 
                 // ---- S^T = K Q^T
-                uint32_t kw[2][KW];
-                uint32_t ksc[2][KB];                    // scale of each block, in both halves
+                float s[KS][NT][4];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int r = slot_lo + 8 * h;
-                    if constexpr (EXACT) {
-                        if constexpr (DT == 64) {
-                            const uint2 x = *reinterpret_cast<const uint2*>(kc + r * 32 + 8 * c);
-                            kw[h][0] = x.x; kw[h][1] = x.y;
-                            const uint32_t y = scales_f16x2(ks[r * 4 + c]);
-                            ksc[h][0] = __byte_perm(y, 0, 0x1010);
+                for (int x = 0; x < KS; ++x) {
+                    const uint8_t* kc = stage + x * kSlots * cb;
+                    const uint8_t* ks = stage + 2 * L::CODES + x * kSlots * nb;
+                    uint32_t kw[2][KW];
+                    uint32_t ksc[2][KB];                // scale of each block, in both halves
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int r = slot_lo + 8 * h;
+                        if constexpr (EXACT) {
+                            if constexpr (DT == 64) {
+                                const uint2 w = *reinterpret_cast<const uint2*>(kc + r * 32 + 8 * c);
+                                kw[h][0] = w.x; kw[h][1] = w.y;
+                                ksc[h][0] = __byte_perm(scales_f16x2(ks[r * 4 + c]), 0, 0x1010);
+                            } else {
+#pragma unroll
+                                for (int p = 0; p < DT / 128; ++p) {
+                                    const uint4 w = *reinterpret_cast<const uint4*>(kc + r * (DT / 2) + 64 * p + 16 * c);
+                                    kw[h][4 * p] = w.x; kw[h][4 * p + 1] = w.y; kw[h][4 * p + 2] = w.z; kw[h][4 * p + 3] = w.w;
+                                    const uint32_t y = scales_f16x2(
+                                        *reinterpret_cast<const uint16_t*>(ks + r * (DT / 16) + 8 * p + 2 * c));
+                                    ksc[h][2 * p] = __byte_perm(y, 0, 0x1010);
+                                    ksc[h][2 * p + 1] = __byte_perm(y, 0, 0x3232);
+                                }
+                            }
                         } else {
 #pragma unroll
-                            for (int p = 0; p < DT / 128; ++p) {
-                                const uint4 x = *reinterpret_cast<const uint4*>(kc + r * (DT / 2) + 64 * p + 16 * c);
-                                kw[h][4 * p] = x.x; kw[h][4 * p + 1] = x.y; kw[h][4 * p + 2] = x.z; kw[h][4 * p + 3] = x.w;
-                                const uint32_t y = scales_f16x2(
-                                    *reinterpret_cast<const uint16_t*>(ks + r * (DT / 16) + 8 * p + 2 * c));
-                                ksc[h][2 * p] = __byte_perm(y, 0, 0x1010);
-                                ksc[h][2 * p + 1] = __byte_perm(y, 0, 0x3232);
+                            for (int i = 0; i < KW; ++i) {
+                                const int wd = k_word<DT>(c, i);
+                                kw[h][i] = 8 * wd < D ? *reinterpret_cast<const uint32_t*>(kc + r * cb + 4 * wd) : 0u;
+                                if (!(i & 1))
+                                    ksc[h][i / 2] = __byte_perm(scales_f16x2(8 * wd < D ? ks[r * nb + wd / 2] : 0), 0, 0x1010);
                             }
                         }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < KW; ++i) {
-                            const int wd = k_word<DT>(c, i);
-                            kw[h][i] = 8 * wd < D ? *reinterpret_cast<const uint32_t*>(kc + r * cb + 4 * wd) : 0u;
-                            if (!(i & 1))
-                                ksc[h][i / 2] = __byte_perm(scales_f16x2(8 * wd < D ? ks[r * nb + wd / 2] : 0), 0, 0x1010);
-                        }
                     }
-                }
-                float s[NT][4];
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                    for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) s[n][j] = 0.f;
+                        for (int j = 0; j < 4; ++j) s[x][n][j] = 0.f;
 #pragma unroll
-                for (int i = 0; i < KW; ++i) {
-                    const __half2 s0 = as_half2(ksc[0][i / 2]), s1 = as_half2(ksc[1][i / 2]);
-                    const uint32_t x0 = kw[0][i], x1 = kw[1][i];
-                    const uint32_t a0[4] = {as_u32(__hmul2(as_half2(codes_f16x2<0>(x0)), s0)),
-                                            as_u32(__hmul2(as_half2(codes_f16x2<0>(x1)), s1)),
-                                            as_u32(__hmul2(as_half2(codes_f16x2<1>(x0)), s0)),
-                                            as_u32(__hmul2(as_half2(codes_f16x2<1>(x1)), s1))};
-                    const uint32_t a1[4] = {as_u32(__hmul2(as_half2(codes_f16x2<2>(x0)), s0)),
-                                            as_u32(__hmul2(as_half2(codes_f16x2<2>(x1)), s1)),
-                                            as_u32(__hmul2(as_half2(codes_f16x2<3>(x0)), s0)),
-                                            as_u32(__hmul2(as_half2(codes_f16x2<3>(x1)), s1))};
+                    for (int i = 0; i < KW; ++i) {
+                        const __half2 s0 = as_half2(ksc[0][i / 2]), s1 = as_half2(ksc[1][i / 2]);
+                        const uint32_t x0 = kw[0][i], x1 = kw[1][i];
+                        const uint32_t a0[4] = {as_u32(__hmul2(as_half2(codes_f16x2<0>(x0)), s0)),
+                                                as_u32(__hmul2(as_half2(codes_f16x2<0>(x1)), s1)),
+                                                as_u32(__hmul2(as_half2(codes_f16x2<1>(x0)), s0)),
+                                                as_u32(__hmul2(as_half2(codes_f16x2<1>(x1)), s1))};
+                        const uint32_t a1[4] = {as_u32(__hmul2(as_half2(codes_f16x2<2>(x0)), s0)),
+                                                as_u32(__hmul2(as_half2(codes_f16x2<2>(x1)), s1)),
+                                                as_u32(__hmul2(as_half2(codes_f16x2<3>(x0)), s0)),
+                                                as_u32(__hmul2(as_half2(codes_f16x2<3>(x1)), s1))};
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        if constexpr (NT == 1) {
-                            mma16816(s[n], a0, qf[2 * i][0], qf[2 * i][1]);
-                            mma16816(s[n], a1, qf[2 * i + 1][0], qf[2 * i + 1][1]);
-                        } else {
-                            const uint2 b0 = sQ[(n * (DT / 16) + 2 * i) * 32 + lane];
-                            const uint2 b1 = sQ[(n * (DT / 16) + 2 * i + 1) * 32 + lane];
-                            mma16816(s[n], a0, b0.x, b0.y);
-                            mma16816(s[n], a1, b1.x, b1.y);
+                        for (int n = 0; n < NT; ++n) {
+                            if constexpr (NT == 1) {
+                                mma16816(s[x][n], a0, qf[2 * i][0], qf[2 * i][1]);
+                                mma16816(s[x][n], a1, qf[2 * i + 1][0], qf[2 * i + 1][1]);
+                            } else {
+                                const uint2 b0 = sQ[(n * (DT / 16) + 2 * i) * 32 + lane];
+                                const uint2 b1 = sQ[(n * (DT / 16) + 2 * i + 1) * 32 + lane];
+                                mma16816(s[x][n], a0, b0.x, b0.y);
+                                mma16816(s[x][n], a1, b1.x, b1.y);
+                            }
                         }
                     }
                 }
 
-                // ---- weights
-                const int ka = k0 + slot_lo;            // this lane's slots: ka, ka + 8
-                bool over = false;
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        float x = s[n][j] * qs[n][j & 1];
-                        if (masked && ka + (j & 2) * 4 >= lim[n][j & 1]) x = -INFINITY;
-                        s[n][j] = x;
-                        over |= x > m[n][j & 1] + kLag;
-                    }
+                // ---- weights: 2^(s qs + kUp - m)
+                const int ka = k0 + slot_lo;            // this lane's slots: ka + 16 x, and 8 further
                 if constexpr (MASS) {
                     float* dst = sp.scores + ((int64_t)(cur.b * units + cur.v) * a.c.cap + ka) * sp.pitch + 2 * c;
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
-                        if (8 * n + 2 * c < sp.pitch) {
-                            if (ka < cur.n) *reinterpret_cast<float2*>(dst + 8 * n) = make_float2(s[n][0], s[n][1]);
-                            if (ka + 8 < cur.n)
-                                *reinterpret_cast<float2*>(dst + 8 * n + (int64_t)8 * sp.pitch) = make_float2(s[n][2], s[n][3]);
-                        }
+                    for (int x = 0; x < KS; ++x)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            if (8 * n + 2 * c < sp.pitch)
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    const int k = ka + kSlots * x + 8 * h;
+                                    if (k < cur.n)
+                                        *reinterpret_cast<float2*>(dst + 8 * n + (int64_t)(kSlots * x + 8 * h) * sp.pitch) =
+                                            make_float2(k < lim[n][0] ? s[x][n][2 * h] * qs[n][0] : -INFINITY,
+                                                        k < lim[n][1] ? s[x][n][2 * h + 1] * qs[n][1] : -INFINITY);
+                                }
                 }
-                if (__any_sync(0xffffffffu, over)) {
+                float e[KS][NT][4];
+                float most = -INFINITY;
+#pragma unroll
+                for (int x = 0; x < KS; ++x)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            // product and sum rounded apart, so that the maximum's own exponent is exact at any size
+                            const float2 y = tc::fadd2(tc::fmul2(make_float2(s[x][n][2 * h], s[x][n][2 * h + 1]),
+                                                                 make_float2(qs[n][0], qs[n][1])),
+                                                       make_float2(up[n][0], up[n][1]));
+                            e[x][n][2 * h] = y.x;
+                            e[x][n][2 * h + 1] = y.y;
+                        }
+                if (masked) {
+#pragma unroll
+                    for (int x = 0; x < KS; ++x)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                if (ka + kSlots * x + (j & 2) * 4 >= lim[n][j & 1]) e[x][n][j] = -INFINITY;
+                }
+#pragma unroll
+                for (int x = 0; x < KS; ++x)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int j = 0; j < 4; j += 2) most = tc::fmax3(most, e[x][n][j], e[x][n][j + 1]);
+                if (__any_sync(0xffffffffu, most > kUp + kLag)) {
+                    // the running maximum moves to this slice's, where that is larger
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
-                            float x = fmaxf(s[n][j], s[n][j + 2]);
-                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-                            x = fmaxf(x, m[n][j]);
-                            const float f = x == m[n][j] ? 1.f : ex2(m[n][j] - x);
-                            m[n][j] = x;
+                            float t = -INFINITY;
+#pragma unroll
+                            for (int x = 0; x < KS; ++x)
+#pragma unroll
+                                for (int h = 0; h < 2; ++h)
+                                    if (!masked || ka + kSlots * x + 8 * h < lim[n][j]) t = fmaxf(t, __fmul_rn(s[x][n][2 * h + j], qs[n][j]));
+                            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
+                            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
+                            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
+                            const float was = up[n][j], now = fminf(was, kUp - t);
+                            const float f = now == was ? 1.f : ex2(now - was);
+                            up[n][j] = now;
                             l[n][j] *= f;
 #pragma unroll
                             for (int i = 0; i < VB; ++i) {
                                 o[n][i][j] *= f;
                                 o[n][i][j + 2] *= f;
                             }
+#pragma unroll
+                            for (int x = 0; x < KS; ++x)
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    float& y = e[x][n][2 * h + j];
+                                    // a row that has seen no slot yet (now = inf) has weight 0, or NaN
+                                    y = masked && ka + kSlots * x + 8 * h >= lim[n][j]
+                                            ? -INFINITY
+                                            : __fadd_rn(__fmul_rn(s[x][n][2 * h + j], qs[n][j]), now);
+                                }
                         }
                 }
-                uint32_t p[NT][2];
+                uint32_t p[KS][NT][2];
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const float b0 = m[n][0] == -INFINITY ? 0.f : m[n][0] - kUp;
-                    const float b1 = m[n][1] == -INFINITY ? 0.f : m[n][1] - kUp;
-                    const float p0 = ex2(s[n][0] - b0), p1 = ex2(s[n][1] - b1);
-                    const float p2 = ex2(s[n][2] - b0), p3 = ex2(s[n][3] - b1);
-                    l[n][0] += p0 + p2;
-                    l[n][1] += p1 + p3;
-                    p[n][0] = transpose8(as_u32(__floats2half2_rn(p0, p1)));
-                    p[n][1] = transpose8(as_u32(__floats2half2_rn(p2, p3)));
-                }
+                for (int x = 0; x < KS; ++x)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        const float p0 = ex2(e[x][n][0]), p1 = ex2(e[x][n][1]), p2 = ex2(e[x][n][2]), p3 = ex2(e[x][n][3]);
+                        const float2 y = tc::fadd2(make_float2(l[n][0], l[n][1]),
+                                                   tc::fadd2(make_float2(p0, p1), make_float2(p2, p3)));
+                        l[n][0] = y.x;
+                        l[n][1] = y.y;
+                        p[x][n][0] = transpose8(as_u32(__floats2half2_rn(p0, p1)));
+                        p[x][n][1] = transpose8(as_u32(__floats2half2_rn(p2, p3)));
+                    }
 
                 // ---- O^T += V^T P^T
-                constexpr int VW = VB >= 4 ? VB / 4 : 1;    // words a lane and slot
-                uint32_t vw[4][VW];
-                uint32_t vsc[2][DT == 256 ? 2 : 1];         // scales of slot pairs
-                uint32_t vraw[4][DT == 256 ? 2 : 1];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if constexpr (EXACT) {
-                        const uint8_t* p8 = vc + vrow[i] * (DT / 2) + VB * g;
-                        if constexpr (DT == 64) vw[i][0] = *reinterpret_cast<const uint32_t*>(p8);
-                        if constexpr (DT == 128) {
-                            const uint2 x = *reinterpret_cast<const uint2*>(p8);
-                            vw[i][0] = x.x; vw[i][1] = x.y;
-                        }
-                        if constexpr (DT == 256) {
-                            const uint4 x = *reinterpret_cast<const uint4*>(p8);
-                            vw[i][0] = x.x; vw[i][1] = x.y; vw[i][2] = x.z; vw[i][3] = x.w;
-                        }
-                        if constexpr (DT == 256) {
-                            const uint32_t y = *reinterpret_cast<const uint16_t*>(vs + vrow[i] * 16 + 2 * g);
-                            vraw[i][0] = y & 0xFF;
-                            vraw[i][1] = y >> 8;
+                for (int x = 0; x < KS; ++x) {
+                    const uint8_t* vc = stage + L::CODES + x * kSlots * cb;
+                    const uint8_t* vs = stage + 2 * L::CODES + L::SCALES + x * kSlots * nb;
+                    uint32_t vw[4][VW];
+                    uint32_t vraw[4][VS];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = (i & 1 ? v_odd : v_even) + (i & 2) * 4;
+                        if constexpr (EXACT) {
+                            const uint8_t* p8 = vc + r * (DT / 2) + VB * g;
+                            if constexpr (DT == 64) vw[i][0] = *reinterpret_cast<const uint32_t*>(p8);
+                            if constexpr (DT == 128) {
+                                const uint2 w = *reinterpret_cast<const uint2*>(p8);
+                                vw[i][0] = w.x; vw[i][1] = w.y;
+                            }
+                            if constexpr (DT == 256) {
+                                const uint4 w = *reinterpret_cast<const uint4*>(p8);
+                                vw[i][0] = w.x; vw[i][1] = w.y; vw[i][2] = w.z; vw[i][3] = w.w;
+                                const uint32_t y = *reinterpret_cast<const uint16_t*>(vs + r * 16 + 2 * g);
+                                vraw[i][0] = y & 0xFF;
+                                vraw[i][1] = y >> 8;
+                            } else {
+                                vraw[i][0] = vs[r * (DT / 16) + (DT == 64 ? g >> 1 : g)];
+                            }
                         } else {
-                            vraw[i][0] = vs[vrow[i] * (DT / 16) + (DT == 64 ? g >> 1 : g)];
-                        }
-                    } else {
 #pragma unroll
-                        for (int w = 0; w < VW; ++w) {
-                            const int wd = VW * g + w;
-                            vw[i][w] = 8 * wd < D ? *reinterpret_cast<const uint32_t*>(vc + vrow[i] * cb + 4 * wd) : 0u;
-                            if (w % 2 == 0) vraw[i][w / 2] = 8 * wd < D ? vs[vrow[i] * nb + wd / 2] : 0u;
-                        }
-                    }
-                }
-                bool nan = false;
-                if (masked) {
-                    // slots behind the last one hold anything: scale 0. NaN scales of slots that some
-                    // rows do not see are kept out of the product and given to the rows that do
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int y = 0; y < (DT == 256 ? 2 : 1); ++y) {
-                            if (k0 + vrow[i] >= cur.n) vraw[i][y] = 0;
-                            if ((vraw[i][y] & 0x7F) == 0x7F) {
-                                nan = true;
-                                vraw[i][y] = 0;
+                            for (int w = 0; w < VW; ++w) {
+                                const int wd = VW * g + w;
+                                vw[i][w] = 8 * wd < D ? *reinterpret_cast<const uint32_t*>(vc + r * cb + 4 * wd) : 0u;
+                                if (w % 2 == 0) vraw[i][w / 2] = 8 * wd < D ? vs[r * nb + wd / 2] : 0u;
                             }
                         }
-                }
+                    }
+                    bool nan = false;
+                    if (masked) {
+                        // slots behind the last one hold anything: scale 0. NaN scales of slots that some
+                        // rows do not see are kept out of the product and given to the rows that do
 #pragma unroll
-                for (int y = 0; y < (DT == 256 ? 2 : 1); ++y) {
-                    vsc[0][y] = scales_f16x2(vraw[0][y] | vraw[1][y] << 8);
-                    vsc[1][y] = scales_f16x2(vraw[2][y] | vraw[3][y] << 8);
-                }
+                        for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int w = 0; w < VW; ++w) {
-                    constexpr uint32_t M = 0x0F0F0F0Fu;
-                    const uint32_t lo0 = pick(M, vw[0][w], vw[1][w] << 4), hi0 = pick(M, vw[0][w] >> 4, vw[1][w]);
-                    const uint32_t lo1 = pick(M, vw[2][w], vw[3][w] << 4), hi1 = pick(M, vw[2][w] >> 4, vw[3][w]);
-                    const __half2 s0 = as_half2(vsc[0][w / 2]), s1 = as_half2(vsc[1][w / 2]);
-                    auto step = [&](int i, uint32_t l0, uint32_t h0, uint32_t l1, uint32_t h1) {
-                        const uint32_t av[4] = {as_u32(__hmul2(as_half2(l0), s0)), as_u32(__hmul2(as_half2(h0), s0)),
-                                                as_u32(__hmul2(as_half2(l1), s1)), as_u32(__hmul2(as_half2(h1), s1))};
+                            for (int y = 0; y < VS; ++y) {
+                                if (k0 + kSlots * x + (i & 1 ? v_odd : v_even) + (i & 2) * 4 >= cur.n) vraw[i][y] = 0;
+                                if ((vraw[i][y] & 0x7F) == 0x7F) {
+                                    nan = true;
+                                    vraw[i][y] = 0;
+                                }
+                            }
+                    }
+                    uint32_t vsc[2][VS];                // scales of slot pairs
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) mma16816(o[n][4 * w + i], av, p[n][0], p[n][1]);
-                    };
-                    step(0, codes_f16x2<0>(lo0), codes_f16x2<0>(hi0), codes_f16x2<0>(lo1), codes_f16x2<0>(hi1));
-                    step(1, codes_f16x2<1>(lo0), codes_f16x2<1>(hi0), codes_f16x2<1>(lo1), codes_f16x2<1>(hi1));
-                    step(2, codes_f16x2<2>(lo0), codes_f16x2<2>(hi0), codes_f16x2<2>(lo1), codes_f16x2<2>(hi1));
-                    step(3, codes_f16x2<3>(lo0), codes_f16x2<3>(hi0), codes_f16x2<3>(lo1), codes_f16x2<3>(hi1));
-                }
-                if (masked && __any_sync(0xffffffffu, nan)) {
-                    for (int k = 0; k < kSlots; ++k)
+                    for (int y = 0; y < VS; ++y) {
+                        vsc[0][y] = scales_f16x2(vraw[0][y] | vraw[1][y] << 8);
+                        vsc[1][y] = scales_f16x2(vraw[2][y] | vraw[3][y] << 8);
+                    }
 #pragma unroll
-                        for (int w = 0; w < VW; ++w) {
-                            const int wd = VW * g + w;
-                            if (8 * wd >= D || k0 + k >= cur.n || (vs[k * nb + wd / 2] & 0x7F) != 0x7F) continue;
+                    for (int w = 0; w < VW; ++w) {
+                        constexpr uint32_t M = 0x0F0F0F0Fu;
+                        const uint32_t lo0 = pick(M, vw[0][w], vw[1][w] << 4), hi0 = pick(M, vw[0][w] >> 4, vw[1][w]);
+                        const uint32_t lo1 = pick(M, vw[2][w], vw[3][w] << 4), hi1 = pick(M, vw[2][w] >> 4, vw[3][w]);
+                        const __half2 s0 = as_half2(vsc[0][w / 2]), s1 = as_half2(vsc[1][w / 2]);
+                        auto step = [&](int i, uint32_t l0, uint32_t h0, uint32_t l1, uint32_t h1) {
+                            const uint32_t av[4] = {as_u32(__hmul2(as_half2(l0), s0)), as_u32(__hmul2(as_half2(h0), s0)),
+                                                    as_u32(__hmul2(as_half2(l1), s1)), as_u32(__hmul2(as_half2(h1), s1))};
 #pragma unroll
-                            for (int n = 0; n < NT; ++n)
+                            for (int n = 0; n < NT; ++n) mma16816(o[n][4 * w + i], av, p[x][n][0], p[x][n][1]);
+                        };
+                        step(0, codes_f16x2<0>(lo0), codes_f16x2<0>(hi0), codes_f16x2<0>(lo1), codes_f16x2<0>(hi1));
+                        step(1, codes_f16x2<1>(lo0), codes_f16x2<1>(hi0), codes_f16x2<1>(lo1), codes_f16x2<1>(hi1));
+                        step(2, codes_f16x2<2>(lo0), codes_f16x2<2>(hi0), codes_f16x2<2>(lo1), codes_f16x2<2>(hi1));
+                        step(3, codes_f16x2<3>(lo0), codes_f16x2<3>(hi0), codes_f16x2<3>(lo1), codes_f16x2<3>(hi1));
+                    }
+                    if (masked && __any_sync(0xffffffffu, nan)) {
+#pragma unroll 1
+                        for (int k = 0; k < kSlots; ++k) {
+                            const int at = k0 + kSlots * x + k;
+                            if (at >= cur.n) break;
 #pragma unroll
-                                for (int j = 0; j < 4; ++j)
+                            for (int w = 0; w < VW; ++w) {
+                                const int wd = VW * g + w;
+                                if (8 * wd >= D || (vs[k * nb + wd / 2] & 0x7F) != 0x7F) continue;
 #pragma unroll
-                                    for (int i = 0; i < 4; ++i)
-                                        if (k0 + k < lim[n][j & 1]) o[n][4 * w + i][j] = __int_as_float(0x7FC00000);
+                                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                                        for (int i = 0; i < 4; ++i)
+                                            if (at < lim[n][j & 1]) o[n][4 * w + i][j] = __int_as_float(0x7FC00000);
+                            }
                         }
+                    }
                 }
             }
             __syncwarp();                               // the slice is read: its stage may be filled again
         }
         fetch();
 
-        if (cur.t == cur.nt - 1 || it == t1 - 1) {
+        if (cur.t == cur.nt - 1 || it == n_tiles - 1) {
             // ---- the unit, or this block's share of it, ends: join the warps
 #pragma unroll
             for (int n = 0; n < NT; ++n)
@@ -563,7 +644,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && DT <= 128 ? 4 : 2)
                     x += __shfl_xor_sync(0xffffffffu, x, 8);
                     x += __shfl_xor_sync(0xffffffffu, x, 16);
                     if (g == 0) {
-                        sM[warp * L::ROWS + 8 * n + 2 * c + j] = m[n][j];
+                        sM[warp * L::ROWS + 8 * n + 2 * c + j] = kUp - up[n][j];
                         sL[warp * L::ROWS + 8 * n + 2 * c + j] = x;
                     }
                 }
@@ -576,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && DT <= 128 ? 4 : 2)
                     const int r = 8 * n + 2 * c + j;
                     float top = sM[r];
                     for (int w = 1; w < kWarps; ++w) top = fmaxf(top, sM[w * L::ROWS + r]);
-                    f[n][j] = m[n][j] == -INFINITY ? 0.f : ex2(m[n][j] - top);
+                    f[n][j] = up[n][j] == INFINITY ? 0.f : ex2(kUp - up[n][j] - top);
                 }
             for (int w = 0; w < kWarps; ++w) {
                 if (warp == w) {
@@ -596,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && DT <= 128 ? 4 : 2)
                 __syncthreads();
             }
             const int rows = min(L::ROWS, sp.R - rt * L::ROWS);
-            const bool begins = it - cur.t >= t0, ends = cur.t == cur.nt - 1;
+            const bool begins = it >= cur.t, ends = cur.t == cur.nt - 1;
             float* part = a.parts + (2 * (int64_t)blockIdx.x + (begins ? 1 : 0)) * sp.slot_floats;
             for (int r = warp; r < rows; r += kWarps) {
                 float top = sM[r], sum = 0.f;
@@ -631,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && DT <= 128 ? 4 : 2)
             }
             fresh = true;
         }
-        if (it + 1 < t1) cur.next(a, units);
+        if (it + 1 < n_tiles) cur.next<L::TILE>(a, units);
     }
     // a wait gave up: this warp's copies in flight end (bounded) before the block does
     for (; used < fetched; ++used) {
@@ -643,80 +724,101 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && DT <= 128 ? 4 : 2)
 }
 
 // Rows of units that no block finished: the partials of the blocks that share the
-// unit, in block order; and the rows of empty sequences. One block per (unit, row).
-constexpr int kMergeThreads = 128;
+// unit, in block order; and the rows of empty sequences. One block per (unit, row):
+// its warps take every eighth partial, so that the loads of a unit spread over many
+// blocks (1 of 8 units of 128K slots lies in 76) are in flight together, and add up
+// their sums in order.
+constexpr int kMergeThreads = 256;
+template <int TILE>
 __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Kv4AttendArgs a, const Split sp, int32_t unit_rows) {
-    __shared__ int64_t scratch[2 * kMergeThreads / 32];
-    __shared__ float weight[kMaxGrid], red[kMergeThreads / 32];
-    const int tid = threadIdx.x, G = a.g.H / a.c.Hkv, units = a.c.Hkv * sp.RT;
+    constexpr int W = kMergeThreads / 32;
+    __shared__ int64_t scratch[2 * W];
+    __shared__ float weight[kMaxGrid], red[W];
+    __shared__ __align__(16) float sums[W][256];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int G = a.g.H / a.c.Hkv, units = a.c.Hkv * sp.RT;
     const int u = blockIdx.x / unit_rows, r = blockIdx.x - u * unit_rows;
     const int b = u / units, v = u - b * units, hk = v / sp.RT, rt = v - hk * sp.RT;
     const int rr = rt * unit_rows + r;
-    if (rr >= sp.R) return;
-    const int h = hk * G + rr % G, i = rr / G, D = a.c.D;
-    const int64_t at = ((int64_t)b * a.g.H + h) * a.g.T + i;
-    __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(a.o) + (int64_t)b * a.g.sb + (int64_t)h * a.g.sh +
-                         (int64_t)i * a.g.st;
-    const int32_t n = slots_of(a, b);
-    int64_t total, before;
-    sum_tiles<kMergeThreads>(a, b, total, before, scratch);
-    total *= units;
-    const bool none = n - a.g.T + 1 + i <= 0;
-    if (none) {
-        for (int d = tid; d < D; d += kMergeThreads) dst[d] = __float2bfloat16(0.f);
-        if (tid == 0) {
-            a.lse[at] = -INFINITY;
-            if (sp.lse2) sp.lse2[at] = -INFINITY;
+    const int i = rr / G, h = hk * G + rr - i * G, D = a.c.D;
+    if (rr < sp.R) {
+        const int32_t n = slots_of(a, b);
+        int64_t total, before;
+        sum_tiles<kMergeThreads, TILE>(a, b, total, before, scratch);
+        grid_wait();                                    // the split kernel's partials
+        total *= units;
+        const int64_t at = ((int64_t)b * a.g.H + h) * a.g.T + i;
+        __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(a.o) + (int64_t)b * a.g.sb + (int64_t)h * a.g.sh +
+                             (int64_t)i * a.g.st;
+        if (n - a.g.T + 1 + i <= 0) {
+            for (int d = tid; d < D; d += kMergeThreads) dst[d] = __float2bfloat16(0.f);
+            if (tid == 0) {
+                a.lse[at] = -INFINITY;
+                if (sp.lse2) sp.lse2[at] = -INFINITY;
+            }
+            return;
         }
-        return;
-    }
-    const int32_t blocks = (int32_t)min((int64_t)a.grid, total);
-    const int64_t first = before * units + (int64_t)v * tiles_of(n), last = first + tiles_of(n) - 1;
-    const int c0 = (int)(((first + 1) * blocks - 1) / total), c1 = (int)(((last + 1) * blocks - 1) / total);
-    if (c0 == c1) return;                               // finished by its block
-    // block c0 holds the unit's begin: there the partial is the block's second
-    auto slot = [&](int c) { return a.parts + (2 * (int64_t)c + (c == c0 ? 1 : 0)) * sp.slot_floats; };
-    const int64_t off_m = (int64_t)unit_rows * D + r, off_l = off_m + unit_rows;
-    auto block_max = [&](float x) {
+        const int32_t blocks = (int32_t)min((int64_t)a.grid, total);
+        const int64_t first = before * units + (int64_t)v * tiles_of<TILE>(n), last = first + tiles_of<TILE>(n) - 1;
+        const int c0 = (int)(((first + 1) * blocks - 1) / total), c1 = (int)(((last + 1) * blocks - 1) / total);
+        if (c0 == c1) return;                           // finished by its block
+        // block c0 holds the unit's begin: there the partial is the block's second
+        auto slot = [&](int c) { return a.parts + (2 * (int64_t)c + (c == c0 ? 1 : 0)) * sp.slot_floats; };
+        const int64_t off_m = (int64_t)unit_rows * D + r, off_l = off_m + unit_rows;
+        float top = -INFINITY;
+        for (int c = c0 + tid; c <= c1; c += kMergeThreads) {
+            weight[c - c0] = slot(c)[off_m];
+            top = fmaxf(top, weight[c - c0]);
+        }
 #pragma unroll
-        for (int m = 16; m > 0; m >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, m));
+        for (int m = 16; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+        if (lane == 0) red[warp] = top;
         __syncthreads();
-        if ((tid & 31) == 0) red[tid >> 5] = x;
-        __syncthreads();
-        return fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-    };
-    float top = -INFINITY;
-    for (int c = c0 + tid; c <= c1; c += kMergeThreads) top = fmaxf(top, slot(c)[off_m]);
-    top = block_max(top);
-    float sum = 0.f;
-    for (int c = c0 + tid; c <= c1; c += kMergeThreads) {
-        const float mc = slot(c)[off_m];
-        const float w = mc == -INFINITY ? 0.f : ex2(mc - top);
-        weight[c - c0] = w;
-        sum += w * slot(c)[off_l];
-    }
 #pragma unroll
-    for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-    __syncthreads();
-    if ((tid & 31) == 0) red[tid >> 5] = sum;
-    __syncthreads();
-    sum = (red[0] + red[1]) + (red[2] + red[3]);
-    const float inv = a.c.v_scale / sum;
-    for (int d = tid; d < D; d += kMergeThreads) {
-        float y = 0.f;
-#pragma unroll 4
-        for (int c = c0; c <= c1; ++c) y = fmaf(weight[c - c0], slot(c)[(int64_t)r * D + d], y);
-        dst[d] = __float2bfloat16(y * inv);
-    }
-    if (tid == 0) {
-        const float l2 = top - kUp + lg2(sum);
-        a.lse[at] = l2 * kLn2;
-        if (sp.lse2) sp.lse2[at] = l2;
+        for (int w = 0; w < W; ++w) top = fmaxf(top, red[w]);
+        __syncthreads();
+        float sum = 0.f;
+        for (int c = c0 + tid; c <= c1; c += kMergeThreads) {
+            const float w = weight[c - c0] == -INFINITY ? 0.f : ex2(weight[c - c0] - top);
+            weight[c - c0] = w;
+            sum += w * slot(c)[off_l];
+        }
+#pragma unroll
+        for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+        if (lane == 0) red[warp] = sum;
+        __syncthreads();
+        sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) sum += red[w];
+        for (int d = 4 * lane; d < D; d += 128) {
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+            for (int c = c0 + warp; c <= c1; c += W) {
+                const float4 x = *reinterpret_cast<const float4*>(slot(c) + (int64_t)r * D + d);
+                const float w = weight[c - c0];
+                y = make_float4(fmaf(w, x.x, y.x), fmaf(w, x.y, y.y), fmaf(w, x.z, y.z), fmaf(w, x.w, y.w));
+            }
+            *reinterpret_cast<float4*>(&sums[warp][d]) = y;
+        }
+        __syncthreads();
+        const float inv = a.c.v_scale / sum;
+        for (int d = tid; d < D; d += kMergeThreads) {
+            float y = 0.f;
+#pragma unroll
+            for (int w = 0; w < W; ++w) y += sums[w][d];
+            dst[d] = __float2bfloat16(y * inv);
+        }
+        if (tid == 0) {
+            const float l2 = top - kUp + lg2(sum);
+            a.lse[at] = l2 * kLn2;
+            if (sp.lse2) sp.lse2[at] = l2;
+        }
     }
 }
 
 // mass_out = mass_in + sum over the rows of 2^(s2 - lse2), from the scores that the split kernel kept.
 __global__ void __launch_bounds__(256) mass_kernel(const Kv4AttendArgs a, const Split sp, int32_t unit_rows) {
+    grid_wait();
     const int chunks = (a.c.cap + 255) / 256;
     const int bh = blockIdx.x / chunks, b = bh / a.c.Hkv, hk = bh - b * a.c.Hkv, G = a.g.H / a.c.Hkv;
     const int32_t n = slots_of(a, b);
@@ -738,10 +840,10 @@ __global__ void __launch_bounds__(256) mass_kernel(const Kv4AttendArgs a, const 
 
 int row_tiles(int D, int64_t R) { return R <= 8 ? 1 : (R <= 16 || D > 128) ? 2 : 4; }
 
-int blocks_per_sm(int D, int nt) { return nt == 1 && D <= 128 ? 4 : 2; }
+int dims_of(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
 
 struct Plan {
-    int nt, grid;
+    int nt, tile, grid;
     Split sp;
     int64_t parts, lse2, scores;      // floats
 };
@@ -755,12 +857,29 @@ Plan plan_of(const Kv4Geom& c, const Geom& g, bool mass) {
     p.sp.pitch = R <= 2 ? 2 : R <= 4 ? 4 : 8 * p.nt;
     p.sp.slot_floats = (int64_t)8 * p.nt * (c.D + 2);
     const int64_t units = (int64_t)c.B * c.Hkv * p.sp.RT;
-    const int64_t tiles = units * ((c.cap + kTileSlots - 1) / kTileSlots);
-    p.grid = (int)std::min<int64_t>(std::min(device_sm_count() * blocks_per_sm(c.D, p.nt), kMaxGrid), tiles);
+    p.tile = tile_slots(dims_of(c.D), p.nt);
+    const int64_t tiles = units * ((c.cap + p.tile - 1) / p.tile);
+    p.grid = (int)std::min<int64_t>(std::min(device_sm_count() * blocks_per_sm(dims_of(c.D), p.nt), kMaxGrid), tiles);
     p.parts = 2 * (int64_t)p.grid * p.sp.slot_floats;
     p.lse2 = mass ? ((int64_t)g.B * g.H * g.T + 63) / 64 * 64 : 0;
     p.scores = mass ? units * c.cap * p.sp.pitch : 0;
     return p;
+}
+
+// A launch that may begin before the kernel ahead of it ends (grid_wait).
+template <typename K>
+cudaError_t launch_after(K kernel, int64_t grid, int threads, cudaStream_t s, const Kv4AttendArgs& a, const Split& sp,
+                         int32_t unit_rows) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(threads);
+    cfg.stream = s;
+    cudaLaunchAttribute at = {};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return counted(cudaLaunchKernelEx(&cfg, kernel, a, sp, unit_rows));
 }
 
 template <int DT, int NT, bool EXACT, bool MASS>
@@ -802,11 +921,9 @@ cudaError_t launch_kv4_attend(const Kv4AttendArgs& args, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     const int unit_rows = 8 * p.nt;
     const int64_t rows = (int64_t)a.c.B * a.c.Hkv * p.sp.RT * unit_rows;
-    merge_kernel<<<(unsigned)rows, kMergeThreads, 0, s>>>(a, p.sp, unit_rows);
-    e = counted(cudaGetLastError());
+    e = launch_after(p.tile == 128 ? merge_kernel<128> : merge_kernel<64>, rows, kMergeThreads, s, a, p.sp, unit_rows);
     if (e != cudaSuccess || !a.mass_out) return e;
-    mass_kernel<<<(unsigned)((int64_t)((a.c.cap + 255) / 256) * a.c.B * a.c.Hkv), 256, 0, s>>>(a, p.sp, unit_rows);
-    return counted(cudaGetLastError());
+    return launch_after(mass_kernel, (int64_t)((a.c.cap + 255) / 256) * a.c.B * a.c.Hkv, 256, s, a, p.sp, unit_rows);
 }
 
 }  // namespace attn
