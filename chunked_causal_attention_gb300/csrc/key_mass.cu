@@ -1,45 +1,419 @@
-// The attention weight of each key over query rows: the simple form, one warp per key.
-#include "kv4_device.cuh"
+// The attention weight of each key, summed over query rows and the heads of its
+// key/value head, from q, k and the forward's log-sum-exp:
+//
+//   mass_j = sum_{h, t visible} exp(scale q_t . k_j - LSE_t)
+//
+// One work item is a tile of 128 keys of one key/value head; it walks every block
+// of at most 128 query rows that sees the tile, for each head of the group, so a
+// key's sum stays with one thread and needs no atomics: the result does not depend
+// on timing. Persistent blocks take items, those with the most rows first within a
+// head, from a work queue (WorkRing in tc_common.cuh). Warp roles:
+//   warp 0      TMA producer: the K tile of an item, Q blocks through a ring
+//   warp 1      MMA issuer and TMEM owner: S^T = K Q^T (M = 128 keys, N = rows of
+//               the block) into one of four 128-column TMEM buffers
+//   warps 4-15  three groups that take the blocks in turn: thread = key (TMEM
+//               lane); it reads its row of S^T, forms 2^(s c - lse2) with the
+//               block's lse2 from shared memory (two columns per instruction where
+//               the pipe allows) and sums
+// Per block 2 * 128 * 128 * D FLOP (512 cycles of an SM at D = 128) stand against
+// 128 * 128 exponentials (512 cycles at 32 a cycle): both pipes are needed whole.
+//
+// Sums: 128 weights of a block in four fp32 chains, blocks with a compensated sum
+// (Kahan), so that a million rows lose no more than a block does.
+//
+// Every mbarrier wait is bounded (ATTN_E_TIMEOUT); items and chunks are checked
+// before use (ATTN_E_BOUNDS). The groups meet at named barriers and leave only by a
+// vote there.
+#include <algorithm>
+
+#include "kv4.h"
+#include "tc_common.cuh"
 
 namespace attn {
 namespace {
 
-__global__ void __launch_bounds__(256) key_mass_rows(const MassArgs a) {
-    const int lane = threadIdx.x & 31;
-    const int j = blockIdx.x * 8 + (threadIdx.x >> 5), bh = blockIdx.y;
-    const int b = bh / a.g.Hkv, hk = bh % a.g.Hkv, G = a.g.H / a.g.Hkv;
-    if (j >= a.g.T) return;
-    const bool on = lane * 8 < a.g.D;
-    float x[8], w = 0.f;
-    const __nv_bfloat16* k = reinterpret_cast<const __nv_bfloat16*>(a.k) + (int64_t)b * a.g.sb_kv +
-                             (int64_t)hk * a.g.sh_kv + (int64_t)j * a.g.st_kv;
-    for (int e = 0; e < 8; ++e) x[e] = on ? __bfloat162float(k[lane * 8 + e]) : 0.f;
-    for (int c = 0; c < a.n; ++c) {
-        const attn_chunk ch = a.chunks[c];
-        if (j < ch.ctx_begin || j >= ch.q_end) continue;
-        for (int h = hk * G; h < hk * G + G; ++h)
-            for (int t = max(ch.q_begin, j); t < ch.q_end; ++t) {
-                const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q) + (int64_t)b * a.g.sb +
-                                         (int64_t)h * a.g.sh + (int64_t)t * a.g.st;
-                float s = 0.f;
-                if (on)
-                    for (int e = 0; e < 8; ++e) s = fmaf(__bfloat162float(q[lane * 8 + e]), x[e], s);
-                for (int m = 16; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
-                const float lse = a.lse[((int64_t)b * a.g.H + h) * a.g.T + t];
-                w += lse == -INFINITY ? 0.f : expf(s * a.g.scale - lse);
+using namespace tc;
+
+constexpr int kGroups = 3;                 // softmax warpgroups
+constexpr int kThreads = 128 + 128 * kGroups;
+constexpr int kBufs = 4;                   // S^T buffers in TMEM
+constexpr uint32_t kTmemCols = 512;
+constexpr int kRows = 128;                 // query rows of a block
+constexpr int kBoxRows = 64;               // rows of a TMA box
+
+template <int DT>
+struct Layout {
+    static constexpr int KST = DT == 256 ? 1 : 3, QST = DT == 256 ? 2 : 3;
+    static constexpr int TILE = 128 * DT * 2;
+    static constexpr int K_OFF = 0, Q_OFF = KST * TILE;
+    static constexpr int LSE_OFF = Q_OFF + QST * TILE;            // [group][2][128] floats
+    static constexpr int PART_OFF = LSE_OFF + kGroups * 2 * 128 * 4;   // [2][group - 1][128] floats
+    static constexpr int BAR_OFF = PART_OFF + 2 * (kGroups - 1) * 128 * 4;
+    static constexpr int B_KFULL = 0, B_KEMPTY = B_KFULL + KST;
+    static constexpr int B_QFULL = B_KEMPTY + KST, B_QEMPTY = B_QFULL + QST;
+    static constexpr int B_SFULL = B_QEMPTY + QST, B_SEMPTY = B_SFULL + kBufs;
+    static constexpr int B_PFULL = B_SEMPTY + kBufs, B_PEMPTY = B_PFULL + 2;
+    static constexpr int B_RFULL = B_PEMPTY + 2, B_REMPTY = B_RFULL + 2;
+    static constexpr int B_DRAIN = B_REMPTY + 2;
+    static constexpr int NBAR = B_DRAIN + 1;
+    static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;
+    static constexpr int BYTES = MISC_OFF + 16;
+    static constexpr size_t ALLOC = (size_t)BYTES + 1024;
+};
+
+// The query blocks of an item in order: chunk, head of the group, block of rows.
+struct Walk {
+    const MassArgs& a;
+    const MassItem it;
+    int32_t c, g, r;          // next chunk, head, row
+    int32_t qe, ctx, r0;      // of the current chunk; r0: first row at or after the tile's first key
+    bool bad;
+    __device__ __forceinline__ Walk(const MassArgs& args, const MassItem& item)
+        : a(args), it(item), c(item.c_lo - 1), g(0), r(0), qe(0), ctx(0), r0(0), bad(false) {
+        step_chunk();
+    }
+    __device__ __forceinline__ void step_chunk() {
+        for (++c; c < it.c_hi; ++c) {
+            const attn_chunk ch = a.chunks[c];
+            if (!(0 <= ch.ctx_begin && ch.ctx_begin <= ch.q_begin && ch.q_begin < ch.q_end && ch.q_end <= a.g.T)) {
+                bad = true;
+                return;
             }
+            if (ch.ctx_begin >= it.j1 || ch.q_end <= it.j0) continue;
+            qe = ch.q_end;
+            ctx = ch.ctx_begin;
+            r0 = max(ch.q_begin, it.j0);
+            g = 0;
+            r = r0;
+            return;
+        }
     }
-    if (lane == 0) {
-        const int64_t at = (int64_t)bh * a.g.T + j;
-        a.mass_out[at] = (a.mass_in ? a.mass_in[at] : 0.f) + w;
+    __device__ __forceinline__ bool more() const { return !bad && c < it.c_hi; }
+    __device__ __forceinline__ int32_t rows() const { return min(kRows, qe - r); }
+    __device__ __forceinline__ void next(int32_t G) {
+        r += kRows;
+        if (r < qe) return;
+        r = r0;
+        if (++g < G) return;
+        step_chunk();
     }
+};
+
+__device__ __forceinline__ bool item_ok(const MassItem& it, const MassArgs& a) {
+    return 0 <= it.j0 && it.j0 < it.j1 && it.j1 - it.j0 <= 128 && it.j1 <= a.g.T && 0 <= it.c_lo && it.c_hi <= a.n;
+}
+
+// Wait for this thread's TMEM loads; r's values are those of the load that the wait completes.
+__device__ __forceinline__ void tmem_ld_done(uint32_t (&r)[32]) {
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+// ROWS rows x DT dims: boxes of 64 dims x 64 rows, dims in strides of 128 rows.
+template <int DT>
+__device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap* map, uint32_t bar, const TcMaps& mp, int row,
+                                          int boxes, int h, int b) {
+    for (int y = 0; y < boxes; ++y) {
+        const int t = row + y * kBoxRows;
+        const int c1 = mp.pos_t == 1 ? t : (mp.pos_h == 1 ? h : b);
+        const int c2 = mp.pos_t == 2 ? t : (mp.pos_h == 2 ? h : b);
+        const int c3 = mp.pos_t == 3 ? t : (mp.pos_h == 3 ? h : b);
+#pragma unroll
+        for (int x = 0; x < DT / 64; ++x) tma_load_4d(dst + x * 128 * 128 + y * kBoxRows * 128, map, bar, x * 64, c1, c2, c3);
+    }
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kThreads, 1)
+    key_mass_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk, const MassArgs a,
+                    const TcMaps mp, const TcMaps mpkv, const int32_t n_work) {
+    using L = Layout<DT>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(sm);
+    auto bar = [&](int i) { return sbase + L::BAR_OFF + 8u * (uint32_t)i; };
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::MISC_OFF);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::MISC_OFF + 4);
+    const WorkRing ring{reinterpret_cast<volatile int32_t*>(sm + L::MISC_OFF + 8), bar(L::B_RFULL), bar(L::B_REMPTY)};
+    const int tid = threadIdx.x, warp = tid >> 5;
+    const int BH = a.g.B * a.g.Hkv, G = a.g.H / a.g.Hkv;
+
+    if (tid == 0) {
+        for (int s = 0; s < L::KST; ++s) {
+            mbar_init(bar(L::B_KFULL + s), 1);
+            mbar_init(bar(L::B_KEMPTY + s), 1);
+        }
+        for (int s = 0; s < L::QST; ++s) {
+            mbar_init(bar(L::B_QFULL + s), 1);
+            mbar_init(bar(L::B_QEMPTY + s), 1);
+        }
+        for (int s = 0; s < kBufs; ++s) {
+            mbar_init(bar(L::B_SFULL + s), 1);
+            mbar_init(bar(L::B_SEMPTY + s), 128);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(bar(L::B_PFULL + s), 128 * (kGroups - 1));
+            mbar_init(bar(L::B_PEMPTY + s), 128);
+            mbar_init(bar(L::B_RFULL + s), 1);
+            mbar_init(bar(L::B_REMPTY + s), 1 + 4 * kGroups);
+        }
+        mbar_init(bar(L::B_DRAIN), 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ producer
+        if (elect_one()) {
+            tma_prefetch_desc(&tmq);
+            tma_prefetch_desc(&tmk);
+            uint32_t kc = 0, qc = 0, ic = 0;
+            int32_t w = a.stall ? n_work : (int32_t)atomicAdd(a.counter, 1u);
+            for (; !a.stall; ++ic) {
+                if (!ring_put(ring, ic, w < n_work ? w : -1, abort_flag, a.status, a.wait_ns)) break;
+                if (w >= n_work || *abort_flag) break;
+                int32_t i, bh;
+                decode_work(w, a.n_items, BH, 1 << 30, i, bh);
+                const MassItem item = a.items[i];
+                if (!item_ok(item, a)) {
+                    set_error(a.status, ATTN_E_BOUNDS);
+                    *abort_flag = 1;
+                    break;
+                }
+                const int b = bh / a.g.Hkv, hk = bh % a.g.Hkv;
+                Walk wk(a, item);
+                bool ok = true;
+                if (wk.more()) {
+                    const uint32_t s = kc % L::KST;
+                    ok = mbar_wait(bar(L::B_KEMPTY + s), ((kc / L::KST) & 1) ^ 1, abort_flag, a.status, a.wait_ns);
+                    if (!ok) break;
+                    mbar_expect_tx(bar(L::B_KFULL + s), L::TILE);
+                    load_rows<DT>(sbase + L::K_OFF + s * L::TILE, &tmk, bar(L::B_KFULL + s), mpkv, item.j0, 2, hk, b);
+                    ++kc;
+                }
+                for (; wk.more(); wk.next(G)) {
+                    const uint32_t s = qc % L::QST;
+                    ok = mbar_wait(bar(L::B_QEMPTY + s), ((qc / L::QST) & 1) ^ 1, abort_flag, a.status, a.wait_ns);
+                    if (!ok) break;
+                    const int boxes = wk.rows() > kBoxRows ? 2 : 1;
+                    mbar_expect_tx(bar(L::B_QFULL + s), boxes * (L::TILE / 2));
+                    load_rows<DT>(sbase + L::Q_OFF + s * L::TILE, &tmq, bar(L::B_QFULL + s), mp, wk.r, boxes, hk * G + wk.g, b);
+                    ++qc;
+                }
+                if (!ok) break;
+                if (wk.bad) {
+                    set_error(a.status, ATTN_E_BOUNDS);
+                    *abort_flag = 1;
+                    break;
+                }
+                w = (int32_t)atomicAdd(a.counter, 1u);
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer
+        if (elect_one()) {
+            uint32_t kc = 0, qc = 0, ic = 0;
+            bool ok = true;
+            for (; ok; ++ic) {
+                int32_t w = -1;
+                ok = ring_get(ring, ic, w, abort_flag, a.status, a.wait_ns);
+                if (!ok || w < 0 || *abort_flag) break;
+                int32_t i, bh;
+                decode_work(w, a.n_items, BH, 1 << 30, i, bh);
+                const MassItem item = a.items[i];
+                if (!item_ok(item, a)) break;
+                Walk wk(a, item);
+                if (!wk.more()) continue;
+                const uint32_t ks = kc % L::KST;
+                ok = mbar_wait(bar(L::B_KFULL + ks), (kc / L::KST) & 1, abort_flag, a.status, a.wait_ns);
+                if (!ok) break;
+                const uint32_t k0 = sbase + L::K_OFF + ks * L::TILE;
+                for (; wk.more(); wk.next(G)) {
+                    const uint32_t qs = qc % L::QST, sb = qc % kBufs;
+                    ok = mbar_wait(bar(L::B_QFULL + qs), (qc / L::QST) & 1, abort_flag, a.status, a.wait_ns) &&
+                         mbar_wait(bar(L::B_SEMPTY + sb), ((qc / kBufs) & 1) ^ 1, abort_flag, a.status, a.wait_ns);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t q0 = sbase + L::Q_OFF + qs * L::TILE;
+                    // as many columns as the block has rows, in steps of 16
+                    const uint32_t id = idesc_bf16(128, (wk.rows() + 15) & ~15, 0, 0);
+#pragma unroll
+                    for (int kk = 0; kk < DT / 16; ++kk) {
+                        const uint32_t off = (kk >> 2) * (128 * 128) + (kk & 3) * 32;
+                        mma_ss(tmem + sb * kRows, sdesc_sw128(k0 + off, 16, 1024), sdesc_sw128(q0 + off, 16, 1024), id, kk > 0);
+                    }
+                    mma_commit(bar(L::B_QEMPTY + qs));
+                    mma_commit(bar(L::B_SFULL + sb));
+                    ++qc;
+                }
+                if (!ok || wk.bad) break;
+                mma_commit(bar(L::B_KEMPTY + ks));
+                ++kc;
+            }
+        }
+    } else if (warp >= 4) {
+        // ------------------------------------------------------------ sums
+        const int grp = (warp >> 2) - 1, key = tid & 127;
+        const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
+        const float c = a.g.scale * kLog2e;
+        const float2 c2 = make_float2(c, c);
+        float* s_lse = reinterpret_cast<float*>(sm + L::LSE_OFF) + grp * 256;
+        float* s_part = reinterpret_cast<float*>(sm + L::PART_OFF);
+        uint32_t qc = 0, mine = 0, ic = 0;
+        bool ok = true;
+        for (; ok; ++ic) {
+            int32_t w = -1;
+            ok = ring_get_warp(ring, ic, w, abort_flag, a.status, a.wait_ns);
+            // the four warps of a group go on together or not at all
+            ok = named_sync_all(1 + grp, 128, ok);
+            if (!ok || w < 0) break;
+            int32_t i, bh;
+            decode_work(w, a.n_items, BH, 1 << 30, i, bh);
+            const MassItem item = a.items[i];
+            if (!item_ok(item, a)) break;                    // the same for every thread
+            const int b = bh / a.g.Hkv, hk = bh % a.g.Hkv;
+            const int j = item.j0 + key;
+            float sum = 0.f, err = 0.f;                      // compensated
+            Walk wk(a, item);
+            for (; wk.more(); wk.next(G), ++qc) {
+                if (qc % kGroups != grp) continue;
+                const int n = wk.rows();
+                float* lse = s_lse + (mine & 1) * 128;
+                ++mine;
+                {
+                    float x = -INFINITY;                     // weight 0: rows past the block, rows without a sum
+                    if (key < n) {
+                        x = a.lse[((int64_t)b * a.g.H + hk * G + wk.g) * a.g.T + wk.r + key];
+                        x = x == -INFINITY ? x : -x * kLog2e;
+                    }
+                    lse[key] = x;
+                }
+                const uint32_t sb = qc % kBufs;
+                ok = mbar_wait_warp(bar(L::B_SFULL + sb), (qc / kBufs) & 1, abort_flag, a.status, a.wait_ns);
+                ok = named_sync_all(1 + grp, 128, ok);
+                if (!ok) break;
+                tc_fence_after();
+                // this key is seen by the columns [lo, n)
+                const int lo = wk.ctx <= j ? max(0, j - wk.r) : kRows;
+                const bool edge = n < kRows || wk.r < item.j1 - 1 || wk.ctx > item.j0;
+                const uint32_t sa = tmem + lane_addr + sb * kRows;
+                const int chunks = (n + 31) / 32;
+                float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                uint32_t r[2][32];
+                tmem_ld32(sa, r[0]);
+                auto weigh = [&](const uint32_t (&x)[32], int col) {
+                    const float4* l4 = reinterpret_cast<const float4*>(lse + col);
+                    if (!edge) {
+#pragma unroll
+                        for (int y = 0; y < 8; ++y) {
+                            const float4 l = l4[y];
+                            const float2 e0 = ffma2(make_float2(__uint_as_float(x[4 * y]), __uint_as_float(x[4 * y + 1])), c2,
+                                                    make_float2(l.x, l.y));
+                            const float2 e1 = ffma2(make_float2(__uint_as_float(x[4 * y + 2]), __uint_as_float(x[4 * y + 3])), c2,
+                                                    make_float2(l.z, l.w));
+                            acc[0] = fadd2(acc[0], make_float2(ex2(e0.x), ex2(e0.y)));
+                            acc[1] = fadd2(acc[1], make_float2(ex2(e1.x), ex2(e1.y)));
+                        }
+                    } else {
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) {
+                            const float e = fmaf(__uint_as_float(x[y]), c, lse[col + y]);
+                            const float p = col + y >= lo && col + y < n ? ex2(e) : 0.f;
+                            if (y & 1) acc[(y >> 1) & 1].y += p; else acc[(y >> 1) & 1].x += p;
+                        }
+                    }
+                };
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    if (x >= chunks) break;
+                    tmem_ld_done(r[x & 1]);
+                    if (x + 1 < chunks) {
+                        tmem_ld32(sa + (x + 1) * 32, r[(x + 1) & 1]);
+                    } else {
+                        // the buffer has been read
+                        tc_fence_before();
+                        mbar_arrive(bar(L::B_SEMPTY + sb));
+                    }
+                    weigh(r[x & 1], x * 32);
+                }
+                const float part = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+                const float y = __fsub_rn(part, err), t = __fadd_rn(sum, y);
+                err = __fsub_rn(__fsub_rn(t, sum), y);
+                sum = t;
+            }
+            if (!ok || wk.bad) break;
+            sum -= err;
+            // the groups' sums meet in the first group, in order
+            const uint32_t slot = ic & 1;
+            if (grp) {
+                ok = mbar_wait_warp(bar(L::B_PEMPTY + slot), ((ic >> 1) & 1) ^ 1, abort_flag, a.status, a.wait_ns);
+                if (ok) {
+                    s_part[(slot * (kGroups - 1) + grp - 1) * 128 + key] = sum;
+                    mbar_arrive(bar(L::B_PFULL + slot));
+                }
+            } else {
+                ok = mbar_wait_warp(bar(L::B_PFULL + slot), (ic >> 1) & 1, abort_flag, a.status, a.wait_ns);
+                if (ok) {
+                    for (int x = 0; x < kGroups - 1; ++x) sum += s_part[(slot * (kGroups - 1) + x) * 128 + key];
+                    mbar_arrive(bar(L::B_PEMPTY + slot));
+                    if (j < item.j1) {
+                        const int64_t at = (int64_t)bh * a.g.T + j;
+                        a.mass_out[at] = (a.mass_in ? a.mass_in[at] : 0.f) + sum;
+                    }
+                }
+            }
+        }
+    }
+    // ---------------------------------------------------------------- teardown
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) {
+        __syncwarp();
+        if (*abort_flag) {
+            if (elect_one()) {
+                mma_commit(bar(L::B_DRAIN));
+                const uint64_t t0 = globaltimer();
+                while (!mbar_try_wait(bar(L::B_DRAIN), 0) && globaltimer() - t0 < a.wait_ns) {
+                }
+            }
+            __syncwarp();
+        }
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+template <int DT>
+cudaError_t launch_d(const MassArgs& a, cudaStream_t s) {
+    CUtensorMap mq, mk;
+    TcMaps mp{1, 2, 3}, mpkv{1, 2, 3};
+    const Geom gkv = a.g.kv();
+    if (!make_tile_map(&mq, a.q, a.g, mp, kBoxRows) || !make_tile_map(&mk, a.k, gkv, mpkv, kBoxRows))
+        return cudaErrorInvalidValue;
+    const int64_t work = (int64_t)a.n_items * a.g.B * a.g.Hkv;
+    if (work > INT32_MAX) return cudaErrorInvalidValue;
+    const size_t smem = Layout<DT>::ALLOC;
+    static_assert(Layout<DT>::ALLOC <= 232448, "shared memory of the key mass kernel");
+    cudaError_t e = cudaFuncSetAttribute(key_mass_kernel<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    const int grid = (int)std::min<int64_t>(work, device_sm_count());
+    key_mass_kernel<DT><<<grid, kThreads, smem, s>>>(mq, mk, a, mp, mpkv, (int32_t)work);
+    return counted(cudaGetLastError());
 }
 
 }  // namespace
 
 cudaError_t launch_key_mass(const MassArgs& a, cudaStream_t s) {
-    key_mass_rows<<<dim3((a.g.T + 7) / 8, a.g.B * a.g.Hkv), 256, 0, s>>>(a);
-    return counted(cudaGetLastError());
+    return a.g.D > 128 ? launch_d<256>(a, s) : a.g.D > 64 ? launch_d<128>(a, s) : launch_d<64>(a, s);
 }
 
 }  // namespace attn

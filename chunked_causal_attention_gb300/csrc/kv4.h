@@ -65,10 +65,17 @@ struct Kv4EvictArgs {
     uint32_t* status;
 };
 
+// Keys [j0, j1) of a key/value head, at most 128; the chunks whose rows may see them
+// are among [c_lo, c_hi).
+struct MassItem {
+    int32_t j0, j1, c_lo, c_hi;
+};
+
 struct MassArgs {
     const void* q; const void* k; const float* lse;
     const float* mass_in; float* mass_out;
     const attn_chunk* chunks; int32_t n;   // in the workspace
+    const MassItem* items; int32_t n_items;
     uint32_t* status;
     uint32_t* counter;
     uint64_t wait_ns; int32_t stall;

@@ -119,8 +119,35 @@ int attend_geom(const attn_shape* shape, const Kv4Geom& c, Geom* g) {
 
 }  // namespace
 
-size_t attn::key_mass_bytes(const Geom&, const attn_chunk*, int32_t n) {
-    return kHeaderBytes + round_up((size_t)n * sizeof(attn_chunk), kAlign);
+// Key tiles of attn_key_mass, those that the most rows see first. Chunks are sorted
+// by rows, so the ones that end after a tile's first key are a tail of the table; of
+// those, the last that starts its context before the tile's end bounds the range.
+static std::vector<MassItem> mass_items(const Geom& g, const attn_chunk* c, int32_t n) {
+    std::vector<int32_t> least(n + 1, INT32_MAX);       // least context start of the chunks [i, n)
+    std::vector<int64_t> rows(n + 1, 0);                // rows of the chunks [0, i)
+    for (int32_t i = n - 1; i >= 0; --i) least[i] = std::min(least[i + 1], c[i].ctx_begin);
+    for (int32_t i = 0; i < n; ++i) rows[i + 1] = rows[i] + (c[i].q_end - c[i].q_begin);
+    struct Costed { MassItem it; int64_t cost; };
+    std::vector<Costed> v;
+    int32_t lo = 0, hi = 0;
+    for (int32_t j0 = 0; j0 < g.T; j0 += std::min(kTile, g.T - j0)) {
+        const int32_t j1 = j0 + std::min(kTile, g.T - j0);
+        while (lo < n && c[lo].q_end <= j0) ++lo;
+        while (hi < n && least[hi] < j1) ++hi;
+        Costed x{{j0, j1, lo, std::max(lo, hi)}, 0};
+        if (lo < hi) x.cost = rows[hi] - rows[lo] - std::max(0, j0 - c[lo].q_begin);
+        v.push_back(x);
+    }
+    std::stable_sort(v.begin(), v.end(), [](const Costed& a, const Costed& b) { return a.cost > b.cost; });
+    std::vector<MassItem> items(v.size());
+    for (size_t i = 0; i < v.size(); ++i) items[i] = v[i].it;
+    return items;
+}
+
+static size_t mass_items_offset(int32_t n) { return kHeaderBytes + round_up((size_t)n * sizeof(attn_chunk), kAlign); }
+
+size_t attn::key_mass_bytes(const Geom& g, const attn_chunk*, int32_t n) {
+    return mass_items_offset(n) + round_up(((size_t)g.T + kTile - 1) / kTile * sizeof(MassItem), kAlign);
 }
 
 extern "C" {
@@ -223,8 +250,13 @@ int attn_key_mass(const void* q, const void* k, const float* lse, const attn_chu
     uint8_t* w = (uint8_t*)ws;
     if (n && launch_upload(w + kHeaderBytes, chunks, (size_t)n * sizeof(attn_chunk), s) != cudaSuccess) return ATTN_E_CUDA;
     a.q = q; a.k = k; a.lse = lse; a.mass_in = mass_in; a.mass_out = mass_out;
+    const std::vector<MassItem> items = mass_items(a.g, chunks, n);
+    const size_t off = mass_items_offset(n);
+    if (launch_upload(w + off, items.data(), items.size() * sizeof(MassItem), s) != cudaSuccess) return ATTN_E_CUDA;
     a.chunks = (const attn_chunk*)(w + kHeaderBytes);
     a.n = n;
+    a.items = (const MassItem*)(w + off);
+    a.n_items = (int32_t)items.size();
     a.status = (uint32_t*)ws;
     a.counter = &((WsHeader*)ws)->counter[0];
     wait_settings(&a.wait_ns, &a.stall);
