@@ -11,10 +11,12 @@
 //   warp 0      TMA producer: the K tile of an item, Q blocks through a ring
 //   warp 1      MMA issuer and TMEM owner: S^T = K Q^T (M = 128 keys, N = rows of
 //               the block) into one of four 128-column TMEM buffers
-//   warps 4-15  three groups that take the blocks in turn: thread = key (TMEM
+//   warp 2      the rows' -lse log2 e into shared memory, up to four blocks ahead
+//   warps 4-11  two groups that take the blocks in turn: thread = key (TMEM
 //               lane); it reads its row of S^T, forms 2^(s c - lse2) with the
 //               block's lse2 from shared memory (two columns per instruction where
-//               the pipe allows) and sums
+//               the pipe allows) and sums. The warps meet no barrier among
+//               themselves
 // Per block 2 * 128 * 128 * D FLOP (512 cycles of an SM at D = 128) stand against
 // 128 * 128 exponentials (512 cycles at 32 a cycle): both pipes are needed whole.
 //
@@ -22,8 +24,7 @@
 // (Kahan), so that a million rows lose no more than a block does.
 //
 // Every mbarrier wait is bounded (ATTN_E_TIMEOUT); items and chunks are checked
-// before use (ATTN_E_BOUNDS). The groups meet at named barriers and leave only by a
-// vote there.
+// before use (ATTN_E_BOUNDS).
 #include <algorithm>
 
 #include "kv4.h"
@@ -34,7 +35,7 @@ namespace {
 
 using namespace tc;
 
-constexpr int kGroups = 3;                 // softmax warpgroups
+constexpr int kGroups = 2;                 // softmax warpgroups
 constexpr int kThreads = 128 + 128 * kGroups;
 constexpr int kBufs = 4;                   // S^T buffers in TMEM
 constexpr uint32_t kTmemCols = 512;
@@ -43,16 +44,17 @@ constexpr int kBoxRows = 64;               // rows of a TMA box
 
 template <int DT>
 struct Layout {
-    static constexpr int KST = DT == 256 ? 1 : 3, QST = DT == 256 ? 2 : 3;
+    static constexpr int KST = DT == 256 ? 1 : 2, QST = DT == 256 ? 2 : DT == 128 ? 4 : 8;
     static constexpr int TILE = 128 * DT * 2;
     static constexpr int K_OFF = 0, Q_OFF = KST * TILE;
-    static constexpr int LSE_OFF = Q_OFF + QST * TILE;            // [group][2][128] floats
-    static constexpr int PART_OFF = LSE_OFF + kGroups * 2 * 128 * 4;   // [2][group - 1][128] floats
+    static constexpr int LSE_OFF = Q_OFF + QST * TILE;            // [buffer][128] floats
+    static constexpr int PART_OFF = LSE_OFF + kBufs * 128 * 4;   // [2][group - 1][128] floats
     static constexpr int BAR_OFF = PART_OFF + 2 * (kGroups - 1) * 128 * 4;
     static constexpr int B_KFULL = 0, B_KEMPTY = B_KFULL + KST;
     static constexpr int B_QFULL = B_KEMPTY + KST, B_QEMPTY = B_QFULL + QST;
     static constexpr int B_SFULL = B_QEMPTY + QST, B_SEMPTY = B_SFULL + kBufs;
-    static constexpr int B_PFULL = B_SEMPTY + kBufs, B_PEMPTY = B_PFULL + 2;
+    static constexpr int B_LEMPTY = B_SEMPTY + kBufs;
+    static constexpr int B_PFULL = B_LEMPTY + kBufs, B_PEMPTY = B_PFULL + 2;
     static constexpr int B_RFULL = B_PEMPTY + 2, B_REMPTY = B_RFULL + 2;
     static constexpr int B_DRAIN = B_REMPTY + 2;
     static constexpr int NBAR = B_DRAIN + 1;
@@ -61,53 +63,41 @@ struct Layout {
     static constexpr size_t ALLOC = (size_t)BYTES + 1024;
 };
 
-// The query blocks of an item in order: chunk, head of the group, block of rows.
-struct Walk {
-    const MassArgs& a;
-    const MassItem it;
-    int32_t c, g, r;          // next chunk, head, row
-    int32_t qe, ctx, r0;      // of the current chunk; r0: first row at or after the tile's first key
-    bool bad;
-    __device__ __forceinline__ Walk(const MassArgs& args, const MassItem& item)
-        : a(args), it(item), c(item.c_lo - 1), g(0), r(0), qe(0), ctx(0), r0(0), bad(false) {
-        step_chunk();
-    }
-    __device__ __forceinline__ void step_chunk() {
-        for (++c; c < it.c_hi; ++c) {
-            const attn_chunk ch = a.chunks[c];
-            if (!(0 <= ch.ctx_begin && ch.ctx_begin <= ch.q_begin && ch.q_begin < ch.q_end && ch.q_end <= a.g.T)) {
-                bad = true;
-                return;
+// The query blocks of an item in order (chunk, head of the group, 128 rows), those
+// numbered `mine` of every `every` counting on from `count`: f(number, context begin,
+// head, first row, rows) until it returns false. False: f did, or a chunk is not one
+// (*bad).
+template <typename F>
+__device__ __forceinline__ bool walk_blocks(const MassArgs& a, const MassItem& it, int G, uint32_t& count, uint32_t every,
+                                            uint32_t mine, bool& bad, F f) {
+    for (int32_t c = it.c_lo; c < it.c_hi; ++c) {
+        const attn_chunk ch = a.chunks[c];
+        if (!(0 <= ch.ctx_begin && ch.ctx_begin <= ch.q_begin && ch.q_begin < ch.q_end && ch.q_end <= a.g.T)) {
+            bad = true;
+            return false;
+        }
+        if (ch.ctx_begin >= it.j1 || ch.q_end <= it.j0) continue;
+        const int32_t r0 = max(ch.q_begin, it.j0), nb = (ch.q_end - r0 + kRows - 1) / kRows;
+        for (int32_t g = 0; g < G; ++g) {
+            for (int32_t x = every == 1 ? 0 : (int32_t)((mine + every - count % every) % every); x < nb; x += every) {
+                const int32_t r = r0 + x * kRows;
+                if (!f(count + x, ch.ctx_begin, g, r, min(kRows, ch.q_end - r))) return false;
             }
-            if (ch.ctx_begin >= it.j1 || ch.q_end <= it.j0) continue;
-            qe = ch.q_end;
-            ctx = ch.ctx_begin;
-            r0 = max(ch.q_begin, it.j0);
-            g = 0;
-            r = r0;
-            return;
+            count += nb;
         }
     }
-    __device__ __forceinline__ bool more() const { return !bad && c < it.c_hi; }
-    __device__ __forceinline__ int32_t rows() const { return min(kRows, qe - r); }
-    __device__ __forceinline__ void next(int32_t G) {
-        r += kRows;
-        if (r < qe) return;
-        r = r0;
-        if (++g < G) return;
-        step_chunk();
-    }
-};
+    return true;
+}
+
+// Whether any row sees a key of the item.
+__device__ __forceinline__ bool seen(const MassArgs& a, const MassItem& it) {
+    for (int32_t c = it.c_lo; c < it.c_hi; ++c)
+        if (a.chunks[c].ctx_begin < it.j1 && a.chunks[c].q_end > it.j0) return true;
+    return false;
+}
 
 __device__ __forceinline__ bool item_ok(const MassItem& it, const MassArgs& a) {
     return 0 <= it.j0 && it.j0 < it.j1 && it.j1 - it.j0 <= 128 && it.j1 <= a.g.T && 0 <= it.c_lo && it.c_hi <= a.n;
-}
-
-// Wait for this thread's TMEM loads; r's values are those of the load that the wait completes.
-__device__ __forceinline__ void tmem_ld_done(uint32_t (&r)[32]) {
-    tmem_ld_wait();
-#pragma unroll
-    for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
 }
 
 // ROWS rows x DT dims: boxes of 64 dims x 64 rows, dims in strides of 128 rows.
@@ -149,14 +139,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(bar(L::B_QEMPTY + s), 1);
         }
         for (int s = 0; s < kBufs; ++s) {
-            mbar_init(bar(L::B_SFULL + s), 1);
+            mbar_init(bar(L::B_SFULL + s), 2);                 // the products and the rows' lse
             mbar_init(bar(L::B_SEMPTY + s), 128);
+            mbar_init(bar(L::B_LEMPTY + s), 128);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(bar(L::B_PFULL + s), 128 * (kGroups - 1));
             mbar_init(bar(L::B_PEMPTY + s), 128);
             mbar_init(bar(L::B_RFULL + s), 1);
-            mbar_init(bar(L::B_REMPTY + s), 1 + 4 * kGroups);
+            mbar_init(bar(L::B_REMPTY + s), 2 + 4 * kGroups);
         }
         mbar_init(bar(L::B_DRAIN), 1);
         *abort_flag = 0;
@@ -190,9 +181,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 const int b = bh / a.g.Hkv, hk = bh % a.g.Hkv;
-                Walk wk(a, item);
-                bool ok = true;
-                if (wk.more()) {
+                bool ok = true, bad = false;
+                if (seen(a, item)) {
                     const uint32_t s = kc % L::KST;
                     ok = mbar_wait(bar(L::B_KEMPTY + s), ((kc / L::KST) & 1) ^ 1, abort_flag, a.status, a.wait_ns);
                     if (!ok) break;
@@ -200,17 +190,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     load_rows<DT>(sbase + L::K_OFF + s * L::TILE, &tmk, bar(L::B_KFULL + s), mpkv, item.j0, 2, hk, b);
                     ++kc;
                 }
-                for (; wk.more(); wk.next(G)) {
-                    const uint32_t s = qc % L::QST;
-                    ok = mbar_wait(bar(L::B_QEMPTY + s), ((qc / L::QST) & 1) ^ 1, abort_flag, a.status, a.wait_ns);
-                    if (!ok) break;
-                    const int boxes = wk.rows() > kBoxRows ? 2 : 1;
+                walk_blocks(a, item, G, qc, 1, 0, bad, [&](uint32_t q, int, int g, int r, int rows) {
+                    const uint32_t s = q % L::QST;
+                    ok = mbar_wait(bar(L::B_QEMPTY + s), ((q / L::QST) & 1) ^ 1, abort_flag, a.status, a.wait_ns);
+                    if (!ok) return false;
+                    const int boxes = rows > kBoxRows ? 2 : 1;
                     mbar_expect_tx(bar(L::B_QFULL + s), boxes * (L::TILE / 2));
-                    load_rows<DT>(sbase + L::Q_OFF + s * L::TILE, &tmq, bar(L::B_QFULL + s), mp, wk.r, boxes, hk * G + wk.g, b);
-                    ++qc;
-                }
+                    load_rows<DT>(sbase + L::Q_OFF + s * L::TILE, &tmq, bar(L::B_QFULL + s), mp, r, boxes, hk * G + g, b);
+                    return true;
+                });
                 if (!ok) break;
-                if (wk.bad) {
+                if (bad) {
                     set_error(a.status, ATTN_E_BOUNDS);
                     *abort_flag = 1;
                     break;
@@ -231,21 +221,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 decode_work(w, a.n_items, BH, 1 << 30, i, bh);
                 const MassItem item = a.items[i];
                 if (!item_ok(item, a)) break;
-                Walk wk(a, item);
-                if (!wk.more()) continue;
+                if (!seen(a, item)) continue;
                 const uint32_t ks = kc % L::KST;
                 ok = mbar_wait(bar(L::B_KFULL + ks), (kc / L::KST) & 1, abort_flag, a.status, a.wait_ns);
                 if (!ok) break;
                 const uint32_t k0 = sbase + L::K_OFF + ks * L::TILE;
-                for (; wk.more(); wk.next(G)) {
-                    const uint32_t qs = qc % L::QST, sb = qc % kBufs;
-                    ok = mbar_wait(bar(L::B_QFULL + qs), (qc / L::QST) & 1, abort_flag, a.status, a.wait_ns) &&
-                         mbar_wait(bar(L::B_SEMPTY + sb), ((qc / kBufs) & 1) ^ 1, abort_flag, a.status, a.wait_ns);
-                    if (!ok) break;
+                bool bad = false;
+                ok = walk_blocks(a, item, G, qc, 1, 0, bad, [&](uint32_t q, int, int, int, int rows) {
+                    const uint32_t qs = q % L::QST, sb = q % kBufs;
+                    if (!mbar_wait(bar(L::B_QFULL + qs), (q / L::QST) & 1, abort_flag, a.status, a.wait_ns) ||
+                        !mbar_wait(bar(L::B_SEMPTY + sb), ((q / kBufs) & 1) ^ 1, abort_flag, a.status, a.wait_ns))
+                        return false;
                     tc_fence_after();
                     const uint32_t q0 = sbase + L::Q_OFF + qs * L::TILE;
                     // as many columns as the block has rows, in steps of 16
-                    const uint32_t id = idesc_bf16(128, (wk.rows() + 15) & ~15, 0, 0);
+                    const uint32_t id = idesc_bf16(128, (rows + 15) & ~15, 0, 0);
 #pragma unroll
                     for (int kk = 0; kk < DT / 16; ++kk) {
                         const uint32_t off = (kk >> 2) * (128 * 128) + (kk & 3) * 32;
@@ -253,12 +243,49 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     mma_commit(bar(L::B_QEMPTY + qs));
                     mma_commit(bar(L::B_SFULL + sb));
-                    ++qc;
-                }
-                if (!ok || wk.bad) break;
+                    return true;
+                });
+                if (!ok) break;
                 mma_commit(bar(L::B_KEMPTY + ks));
                 ++kc;
             }
+        }
+    } else if (warp == 2) {
+        // ------------------------------------------------------------ log-sum-exps
+        const int lane = tid & 31;
+        uint32_t qc = 0, ic = 0;
+        bool ok = true;
+        for (; ok; ++ic) {
+            int32_t w = -1;
+            ok = ring_get_warp(ring, ic, w, abort_flag, a.status, a.wait_ns);
+            if (!ok || w < 0) break;
+            int32_t i, bh;
+            decode_work(w, a.n_items, BH, 1 << 30, i, bh);
+            const MassItem item = a.items[i];
+            if (!item_ok(item, a)) break;
+            const int b = bh / a.g.Hkv, hk = bh % a.g.Hkv;
+            bool bad = false;
+            ok = walk_blocks(a, item, G, qc, 1, 0, bad, [&](uint32_t q, int, int g, int r, int n) {
+                const uint32_t sb = q % kBufs;
+                const float* src = a.lse + ((int64_t)b * a.g.H + hk * G + g) * a.g.T + r;
+                float x[4];
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    // weight 0: rows past the block, rows without a sum
+                    x[y] = -INFINITY;
+                    if (32 * y + lane < n) {
+                        x[y] = src[32 * y + lane];
+                        x[y] = x[y] == -INFINITY ? x[y] : -x[y] * kLog2e;
+                    }
+                }
+                if (!mbar_wait_warp(bar(L::B_LEMPTY + sb), ((q / kBufs) & 1) ^ 1, abort_flag, a.status, a.wait_ns)) return false;
+                float* dst = reinterpret_cast<float*>(sm + L::LSE_OFF) + sb * 128;
+#pragma unroll
+                for (int y = 0; y < 4; ++y) dst[32 * y + lane] = x[y];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(L::B_SFULL + sb));
+                return true;
+            });
         }
     } else if (warp >= 4) {
         // ------------------------------------------------------------ sums
@@ -266,91 +293,71 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
         const float c = a.g.scale * kLog2e;
         const float2 c2 = make_float2(c, c);
-        float* s_lse = reinterpret_cast<float*>(sm + L::LSE_OFF) + grp * 256;
         float* s_part = reinterpret_cast<float*>(sm + L::PART_OFF);
-        uint32_t qc = 0, mine = 0, ic = 0;
+        uint32_t qc = 0, ic = 0;
         bool ok = true;
         for (; ok; ++ic) {
             int32_t w = -1;
             ok = ring_get_warp(ring, ic, w, abort_flag, a.status, a.wait_ns);
-            // the four warps of a group go on together or not at all
-            ok = named_sync_all(1 + grp, 128, ok);
             if (!ok || w < 0) break;
             int32_t i, bh;
             decode_work(w, a.n_items, BH, 1 << 30, i, bh);
             const MassItem item = a.items[i];
-            if (!item_ok(item, a)) break;                    // the same for every thread
-            const int b = bh / a.g.Hkv, hk = bh % a.g.Hkv;
+            if (!item_ok(item, a)) break;
             const int j = item.j0 + key;
             float sum = 0.f, err = 0.f;                      // compensated
-            Walk wk(a, item);
-            for (; wk.more(); wk.next(G), ++qc) {
-                if (qc % kGroups != grp) continue;
-                const int n = wk.rows();
-                float* lse = s_lse + (mine & 1) * 128;
-                ++mine;
-                {
-                    float x = -INFINITY;                     // weight 0: rows past the block, rows without a sum
-                    if (key < n) {
-                        x = a.lse[((int64_t)b * a.g.H + hk * G + wk.g) * a.g.T + wk.r + key];
-                        x = x == -INFINITY ? x : -x * kLog2e;
-                    }
-                    lse[key] = x;
-                }
-                const uint32_t sb = qc % kBufs;
-                ok = mbar_wait_warp(bar(L::B_SFULL + sb), (qc / kBufs) & 1, abort_flag, a.status, a.wait_ns);
-                ok = named_sync_all(1 + grp, 128, ok);
-                if (!ok) break;
+            bool bad = false;
+            ok = walk_blocks(a, item, G, qc, kGroups, grp, bad, [&](uint32_t q, int ctx, int, int row0, int n) {
+                const uint32_t sb = q % kBufs;
+                const float* lse = reinterpret_cast<const float*>(sm + L::LSE_OFF) + sb * 128;
+                if (!mbar_wait_warp(bar(L::B_SFULL + sb), (q / kBufs) & 1, abort_flag, a.status, a.wait_ns)) return false;
                 tc_fence_after();
                 // this key is seen by the columns [lo, n)
-                const int lo = wk.ctx <= j ? max(0, j - wk.r) : kRows;
-                const bool edge = n < kRows || wk.r < item.j1 - 1 || wk.ctx > item.j0;
+                const int lo = ctx <= j ? max(0, j - row0) : kRows;
+                const bool edge = n < kRows || row0 < item.j1 - 1 || ctx > item.j0;
                 const uint32_t sa = tmem + lane_addr + sb * kRows;
-                const int chunks = (n + 31) / 32;
+                uint32_t r[4][32];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) tmem_ld32(sa + x * 32, r[x]);   // columns past n: what an earlier block left
+                tmem_ld_wait();
+                tc_fence_before();
+                mbar_arrive(bar(L::B_SEMPTY + sb));          // the buffer has been read
                 float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                uint32_t r[2][32];
-                tmem_ld32(sa, r[0]);
-                auto weigh = [&](const uint32_t (&x)[32], int col) {
-                    const float4* l4 = reinterpret_cast<const float4*>(lse + col);
-                    if (!edge) {
+                if (!edge) {
+                    const float4* l4 = reinterpret_cast<const float4*>(lse);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
 #pragma unroll
                         for (int y = 0; y < 8; ++y) {
-                            const float4 l = l4[y];
-                            const float2 e0 = ffma2(make_float2(__uint_as_float(x[4 * y]), __uint_as_float(x[4 * y + 1])), c2,
-                                                    make_float2(l.x, l.y));
-                            const float2 e1 = ffma2(make_float2(__uint_as_float(x[4 * y + 2]), __uint_as_float(x[4 * y + 3])), c2,
-                                                    make_float2(l.z, l.w));
+                            const float4 l = l4[8 * x + y];
+                            const float2 e0 = ffma2(make_float2(__uint_as_float(r[x][4 * y]), __uint_as_float(r[x][4 * y + 1])),
+                                                    c2, make_float2(l.x, l.y));
+                            const float2 e1 = ffma2(make_float2(__uint_as_float(r[x][4 * y + 2]), __uint_as_float(r[x][4 * y + 3])),
+                                                    c2, make_float2(l.z, l.w));
                             acc[0] = fadd2(acc[0], make_float2(ex2(e0.x), ex2(e0.y)));
                             acc[1] = fadd2(acc[1], make_float2(ex2(e1.x), ex2(e1.y)));
                         }
-                    } else {
+                } else {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        if (32 * x >= n) break;
 #pragma unroll
                         for (int y = 0; y < 32; ++y) {
-                            const float e = fmaf(__uint_as_float(x[y]), c, lse[col + y]);
-                            const float p = col + y >= lo && col + y < n ? ex2(e) : 0.f;
+                            const int col = 32 * x + y;
+                            const float e = fmaf(__uint_as_float(r[x][y]), c, lse[col]);
+                            const float p = col >= lo && col < n ? ex2(e) : 0.f;
                             if (y & 1) acc[(y >> 1) & 1].y += p; else acc[(y >> 1) & 1].x += p;
                         }
                     }
-                };
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    if (x >= chunks) break;
-                    tmem_ld_done(r[x & 1]);
-                    if (x + 1 < chunks) {
-                        tmem_ld32(sa + (x + 1) * 32, r[(x + 1) & 1]);
-                    } else {
-                        // the buffer has been read
-                        tc_fence_before();
-                        mbar_arrive(bar(L::B_SEMPTY + sb));
-                    }
-                    weigh(r[x & 1], x * 32);
                 }
+                mbar_arrive(bar(L::B_LEMPTY + sb));
                 const float part = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
                 const float y = __fsub_rn(part, err), t = __fadd_rn(sum, y);
                 err = __fsub_rn(__fsub_rn(t, sum), y);
                 sum = t;
-            }
-            if (!ok || wk.bad) break;
+                return true;
+            });
+            if (!ok) break;
             sum -= err;
             // the groups' sums meet in the first group, in order
             const uint32_t slot = ic & 1;
