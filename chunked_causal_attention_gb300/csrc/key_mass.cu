@@ -12,11 +12,12 @@
 //   warp 1      MMA issuer and TMEM owner: S^T = K Q^T (M = 128 keys, N = rows of
 //               the block) into one of four 128-column TMEM buffers
 //   warp 2      the rows' -lse log2 e into shared memory, up to four blocks ahead
-//   warps 4-11  two groups that take the blocks in turn: thread = key (TMEM
+//   warps 4-15  three groups that take the blocks in turn: thread = key (TMEM
 //               lane); it reads its row of S^T, forms 2^(s c - lse2) with the
 //               block's lse2 from shared memory (two columns per instruction where
 //               the pipe allows) and sums. The warps meet no barrier among
 //               themselves
+//   warp 3      adds up the groups' sums of a finished item, in order, and writes them
 // Per block 2 * 128 * 128 * D FLOP (512 cycles of an SM at D = 128) stand against
 // 128 * 128 exponentials (512 cycles at 32 a cycle): both pipes are needed whole.
 //
@@ -35,7 +36,7 @@ namespace {
 
 using namespace tc;
 
-constexpr int kGroups = 2;                 // softmax warpgroups
+constexpr int kGroups = 3;                 // softmax warpgroups
 constexpr int kThreads = 128 + 128 * kGroups;
 constexpr int kBufs = 4;                   // S^T buffers in TMEM
 constexpr uint32_t kTmemCols = 512;
@@ -48,8 +49,10 @@ struct Layout {
     static constexpr int TILE = 128 * DT * 2;
     static constexpr int K_OFF = 0, Q_OFF = KST * TILE;
     static constexpr int LSE_OFF = Q_OFF + QST * TILE;            // [buffer][128] floats
-    static constexpr int PART_OFF = LSE_OFF + kBufs * 128 * 4;   // [2][group - 1][128] floats
-    static constexpr int BAR_OFF = PART_OFF + 2 * (kGroups - 1) * 128 * 4;
+    static constexpr int PART_OFF = LSE_OFF + kBufs * 128 * 4;   // [2][group][128] floats
+    static constexpr int ITEM_OFF = PART_OFF + 2 * kGroups * 128 * 4;           // [2] items handed out
+    static constexpr int TAG_OFF = ITEM_OFF + 2 * 16;                            // [buffer] block whose lse it holds, plus 1
+    static constexpr int BAR_OFF = TAG_OFF + kBufs * 4;
     static constexpr int B_KFULL = 0, B_KEMPTY = B_KFULL + KST;
     static constexpr int B_QFULL = B_KEMPTY + KST, B_QEMPTY = B_QFULL + QST;
     static constexpr int B_SFULL = B_QEMPTY + QST, B_SEMPTY = B_SFULL + kBufs;
@@ -63,13 +66,15 @@ struct Layout {
     static constexpr size_t ALLOC = (size_t)BYTES + 1024;
 };
 
-// The query blocks of an item in order (chunk, head of the group, 128 rows), those
-// numbered `mine` of every `every` counting on from `count`: f(number, context begin,
-// head, first row, rows) until it returns false. False: f did, or a chunk is not one
-// (*bad).
+// The query blocks of an item in order (chunk, head of the group, 128 rows): of every
+// `every` the one numbered `mine`, counting within the item, so that which group sums a
+// block does not depend on the items before. f(number, context begin, head, first row,
+// rows) until it returns false, the number counting on from `count`. False: f did, or a
+// chunk is not one (bad).
 template <typename F>
 __device__ __forceinline__ bool walk_blocks(const MassArgs& a, const MassItem& it, int G, uint32_t& count, uint32_t every,
                                             uint32_t mine, bool& bad, F f) {
+    const uint32_t start = count;
     for (int32_t c = it.c_lo; c < it.c_hi; ++c) {
         const attn_chunk ch = a.chunks[c];
         if (!(0 <= ch.ctx_begin && ch.ctx_begin <= ch.q_begin && ch.q_begin < ch.q_end && ch.q_end <= a.g.T)) {
@@ -79,7 +84,7 @@ __device__ __forceinline__ bool walk_blocks(const MassArgs& a, const MassItem& i
         if (ch.ctx_begin >= it.j1 || ch.q_end <= it.j0) continue;
         const int32_t r0 = max(ch.q_begin, it.j0), nb = (ch.q_end - r0 + kRows - 1) / kRows;
         for (int32_t g = 0; g < G; ++g) {
-            for (int32_t x = every == 1 ? 0 : (int32_t)((mine + every - count % every) % every); x < nb; x += every) {
+            for (int32_t x = every == 1 ? 0 : (int32_t)((mine + every - (count - start) % every) % every); x < nb; x += every) {
                 const int32_t r = r0 + x * kRows;
                 if (!f(count + x, ch.ctx_begin, g, r, min(kRows, ch.q_end - r))) return false;
             }
@@ -89,11 +94,31 @@ __device__ __forceinline__ bool walk_blocks(const MassArgs& a, const MassItem& i
     return true;
 }
 
+// A group sums the blocks x of an item with x % kGroups == turn: the first block goes to
+// another group from tile to tile, for items of few blocks.
+__device__ __forceinline__ uint32_t turn_of(const MassItem& it, int grp) { return (uint32_t)(grp + it.j0 / 128) % kGroups; }
 // Whether any row sees a key of the item.
 __device__ __forceinline__ bool seen(const MassArgs& a, const MassItem& it) {
     for (int32_t c = it.c_lo; c < it.c_hi; ++c)
         if (a.chunks[c].ctx_begin < it.j1 && a.chunks[c].q_end > it.j0) return true;
     return false;
+}
+
+// Wait, for a whole warp, until *tag is `want`; bounded like an mbarrier wait.
+__device__ __noinline__ bool tag_wait(volatile uint32_t* tag, uint32_t want, volatile int* abort, uint32_t* status,
+                                      uint64_t limit_ns) {
+    const uint64_t t0 = globaltimer();
+    bool ok = true;
+    while (ok && *tag != want) {
+        if (*abort) {
+            ok = false;
+        } else if (globaltimer() - t0 > limit_ns) {
+            *abort = 1;
+            set_error(status, ATTN_E_TIMEOUT);
+            ok = false;
+        }
+    }
+    return __all_sync(0xffffffffu, ok);
 }
 
 __device__ __forceinline__ bool item_ok(const MassItem& it, const MassArgs& a) {
@@ -128,6 +153,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const WorkRing ring{reinterpret_cast<volatile int32_t*>(sm + L::MISC_OFF + 8), bar(L::B_RFULL), bar(L::B_REMPTY)};
     const int tid = threadIdx.x, warp = tid >> 5;
     const int BH = a.g.B * a.g.Hkv, G = a.g.H / a.g.Hkv;
+    MassItem* s_item = reinterpret_cast<MassItem*>(sm + L::ITEM_OFF);
+    volatile uint32_t* s_tag = reinterpret_cast<volatile uint32_t*>(sm + L::TAG_OFF);
+    // a role that is a whole warp takes the next item: false at the end
+    auto take_warp = [&](uint32_t ic, MassItem& item, int32_t& bh) {
+        if (!mbar_wait_warp(ring.full + 8 * (ic & 1), (ic >> 1) & 1, abort_flag, a.status, a.wait_ns)) return false;
+        bh = ring.slot[ic & 1];
+        item = s_item[ic & 1];
+        __syncwarp();
+        if ((tid & 31) == 0) mbar_arrive(ring.empty + 8 * (ic & 1));
+        return bh >= 0;
+    };
 
     if (tid == 0) {
         for (int s = 0; s < L::KST; ++s) {
@@ -140,14 +176,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int s = 0; s < kBufs; ++s) {
             mbar_init(bar(L::B_SFULL + s), 2);                 // the products and the rows' lse
+            s_tag[s] = 0;
             mbar_init(bar(L::B_SEMPTY + s), 128);
             mbar_init(bar(L::B_LEMPTY + s), 128);
         }
         for (int s = 0; s < 2; ++s) {
-            mbar_init(bar(L::B_PFULL + s), 128 * (kGroups - 1));
-            mbar_init(bar(L::B_PEMPTY + s), 128);
+            mbar_init(bar(L::B_PFULL + s), 128 * kGroups);
+            mbar_init(bar(L::B_PEMPTY + s), 32);
             mbar_init(bar(L::B_RFULL + s), 1);
-            mbar_init(bar(L::B_REMPTY + s), 2 + 4 * kGroups);
+            mbar_init(bar(L::B_REMPTY + s), 3 + 4 * kGroups);
         }
         mbar_init(bar(L::B_DRAIN), 1);
         *abort_flag = 0;
@@ -168,18 +205,34 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_prefetch_desc(&tmq);
             tma_prefetch_desc(&tmk);
             uint32_t kc = 0, qc = 0, ic = 0;
-            int32_t w = a.stall ? n_work : (int32_t)atomicAdd(a.counter, 1u);
-            for (; !a.stall; ++ic) {
-                if (!ring_put(ring, ic, w < n_work ? w : -1, abort_flag, a.status, a.wait_ns)) break;
-                if (w >= n_work || *abort_flag) break;
-                int32_t i, bh;
+            // An item is read one ahead, so that the list is not waited for between
+            // items. (Claiming two ahead before the loads took 259 us at 8K tokens against 251: the
+            // blocks end less evenly.)
+            auto item_of = [&](int32_t w, int32_t& bh) {
+                int32_t i = 0;
+                bh = 0;
+                if (w >= n_work) return MassItem{0, 0, 0, 0};
                 decode_work(w, a.n_items, BH, 1 << 30, i, bh);
-                const MassItem item = a.items[i];
-                if (!item_ok(item, a)) {
-                    set_error(a.status, ATTN_E_BOUNDS);
-                    *abort_flag = 1;
-                    break;
+                return a.items[i];
+            };
+            int32_t w = a.stall ? n_work : (int32_t)atomicAdd(a.counter, 1u);
+            int32_t w1 = a.stall ? n_work : (int32_t)atomicAdd(a.counter, 1u);
+            int32_t w2 = n_work, bh = 0, bh1 = 0;
+            MassItem item = item_of(w, bh), item1 = item;
+            for (; !a.stall; ++ic, w = w1, w1 = w2, item = item1, bh = bh1) {
+                if (w < n_work) {
+                    if (!item_ok(item, a)) {
+                        set_error(a.status, ATTN_E_BOUNDS);
+                        *abort_flag = 1;
+                        break;
+                    }
+                    // the slot is free once every role has taken the item before the last (ring_put waits for it too)
+                    if (!mbar_wait(bar(L::B_REMPTY + (ic & 1)), ((ic >> 1) & 1) ^ 1, abort_flag, a.status, a.wait_ns)) break;
+                    s_item[ic & 1] = item;
                 }
+                if (!ring_put(ring, ic, w < n_work ? bh : -1, abort_flag, a.status, a.wait_ns)) break;
+                if (w >= n_work || *abort_flag) break;
+                item1 = item_of(w1, bh1);
                 const int b = bh / a.g.Hkv, hk = bh % a.g.Hkv;
                 bool ok = true, bad = false;
                 if (seen(a, item)) {
@@ -205,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     *abort_flag = 1;
                     break;
                 }
-                w = (int32_t)atomicAdd(a.counter, 1u);
+                w2 = (int32_t)atomicAdd(a.counter, 1u);
             }
         }
     } else if (warp == 1) {
@@ -214,13 +267,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t kc = 0, qc = 0, ic = 0;
             bool ok = true;
             for (; ok; ++ic) {
-                int32_t w = -1;
-                ok = ring_get(ring, ic, w, abort_flag, a.status, a.wait_ns);
-                if (!ok || w < 0 || *abort_flag) break;
-                int32_t i, bh;
-                decode_work(w, a.n_items, BH, 1 << 30, i, bh);
-                const MassItem item = a.items[i];
-                if (!item_ok(item, a)) break;
+                if (!mbar_wait(ring.full + 8 * (ic & 1), (ic >> 1) & 1, abort_flag, a.status, a.wait_ns)) break;
+                const int32_t bh = ring.slot[ic & 1];
+                const MassItem item = s_item[ic & 1];
+                mbar_arrive(ring.empty + 8 * (ic & 1));
+                if (bh < 0 || *abort_flag) break;
                 if (!seen(a, item)) continue;
                 const uint32_t ks = kc % L::KST;
                 ok = mbar_wait(bar(L::B_KFULL + ks), (kc / L::KST) & 1, abort_flag, a.status, a.wait_ns);
@@ -256,13 +307,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t qc = 0, ic = 0;
         bool ok = true;
         for (; ok; ++ic) {
-            int32_t w = -1;
-            ok = ring_get_warp(ring, ic, w, abort_flag, a.status, a.wait_ns);
-            if (!ok || w < 0) break;
-            int32_t i, bh;
-            decode_work(w, a.n_items, BH, 1 << 30, i, bh);
-            const MassItem item = a.items[i];
-            if (!item_ok(item, a)) break;
+            int32_t bh;
+            MassItem item;
+            if (!take_warp(ic, item, bh)) break;
             const int b = bh / a.g.Hkv, hk = bh % a.g.Hkv;
             bool bad = false;
             ok = walk_blocks(a, item, G, qc, 1, 0, bad, [&](uint32_t q, int, int g, int r, int n) {
@@ -282,6 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float* dst = reinterpret_cast<float*>(sm + L::LSE_OFF) + sb * 128;
 #pragma unroll
                 for (int y = 0; y < 4; ++y) dst[32 * y + lane] = x[y];
+                if (lane == 0) s_tag[sb] = q + 1;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(L::B_SFULL + sb));
                 return true;
@@ -297,57 +345,61 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t qc = 0, ic = 0;
         bool ok = true;
         for (; ok; ++ic) {
-            int32_t w = -1;
-            ok = ring_get_warp(ring, ic, w, abort_flag, a.status, a.wait_ns);
-            if (!ok || w < 0) break;
-            int32_t i, bh;
-            decode_work(w, a.n_items, BH, 1 << 30, i, bh);
-            const MassItem item = a.items[i];
-            if (!item_ok(item, a)) break;
+            int32_t bh;
+            MassItem item;
+            if (!take_warp(ic, item, bh)) break;
             const int j = item.j0 + key;
             float sum = 0.f, err = 0.f;                      // compensated
             bool bad = false;
-            ok = walk_blocks(a, item, G, qc, kGroups, grp, bad, [&](uint32_t q, int ctx, int, int row0, int n) {
+            ok = walk_blocks(a, item, G, qc, kGroups, turn_of(item, grp), bad, [&](uint32_t q, int ctx, int, int row0, int n) {
                 const uint32_t sb = q % kBufs;
                 const float* lse = reinterpret_cast<const float*>(sm + L::LSE_OFF) + sb * 128;
+                // A parity tells neighbouring phases apart only, and a group that had no block for a while may
+                // come before the phase ahead of its own has ended: the buffer's tag names the block
+                // whose lse it holds, written once the block before it there has been summed.
+                if (__any_sync(0xffffffffu, s_tag[sb] != q + 1) && !tag_wait(s_tag + sb, q + 1, abort_flag, a.status, a.wait_ns)) return false;
                 if (!mbar_wait_warp(bar(L::B_SFULL + sb), (q / kBufs) & 1, abort_flag, a.status, a.wait_ns)) return false;
                 tc_fence_after();
                 // this key is seen by the columns [lo, n)
                 const int lo = ctx <= j ? max(0, j - row0) : kRows;
                 const bool edge = n < kRows || row0 < item.j1 - 1 || ctx > item.j0;
                 const uint32_t sa = tmem + lane_addr + sb * kRows;
-                uint32_t r[4][32];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) tmem_ld32(sa + x * 32, r[x]);   // columns past n: what an earlier block left
-                tmem_ld_wait();
-                tc_fence_before();
-                mbar_arrive(bar(L::B_SEMPTY + sb));          // the buffer has been read
                 float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                if (!edge) {
-                    const float4* l4 = reinterpret_cast<const float4*>(lse);
+#pragma unroll 1
+                for (int half = 0; half < kRows; half += 64) {
+                    uint32_t r[2][32];
+                    tmem_ld32(sa + half, r[0]);              // columns past n: what an earlier block left
+                    tmem_ld32(sa + half + 32, r[1]);
+                    tmem_ld_wait();
+                    if (half) {
+                        tc_fence_before();
+                        mbar_arrive(bar(L::B_SEMPTY + sb));  // the buffer has been read
+                    }
+                    if (!edge) {
+                        const float4* l4 = reinterpret_cast<const float4*>(lse + half);
 #pragma unroll
-                    for (int x = 0; x < 4; ++x)
+                        for (int x = 0; x < 2; ++x)
 #pragma unroll
-                        for (int y = 0; y < 8; ++y) {
-                            const float4 l = l4[8 * x + y];
-                            const float2 e0 = ffma2(make_float2(__uint_as_float(r[x][4 * y]), __uint_as_float(r[x][4 * y + 1])),
-                                                    c2, make_float2(l.x, l.y));
-                            const float2 e1 = ffma2(make_float2(__uint_as_float(r[x][4 * y + 2]), __uint_as_float(r[x][4 * y + 3])),
-                                                    c2, make_float2(l.z, l.w));
-                            acc[0] = fadd2(acc[0], make_float2(ex2(e0.x), ex2(e0.y)));
-                            acc[1] = fadd2(acc[1], make_float2(ex2(e1.x), ex2(e1.y)));
-                        }
-                } else {
+                            for (int y = 0; y < 8; ++y) {
+                                const float4 l = l4[8 * x + y];
+                                const float2 e0 = ffma2(make_float2(__uint_as_float(r[x][4 * y]), __uint_as_float(r[x][4 * y + 1])),
+                                                        c2, make_float2(l.x, l.y));
+                                const float2 e1 = ffma2(make_float2(__uint_as_float(r[x][4 * y + 2]), __uint_as_float(r[x][4 * y + 3])),
+                                                        c2, make_float2(l.z, l.w));
+                                acc[0] = fadd2(acc[0], make_float2(ex2(e0.x), ex2(e0.y)));
+                                acc[1] = fadd2(acc[1], make_float2(ex2(e1.x), ex2(e1.y)));
+                            }
+                    } else if (half < n) {
+                        const int from = lo - half, to = n - half;
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        if (32 * x >= n) break;
+                        for (int x = 0; x < 2; ++x)
 #pragma unroll
-                        for (int y = 0; y < 32; ++y) {
-                            const int col = 32 * x + y;
-                            const float e = fmaf(__uint_as_float(r[x][y]), c, lse[col]);
-                            const float p = col >= lo && col < n ? ex2(e) : 0.f;
-                            if (y & 1) acc[(y >> 1) & 1].y += p; else acc[(y >> 1) & 1].x += p;
-                        }
+                            for (int y = 0; y < 32; ++y) {
+                                const int col = 32 * x + y;
+                                const float e = fmaf(__uint_as_float(r[x][y]), c, lse[half + col]);
+                                const float p = col >= from && col < to ? ex2(e) : 0.f;
+                                if (y & 1) acc[(y >> 1) & 1].y += p; else acc[(y >> 1) & 1].x += p;
+                            }
                     }
                 }
                 mbar_arrive(bar(L::B_LEMPTY + sb));
@@ -359,25 +411,36 @@ __global__ void __launch_bounds__(kThreads, 1)
             });
             if (!ok) break;
             sum -= err;
-            // the groups' sums meet in the first group, in order
             const uint32_t slot = ic & 1;
-            if (grp) {
-                ok = mbar_wait_warp(bar(L::B_PEMPTY + slot), ((ic >> 1) & 1) ^ 1, abort_flag, a.status, a.wait_ns);
-                if (ok) {
-                    s_part[(slot * (kGroups - 1) + grp - 1) * 128 + key] = sum;
-                    mbar_arrive(bar(L::B_PFULL + slot));
-                }
-            } else {
-                ok = mbar_wait_warp(bar(L::B_PFULL + slot), (ic >> 1) & 1, abort_flag, a.status, a.wait_ns);
-                if (ok) {
-                    for (int x = 0; x < kGroups - 1; ++x) sum += s_part[(slot * (kGroups - 1) + x) * 128 + key];
-                    mbar_arrive(bar(L::B_PEMPTY + slot));
-                    if (j < item.j1) {
-                        const int64_t at = (int64_t)bh * a.g.T + j;
-                        a.mass_out[at] = (a.mass_in ? a.mass_in[at] : 0.f) + sum;
-                    }
-                }
+            ok = mbar_wait_warp(bar(L::B_PEMPTY + slot), ((ic >> 1) & 1) ^ 1, abort_flag, a.status, a.wait_ns);
+            if (!ok) break;
+            s_part[(slot * kGroups + grp) * 128 + key] = sum;
+            mbar_arrive(bar(L::B_PFULL + slot));
+        }
+    } else {
+        // ------------------------------------------------------------ results
+        const int lane = tid & 31;
+        const float* s_part = reinterpret_cast<const float*>(sm + L::PART_OFF);
+        for (uint32_t ic = 0;; ++ic) {
+            int32_t bh;
+            MassItem item;
+            if (!take_warp(ic, item, bh)) break;
+            float base[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const int j = item.j0 + 32 * y + lane;
+                base[y] = a.mass_in && j < item.j1 ? a.mass_in[(int64_t)bh * a.g.T + j] : 0.f;
             }
+            const uint32_t slot = ic & 1;
+            if (!mbar_wait_warp(bar(L::B_PFULL + slot), (ic >> 1) & 1, abort_flag, a.status, a.wait_ns)) break;
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const int key = 32 * y + lane, j = item.j0 + key;
+                float sum = 0.f;
+                for (int x = 0; x < kGroups; ++x) sum += s_part[(slot * kGroups + x) * 128 + key];
+                if (j < item.j1) a.mass_out[(int64_t)bh * a.g.T + j] = base[y] + sum;
+            }
+            mbar_arrive(bar(L::B_PEMPTY + slot));
         }
     }
     // ---------------------------------------------------------------- teardown
