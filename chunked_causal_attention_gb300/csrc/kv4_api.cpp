@@ -220,6 +220,7 @@ int attn_kv4_evict(const attn_kv4_cache* src, const int32_t* lens, const float* 
         return ATTN_E_INVAL;
     if (!aligned(mass, 16) || !aligned(mass_out, 16) || !aligned(slots, 4) || !aligned(lens, 4) || !aligned(lens_out, 4))
         return ATTN_E_ALIGN;
+    if ((int64_t)a.src.B * a.src.Hkv * keep > INT32_MAX) return ATTN_E_INVAL;
     if (overlap(a.src, a.dst)) return ATTN_E_INVAL;
     const size_t rows = (size_t)a.src.B * a.src.Hkv;
     const size_t n_in = ((rows - 1) * mass_ld + std::min<int64_t>(mass_ld, a.src.cap)) * 4;

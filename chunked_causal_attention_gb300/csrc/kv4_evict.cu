@@ -1,10 +1,15 @@
 // Eviction by accumulated attention weight: choose the slots, then move them.
 //
 // Choosing is a radix selection: the masses map to 32-bit keys that order as they
-// do, and four histograms of eight bits each narrow down the value of the last
-// slot that is kept; a second pass counts the slots above it and the ties, of
-// which the lowest are kept, and writes the slots in order. One block per
-// (sequence, key/value head).
+// do, and four histograms of eight bits each narrow down the key of the last slot
+// that is kept; then the slots above it and the first of those equal to it are
+// written in order. A cluster of up to eight blocks shares a (sequence, key/value
+// head): each holds a stretch of the masses, read from memory once, as keys in its
+// shared memory; every block reads the others' histograms and comes to the same
+// digit, so a pass costs one cluster barrier.
+//
+// Moving is bound by the latency of two dependent reads (slot, row) and by bytes: a
+// thread takes one 16-byte piece of a row.
 #include <algorithm>
 
 #include "kv4_device.cuh"
@@ -15,6 +20,10 @@ namespace {
 using namespace kv4;
 
 constexpr int kThreads = 1024;
+constexpr int kPer = 4;                        // neighbouring masses of a thread and tile
+constexpr int kChunk = kThreads * kPer;
+constexpr int kMaxCluster = 8;
+constexpr int kHeldTiles = 8;                  // tiles of keys kept in shared memory (128 KB); the others are read again
 
 // Orders as the masses do: NaN above everything, -0 as 0.
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -23,7 +32,23 @@ __device__ __forceinline__ uint32_t order_key(float x) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// Exclusive prefix sum of x over the block and the block's total.
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+// A 32-bit word of block `rank`'s shared memory, at the address of this block's `p`.
+__device__ __forceinline__ uint32_t cluster_load(const uint32_t* p, uint32_t rank) {
+    uint32_t a = smem_u32(p), v;
+    asm volatile("mapa.shared::cluster.u32 %0, %0, %1;\n" : "+r"(a) : "r"(rank));
+    asm volatile("ld.shared::cluster.u32 %0, [%1];\n" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+
+// Exclusive prefix sum of x over the block, and the block's sum.
 __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* warp_sums, uint32_t& total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint32_t y = x;
@@ -34,103 +59,235 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* warp_sums, 
     }
     if (lane == 31) warp_sums[warp] = y;
     __syncthreads();
-    uint32_t before = 0;
-    total = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) before += warp_sums[w];
-        total += warp_sums[w];
+    uint32_t w = warp_sums[lane];                        // kThreads / 32 == 32 warps
+    uint32_t v = w;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        const uint32_t z = __shfl_up_sync(0xffffffffu, v, m);
+        if (lane >= m) v += z;
     }
+    total = __shfl_sync(0xffffffffu, v, 31);
+    const uint32_t before = __shfl_sync(0xffffffffu, v - w, warp);
     __syncthreads();
     return before + y - x;
 }
 
-__global__ void __launch_bounds__(kThreads) choose_kernel(const Kv4EvictArgs a) {
-    const int bh = blockIdx.x, b = bh / a.src.Hkv;
+__global__ void __launch_bounds__(kThreads) choose_kernel(const Kv4EvictArgs a, const int32_t blocks) {
+    extern __shared__ __align__(16) uint32_t held[];     // keys of the first kHeldTiles tiles
+    __shared__ uint32_t hist[2][256], warp_sums[32], found[2], counts[2];
+    const int rank = (int)cluster_rank(), bh = blockIdx.x / blocks, b = bh / a.src.Hkv, tid = threadIdx.x;
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     const int n = length_of(a.lens, b, (int32_t)min((int64_t)a.src.cap, a.mass_ld), a.status);
     const int m = min(n, a.keep), recent = min(m, a.recent);
-    const int cand = n - recent, want = m - recent;       // choose `want` of the slots [0, cand)
+    const int cand = n - recent, want = m - recent;      // choose `want` of the slots [0, cand)
     const float* mass = a.mass + (int64_t)bh * a.mass_ld;
     int32_t* out = a.slots + (int64_t)bh * a.keep;
-    __shared__ uint32_t hist[256], warp_sums[kThreads / 32], sh_prefix, sh_left;
-    uint32_t prefix = 0, left = want;                     // key of the last kept slot; how many of it and below its prefix
-    if (want < cand && want > 0) {
+    const bool choose = want > 0 && want < cand;         // the same for every block of the cluster
+    // this block's stretch: whole tiles
+    const int tiles = (cand + kChunk - 1) / kChunk, per = (tiles + blocks - 1) / blocks;
+    const int first = min(rank * per, tiles), last = min(first + per, tiles);
+    if (choose) {
+        auto keys = [&](int tile, uint32_t (&u)[kPer]) {
+            if (tile - first < kHeldTiles) {
+                const uint4 x = *reinterpret_cast<const uint4*>(held + (tile - first) * kChunk + tid * kPer);
+                u[0] = x.x; u[1] = x.y; u[2] = x.z; u[3] = x.w;
+            } else {
+                const int j = tile * kChunk + tid * kPer;
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) u[i] = j + i < cand ? order_key(mass[j + i]) : 0u;
+            }
+        };
+        uint32_t prefix = 0, left = want;                // key of the last kept slot; slots still to choose with its prefix
         for (int pass = 0; pass < 4; ++pass) {
             const int shift = 24 - 8 * pass;
-            for (int i = threadIdx.x; i < 256; i += kThreads) hist[i] = 0;
+            uint32_t* h = hist[pass & 1];
+            if (tid < 256) h[tid] = 0;
             __syncthreads();
-            for (int j = threadIdx.x; j < cand; j += kThreads) {
-                const uint32_t u = order_key(mass[j]);
-                if (pass == 0 || (u >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(u >> shift) & 255u], 1u);
+            for (int tile = first; tile < last; ++tile) {
+                uint32_t u[kPer];
+                const int j = tile * kChunk + tid * kPer;
+                if (pass == 0) {
+#pragma unroll
+                    for (int i = 0; i < kPer; ++i) u[i] = j + i < cand ? order_key(mass[j + i]) : 0u;
+                    if (tile - first < kHeldTiles)
+                        *reinterpret_cast<uint4*>(held + (tile - first) * kChunk + tid * kPer) = make_uint4(u[0], u[1], u[2], u[3]);
+                } else {
+                    keys(tile, u);
+                }
+#pragma unroll
+                for (int i = 0; i < kPer; ++i)
+                    if (j + i < cand && (pass == 0 || (u[i] >> (shift + 8)) == (prefix >> (shift + 8))))
+                        atomicAdd(&h[(u[i] >> shift) & 255u], 1u);
+            }
+            cluster_sync();
+            if (tid < 256) {
+                uint32_t x = 0;
+                for (int r = 0; r < blocks; ++r) x += cluster_load(h + tid, r);
+                // slots with a digit above this one, by a scan from the top
+                uint32_t y = x;
+                const int lane = tid & 31;
+#pragma unroll
+                for (int s = 1; s < 32; s <<= 1) {
+                    const uint32_t z = __shfl_down_sync(0xffffffffu, y, s);
+                    if (lane + s < 32) y += z;
+                }
+                if (lane == 0) warp_sums[tid >> 5] = y;
+                asm volatile("bar.sync 1, 256;\n" ::: "memory");
+                for (int w = (tid >> 5) + 1; w < 8; ++w) y += warp_sums[w];
+                if (y >= left && y - x < left) {
+                    found[0] = prefix | ((uint32_t)tid << shift);
+                    found[1] = left - (y - x);
+                }
             }
             __syncthreads();
-            if (threadIdx.x == 0) {
-                uint32_t above = 0;
-                int d = 255;
-                while (d > 0 && above + hist[d] < left) above += hist[d--];
-                sh_prefix = prefix | ((uint32_t)d << shift);
-                sh_left = left - above;
-            }
-            __syncthreads();
-            prefix = sh_prefix;
-            left = sh_left;
+            prefix = found[0];
+            left = found[1];
         }
-    }
-    // kept: keys above `prefix`, and the first `left` of those equal to it
-    uint32_t base = 0, ties = 0;
-    if (want >= cand) {
-        for (int j = threadIdx.x; j < cand; j += kThreads) out[j] = j;
+        // how many of this block are above the key and equal to it, and of the blocks before
+        uint32_t above = 0, equal = 0;
+        for (int tile = first; tile < last; ++tile) {
+            uint32_t u[kPer];
+            keys(tile, u);
+            const int j = tile * kChunk + tid * kPer;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                above += j + i < cand && u[i] > prefix;
+                equal += j + i < cand && u[i] == prefix;
+            }
+        }
+        uint32_t t_above, t_equal;
+        block_scan(above, warp_sums, t_above);
+        block_scan(equal, warp_sums, t_equal);
+        if (tid == 0) {
+            counts[0] = t_above;
+            counts[1] = t_equal;
+        }
+        cluster_sync();
+        uint32_t base = 0, ties = 0;
+        for (int r = 0; r < rank; ++r) {
+            base += cluster_load(&counts[0], r);
+            ties += cluster_load(&counts[1], r);
+        }
+        base += min(ties, left);                         // of the ties before, the first `left` are kept
+        for (int tile = first; tile < last; ++tile) {
+            uint32_t u[kPer];
+            keys(tile, u);
+            const int j = tile * kChunk + tid * kPer;
+            uint32_t eq = 0, tot;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) eq += j + i < cand && u[i] == prefix;
+            uint32_t rank_eq = ties + block_scan(eq, warp_sums, tot);
+            ties += tot;
+            uint32_t kept = 0;
+            bool k[kPer];
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const bool in = j + i < cand, e = in && u[i] == prefix;
+                k[i] = in && (u[i] > prefix || (e && rank_eq < left));
+                rank_eq += e;
+                kept += k[i];
+            }
+            uint32_t at = base + block_scan(kept, warp_sums, tot);
+            base += tot;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                if (k[i] && at < (uint32_t)want) out[at++] = j + i;
+        }
+        cluster_sync();                                  // no block leaves while another may read its shared memory
     } else if (want > 0) {
-        for (int j0 = 0; j0 < cand; j0 += kThreads) {
-            const int j = j0 + threadIdx.x;
-            const uint32_t u = j < cand ? order_key(mass[j]) : 0u;
-            const bool eq = j < cand && u == prefix;
-            uint32_t tile_ties, tile_kept;
-            const uint32_t rank = ties + block_scan(eq, warp_sums, tile_ties);
-            const bool kept = (j < cand && u > prefix) || (eq && rank < left);
-            const uint32_t at = base + block_scan(kept, warp_sums, tile_kept);
-            if (kept && at < (uint32_t)want) out[at] = j;
-            ties += tile_ties;
-            base += tile_kept;
-        }
+        for (int j = rank * kThreads + tid; j < cand; j += blocks * kThreads) out[j] = j;
     }
-    for (int i = threadIdx.x; i < recent; i += kThreads) out[want + i] = cand + i;
-    for (int i = m + threadIdx.x; i < a.keep; i += kThreads) out[i] = -1;
+    for (int i = rank * kThreads + tid; i < recent; i += blocks * kThreads) out[want + i] = cand + i;
+    for (int i = m + rank * kThreads + tid; i < a.keep; i += blocks * kThreads) out[i] = -1;
 }
 
-// One warp per kept row: its codes, scales and mass. Block (0, 0) writes the lengths.
-__global__ void __launch_bounds__(256) move_kernel(const Kv4EvictArgs a) {
-    const int chunks = (a.keep + 7) / 8, bh = blockIdx.x / chunks, chunk = blockIdx.x - bh * chunks;
-    const int b = bh / a.src.Hkv, h = bh % a.src.Hkv, lane = threadIdx.x & 31;
-    if (chunk == 0 && h == 0 && threadIdx.x == 0) {
-        const int n = min(max(a.lens[b], 0), (int)min((int64_t)a.src.cap, a.mass_ld));
-        a.lens_out[b] = min(n, a.keep);
+// The kept rows' codes, scales and masses; a thread per piece. CB, SB: bytes of a
+// piece of codes (16 or 4) and of scales (8 or 1).
+template <int CB, int SB>
+__global__ void __launch_bounds__(256) move_kernel(const Kv4EvictArgs a, const FastDiv by_pieces, const FastDiv by_keep) {
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");     // the slots
+    const int nc = a.src.cb / CB, ns = a.src.nb / SB;
+    const int64_t all = (int64_t)a.src.B * a.src.Hkv * a.keep * (int64_t)by_pieces.d;
+    for (int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x; x < all; x += (int64_t)gridDim.x * 256) {
+        const uint32_t r = all <= INT32_MAX ? by_pieces.div((uint32_t)x) : (uint32_t)(x / by_pieces.d);
+        int p = (int)(x - (int64_t)r * by_pieces.d);
+        const uint32_t bh = by_keep.div(r);
+        const int i = (int)(r - bh * by_keep.d);
+        const int b = bh / a.src.Hkv, h = bh - b * a.src.Hkv;
+        const int j = a.slots[r];
+        if (j < 0 || j >= a.src.cap) continue;
+        const int64_t from = (int64_t)b * a.src.sb + (int64_t)h * a.src.sh + j;
+        const int64_t to = (int64_t)b * a.dst.sb + (int64_t)h * a.dst.sh + i;
+        auto copy = [&](uint8_t* d, const uint8_t* s, int bytes) {
+            if (bytes == 16) *reinterpret_cast<uint4*>(d) = *reinterpret_cast<const uint4*>(s);
+            else if (bytes == 8) *reinterpret_cast<uint2*>(d) = *reinterpret_cast<const uint2*>(s);
+            else if (bytes == 4) *reinterpret_cast<uint32_t*>(d) = *reinterpret_cast<const uint32_t*>(s);
+            else *d = *s;
+        };
+        if (p < 2 * nc) {
+            const bool v = p >= nc;
+            p -= v ? nc : 0;
+            copy((v ? a.dst.vc : a.dst.kc) + to * a.dst.cb + p * CB, (v ? a.src.vc : a.src.kc) + from * a.src.cb + p * CB, CB);
+        } else if (p < 2 * (nc + ns)) {
+            p -= 2 * nc;
+            const bool v = p >= ns;
+            p -= v ? ns : 0;
+            copy((v ? a.dst.vs : a.dst.ks) + to * a.dst.nb + p * SB, (v ? a.src.vs : a.src.ks) + from * a.src.nb + p * SB, SB);
+        } else {
+            a.mass_out[(int64_t)bh * a.mass_out_ld + i] = a.mass[(int64_t)bh * a.mass_ld + j];
+        }
     }
-    const int i = chunk * 8 + (threadIdx.x >> 5);
-    if (i >= a.keep) return;
-    const int j = a.slots[(int64_t)bh * a.keep + i];
-    if (j < 0 || j >= a.src.cap) return;
-    const int64_t from = (int64_t)b * a.src.sb + (int64_t)h * a.src.sh + j;
-    const int64_t to = (int64_t)b * a.dst.sb + (int64_t)h * a.dst.sh + i;
-    for (int w = lane; w < a.src.cb / 4; w += 32) {
-        reinterpret_cast<uint32_t*>(a.dst.kc + to * a.dst.cb)[w] = reinterpret_cast<const uint32_t*>(a.src.kc + from * a.src.cb)[w];
-        reinterpret_cast<uint32_t*>(a.dst.vc + to * a.dst.cb)[w] = reinterpret_cast<const uint32_t*>(a.src.vc + from * a.src.cb)[w];
-    }
-    if (lane < a.src.nb) {
-        a.dst.ks[to * a.dst.nb + lane] = a.src.ks[from * a.src.nb + lane];
-        a.dst.vs[to * a.dst.nb + lane] = a.src.vs[from * a.src.nb + lane];
-    }
-    if (lane == 0 && a.mass_out) a.mass_out[(int64_t)bh * a.mass_out_ld + i] = a.mass[(int64_t)bh * a.mass_ld + j];
+    // lens_out may be lens: every block of the kernel before has read it by now, and this thread alone does here
+    if (blockIdx.x == 0)
+        for (int b = threadIdx.x; b < a.src.B; b += 256) {
+            const int n = min(max(a.lens[b], 0), (int)min((int64_t)a.src.cap, a.mass_ld));
+            a.lens_out[b] = min(n, a.keep);
+        }
+}
+
+template <int CB, int SB>
+cudaError_t launch_move(const Kv4EvictArgs& a, cudaStream_t s) {
+    const uint32_t pieces = 2 * (a.src.cb / CB + a.src.nb / SB) + (a.mass_out ? 1 : 0);
+    const int64_t all = (int64_t)a.src.B * a.src.Hkv * a.keep * pieces;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)std::min<int64_t>((all + 255) / 256, (int64_t)device_sm_count() * 32));
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cudaLaunchAttribute at = {};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return counted(cudaLaunchKernelEx(&cfg, move_kernel<CB, SB>, a, FastDiv::of(pieces), FastDiv::of((uint32_t)a.keep)));
 }
 
 }  // namespace
 
 cudaError_t launch_kv4_evict(const Kv4EvictArgs& a, cudaStream_t s) {
-    const int BH = a.src.B * a.src.Hkv;
-    choose_kernel<<<BH, kThreads, 0, s>>>(a);
-    cudaError_t e = counted(cudaGetLastError());
+    const int64_t BH = (int64_t)a.src.B * a.src.Hkv;
+    // blocks of a cluster: a power of two, no more than there are tiles in the cache
+    int blocks = 1;
+    while (blocks < kMaxCluster && (int64_t)blocks * kChunk < a.src.cap) blocks *= 2;
+    const int tiles = (a.src.cap + kChunk - 1) / kChunk;
+    const int smem = std::min((tiles + blocks - 1) / blocks, kHeldTiles) * kChunk * 4;
+    cudaError_t e = cudaFuncSetAttribute(choose_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    move_kernel<<<(unsigned)((int64_t)((a.keep + 7) / 8) * BH), 256, 0, s>>>(a);
-    return counted(cudaGetLastError());
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(BH * blocks));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at = {};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = blocks;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    e = counted(cudaLaunchKernelEx(&cfg, choose_kernel, a, (int32_t)blocks));
+    if (e != cudaSuccess) return e;
+    const bool wide = a.src.cb % 16 == 0, scales = a.src.nb % 8 == 0;
+    return wide ? (scales ? launch_move<16, 8>(a, s) : launch_move<16, 1>(a, s))
+                : (scales ? launch_move<4, 8>(a, s) : launch_move<4, 1>(a, s));
 }
 
 }  // namespace attn

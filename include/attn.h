@@ -395,7 +395,7 @@ int attn_kv4_attend(const void* q, const attn_shape* shape, const attn_kv4_cache
  *   mass_out[b][h][i] = mass[b][h][slots[b][h][i]]   (mass_out may be NULL)
  * Rows m and on of dst and mass_out are left as they were. mass: rows of mass_ld
  * fp32; mass_out: rows of mass_out_ld >= keep; slots: int32 [B][Hkv][keep]
- * contiguous. src and dst have the same B, Hkv, D and tensor scales, dst.cap >= keep >= 1,
+ * contiguous (fewer than 2^31). src and dst have the same B, Hkv, D and tensor scales, dst.cap >= keep >= 1,
  * 0 <= recent; src and dst, and mass and mass_out, must not overlap, and lens_out
  * may equal lens. Lengths out of range as in attn_kv4_attend. Errors as
  * attn_kv4_store. */

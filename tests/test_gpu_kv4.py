@@ -461,7 +461,7 @@ def test_evict(kind, keep, recent, D):
             assert (mo[b, h, m:] == -7).all()
 
 
-@pytest.mark.parametrize("cap,keep,recent", [(20000, 1000, 17), (20000, 19990, 0), (70000, 4096, 4096), (70000, 5000, 64)])
+@pytest.mark.parametrize("cap,keep,recent", [(20000, 1000, 17), (20000, 19990, 0), (70000, 4096, 4096), (70000, 5000, 64), (300000, 6000, 5)])
 def test_evict_long(cap, keep, recent):
     rng = np.random.default_rng(cap + keep)
     src = random_cache(1, 3, cap, 64, 22)
