@@ -19,11 +19,9 @@ namespace {
 
 using namespace kv4;
 
-constexpr int kThreads = 1024;
 constexpr int kPer = 4;                        // neighbouring masses of a thread and tile
-constexpr int kChunk = kThreads * kPer;
 constexpr int kMaxCluster = 8;
-constexpr int kHeldTiles = 8;                  // tiles of keys kept in shared memory (128 KB); the others are read again
+constexpr int kHeld = 32768;                   // keys that a block keeps in shared memory; the others it reads again
 
 // Orders as the masses do: NaN above everything, -0 as 0.
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -49,6 +47,7 @@ __device__ __forceinline__ uint32_t cluster_load(const uint32_t* p, uint32_t ran
 }
 
 // Exclusive prefix sum of x over the block, and the block's sum.
+template <int THREADS>
 __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* warp_sums, uint32_t& total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint32_t y = x;
@@ -59,7 +58,7 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* warp_sums, 
     }
     if (lane == 31) warp_sums[warp] = y;
     __syncthreads();
-    uint32_t w = warp_sums[lane];                        // kThreads / 32 == 32 warps
+    const uint32_t w = lane < THREADS / 32 ? warp_sums[lane] : 0u;
     uint32_t v = w;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
@@ -72,7 +71,9 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* warp_sums, 
     return before + y - x;
 }
 
-__global__ void __launch_bounds__(kThreads) choose_kernel(const Kv4EvictArgs a, const int32_t blocks) {
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) choose_kernel(const Kv4EvictArgs a, const int32_t blocks) {
+    constexpr int kChunk = THREADS * kPer, kHeldTiles = kHeld / kChunk;
     extern __shared__ __align__(16) uint32_t held[];     // keys of the first kHeldTiles tiles
     __shared__ uint32_t hist[2][256], warp_sums[32], found[2], counts[2];
     const int rank = (int)cluster_rank(), bh = blockIdx.x / blocks, b = bh / a.src.Hkv, tid = threadIdx.x;
@@ -121,8 +122,11 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const Kv4EvictArgs a, 
             }
             cluster_sync();
             if (tid < 256) {
-                uint32_t x = 0;
-                for (int r = 0; r < blocks; ++r) x += cluster_load(h + tid, r);
+                uint32_t x = 0, v[kMaxCluster];
+#pragma unroll
+                for (int r = 0; r < kMaxCluster; ++r) v[r] = r < blocks ? cluster_load(h + tid, r) : 0u;
+#pragma unroll
+                for (int r = 0; r < kMaxCluster; ++r) x += v[r];
                 // slots with a digit above this one, by a scan from the top
                 uint32_t y = x;
                 const int lane = tid & 31;
@@ -156,8 +160,8 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const Kv4EvictArgs a, 
             }
         }
         uint32_t t_above, t_equal;
-        block_scan(above, warp_sums, t_above);
-        block_scan(equal, warp_sums, t_equal);
+        block_scan<THREADS>(above, warp_sums, t_above);
+        block_scan<THREADS>(equal, warp_sums, t_equal);
         if (tid == 0) {
             counts[0] = t_above;
             counts[1] = t_equal;
@@ -176,7 +180,7 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const Kv4EvictArgs a, 
             uint32_t eq = 0, tot;
 #pragma unroll
             for (int i = 0; i < kPer; ++i) eq += j + i < cand && u[i] == prefix;
-            uint32_t rank_eq = ties + block_scan(eq, warp_sums, tot);
+            uint32_t rank_eq = ties + block_scan<THREADS>(eq, warp_sums, tot);
             ties += tot;
             uint32_t kept = 0;
             bool k[kPer];
@@ -187,7 +191,7 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const Kv4EvictArgs a, 
                 rank_eq += e;
                 kept += k[i];
             }
-            uint32_t at = base + block_scan(kept, warp_sums, tot);
+            uint32_t at = base + block_scan<THREADS>(kept, warp_sums, tot);
             base += tot;
 #pragma unroll
             for (int i = 0; i < kPer; ++i)
@@ -195,51 +199,84 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const Kv4EvictArgs a, 
         }
         cluster_sync();                                  // no block leaves while another may read its shared memory
     } else if (want > 0) {
-        for (int j = rank * kThreads + tid; j < cand; j += blocks * kThreads) out[j] = j;
+        for (int j = rank * THREADS + tid; j < cand; j += blocks * THREADS) out[j] = j;
     }
-    for (int i = rank * kThreads + tid; i < recent; i += blocks * kThreads) out[want + i] = cand + i;
-    for (int i = m + rank * kThreads + tid; i < a.keep; i += blocks * kThreads) out[i] = -1;
+    for (int i = rank * THREADS + tid; i < recent; i += blocks * THREADS) out[want + i] = cand + i;
+    for (int i = m + rank * THREADS + tid; i < a.keep; i += blocks * THREADS) out[i] = -1;
 }
 
-// The kept rows' codes, scales and masses; a thread per piece. CB, SB: bytes of a
-// piece of codes (16 or 4) and of scales (8 or 1).
+// The kept rows' codes, scales and masses. A thread takes one piece (CB bytes of codes,
+// SB of scales, or the mass) of kMoves rows at a time, so that the two reads that depend
+// on each other (slot, piece) are in flight for several rows.
+constexpr int kMoves = 4;
+constexpr int kMoveThreads = 256;
 template <int CB, int SB>
-__global__ void __launch_bounds__(256) move_kernel(const Kv4EvictArgs a, const FastDiv by_pieces, const FastDiv by_keep) {
+__global__ void __launch_bounds__(kMoveThreads)
+    move_kernel(const Kv4EvictArgs a, const int32_t pieces, const FastDiv by_keep, const FastDiv by_h) {
+    const int nc = a.src.cb / CB, ns = a.src.nb / SB, rows_per_block = kMoveThreads / pieces;
+    const int r0 = threadIdx.x / pieces;
+    int p = threadIdx.x - r0 * pieces;
+    const uint8_t* src;
+    uint8_t* dst;
+    int pitch, bytes;
+    int64_t fb = a.src.sb, fh = a.src.sh, tb = a.dst.sb, th = a.dst.sh;   // rows from and to, of a sequence and a head
+    if (p < 2 * nc) {
+        const bool v = p >= nc;
+        p -= v ? nc : 0;
+        src = (v ? a.src.vc : a.src.kc) + p * CB;
+        dst = (v ? a.dst.vc : a.dst.kc) + p * CB;
+        pitch = a.src.cb;
+        bytes = CB;
+    } else if (p < 2 * (nc + ns)) {
+        p -= 2 * nc;
+        const bool v = p >= ns;
+        p -= v ? ns : 0;
+        src = (v ? a.src.vs : a.src.ks) + p * SB;
+        dst = (v ? a.dst.vs : a.dst.ks) + p * SB;
+        pitch = a.src.nb;
+        bytes = SB;
+    } else {
+        src = reinterpret_cast<const uint8_t*>(a.mass);
+        dst = reinterpret_cast<uint8_t*>(a.mass_out);
+        pitch = bytes = 4;
+        fb = a.mass_ld * a.src.Hkv;
+        fh = a.mass_ld;
+        tb = a.mass_out_ld * a.src.Hkv;
+        th = a.mass_out_ld;
+    }
     asm volatile("griddepcontrol.wait;\n" ::: "memory");     // the slots
-    const int nc = a.src.cb / CB, ns = a.src.nb / SB;
-    const int64_t all = (int64_t)a.src.B * a.src.Hkv * a.keep * (int64_t)by_pieces.d;
-    for (int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x; x < all; x += (int64_t)gridDim.x * 256) {
-        const uint32_t r = all <= INT32_MAX ? by_pieces.div((uint32_t)x) : (uint32_t)(x / by_pieces.d);
-        int p = (int)(x - (int64_t)r * by_pieces.d);
-        const uint32_t bh = by_keep.div(r);
-        const int i = (int)(r - bh * by_keep.d);
-        const int b = bh / a.src.Hkv, h = bh - b * a.src.Hkv;
-        const int j = a.slots[r];
-        if (j < 0 || j >= a.src.cap) continue;
-        const int64_t from = (int64_t)b * a.src.sb + (int64_t)h * a.src.sh + j;
-        const int64_t to = (int64_t)b * a.dst.sb + (int64_t)h * a.dst.sh + i;
-        auto copy = [&](uint8_t* d, const uint8_t* s, int bytes) {
-            if (bytes == 16) *reinterpret_cast<uint4*>(d) = *reinterpret_cast<const uint4*>(s);
-            else if (bytes == 8) *reinterpret_cast<uint2*>(d) = *reinterpret_cast<const uint2*>(s);
-            else if (bytes == 4) *reinterpret_cast<uint32_t*>(d) = *reinterpret_cast<const uint32_t*>(s);
-            else *d = *s;
-        };
-        if (p < 2 * nc) {
-            const bool v = p >= nc;
-            p -= v ? nc : 0;
-            copy((v ? a.dst.vc : a.dst.kc) + to * a.dst.cb + p * CB, (v ? a.src.vc : a.src.kc) + from * a.src.cb + p * CB, CB);
-        } else if (p < 2 * (nc + ns)) {
-            p -= 2 * nc;
-            const bool v = p >= ns;
-            p -= v ? ns : 0;
-            copy((v ? a.dst.vs : a.dst.ks) + to * a.dst.nb + p * SB, (v ? a.src.vs : a.src.ks) + from * a.src.nb + p * SB, SB);
-        } else {
-            a.mass_out[(int64_t)bh * a.mass_out_ld + i] = a.mass[(int64_t)bh * a.mass_ld + j];
+    const int64_t rows = (int64_t)a.src.B * a.src.Hkv * a.keep, step = (int64_t)gridDim.x * rows_per_block;
+    for (int64_t base = (int64_t)blockIdx.x * rows_per_block + r0; r0 < rows_per_block && base < rows; base += step * kMoves) {
+        int32_t j[kMoves];
+#pragma unroll
+        for (int x = 0; x < kMoves; ++x) j[x] = base + x * step < rows ? a.slots[base + x * step] : -1;
+        int64_t to[kMoves];
+        uint4 v[kMoves];
+#pragma unroll
+        for (int x = 0; x < kMoves; ++x) {
+            if (j[x] < 0 || j[x] >= a.src.cap) continue;
+            const uint32_t r = (uint32_t)(base + x * step), bh = by_keep.div(r), b = by_h.div(bh);
+            const int32_t i = (int32_t)(r - bh * by_keep.d), h = (int32_t)(bh - b * by_h.d);
+            const uint8_t* f = src + (b * fb + h * fh + j[x]) * pitch;
+            to[x] = (b * tb + h * th + i) * pitch;
+            if (bytes == 16) v[x] = *reinterpret_cast<const uint4*>(f);
+            else if (bytes == 8) *reinterpret_cast<uint2*>(&v[x]) = *reinterpret_cast<const uint2*>(f);
+            else if (bytes == 4) v[x].x = *reinterpret_cast<const uint32_t*>(f);
+            else v[x].x = *f;
+        }
+#pragma unroll
+        for (int x = 0; x < kMoves; ++x) {
+            if (j[x] < 0 || j[x] >= a.src.cap) continue;
+            uint8_t* t = dst + to[x];
+            if (bytes == 16) *reinterpret_cast<uint4*>(t) = v[x];
+            else if (bytes == 8) *reinterpret_cast<uint2*>(t) = make_uint2(v[x].x, v[x].y);
+            else if (bytes == 4) *reinterpret_cast<uint32_t*>(t) = v[x].x;
+            else *t = (uint8_t)v[x].x;
         }
     }
-    // lens_out may be lens: every block of the kernel before has read it by now, and this thread alone does here
+    // lens_out may be lens: every block of the kernel before has read it by now, and this block alone does here
     if (blockIdx.x == 0)
-        for (int b = threadIdx.x; b < a.src.B; b += 256) {
+        for (int b = threadIdx.x; b < a.src.B; b += kMoveThreads) {
             const int n = min(max(a.lens[b], 0), (int)min((int64_t)a.src.cap, a.mass_ld));
             a.lens_out[b] = min(n, a.keep);
         }
@@ -247,34 +284,37 @@ __global__ void __launch_bounds__(256) move_kernel(const Kv4EvictArgs a, const F
 
 template <int CB, int SB>
 cudaError_t launch_move(const Kv4EvictArgs& a, cudaStream_t s) {
-    const uint32_t pieces = 2 * (a.src.cb / CB + a.src.nb / SB) + (a.mass_out ? 1 : 0);
-    const int64_t all = (int64_t)a.src.B * a.src.Hkv * a.keep * pieces;
+    const int pieces = 2 * (a.src.cb / CB + a.src.nb / SB) + (a.mass_out ? 1 : 0);
+    const int64_t rows = (int64_t)a.src.B * a.src.Hkv * a.keep, per = kMoveThreads / pieces;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)std::min<int64_t>((all + 255) / 256, (int64_t)device_sm_count() * 32));
-    cfg.blockDim = dim3(256);
+    cfg.gridDim = dim3((unsigned)std::min<int64_t>((rows + per - 1) / per, (int64_t)device_sm_count() * 8));
+    cfg.blockDim = dim3(kMoveThreads);
     cfg.stream = s;
     cudaLaunchAttribute at = {};
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return counted(cudaLaunchKernelEx(&cfg, move_kernel<CB, SB>, a, FastDiv::of(pieces), FastDiv::of((uint32_t)a.keep)));
+    return counted(cudaLaunchKernelEx(&cfg, move_kernel<CB, SB>, a, (int32_t)pieces, FastDiv::of((uint32_t)a.keep),
+                                      FastDiv::of((uint32_t)a.src.Hkv)));
 }
 
-}  // namespace
-
-cudaError_t launch_kv4_evict(const Kv4EvictArgs& a, cudaStream_t s) {
+template <int THREADS>
+cudaError_t launch_choose(const Kv4EvictArgs& a, cudaStream_t s) {
+    constexpr int kChunk = THREADS * kPer;
     const int64_t BH = (int64_t)a.src.B * a.src.Hkv;
     // blocks of a cluster: a power of two, no more than there are tiles in the cache
     int blocks = 1;
     while (blocks < kMaxCluster && (int64_t)blocks * kChunk < a.src.cap) blocks *= 2;
+    // enough blocks for every SM without them: one a head
+    if (BH >= 2 * device_sm_count()) blocks = 1;
     const int tiles = (a.src.cap + kChunk - 1) / kChunk;
-    const int smem = std::min((tiles + blocks - 1) / blocks, kHeldTiles) * kChunk * 4;
-    cudaError_t e = cudaFuncSetAttribute(choose_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const int smem = std::min((tiles + blocks - 1) / blocks * kChunk, kHeld) * 4;
+    cudaError_t e = cudaFuncSetAttribute(choose_kernel<THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(BH * blocks));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(THREADS);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute at = {};
@@ -283,7 +323,14 @@ cudaError_t launch_kv4_evict(const Kv4EvictArgs& a, cudaStream_t s) {
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    e = counted(cudaLaunchKernelEx(&cfg, choose_kernel, a, (int32_t)blocks));
+    return counted(cudaLaunchKernelEx(&cfg, choose_kernel<THREADS>, a, (int32_t)blocks));
+}
+
+}  // namespace
+
+cudaError_t launch_kv4_evict(const Kv4EvictArgs& a, cudaStream_t s) {
+    // many heads: smaller blocks, more of them on an SM at once
+    cudaError_t e = (int64_t)a.src.B * a.src.Hkv >= 2 * device_sm_count() ? launch_choose<512>(a, s) : launch_choose<1024>(a, s);
     if (e != cudaSuccess) return e;
     const bool wide = a.src.cb % 16 == 0, scales = a.src.nb % 8 == 0;
     return wide ? (scales ? launch_move<16, 8>(a, s) : launch_move<16, 1>(a, s))

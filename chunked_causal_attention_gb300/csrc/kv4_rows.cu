@@ -1,9 +1,9 @@
 // Rows of the 4-bit cache: quantise and store, load and dequantise.
 //
 // Both are bound by memory: a row of D dims is 2D bytes of bf16 on one side and
-// D/2 + D/16 on the other. Two adjacent lanes share a block of 16 dims; each
-// holds 8 (one 16-byte bf16 access, one 4-byte code access) and they exchange
-// the block's maximum with one shuffle.
+// D/2 + D/16 on the other. A thread takes a block of 16 dims (two 16-byte accesses
+// of bf16, one of 8 bytes of codes, one scale) of two rows at a time, so that its
+// loads are in flight together.
 //
 // Quantising: s = e4m3(max / (6 ts)) by one IEEE division a block, so a maximum
 // that lies between two scales rounds to even as its exact quotient does. The
@@ -16,6 +16,7 @@
 #include <algorithm>
 
 #include "kv4_device.cuh"
+#include "tc_common.cuh"
 
 namespace attn {
 namespace {
@@ -23,6 +24,7 @@ namespace {
 using namespace kv4;
 
 constexpr int kThreads = 256;
+constexpr int kAtOnce = 2;      // rows of a thread in flight
 
 // Row r of the call: which sequence and head, the offset of its bf16 row, its cache row. False: skipped.
 __device__ __forceinline__ bool locate(const Kv4RowsArgs& a, uint32_t r, int64_t& off, int64_t& row) {
@@ -54,75 +56,114 @@ __device__ __forceinline__ bool locate(const Kv4RowsArgs& a, uint32_t r, int64_t
     return true;
 }
 
-// blockIdx.y: 0 keys, 1 values. Thread = (row of the block's group, 8 dims); a
-// row takes 2 * nb threads, so the two of a block of 16 dims are adjacent lanes.
+// |x| of two bf16, the larger of each half: as bits they order like the values, infinities and NaN last.
+__device__ __forceinline__ uint32_t larger2(uint32_t top, uint32_t u) { return __vmaxu2(top, u & 0x7FFF7FFFu); }
+
+// Eight values (four words of bf16) to four bytes of codes, inv = 1 / d.
+__device__ __forceinline__ uint32_t codes8(const uint4& w, float inv) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    uint32_t c = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float lo = __uint_as_float(u[i] << 16), hi = __uint_as_float(u[i] & 0xFFFF0000u);
+        // |x| / d to a multiple of 2^-18, the sign of zero kept
+        const float2 y = tc::fadd2(tc::ffma2(make_float2(fabsf(lo), fabsf(hi)), make_float2(inv, inv), make_float2(48.f, 48.f)),
+                                   make_float2(-48.f, -48.f));
+        c |= e2m1x2(copysignf(y.x, lo), copysignf(y.y, hi)) << (8 * i);
+    }
+    return c;
+}
+
+// Four bytes of codes to eight values times d.
+__device__ __forceinline__ uint4 values8(uint32_t c, float d) {
+    const uint32_t f[4] = {codes_f16x2<0>(c), codes_f16x2<1>(c), codes_f16x2<2>(c), codes_f16x2<3>(c)};
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 y = __half22float2(as_half2(f[i]));
+        u[i] = pack_bf16(y.x * d, y.y * d);
+    }
+    return make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+// blockIdx.y: 0 keys, 1 values. A thread is (row of the block's group, block of 16 dims).
 template <bool STORE>
 __global__ void __launch_bounds__(kThreads) kv4_rows_kernel(const Kv4RowsArgs a, int32_t rows_per_block) {
-    const int per = 2 * a.c.nb;
+    const int per = a.c.nb;
     const int r0 = threadIdx.x / per, part = threadIdx.x - r0 * per;
-    const bool on = r0 < rows_per_block && part * 8 < a.c.D;     // lanes past D help their neighbour's shuffle only
+    if (r0 >= rows_per_block) return;
+    const bool second = part * 16 + 8 < a.c.D;           // D need not be a multiple of 16
     const bool val = blockIdx.y != 0;
     uint8_t* codes = val ? a.c.vc : a.c.kc;
     uint8_t* scales = val ? a.c.vs : a.c.ks;
     const float ts = val ? a.c.v_scale : a.c.k_scale;
-    __nv_bfloat16* x = reinterpret_cast<__nv_bfloat16*>(val ? a.v : a.k);
-    const int64_t step = (int64_t)gridDim.x * rows_per_block;
-    for (int64_t base = (int64_t)blockIdx.x * rows_per_block; base < a.rows; base += step) {
-        const int64_t r = base + r0;
-        int64_t off = 0, row = 0;
-        bool live = on && r < a.rows;
-        if (live && !locate(a, (uint32_t)r, off, row)) {
-            live = false;
-            set_error(a.status, ATTN_E_BOUNDS);
+    __nv_bfloat16* x = reinterpret_cast<__nv_bfloat16*>(val ? a.v : a.k) + part * 16;
+    const int64_t step = (int64_t)gridDim.x * rows_per_block * kAtOnce;
+    for (int64_t base = (int64_t)blockIdx.x * rows_per_block * kAtOnce; base < a.rows; base += step) {
+        int64_t off[kAtOnce], row[kAtOnce];
+        bool live[kAtOnce];
+        uint4 w[kAtOnce][2];
+        uint2 c[kAtOnce];
+        uint32_t s8[kAtOnce];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            const int64_t r = base + i * rows_per_block + r0;
+            live[i] = r < a.rows;
+            off[i] = row[i] = 0;
+            if (live[i] && !locate(a, (uint32_t)r, off[i], row[i])) {
+                live[i] = false;
+                set_error(a.status, ATTN_E_BOUNDS);
+            }
+            w[i][0] = w[i][1] = make_uint4(0, 0, 0, 0);
+            c[i] = make_uint2(0, 0);
+            s8[i] = 0;
+            if (live[i]) {
+                if constexpr (STORE) {
+                    w[i][0] = *reinterpret_cast<const uint4*>(x + off[i]);
+                    if (second) w[i][1] = *reinterpret_cast<const uint4*>(x + off[i] + 8);
+                } else {
+                    const uint8_t* p = codes + row[i] * a.c.cb + part * 8;
+                    c[i].x = *reinterpret_cast<const uint32_t*>(p);       // rows start at multiples of 4 bytes
+                    if (second) c[i].y = *reinterpret_cast<const uint32_t*>(p + 4);
+                    s8[i] = scales[row[i] * a.c.nb + part];
+                }
+            }
         }
-        if constexpr (STORE) {
-            uint4 w = make_uint4(0, 0, 0, 0);
-            if (live) w = *reinterpret_cast<const uint4*>(x + off + part * 8);
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-            // |x| as bf16 bits orders like the values, infinities and NaN last
-            uint32_t top = 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) top = max(top, max(u[i] & 0x7FFFu, (u[i] >> 16) & 0x7FFFu));
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            const float amax = __uint_as_float(top << 16);
-            const uint32_t s8 = top >= 0x7F80u ? 0x7Fu : e4m3(__fdiv_rn(amax, 6.f * ts));
-            const float s = __half2float(__low2half(as_half2(scales_f16x2(s8))));
-            const float d = s * ts;
-            const float inv = s > 0.f ? __frcp_rn(d) : 0.f;     // 0 and NaN scales: codes 0
-            uint32_t c = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float lo = __uint_as_float(u[i] << 16), hi = __uint_as_float(u[i] & 0xFFFF0000u);
-                // to a multiple of 2^-18, the sign of zero kept
-                const float y0 = copysignf((fabsf(lo) * inv + 48.f) - 48.f, lo);
-                const float y1 = copysignf((fabsf(hi) * inv + 48.f) - 48.f, hi);
-                c |= e2m1x2(y0, y1) << (8 * i);
+        for (int i = 0; i < kAtOnce; ++i) {
+            if (!live[i]) continue;
+            if constexpr (STORE) {
+                const uint4 p = w[i][0], q = w[i][1];
+                uint32_t top = larger2(larger2(larger2(larger2(0u, p.x), p.y), p.z), p.w);
+                top = larger2(larger2(larger2(larger2(top, q.x), q.y), q.z), q.w);
+                top = max(top & 0xFFFFu, top >> 16);
+                const uint32_t s = top >= 0x7F80u ? 0x7Fu : e4m3(__fdiv_rn(__uint_as_float(top << 16), 6.f * ts));
+                const float f = __half2float(__low2half(as_half2(scales_f16x2(s))));
+                // 0 and NaN scales: codes 0
+                const float inv = f > 0.f ? __frcp_rn(f * ts) : 0.f;
+                uint32_t c0 = codes8(p, inv), c1 = codes8(q, inv);
+                if (s == 0x7Fu) c0 = c1 = 0;
+                uint8_t* d = codes + row[i] * a.c.cb + part * 8;
+                if (second && (a.c.cb & 7) == 0) {
+                    *reinterpret_cast<uint2*>(d) = make_uint2(c0, c1);
+                } else {
+                    *reinterpret_cast<uint32_t*>(d) = c0;
+                    if (second) *reinterpret_cast<uint32_t*>(d + 4) = c1;
+                }
+                scales[row[i] * a.c.nb + part] = (uint8_t)s;
+            } else {
+                const float d = __half2float(__low2half(as_half2(scales_f16x2(s8[i])))) * ts;
+                *reinterpret_cast<uint4*>(x + off[i]) = values8(c[i].x, d);
+                if (second) *reinterpret_cast<uint4*>(x + off[i] + 8) = values8(c[i].y, d);
             }
-            if (s8 == 0x7Fu) c = 0;
-            if (live) {
-                *reinterpret_cast<uint32_t*>(codes + row * a.c.cb + part * 4) = c;
-                if (!(part & 1)) scales[row * a.c.nb + (part >> 1)] = (uint8_t)s8;
-            }
-        } else if (live) {
-            const uint32_t c = *reinterpret_cast<const uint32_t*>(codes + row * a.c.cb + part * 4);
-            const uint32_t s8 = scales[row * a.c.nb + (part >> 1)];
-            const float d = __half2float(__low2half(as_half2(scales_f16x2(s8)))) * ts;
-            const uint32_t f[4] = {codes_f16x2<0>(c), codes_f16x2<1>(c), codes_f16x2<2>(c), codes_f16x2<3>(c)};
-            uint32_t u[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 y = __half22float2(as_half2(f[i]));
-                u[i] = pack_bf16(y.x * d, y.y * d);
-            }
-            *reinterpret_cast<uint4*>(x + off + part * 8) = make_uint4(u[0], u[1], u[2], u[3]);
         }
     }
 }
 
 template <bool STORE>
 cudaError_t launch(const Kv4RowsArgs& a, cudaStream_t s) {
-    const int rows_per_block = kThreads / (2 * a.c.nb);
-    const int64_t blocks = (a.rows + rows_per_block - 1) / rows_per_block;
+    const int rows_per_block = kThreads / a.c.nb;
+    const int64_t blocks = (a.rows + rows_per_block * kAtOnce - 1) / (rows_per_block * kAtOnce);
     const dim3 grid((unsigned)std::min<int64_t>(blocks, (int64_t)device_sm_count() * 16), 2);
     kv4_rows_kernel<STORE><<<grid, kThreads, 0, s>>>(a, rows_per_block);
     return counted(cudaGetLastError());
