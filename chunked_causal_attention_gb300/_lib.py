@@ -410,7 +410,8 @@ def _stream_of(stream, t) -> Optional[int]:
     """The given stream, or the current one of t's device."""
     if stream is None:
         import torch
-        return torch.cuda.current_stream(t.device).cuda_stream
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)     # without the Stream object around it
+        return torch.cuda.current_stream(t.device).cuda_stream if raw is None else raw(t.device.index)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -437,6 +438,11 @@ def attn_kv4_workspace_size(cache: attn_kv4_cache, shape: Optional[attn_shape], 
     _check("attn_kv4_workspace_size", lib().attn_kv4_workspace_size(
         ctypes.byref(cache), None if shape is None else ctypes.byref(shape), op, ctypes.byref(out)))
     return out.value
+
+
+def _same_rows(a, b) -> bool:
+    """Tensors of equal sizes whose strides agree where a size is above 1."""
+    return all(n == 1 or x == y for n, x, y in zip(a.shape, a.stride(), b.stride()))
 
 
 def _kv4_rows_args(fn: str, k, v, shape, cache, pos, cu_seqlens, ws) -> None:

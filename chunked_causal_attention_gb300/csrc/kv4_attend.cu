@@ -885,8 +885,11 @@ cudaError_t launch_after(K kernel, int64_t grid, int threads, cudaStream_t s, co
 template <int DT, int NT, bool EXACT, bool MASS>
 cudaError_t launch_split(const Kv4AttendArgs& a, const Plan& p, cudaStream_t s) {
     constexpr int bytes = Layout<DT, NT>::BYTES;
-    cudaError_t e = cudaFuncSetAttribute(split_kernel<DT, NT, EXACT, MASS>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess) return e;
+    if (bytes > 48 * 1024) {                     // what a block may have without asking
+        const cudaError_t e =
+            cudaFuncSetAttribute(split_kernel<DT, NT, EXACT, MASS>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != cudaSuccess) return e;
+    }
     split_kernel<DT, NT, EXACT, MASS><<<p.grid, kThreads, bytes, s>>>(a, p.sp);
     return counted(cudaGetLastError());
 }

@@ -310,8 +310,10 @@ cudaError_t launch_choose(const Kv4EvictArgs& a, cudaStream_t s) {
     if (BH >= 2 * device_sm_count()) blocks = 1;
     const int tiles = (a.src.cap + kChunk - 1) / kChunk;
     const int smem = std::min((tiles + blocks - 1) / blocks * kChunk, kHeld) * 4;
-    cudaError_t e = cudaFuncSetAttribute(choose_kernel<THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
+    if (smem > 40 * 1024) {                      // 48 KB with the static part is what a block may have without asking
+        const cudaError_t e = cudaFuncSetAttribute(choose_kernel<THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(BH * blocks));
     cfg.blockDim = dim3(THREADS);

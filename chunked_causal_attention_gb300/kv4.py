@@ -13,6 +13,7 @@ graph and replayed. Torch provides memory and streams only.
 """
 from __future__ import annotations
 
+import ctypes
 from typing import Optional
 
 from . import _lib
@@ -52,9 +53,32 @@ class KV4Cache:
         self.desc = _lib.attn_kv4_cache(B, Hkv, cap, D, sb, sh, *(t.data_ptr() for t in arrays), self.k_scale,
                                         self.v_scale)
         _lib.attn_kv4_workspace_size(self.desc, None, _lib.KV4_ROWS)      # the library's own checks
+        self._ref = ctypes.byref(self.desc)
+        self._shapes = {}
 
-    def _for(self, fn: str, t) -> None:
-        if t.device != self.device:
+    def _shape(self, x, scale: Optional[float], packed: bool):
+        """The attn_shape of a tensor and a reference to it, kept by sizes, strides and scale: a
+        decode loop asks for the same one at every step."""
+        key = (x.shape, x.stride(), scale, packed)
+        got = self._shapes.get(key)
+        if got is None:
+            if x.dim() != (3 if packed else 4) or x.shape[-1] != self.D or x.stride(-1) != 1:
+                raise AttnError("attn_shape", ATTN_E_INVAL)
+            shape = _lib.shape_of(x, scale, packed)
+            if len(self._shapes) >= 64:
+                self._shapes.clear()
+            got = self._shapes[key] = (shape, ctypes.byref(shape))
+        return got
+
+    def _check(self, fn: str, ints, numel: int, *others) -> None:
+        """An int32 tensor of numel elements, and others, on the cache's device (a GPU)."""
+        import torch
+        dev = self.device
+        ok = (dev.type == "cuda" and ints.dtype is torch.int32 and ints.device == dev and ints.numel() == numel
+              and ints.is_contiguous())
+        for t in others:
+            ok = ok and (t is None or t.device == dev)
+        if not ok:
             raise AttnError(fn, ATTN_E_INVAL)
 
 
@@ -80,24 +104,45 @@ def kv4_workspace(cache: KV4Cache, q=None, mass: bool = False):
 def kv4_store(cache: KV4Cache, k, v, pos, cu_seqlens=None, ws=None, stream=None) -> None:
     """Store rows: k, v bf16 [B, Hkv, T, D], row t of sequence b in slot pos[b] + t;
     with cu_seqlens (int32 [B + 1]) packed [T, Hkv, D], each sequence's tokens from pos[b] on."""
-    cache._for("kv4_store", k)
     if ws is None:
         ws = kv4_workspace(cache)
-    _lib.attn_kv4_store(k, v, _lib.shape_of(k, 1.0, cu_seqlens is not None), cache.desc, pos, cu_seqlens, ws, stream)
+    _, ref = cache._shape(k, 1.0, cu_seqlens is not None)
+    _rows_checks("kv4_store", cache, k, v, pos, cu_seqlens, ws)
+    with _lib._on(k):
+        _lib._check("attn_kv4_store", _lib.lib().attn_kv4_store(
+            k.data_ptr(), v.data_ptr(), ref, cache._ref, pos.data_ptr(), _lib._ptr(cu_seqlens), ws.data_ptr(),
+            ws.numel() * ws.element_size(), _lib._stream_of(stream, k)))
+
+
+def _rows_checks(fn: str, cache: KV4Cache, k, v, pos, cu_seqlens, ws) -> None:
+    import torch
+    cache._check(fn, pos, cache.B, k, v, ws)
+    if cu_seqlens is not None:
+        cache._check(fn, cu_seqlens, cache.B + 1)
+    if not (k.dtype is torch.bfloat16 and v.dtype is torch.bfloat16 and k.shape == v.shape
+            and (k.stride() == v.stride() or _lib._same_rows(k, v))):
+        raise AttnError(fn, ATTN_E_INVAL)
 
 
 def kv4_load(cache: KV4Cache, pos, T: int, cu_seqlens=None, k=None, v=None, ws=None, stream=None):
     """The values of T rows from slot pos[b] on, bf16 [B, Hkv, T, D]; with cu_seqlens
     packed [T, Hkv, D]. k and v may be given (rows outside the cache stay as they were)."""
     import torch
-    if k is None or v is None:
-        shape = (T, cache.Hkv, cache.D) if cu_seqlens is not None else (cache.B, cache.Hkv, T, cache.D)
-        k = torch.empty(shape, dtype=torch.bfloat16, device=cache.device) if k is None else k
-        v = torch.empty(shape, dtype=torch.bfloat16, device=cache.device) if v is None else v
-    cache._for("kv4_load", k)
+    shape = (T, cache.Hkv, cache.D) if cu_seqlens is not None else (cache.B, cache.Hkv, T, cache.D)
+    if k is None:
+        k = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
+    if v is None:
+        v = torch.empty_like(k)
     if ws is None:
         ws = kv4_workspace(cache)
-    _lib.attn_kv4_load(cache.desc, pos, cu_seqlens, _lib.shape_of(k, 1.0, cu_seqlens is not None), k, v, ws, stream)
+    _, ref = cache._shape(k, 1.0, cu_seqlens is not None)
+    _rows_checks("kv4_load", cache, k, v, pos, cu_seqlens, ws)
+    if k.shape != shape:
+        raise AttnError("kv4_load", ATTN_E_INVAL)
+    with _lib._on(k):
+        _lib._check("attn_kv4_load", _lib.lib().attn_kv4_load(
+            cache._ref, pos.data_ptr(), _lib._ptr(cu_seqlens), ref, k.data_ptr(), v.data_ptr(), ws.data_ptr(),
+            ws.numel() * ws.element_size(), _lib._stream_of(stream, k)))
     return k, v
 
 
@@ -107,13 +152,22 @@ def kv4_attention(q, cache: KV4Cache, lens, scale: Optional[float] = None, mass_
     lens[b] slots in use (their own included). mass_out fp32 [B, Hkv, n]: each slot's
     weight over the call's rows is added to mass_in (None: zeros; may be mass_out)."""
     import torch
-    cache._for("kv4_attention", q)
-    shape = _lib.shape_of(q, scale)
-    o = torch.empty_strided(q.shape, q.stride(), dtype=q.dtype, device=q.device)
-    lse = torch.empty((shape.B, shape.H, shape.T), dtype=torch.float32, device=q.device)
+    shape, ref = cache._shape(q, scale, False)
     if ws is None:
         ws = kv4_workspace(cache, q, mass_out is not None)
-    _lib.attn_kv4_attend(q, shape, cache.desc, lens, o, lse, mass_in, mass_out, ws, stream)
+    cache._check("kv4_attention", lens, cache.B, q, ws, mass_in, mass_out)
+    if q.dtype is not torch.bfloat16:
+        raise AttnError("kv4_attention", ATTN_E_INVAL)
+    ld = 0
+    if mass_in is not None or mass_out is not None:
+        ld = _lib._mass_ld("kv4_attention", cache.desc, mass_in, mass_out)
+    o = torch.empty_like(q) if q.is_contiguous() else \
+        torch.empty_strided(q.shape, q.stride(), dtype=q.dtype, device=q.device)
+    lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+    with _lib._on(q):
+        _lib._check("attn_kv4_attend", _lib.lib().attn_kv4_attend(
+            q.data_ptr(), ref, cache._ref, lens.data_ptr(), o.data_ptr(), lse.data_ptr(), _lib._ptr(mass_in),
+            _lib._ptr(mass_out), ld, ws.data_ptr(), ws.numel() * ws.element_size(), _lib._stream_of(stream, q)))
     return o, lse
 
 
@@ -123,8 +177,8 @@ def kv4_evict(cache: KV4Cache, lens, mass, keep: int, recent: int, out: KV4Cache
     and those with the highest mass, moved to the front of `out` in their order.
     Returns (lens_out, slots): int32 [B] and the source slots int32 [B, Hkv, keep]."""
     import torch
-    cache._for("kv4_evict", lens)
-    out._for("kv4_evict", lens)
+    if out.device != cache.device or lens.device != cache.device:
+        raise AttnError("kv4_evict", ATTN_E_INVAL)
     slots = torch.empty((cache.B, cache.Hkv, max(int(keep), 0)), dtype=torch.int32, device=lens.device)
     if lens_out is None:
         lens_out = torch.empty_like(lens)
