@@ -838,7 +838,15 @@ __global__ void __launch_bounds__(256) mass_kernel(const Kv4AttendArgs a, const 
     a.mass_out[at] = (a.mass_in ? a.mass_in[at] : 0.f) + w;
 }
 
-int row_tiles(int D, int64_t R) { return R <= 8 ? 1 : (R <= 16 || D > 128) ? 2 : 4; }
+// Groups of 8 rows that share a pass over the slots. Four of them save conversions, but
+// leave two blocks of 255 registers on an SM: at D = 128 and 32 rows 224 against 248 us
+// for 4 sequences of 64K slots and 8 heads, 44 against 29 us for 2K slots, and two groups
+// were no faster than one at any size. So four only for at least 32 rows and long caches;
+// above 128 dims two (252 registers already with one).
+int row_groups(int D, int64_t R, int64_t slots) {
+    if (D > 128) return R <= 8 ? 1 : 2;
+    return R >= 32 && slots >= (int64_t)1 << 20 ? 4 : 1;
+}
 
 int dims_of(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
 
@@ -851,7 +859,7 @@ struct Plan {
 Plan plan_of(const Kv4Geom& c, const Geom& g, bool mass) {
     Plan p;
     const int64_t R = (int64_t)(g.H / c.Hkv) * g.T;
-    p.nt = row_tiles(c.D, R);
+    p.nt = row_groups(c.D, R, (int64_t)c.B * c.Hkv * c.cap);
     p.sp.R = (int32_t)R;
     p.sp.RT = (int32_t)((R + 8 * p.nt - 1) / (8 * p.nt));
     p.sp.pitch = R <= 2 ? 2 : R <= 4 ? 4 : 8 * p.nt;
@@ -915,12 +923,9 @@ cudaError_t launch_kv4_attend(const Kv4AttendArgs& args, cudaStream_t s) {
     p.sp.scores = a.mass_out ? a.parts + p.parts + p.lse2 : nullptr;
     wait_settings(&p.sp.wait_ns, &p.sp.stall);
     cudaError_t e;
-    if (a.c.D <= 64)
-        e = p.nt == 1 ? launch_dims<64, 1>(a, p, s) : p.nt == 2 ? launch_dims<64, 2>(a, p, s) : launch_dims<64, 4>(a, p, s);
-    else if (a.c.D <= 128)
-        e = p.nt == 1 ? launch_dims<128, 1>(a, p, s) : p.nt == 2 ? launch_dims<128, 2>(a, p, s) : launch_dims<128, 4>(a, p, s);
-    else
-        e = p.nt == 1 ? launch_dims<256, 1>(a, p, s) : launch_dims<256, 2>(a, p, s);
+    if (a.c.D <= 64) e = p.nt == 1 ? launch_dims<64, 1>(a, p, s) : launch_dims<64, 4>(a, p, s);
+    else if (a.c.D <= 128) e = p.nt == 1 ? launch_dims<128, 1>(a, p, s) : launch_dims<128, 4>(a, p, s);
+    else e = p.nt == 1 ? launch_dims<256, 1>(a, p, s) : launch_dims<256, 2>(a, p, s);
     if (e != cudaSuccess) return e;
     const int unit_rows = 8 * p.nt;
     const int64_t rows = (int64_t)a.c.B * a.c.Hkv * p.sp.RT * unit_rows;
