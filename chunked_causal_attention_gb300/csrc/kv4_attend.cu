@@ -15,8 +15,9 @@
 // them in block order, so results do not depend on timing.
 //
 // Warps. Each of a block's four warps takes 16 or 32 slots of every tile, with its own
-// ring of bulk copies, running maximum and accumulators, and meets the others only
-// at a unit's end.
+// running maximum and accumulators, and meets the others only at a unit's end. A tile
+// is four bulk copies into a stage of shared memory; the last warp to have read a
+// stage has it filled again.
 //
 // Products. With few rows the matrix product's M side is the cache's: S^T = K Q^T
 // (16 slots x 8 rows) and O^T = V^T P^T (16 dims x 8 rows), mma m16n8k16 in fp16.
@@ -34,6 +35,7 @@
 // of the row's largest are flushed (1M of them would be 2^-15 of the sum). l is
 // summed in fp32, one partial sum a lane.
 #include <algorithm>
+#include <type_traits>
 
 #include "kv4_device.cuh"
 #include "tc_common.cuh"
@@ -71,9 +73,9 @@ template <int DT, int NT>
 struct Layout {
     static constexpr int KS = fragments(DT, NT), SLOTS = kSlots * KS, TILE = tile_slots(DT, NT);
     static constexpr int STAGES = KS == 2 ? 2 : DT == 256 ? 3 : 4;
-    static constexpr int CODES = SLOTS * DT / 2, SCALES = SLOTS * DT / 16;
+    static constexpr int CODES = TILE * DT / 2, SCALES = TILE * DT / 16;   // of K; then V's
     static constexpr int STAGE = 2 * (CODES + SCALES);
-    static constexpr int RING = kWarps * STAGES * STAGE;
+    static constexpr int RING = STAGES * STAGE;
     static constexpr int ROWS = 8 * NT;
     static constexpr int O_PITCH = DT + 8;
     static constexpr int O_OFF = RING;
@@ -82,7 +84,8 @@ struct Layout {
     static constexpr int QS_OFF = Q_OFF + Q_BYTES;                  // score factor of each row
     static constexpr int ML_OFF = QS_OFF + ROWS * 4;               // m then l of each warp and row
     static constexpr int BAR_OFF = ML_OFF + 2 * kWarps * ROWS * 4;
-    static constexpr int MISC_OFF = BAR_OFF + kWarps * STAGES * 8;
+    static constexpr int DONE_OFF = BAR_OFF + STAGES * 8;    // of each stage: warps that have read it, times it was filled
+    static constexpr int MISC_OFF = DONE_OFF + STAGES * 8;
     static constexpr int BYTES = MISC_OFF + 64;
 };
 
@@ -202,14 +205,19 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(DT, NT)) split_kernel(
     float* sL = sM + kWarps * L::ROWS;
     volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::MISC_OFF);
     int64_t* scratch = reinterpret_cast<int64_t*>(sm + L::O_OFF);
-    const uint32_t ring = smem_u32(sm) + warp * L::STAGES * L::STAGE;
-    const uint8_t* ring_p = sm + warp * L::STAGES * L::STAGE;
-    const uint32_t bar = smem_u32(sm) + L::BAR_OFF + warp * L::STAGES * 8;
+    const uint32_t ring = smem_u32(sm), bar = ring + L::BAR_OFF;
+    uint32_t* done = reinterpret_cast<uint32_t*>(sm + L::DONE_OFF);
+    volatile uint32_t* filled = done + L::STAGES;
 
-    if (lane == 0)
-        for (int s = 0; s < L::STAGES; ++s) tc::mbar_init(bar + 8 * s, 1);
-    if (tid == 0) *abort_flag = 0;
-    tc::fence_barrier_init();
+    if (tid == 0) {
+        for (int s = 0; s < L::STAGES; ++s) {
+            tc::mbar_init(bar + 8 * s, 1);
+            done[s] = 0;
+            filled[s] = 0;
+        }
+        *abort_flag = 0;
+        tc::fence_barrier_init();
+    }
 
     grid_go();
 
@@ -236,38 +244,35 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(DT, NT)) split_kernel(
         cur.t = (int32_t)(left - (int64_t)cur.v * cur.nt);
     }
 
-    // ---- bulk copies of this warp's slices, in list order
+    // ---- bulk copies of the tiles, in list order. Every warp follows the cursor; a stage is
+    // filled again by the warp that is the last to have read it
     Cursor ahead = cur;
     int64_t ahead_row = 0;                              // cache row of slot 0 of the unit ahead
     auto unit_row = [&]() { ahead_row = (int64_t)ahead.b * a.c.sb + (int64_t)(ahead.v / sp.RT) * a.c.sh; };
     unit_row();
-    int32_t to_fetch = n_tiles;
-    uint32_t fetched = 0, fetch_stage = 0, used = 0, use_stage = 0, use_parity = 0;
-    bool ok = true;
-    auto fetch = [&]() {
-        if (to_fetch <= 0) return;
-        --to_fetch;
-        const int32_t k0 = ahead.t * L::TILE + warp * L::SLOTS;
-        if (k0 < ahead.n && ok) {
-            if (lane == 0 && !sp.stall) {
-                const int64_t row = ahead_row + k0;
-                const uint32_t dst = ring + fetch_stage * L::STAGE, f = bar + 8 * fetch_stage;
-                // whole slices, but no further than the 16 slots that hold the last one (the capacity is a multiple of 16)
-                const uint32_t slots = KS == 1 ? kSlots : min(L::SLOTS, (ahead.n - k0 + kSlots - 1) & ~(kSlots - 1));
-                const uint32_t nc = slots * cb, ns = slots * nb;
-                tc::mbar_expect_tx(f, 2 * (nc + ns));
-                bulk_load(dst, a.c.kc + row * cb, nc, f);
-                bulk_load(dst + 2 * L::CODES, a.c.ks + row * nb, ns, f);
-                bulk_load(dst + L::CODES, a.c.vc + row * cb, nc, f);
-                bulk_load(dst + 2 * L::CODES + L::SCALES, a.c.vs + row * nb, ns, f);
-            }
-            ++fetched;
-            fetch_stage = fetch_stage + 1 == L::STAGES ? 0 : fetch_stage + 1;
-        }
-        if (to_fetch > 0 && ahead.next<L::TILE>(a, units)) unit_row();
+    auto issue = [&](uint32_t s) {                      // one thread
+        const int32_t k0 = ahead.t * L::TILE;
+        const int64_t row = ahead_row + k0;
+        const uint32_t dst = ring + s * L::STAGE, f = bar + 8 * s;
+        // no further than the 16 slots that hold the last one (the capacity is a multiple of 16)
+        const uint32_t slots = min(L::TILE, (ahead.n - k0 + kSlots - 1) & ~(kSlots - 1));
+        const uint32_t nc = slots * cb, ns = slots * nb;
+        filled[s] = filled[s] + 1;
+        tc::mbar_expect_tx(f, 2 * (nc + ns));
+        bulk_load(dst, a.c.kc + row * cb, nc, f);
+        bulk_load(dst + 2 * L::CODES, a.c.ks + row * nb, ns, f);
+        bulk_load(dst + L::CODES, a.c.vc + row * cb, nc, f);
+        bulk_load(dst + 2 * L::CODES + L::SCALES, a.c.vs + row * nb, ns, f);
     };
+    bool ok = true;
+    int32_t to_fetch = n_tiles;
 #pragma unroll
-    for (int s = 0; s < L::STAGES; ++s) fetch();
+    for (int s = 0; s < L::STAGES; ++s)
+        if (to_fetch > 0) {
+            if (tid == 0 && !sp.stall) issue(s);
+            if (--to_fetch > 0 && ahead.next<L::TILE>(a, units)) unit_row();
+        }
+    uint32_t stage = 0, parity = 0;
 
     // slot of a 16-row fragment row: neighbours in a different half of a bank line for K's and V's reads
     const int slot_lo = g ^ ((g >> 1) & 1);
@@ -357,24 +362,21 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(DT, NT)) split_kernel(
                     for (int j = 0; j < 4; ++j) o[n][i][j] = 0.f;
         }
 
+        // every warp waits for every tile, also one it has no slots of: a parity tells neighbouring phases apart only
+        if (ok) ok = tc::mbar_wait_warp(bar + 8 * stage, parity, abort_flag, a.status, sp.wait_ns);
         const int32_t k0 = cur.t * L::TILE + warp * L::SLOTS;
-        if (k0 < cur.n) {
-            if (ok) ok = tc::mbar_wait_warp(bar + 8 * use_stage, use_parity, abort_flag, a.status, sp.wait_ns);
-            if (ok) {
-                const uint8_t* stage = ring_p + use_stage * L::STAGE;
-                const bool masked = k0 + L::SLOTS > lim_min;
-                ++used;
-                if (++use_stage == L::STAGES) {
-                    use_stage = 0;
-                    use_parity ^= 1;
-                }
-
+        if (k0 < cur.n && ok) {
+            const uint8_t* slice = sm + stage * L::STAGE + warp * L::SLOTS * cb;                 // codes
+            const uint8_t* slice_s = sm + stage * L::STAGE + 2 * L::CODES + warp * L::SLOTS * nb;  // scales
+            // the slots that some row does not see are few: a copy of the code of their own
+            auto work = [&](auto masked_) {
+                constexpr bool masked = decltype(masked_)::value;
                 // ---- S^T = K Q^T
                 float s[KS][NT][4];
 #pragma unroll
                 for (int x = 0; x < KS; ++x) {
-                    const uint8_t* kc = stage + x * kSlots * cb;
-                    const uint8_t* ks = stage + 2 * L::CODES + x * kSlots * nb;
+                    const uint8_t* kc = slice + x * kSlots * cb;
+                    const uint8_t* ks = slice_s + x * kSlots * nb;
                     uint32_t kw[2][KW];
                     uint32_t ksc[2][KB];                // scale of each block, in both halves
 #pragma unroll
@@ -538,8 +540,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(DT, NT)) split_kernel(
                 // ---- O^T += V^T P^T
 #pragma unroll
                 for (int x = 0; x < KS; ++x) {
-                    const uint8_t* vc = stage + L::CODES + x * kSlots * cb;
-                    const uint8_t* vs = stage + 2 * L::CODES + L::SCALES + x * kSlots * nb;
+                    const uint8_t* vc = slice + L::CODES + x * kSlots * cb;
+                    const uint8_t* vs = slice_s + L::SCALES + x * kSlots * nb;
                     uint32_t vw[4][VW];
                     uint32_t vraw[4][VS];
 #pragma unroll
@@ -628,10 +630,23 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(DT, NT)) split_kernel(
                         }
                     }
                 }
-            }
-            __syncwarp();                               // the slice is read: its stage may be filled again
+            };
+            if (k0 + L::SLOTS > lim_min) work(std::true_type{});
+            else work(std::false_type{});
         }
-        fetch();
+        __syncwarp();                                   // the slice is read
+        if (to_fetch > 0) {
+            if (lane == 0) {
+                __threadfence_block();
+                // counts to kWarps and back to 0
+                if (atomicInc(done + stage, kWarps - 1) == kWarps - 1 && ok && !sp.stall) issue(stage);
+            }
+            if (--to_fetch > 0 && ahead.next<L::TILE>(a, units)) unit_row();
+        }
+        if (++stage == L::STAGES) {
+            stage = 0;
+            parity ^= 1;
+        }
 
         if (cur.t == cur.nt - 1 || it == n_tiles - 1) {
             // ---- the unit, or this block's share of it, ends: join the warps
@@ -714,13 +729,14 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(DT, NT)) split_kernel(
         }
         if (it + 1 < n_tiles) cur.next<L::TILE>(a, units);
     }
-    // a wait gave up: this warp's copies in flight end (bounded) before the block does
-    for (; used < fetched; ++used) {
-        const uint64_t begin = tc::globaltimer();
-        while (!tc::mbar_try_wait(bar + 8 * (used % L::STAGES), (used / L::STAGES) & 1) &&
-               tc::globaltimer() - begin < sp.wait_ns) {
+    // a wait gave up: copies in flight end (bounded) before the block does; no stage is filled after the last unit's barriers
+    if (!ok && tid == 0)
+        for (int s = 0; s < L::STAGES; ++s) {
+            const uint64_t begin = tc::globaltimer();
+            while (filled[s] && !tc::mbar_try_wait(bar + 8 * s, (filled[s] - 1) & 1) &&
+                   tc::globaltimer() - begin < sp.wait_ns) {
+            }
         }
-    }
 }
 
 // Rows of units that no block finished: the partials of the blocks that share the
