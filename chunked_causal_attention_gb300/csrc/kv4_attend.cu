@@ -50,7 +50,7 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kSlots = 16;                 // slots of a fragment; a warp's slice is one or two of them
 constexpr float kLag = 4.f;                // how far (log2) a score may pass the running maximum
 constexpr float kUp = 11.f;                // weights are held times 2^kUp
-constexpr int kMaxGrid = 1024;
+constexpr int kMaxGrid = 1024;            // blocks of the split kernel
 
 // What the launch derives from the shapes.
 struct Split {
@@ -129,6 +129,11 @@ __device__ __forceinline__ int32_t tiles_of(int32_t n) { return (n + TILE - 1) /
 
 // First tile of block c when `total` tiles are dealt to `blocks` blocks.
 __device__ __forceinline__ int64_t first_tile(int64_t c, int64_t total, int32_t blocks) { return c * total / blocks; }
+
+// The block that holds tile x.
+__device__ __forceinline__ int32_t block_of(int64_t x, int64_t total, int32_t blocks) {
+    return (int32_t)(((x + 1) * blocks - 1) / total);
+}
 
 // Block-wide sums over the sequences of their tiles: of all, and of those before sequence `upto`.
 template <int THREADS, int TILE>
@@ -740,95 +745,125 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(DT, NT)) split_kernel(
 }
 
 // Rows of units that no block finished: the partials of the blocks that share the
-// unit, in block order; and the rows of empty sequences. One block per (unit, row):
-// its warps take every eighth partial, so that the loads of a unit spread over many
-// blocks (1 of 8 units of 128K slots lies in 76) are in flight together, and add up
-// their sums in order.
-constexpr int kMergeThreads = 256;
-template <int TILE>
+// unit, in block order; and the rows of empty sequences. WPR warps take a row, each
+// every WPR-th partial, and add up their sums in order: eight where few rows have many
+// partials (1 of 8 units of 128K slots lies in 76 blocks), so that their loads are in
+// flight together, one where there are many rows. Lanes hold the weights of 32
+// partials and four dims each.
+constexpr int kMergeWarps = 8;
+constexpr int kMergeThreads = 32 * kMergeWarps;
+template <int TILE, int WPR>
 __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Kv4AttendArgs a, const Split sp, int32_t unit_rows) {
-    constexpr int W = kMergeThreads / 32;
-    __shared__ int64_t scratch[2 * W];
-    __shared__ float weight[kMaxGrid], red[W];
-    __shared__ __align__(16) float sums[W][256];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int G = a.g.H / a.c.Hkv, units = a.c.Hkv * sp.RT;
-    const int u = blockIdx.x / unit_rows, r = blockIdx.x - u * unit_rows;
+    constexpr int ROWS = kMergeWarps / WPR;             // of a block
+    __shared__ int64_t scratch[2 * kMergeWarps];
+    __shared__ int32_t range[3];
+    __shared__ float red[2][kMergeWarps];
+    __shared__ __align__(16) float sums[WPR == 1 ? 1 : kMergeWarps][WPR == 1 ? 4 : 256];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, part = warp % WPR;
+    const int G = a.g.H / a.c.Hkv, units = a.c.Hkv * sp.RT, groups = unit_rows / ROWS;
+    const int u = blockIdx.x / groups, r = (blockIdx.x - u * groups) * ROWS + warp / WPR;
     const int b = u / units, v = u - b * units, hk = v / sp.RT, rt = v - hk * sp.RT;
     const int rr = rt * unit_rows + r;
     const int i = rr / G, h = hk * G + rr - i * G, D = a.c.D;
-    if (rr < sp.R) {
-        const int32_t n = slots_of(a, b);
-        int64_t total, before;
-        sum_tiles<kMergeThreads, TILE>(a, b, total, before, scratch);
-        grid_wait();                                    // the split kernel's partials
+    if (rt * unit_rows + (blockIdx.x - u * groups) * ROWS >= sp.R) return;      // no row of the block is one
+    const int32_t n = slots_of(a, b);
+    int64_t total, before;
+    sum_tiles<kMergeThreads, TILE>(a, b, total, before, scratch);
+    if (tid == 0) {
         total *= units;
-        const int64_t at = ((int64_t)b * a.g.H + h) * a.g.T + i;
-        __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(a.o) + (int64_t)b * a.g.sb + (int64_t)h * a.g.sh +
-                             (int64_t)i * a.g.st;
-        if (n - a.g.T + 1 + i <= 0) {
-            for (int d = tid; d < D; d += kMergeThreads) dst[d] = __float2bfloat16(0.f);
-            if (tid == 0) {
-                a.lse[at] = -INFINITY;
-                if (sp.lse2) sp.lse2[at] = -INFINITY;
+        const int32_t blocks = (int32_t)min((int64_t)a.grid, total), nt = tiles_of<TILE>(n);
+        const int64_t first = before * units + (int64_t)v * nt;
+        range[0] = nt ? block_of(first, total, blocks) : 0;
+        range[1] = nt ? block_of(first + nt - 1, total, blocks) : 0;
+    }
+    grid_wait();                                        // the split kernel's partials
+    __syncthreads();
+    const int c0 = range[0], c1 = range[1];
+    const bool row = rr < sp.R, none = n - a.g.T + 1 + i <= 0;
+    const int64_t at = ((int64_t)b * a.g.H + h) * a.g.T + i;
+    __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(a.o) + (int64_t)b * a.g.sb + (int64_t)h * a.g.sh +
+                         (int64_t)i * a.g.st;
+    if (row && none && part == 0) {
+        for (int d = lane; d < D; d += 32) dst[d] = __float2bfloat16(0.f);
+        if (lane == 0) {
+            a.lse[at] = -INFINITY;
+            if (sp.lse2) sp.lse2[at] = -INFINITY;
+        }
+    }
+    if (c0 == c1) return;                               // finished by its block; the same for the whole block
+    // block c0 holds the unit's begin: there the partial is the block's second
+    auto slot = [&](int c) { return a.parts + (2 * (int64_t)c + (c == c0 ? 1 : 0)) * sp.slot_floats; };
+    const int64_t off_m = (int64_t)unit_rows * D + r, off_l = off_m + unit_rows;
+    const bool live = row && !none;
+    float top = -INFINITY;
+    if (live)
+        for (int c = c0 + part + WPR * lane; c <= c1; c += WPR * 32) top = fmaxf(top, slot(c)[off_m]);
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+    if (WPR > 1) {
+        if (lane == 0) red[0][warp] = top;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < WPR; ++w) top = fmaxf(top, red[0][warp - part + w]);
+    }
+    float sum = 0.f;
+    float4 y[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+    if (live)
+        for (int base = c0 + part; base <= c1; base += WPR * 32) {
+            const int mine = base + WPR * lane;
+            float w = 0.f;
+            if (mine <= c1) {
+                const float mc = slot(mine)[off_m];
+                w = mc == -INFINITY ? 0.f : ex2(mc - top);
+                sum += w * slot(mine)[off_l];
             }
-            return;
-        }
-        const int32_t blocks = (int32_t)min((int64_t)a.grid, total);
-        const int64_t first = before * units + (int64_t)v * tiles_of<TILE>(n), last = first + tiles_of<TILE>(n) - 1;
-        const int c0 = (int)(((first + 1) * blocks - 1) / total), c1 = (int)(((last + 1) * blocks - 1) / total);
-        if (c0 == c1) return;                           // finished by its block
-        // block c0 holds the unit's begin: there the partial is the block's second
-        auto slot = [&](int c) { return a.parts + (2 * (int64_t)c + (c == c0 ? 1 : 0)) * sp.slot_floats; };
-        const int64_t off_m = (int64_t)unit_rows * D + r, off_l = off_m + unit_rows;
-        float top = -INFINITY;
-        for (int c = c0 + tid; c <= c1; c += kMergeThreads) {
-            weight[c - c0] = slot(c)[off_m];
-            top = fmaxf(top, weight[c - c0]);
-        }
+            const int count = min(32, (c1 - base) / WPR + 1);
+#pragma unroll 8
+            for (int k = 0; k < count; ++k) {
+                const float f = __shfl_sync(0xffffffffu, w, k);
+                const float* p = slot(base + WPR * k) + (int64_t)r * D + 4 * lane;
 #pragma unroll
-        for (int m = 16; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-        if (lane == 0) red[warp] = top;
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < W; ++w) top = fmaxf(top, red[w]);
-        __syncthreads();
-        float sum = 0.f;
-        for (int c = c0 + tid; c <= c1; c += kMergeThreads) {
-            const float w = weight[c - c0] == -INFINITY ? 0.f : ex2(weight[c - c0] - top);
-            weight[c - c0] = w;
-            sum += w * slot(c)[off_l];
+                for (int x = 0; x < 2; ++x)
+                    if (4 * lane + 128 * x < D) {
+                        const float4 z = *reinterpret_cast<const float4*>(p + 128 * x);
+                        y[x] = make_float4(fmaf(f, z.x, y[x].x), fmaf(f, z.y, y[x].y), fmaf(f, z.z, y[x].z), fmaf(f, z.w, y[x].w));
+                    }
+            }
         }
 #pragma unroll
-        for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-        if (lane == 0) red[warp] = sum;
+    for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+    if (WPR > 1) {
+        if (lane == 0) red[1][warp] = sum;
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+            if (4 * lane + 128 * x < D) *reinterpret_cast<float4*>(&sums[warp][4 * lane + 128 * x]) = y[x];
         __syncthreads();
+        if (part) return;
         sum = 0.f;
 #pragma unroll
-        for (int w = 0; w < W; ++w) sum += red[w];
-        for (int d = 4 * lane; d < D; d += 128) {
-            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-            for (int c = c0 + warp; c <= c1; c += W) {
-                const float4 x = *reinterpret_cast<const float4*>(slot(c) + (int64_t)r * D + d);
-                const float w = weight[c - c0];
-                y = make_float4(fmaf(w, x.x, y.x), fmaf(w, x.y, y.y), fmaf(w, x.z, y.z), fmaf(w, x.w, y.w));
-            }
-            *reinterpret_cast<float4*>(&sums[warp][d]) = y;
-        }
-        __syncthreads();
-        const float inv = a.c.v_scale / sum;
-        for (int d = tid; d < D; d += kMergeThreads) {
-            float y = 0.f;
+        for (int w = 0; w < WPR; ++w) sum += red[1][warp + w];
 #pragma unroll
-            for (int w = 0; w < W; ++w) y += sums[w][d];
-            dst[d] = __float2bfloat16(y * inv);
-        }
-        if (tid == 0) {
-            const float l2 = top - kUp + lg2(sum);
-            a.lse[at] = l2 * kLn2;
-            if (sp.lse2) sp.lse2[at] = l2;
-        }
+        for (int x = 0; x < 2; ++x)
+            if (4 * lane + 128 * x < D) {
+                y[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < WPR; ++w) {
+                    const float4 z = *reinterpret_cast<const float4*>(&sums[warp + w][4 * lane + 128 * x]);
+                    y[x] = make_float4(y[x].x + z.x, y[x].y + z.y, y[x].z + z.z, y[x].w + z.w);
+                }
+            }
+    }
+    if (!live) return;
+    const float inv = a.c.v_scale / sum;
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+        if (4 * lane + 128 * x < D)
+            *reinterpret_cast<uint2*>(dst + 4 * lane + 128 * x) =
+                make_uint2(pack_bf16(y[x].x * inv, y[x].y * inv), pack_bf16(y[x].z * inv, y[x].w * inv));
+    if (lane == 0) {
+        const float l2 = top - kUp + lg2(sum);
+        a.lse[at] = l2 * kLn2;
+        if (sp.lse2) sp.lse2[at] = l2;
     }
 }
 
@@ -944,8 +979,12 @@ cudaError_t launch_kv4_attend(const Kv4AttendArgs& args, cudaStream_t s) {
     else e = p.nt == 1 ? launch_dims<256, 1>(a, p, s) : launch_dims<256, 2>(a, p, s);
     if (e != cudaSuccess) return e;
     const int unit_rows = 8 * p.nt;
-    const int64_t rows = (int64_t)a.c.B * a.c.Hkv * p.sp.RT * unit_rows;
-    e = launch_after(p.tile == 128 ? merge_kernel<128> : merge_kernel<64>, rows, kMergeThreads, s, a, p.sp, unit_rows);
+    const int64_t units = (int64_t)a.c.B * a.c.Hkv * p.sp.RT;
+    // eight warps a row while that leaves the SMs fewer than two blocks each
+    const bool few = units * std::min(unit_rows, p.sp.R) <= 2 * device_sm_count();
+    e = launch_after(few ? (p.tile == 128 ? merge_kernel<128, 8> : merge_kernel<64, 8>)
+                         : (p.tile == 128 ? merge_kernel<128, 1> : merge_kernel<64, 1>),
+                     units * unit_rows / (few ? 1 : kMergeWarps), kMergeThreads, s, a, p.sp, unit_rows);
     if (e != cudaSuccess || !a.mass_out) return e;
     return launch_after(mass_kernel, (int64_t)((a.c.cap + 255) / 256) * a.c.B * a.c.Hkv, 256, s, a, p.sp, unit_rows);
 }
