@@ -63,7 +63,7 @@ struct Split {
     int32_t stall;
 };
 
-__host__ __device__ constexpr int blocks_per_sm(int dt, int nt) { return nt == 1 && dt <= 128 ? 4 : 2; }
+__host__ __device__ constexpr int blocks_per_sm(int dt, int nt) { return nt > 1 ? 2 : dt <= 128 ? 4 : 3; }
 
 // Fragments of 16 slots in a warp's slice: two where the registers of a second one are there.
 __host__ __device__ constexpr int fragments(int dt, int nt) { return nt == 1 && dt <= 128 ? 2 : 1; }
@@ -80,7 +80,8 @@ struct Layout {
     static constexpr int O_PITCH = DT + 8;
     static constexpr int O_OFF = RING;
     static constexpr int Q_OFF = O_OFF + ROWS * O_PITCH * 4;
-    static constexpr int Q_BYTES = NT == 1 ? 0 : NT * (DT / 16) * 32 * 8;
+    static constexpr bool Q_REGS = NT == 1 && DT <= 128;            // the queries' fragments stay in registers
+    static constexpr int Q_BYTES = Q_REGS ? 0 : NT * (DT / 16) * 32 * 8;
     static constexpr int QS_OFF = Q_OFF + Q_BYTES;                  // score factor of each row
     static constexpr int ML_OFF = QS_OFF + ROWS * 4;               // m then l of each warp and row
     static constexpr int BAR_OFF = ML_OFF + 2 * kWarps * ROWS * 4;
@@ -127,12 +128,17 @@ __device__ __forceinline__ int32_t slots_of(const Kv4AttendArgs& a, int32_t b) {
 template <int TILE>
 __device__ __forceinline__ int32_t tiles_of(int32_t n) { return (n + TILE - 1) / TILE; }
 
+// a / b, both not negative, by a 32-bit division where it does (a third of the time).
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+    return (((uint64_t)a | (uint64_t)b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // First tile of block c when `total` tiles are dealt to `blocks` blocks.
-__device__ __forceinline__ int64_t first_tile(int64_t c, int64_t total, int32_t blocks) { return c * total / blocks; }
+__device__ __forceinline__ int64_t first_tile(int64_t c, int64_t total, int32_t blocks) { return divide(c * total, blocks); }
 
 // The block that holds tile x.
 __device__ __forceinline__ int32_t block_of(int64_t x, int64_t total, int32_t blocks) {
-    return (int32_t)(((x + 1) * blocks - 1) / total);
+    return (int32_t)divide((x + 1) * blocks - 1, total);
 }
 
 // Block-wide sums over the sequences of their tiles: of all, and of those before sequence `upto`.
@@ -245,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(DT, NT)) split_kernel(
             cur.n = slots_of(a, cur.b);
             cur.nt = tiles_of<L::TILE>(cur.n);
         }
-        cur.v = (int32_t)(left / cur.nt);
+        cur.v = (int32_t)divide(left, cur.nt);
         cur.t = (int32_t)(left - (int64_t)cur.v * cur.nt);
     }
 
@@ -284,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(DT, NT)) split_kernel(
     // the fragment's columns 2c, 2c+1 (and 8 further): the same permutation
     const int v_even = (2 * c) ^ (c & 1), v_odd = (2 * c + 1) ^ (c & 1);
 
-    uint32_t qf[NT == 1 ? DT / 16 : 1][2];
+    uint32_t qf[L::Q_REGS ? DT / 16 : 1][2];
     float qs[NT][2], l[NT][2];
     float up[NT][2];                                    // kUp - m, m the running maximum
     int32_t lim[NT][2];                                 // slots [0, lim) seen
@@ -303,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(DT, NT)) split_kernel(
             const int rows = min(L::ROWS, sp.R - rt * L::ROWS);
 #pragma unroll 1
             for (int n = 0; n < NT; ++n) {
-                if (NT > 1 && (n & (kWarps - 1)) != warp) continue;
+                if (!L::Q_REGS && (n & (kWarps - 1)) != warp) continue;
                 const int r = rt * L::ROWS + 8 * n + g;
                 const bool on = 8 * n + g < rows;
                 const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q) + (int64_t)cur.b * a.g.sb +
@@ -326,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(DT, NT)) split_kernel(
                 lift = min(lift, 120);
                 if (top == 0 || top >= 0x7F80u) lift = 0;
                 const float f = __int_as_float((127 + lift) << 23);
-                if (c == 0 && (NT > 1 || warp == 0))
+                if (c == 0 && (!L::Q_REGS || warp == 0))
                     sQS[8 * n + g] = a.g.scale * kLog2e * __int_as_float((127 - lift) << 23) * a.c.k_scale;
 #pragma unroll
                 for (int i = 0; i < KW; ++i)
@@ -339,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(DT, NT)) split_kernel(
                             p[j] = as_u32(__floats2half2_rn(__uint_as_float(x << 16) * f,
                                                             __uint_as_float(x & 0xFFFF0000u) * f));
                         }
-                        if constexpr (NT == 1) {
+                        if constexpr (L::Q_REGS) {
                             qf[2 * i + half][0] = p[0];
                             qf[2 * i + half][1] = p[1];
                         } else {
@@ -431,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(DT, NT)) split_kernel(
                                                 as_u32(__hmul2(as_half2(codes_f16x2<3>(x1)), s1))};
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
-                            if constexpr (NT == 1) {
+                            if constexpr (L::Q_REGS) {
                                 mma16816(s[x][n], a0, qf[2 * i][0], qf[2 * i][1]);
                                 mma16816(s[x][n], a1, qf[2 * i + 1][0], qf[2 * i + 1][1]);
                             } else {
@@ -765,7 +771,11 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Kv4AttendArg
     const int b = u / units, v = u - b * units, hk = v / sp.RT, rt = v - hk * sp.RT;
     const int rr = rt * unit_rows + r;
     const int i = rr / G, h = hk * G + rr - i * G, D = a.c.D;
-    if (rt * unit_rows + (blockIdx.x - u * groups) * ROWS >= sp.R) return;      // no row of the block is one
+    // every block waits for the kernel before, so that this one does not end ahead of it
+    if (rt * unit_rows + (blockIdx.x - u * groups) * ROWS >= sp.R) {            // no row of the block is one
+        grid_wait();
+        return;
+    }
     const int32_t n = slots_of(a, b);
     int64_t total, before;
     sum_tiles<kMergeThreads, TILE>(a, b, total, before, scratch);
@@ -867,26 +877,58 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Kv4AttendArg
     }
 }
 
-// mass_out = mass_in + sum over the rows of 2^(s2 - lse2), from the scores that the split kernel kept.
-__global__ void __launch_bounds__(256) mass_kernel(const Kv4AttendArgs a, const Split sp, int32_t unit_rows) {
-    grid_wait();
-    const int chunks = (a.c.cap + 255) / 256;
+// mass_out = mass_in + sum over the rows of 2^(s2 - lse2), from the scores that the
+// split kernel kept; a thread takes kMassSlots slots, kMassThreads apart, V scores of
+// a slot at a time.
+constexpr int kMassThreads = 256, kMassSlots = 4;
+template <int V>
+__global__ void __launch_bounds__(kMassThreads) mass_kernel(const Kv4AttendArgs a, const Split sp, int32_t unit_rows) {
+    __shared__ float s_lse[32];
+    const int chunks = (a.c.cap + kMassThreads * kMassSlots - 1) / (kMassThreads * kMassSlots);
     const int bh = blockIdx.x / chunks, b = bh / a.c.Hkv, hk = bh - b * a.c.Hkv, G = a.g.H / a.c.Hkv;
     const int32_t n = slots_of(a, b);
-    const int j = (blockIdx.x - bh * chunks) * 256 + threadIdx.x;
-    if (j >= n) return;
-    float w = 0.f;
+    const int j0 = (blockIdx.x - bh * chunks) * kMassThreads * kMassSlots + threadIdx.x;
+    if (j0 - (int)threadIdx.x >= n) {
+        grid_wait();
+        return;
+    }
+    float sum[kMassSlots], base[kMassSlots];
+    const int64_t at = (int64_t)bh * a.mass_ld + j0;
+#pragma unroll
+    for (int x = 0; x < kMassSlots; ++x) {
+        sum[x] = 0.f;
+        base[x] = a.mass_in && j0 + x * kMassThreads < n ? a.mass_in[at + x * kMassThreads] : 0.f;
+    }
+    grid_wait();                                        // scores and sums
     for (int rt = 0; rt < sp.RT; ++rt) {
-        const float* s = sp.scores + ((int64_t)((int64_t)bh * sp.RT + rt) * a.c.cap + j) * sp.pitch;
-        const int rows = min(unit_rows, sp.R - rt * unit_rows);
-        for (int r = 0; r < rows; ++r) {
-            const int rr = rt * unit_rows + r;
-            const float l2 = sp.lse2[((int64_t)b * a.g.H + hk * G + rr % G) * a.g.T + rr / G];
-            w += l2 == -INFINITY ? 0.f : ex2(s[r] - l2);
+        __syncthreads();
+        if (threadIdx.x < sp.pitch) {
+            // rows that see nothing, and columns past the rows, weigh nothing
+            const int rr = rt * unit_rows + threadIdx.x;
+            float l2 = rr < sp.R ? sp.lse2[((int64_t)b * a.g.H + hk * G + rr % G) * a.g.T + rr / G] : INFINITY;
+            s_lse[threadIdx.x] = l2 == -INFINITY ? INFINITY : l2;
+        }
+        __syncthreads();
+        const float* s = sp.scores + ((int64_t)((int64_t)bh * sp.RT + rt) * a.c.cap + j0) * sp.pitch;
+        for (int r = 0; r < sp.pitch; r += V) {
+            float y[kMassSlots][V];
+#pragma unroll
+            for (int x = 0; x < kMassSlots; ++x)
+                if (j0 + x * kMassThreads < n) {
+                    const float* p = s + (int64_t)x * kMassThreads * sp.pitch + r;
+                    if constexpr (V == 4) *reinterpret_cast<float4*>(y[x]) = *reinterpret_cast<const float4*>(p);
+                    else *reinterpret_cast<float2*>(y[x]) = *reinterpret_cast<const float2*>(p);
+                }
+#pragma unroll
+            for (int x = 0; x < kMassSlots; ++x)
+                if (j0 + x * kMassThreads < n)
+#pragma unroll
+                    for (int i = 0; i < V; ++i) sum[x] += ex2(y[x][i] - s_lse[r + i]);
         }
     }
-    const int64_t at = (int64_t)bh * a.mass_ld + j;
-    a.mass_out[at] = (a.mass_in ? a.mass_in[at] : 0.f) + w;
+#pragma unroll
+    for (int x = 0; x < kMassSlots; ++x)
+        if (j0 + x * kMassThreads < n) a.mass_out[at + x * kMassThreads] = base[x] + sum[x];
 }
 
 // Groups of 8 rows that share a pass over the slots. Four of them save conversions, but
@@ -986,7 +1028,9 @@ cudaError_t launch_kv4_attend(const Kv4AttendArgs& args, cudaStream_t s) {
                          : (p.tile == 128 ? merge_kernel<128, 1> : merge_kernel<64, 1>),
                      units * unit_rows / (few ? 1 : kMergeWarps), kMergeThreads, s, a, p.sp, unit_rows);
     if (e != cudaSuccess || !a.mass_out) return e;
-    return launch_after(mass_kernel, (int64_t)((a.c.cap + 255) / 256) * a.c.B * a.c.Hkv, 256, s, a, p.sp, unit_rows);
+    constexpr int per = kMassThreads * kMassSlots;
+    return launch_after(p.sp.pitch % 4 ? mass_kernel<2> : mass_kernel<4>, (int64_t)((a.c.cap + per - 1) / per) * a.c.B * a.c.Hkv,
+                        kMassThreads, s, a, p.sp, unit_rows);
 }
 
 }  // namespace attn
