@@ -109,13 +109,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     return y;
 }
 
-// Programmatic dependent launch: a kernel launched with it may start while the one
-// before it in the stream runs, and waits here until that one has ended and its
-// writes are visible.
-__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
-// Let the next kernel of the stream be launched.
-__device__ __forceinline__ void grid_go() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
-
 // The bits of a where m is set, of b elsewhere.
 __device__ __forceinline__ uint32_t pick(uint32_t m, uint32_t a, uint32_t b) { return (a & m) | (b & ~m); }
 
@@ -230,6 +223,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(DT, NT)) split_kernel(
         tc::fence_barrier_init();
     }
 
+    grid_wait();
     grid_go();
 
     // ---- this block's stretch of the tile list
@@ -967,22 +961,6 @@ Plan plan_of(const Kv4Geom& c, const Geom& g, bool mass) {
     return p;
 }
 
-// A launch that may begin before the kernel ahead of it ends (grid_wait).
-template <typename K>
-cudaError_t launch_after(K kernel, int64_t grid, int threads, cudaStream_t s, const Kv4AttendArgs& a, const Split& sp,
-                         int32_t unit_rows) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(threads);
-    cfg.stream = s;
-    cudaLaunchAttribute at = {};
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return counted(cudaLaunchKernelEx(&cfg, kernel, a, sp, unit_rows));
-}
-
 template <int DT, int NT, bool EXACT, bool MASS>
 cudaError_t launch_split(const Kv4AttendArgs& a, const Plan& p, cudaStream_t s) {
     constexpr int bytes = Layout<DT, NT>::BYTES;
@@ -991,8 +969,7 @@ cudaError_t launch_split(const Kv4AttendArgs& a, const Plan& p, cudaStream_t s) 
             cudaFuncSetAttribute(split_kernel<DT, NT, EXACT, MASS>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != cudaSuccess) return e;
     }
-    split_kernel<DT, NT, EXACT, MASS><<<p.grid, kThreads, bytes, s>>>(a, p.sp);
-    return counted(cudaGetLastError());
+    return launch_early(split_kernel<DT, NT, EXACT, MASS>, dim3(p.grid), kThreads, bytes, 1, s, a, p.sp);
 }
 
 template <int DT, int NT>
@@ -1024,13 +1001,14 @@ cudaError_t launch_kv4_attend(const Kv4AttendArgs& args, cudaStream_t s) {
     const int64_t units = (int64_t)a.c.B * a.c.Hkv * p.sp.RT;
     // eight warps a row while that leaves the SMs fewer than two blocks each
     const bool few = units * std::min(unit_rows, p.sp.R) <= 2 * device_sm_count();
-    e = launch_after(few ? (p.tile == 128 ? merge_kernel<128, 8> : merge_kernel<64, 8>)
+    e = launch_early(few ? (p.tile == 128 ? merge_kernel<128, 8> : merge_kernel<64, 8>)
                          : (p.tile == 128 ? merge_kernel<128, 1> : merge_kernel<64, 1>),
-                     units * unit_rows / (few ? 1 : kMergeWarps), kMergeThreads, s, a, p.sp, unit_rows);
+                     dim3((unsigned)(units * unit_rows / (few ? 1 : kMergeWarps))), kMergeThreads, 0, 1, s, a, p.sp, unit_rows);
     if (e != cudaSuccess || !a.mass_out) return e;
     constexpr int per = kMassThreads * kMassSlots;
-    return launch_after(p.sp.pitch % 4 ? mass_kernel<2> : mass_kernel<4>, (int64_t)((a.c.cap + per - 1) / per) * a.c.B * a.c.Hkv,
-                        kMassThreads, s, a, p.sp, unit_rows);
+    return launch_early(p.sp.pitch % 4 ? mass_kernel<2> : mass_kernel<4>,
+                        dim3((unsigned)((int64_t)((a.c.cap + per - 1) / per) * a.c.B * a.c.Hkv)), kMassThreads, 0, 1, s, a, p.sp,
+                        unit_rows);
 }
 
 }  // namespace attn

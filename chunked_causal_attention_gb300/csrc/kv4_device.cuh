@@ -10,6 +10,39 @@
 namespace attn {
 namespace kv4 {
 
+// Programmatic dependent launch: a kernel launched with it may start while the one
+// before it in the stream runs, and waits in grid_wait until that one has ended and its
+// writes are visible. Every block of every kernel here waits, so that no kernel ends
+// ahead of the one before it, and lets the next one go only then: what a kernel reads
+// before its own wait has to be older than the kernel before it.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+// Let the next kernel of the stream be launched.
+__device__ __forceinline__ void grid_go() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
+
+// A launch that may begin before the kernel ahead of it ends. Clusters (cluster > 1 blocks
+// each) are launched after it: they wait for whole groups of SMs, and were slower early
+// (eviction from 128K slots 32 against 25 us).
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t s, const A&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at = {};
+    if (cluster > 1) {
+        at.id = cudaLaunchAttributeClusterDimension;
+        at.val.clusterDim.x = cluster;
+        at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    } else {
+        at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at.val.programmaticStreamSerializationAllowed = 1;
+    }
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return counted(cudaLaunchKernelEx(&cfg, kernel, args...));
+}
+
 // The two e2m1 codes of byte I of w as f16x2 (low code in the low half).
 template <int I>
 __device__ __forceinline__ uint32_t codes_f16x2(uint32_t w) {

@@ -77,7 +77,8 @@ __global__ void __launch_bounds__(THREADS) choose_kernel(const Kv4EvictArgs a, c
     extern __shared__ __align__(16) uint32_t held[];     // keys of the first kHeldTiles tiles
     __shared__ uint32_t hist[2][256], warp_sums[32], found[2], counts[2];
     const int rank = (int)cluster_rank(), bh = blockIdx.x / blocks, b = bh / a.src.Hkv, tid = threadIdx.x;
-    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    grid_wait();
+    grid_go();
     const int n = length_of(a.lens, b, (int32_t)min((int64_t)a.src.cap, a.mass_ld), a.status);
     const int m = min(n, a.keep), recent = min(m, a.recent);
     const int cand = n - recent, want = m - recent;      // choose `want` of the slots [0, cand)
@@ -244,7 +245,8 @@ __global__ void __launch_bounds__(kMoveThreads)
         tb = a.mass_out_ld * a.src.Hkv;
         th = a.mass_out_ld;
     }
-    asm volatile("griddepcontrol.wait;\n" ::: "memory");     // the slots
+    grid_wait();                                         // the slots
+    grid_go();
     const int64_t rows = (int64_t)a.src.B * a.src.Hkv * a.keep, step = (int64_t)gridDim.x * rows_per_block;
     for (int64_t base = (int64_t)blockIdx.x * rows_per_block + r0; r0 < rows_per_block && base < rows; base += step * kMoves) {
         int32_t j[kMoves];
@@ -286,17 +288,9 @@ template <int CB, int SB>
 cudaError_t launch_move(const Kv4EvictArgs& a, cudaStream_t s) {
     const int pieces = 2 * (a.src.cb / CB + a.src.nb / SB) + (a.mass_out ? 1 : 0);
     const int64_t rows = (int64_t)a.src.B * a.src.Hkv * a.keep, per = kMoveThreads / pieces;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)std::min<int64_t>((rows + per - 1) / per, (int64_t)device_sm_count() * 8));
-    cfg.blockDim = dim3(kMoveThreads);
-    cfg.stream = s;
-    cudaLaunchAttribute at = {};
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return counted(cudaLaunchKernelEx(&cfg, move_kernel<CB, SB>, a, (int32_t)pieces, FastDiv::of((uint32_t)a.keep),
-                                      FastDiv::of((uint32_t)a.src.Hkv)));
+    return launch_early(move_kernel<CB, SB>, dim3((unsigned)std::min<int64_t>((rows + per - 1) / per, (int64_t)device_sm_count() * 8)),
+                        kMoveThreads, 0, 1, s, a, (int32_t)pieces, FastDiv::of((uint32_t)a.keep),
+                        FastDiv::of((uint32_t)a.src.Hkv));
 }
 
 template <int THREADS>
@@ -314,18 +308,7 @@ cudaError_t launch_choose(const Kv4EvictArgs& a, cudaStream_t s) {
         const cudaError_t e = cudaFuncSetAttribute(choose_kernel<THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
     }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(BH * blocks));
-    cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute at = {};
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = blocks;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return counted(cudaLaunchKernelEx(&cfg, choose_kernel<THREADS>, a, (int32_t)blocks));
+    return launch_early(choose_kernel<THREADS>, dim3((unsigned)(BH * blocks)), THREADS, smem, blocks, s, a, (int32_t)blocks);
 }
 
 }  // namespace

@@ -89,6 +89,8 @@ __device__ __forceinline__ uint4 values8(uint32_t c, float d) {
 // blockIdx.y: 0 keys, 1 values. A thread is (row of the block's group, block of 16 dims).
 template <bool STORE>
 __global__ void __launch_bounds__(kThreads) kv4_rows_kernel(const Kv4RowsArgs a, int32_t rows_per_block) {
+    grid_wait();
+    grid_go();
     const int per = a.c.nb;
     const int r0 = threadIdx.x / per, part = threadIdx.x - r0 * per;
     if (r0 >= rows_per_block) return;
@@ -165,8 +167,7 @@ cudaError_t launch(const Kv4RowsArgs& a, cudaStream_t s) {
     const int rows_per_block = kThreads / a.c.nb;
     const int64_t blocks = (a.rows + rows_per_block * kAtOnce - 1) / (rows_per_block * kAtOnce);
     const dim3 grid((unsigned)std::min<int64_t>(blocks, (int64_t)device_sm_count() * 16), 2);
-    kv4_rows_kernel<STORE><<<grid, kThreads, 0, s>>>(a, rows_per_block);
-    return counted(cudaGetLastError());
+    return launch_early(kv4_rows_kernel<STORE>, grid, kThreads, 0, 1, s, a, (int32_t)rows_per_block);
 }
 
 }  // namespace
