@@ -462,6 +462,259 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
+// ------------------------------------------------------------------ few rows over many keys
+//
+// The rows of one chunk, a window at the end of a long prompt, are few: with all heads
+// of a group (row p of w G: head p / w, token q_begin + p mod w) they fill NB blocks of
+// 128, which stay in shared memory while the keys stream past. A block of the grid takes
+// an equal stretch of the (head, key tile) list; at the start of each head all threads
+// lay its queries out as TMA would (128-byte swizzle), with -lse log2 e and the token of
+// each row. A key tile is one group's: its rows' weights are summed by one thread in
+// order. The keys' bytes are the bound: 32 KB at D = 128 are 1390 cycles of an SM's share
+// of the memory rate, two blocks of products and exponentials 1024.
+template <int DT>
+struct WinLayout {
+    static constexpr int TILE = 128 * DT * 2;
+    static constexpr int MAX_NB = DT == 64 ? 8 : DT == 128 ? 4 : 1;
+    static constexpr int MAX_KST = 6;
+    static constexpr int B_KFULL = 0, B_KEMPTY = B_KFULL + MAX_KST;
+    static constexpr int B_SFULL = B_KEMPTY + MAX_KST, B_SEMPTY = B_SFULL + kGroups * kBufs;
+    static constexpr int B_DRAIN = B_SEMPTY + kBufs, NBAR = B_DRAIN + 1;
+    static constexpr int BAR_BYTES = NBAR * 8 + 16;
+    static int key_stages(int nb) { return std::min(MAX_KST, (212 * 1024 - nb * (TILE + 1024)) / TILE); }
+    static size_t bytes(int nb, int kst) { return (size_t)(nb + kst) * TILE + nb * 1024 + BAR_BYTES + 1024; }
+};
+
+template <int DT>
+__global__ void __launch_bounds__(kThreads, 1)
+    key_mass_window_kernel(const __grid_constant__ CUtensorMap tmk, const MassArgs a, const TcMaps mpkv, const attn_chunk ch,
+                           const int32_t nb, const int32_t kst) {
+    using L = WinLayout<DT>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(sm), k_off = nb * L::TILE;
+    float* s_lse = reinterpret_cast<float*>(sm + (size_t)(nb + kst) * L::TILE);
+    int32_t* s_tok = reinterpret_cast<int32_t*>(s_lse + nb * 128);
+    const uint32_t bar0 = smem_u32(s_tok + nb * 128);
+    auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
+    uint8_t* misc = reinterpret_cast<uint8_t*>(s_tok + nb * 128) + L::NBAR * 8;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 4);
+    const int tid = threadIdx.x, warp = tid >> 5;
+    const int G = a.g.H / a.g.Hkv, w = ch.q_end - ch.q_begin, R = w * G;
+    const int tiles = (a.g.T + 127) / 128;
+
+    if (tid == 0) {
+        for (int s = 0; s < kst; ++s) {
+            mbar_init(bar(L::B_KFULL + s), 1);
+            mbar_init(bar(L::B_KEMPTY + s), 1);
+        }
+        for (int s = 0; s < kGroups * kBufs; ++s) mbar_init(bar(L::B_SFULL + s), 1);
+        for (int s = 0; s < kBufs; ++s) mbar_init(bar(L::B_SEMPTY + s), 128);
+        mbar_init(bar(L::B_DRAIN), 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    const int64_t total = (int64_t)a.g.B * a.g.Hkv * tiles;
+    const int64_t begin = blockIdx.x * total / gridDim.x, end = (blockIdx.x + 1) * total / gridDim.x;
+    // whether any row sees a key of the tile, and whether all rows see all of its keys
+    auto seen_tile = [&](int j0) { return j0 < ch.q_end && j0 + 128 > ch.ctx_begin; };
+    uint32_t kc = 0, qc = 0, tc_ = 0, dealt = 0, mine = 0;      // key tiles, blocks, tiles, blocks of each group, of this one
+    bool ok = true;
+    for (int64_t x0 = begin; x0 < end;) {
+        const int bh = (int)(x0 / tiles), first = (int)(x0 - (int64_t)bh * tiles);
+        const int count = (int)min((int64_t)(tiles - first), end - x0);
+        const int b = bh / a.g.Hkv, hk = bh % a.g.Hkv;
+        // ---------------------------------------------------------------- queries of the head
+        for (int i = tid; i < nb * 128 * (DT / 8); i += kThreads) {
+            const int p = i / (DT / 8), c16 = i % (DT / 8);
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (p < R && c16 * 8 < a.g.D)
+                v = *reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.q) + (int64_t)b * a.g.sb +
+                                                    (int64_t)(hk * G + p / w) * a.g.sh +
+                                                    (int64_t)(ch.q_begin + p % w) * a.g.st + c16 * 8);
+            const int row = p & 127;
+            *reinterpret_cast<uint4*>(sm + (p >> 7) * L::TILE + (c16 >> 3) * (128 * 128) + row * 128 +
+                                      (((c16 & 7) ^ (row & 7)) << 4)) = v;
+        }
+        for (int p = tid; p < nb * 128; p += kThreads) {
+            float l = -INFINITY;                        // weight 0: rows past the last, rows without a sum
+            const int t = ch.q_begin + p % w;
+            if (p < R) {
+                l = a.lse[((int64_t)b * a.g.H + hk * G + p / w) * a.g.T + t];
+                l = l == -INFINITY ? l : -l * kLog2e;
+            }
+            s_lse[p] = l;
+            s_tok[p] = p < R ? t : -1;
+        }
+        fence_proxy_async_smem();
+        __syncthreads();
+        if (warp == 0) {
+            // ------------------------------------------------------------ producer
+            if (elect_one() && !a.stall) {
+                for (int i = 0; i < count && ok; ++i) {
+                    const int j0 = (first + i) * 128;
+                    if (!seen_tile(j0)) continue;
+                    const uint32_t s = kc % kst;
+                    ok = mbar_wait(bar(L::B_KEMPTY + s), ((kc / kst) & 1) ^ 1, abort_flag, a.status, a.wait_ns);
+                    if (!ok) break;
+                    mbar_expect_tx(bar(L::B_KFULL + s), L::TILE);
+                    load_rows<DT>(sbase + k_off + s * L::TILE, &tmk, bar(L::B_KFULL + s), mpkv, j0, 2, hk, b);
+                    ++kc;
+                }
+            }
+        } else if (warp == 1) {
+            // ------------------------------------------------------------ MMA issuer
+            if (elect_one()) {
+                for (int i = 0; i < count && ok; ++i, ++tc_) {
+                    if (!seen_tile((first + i) * 128)) continue;
+                    const uint32_t s = kc % kst, grp = tc_ % kGroups;
+                    ok = mbar_wait(bar(L::B_KFULL + s), (kc / kst) & 1, abort_flag, a.status, a.wait_ns);
+                    for (int x = 0; x < nb && ok; ++x, ++qc) {
+                        const uint32_t sb = qc % kBufs;
+                        ok = mbar_wait(bar(L::B_SEMPTY + sb), ((qc / kBufs) & 1) ^ 1, abort_flag, a.status, a.wait_ns);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t id = idesc_bf16(128, (min(128, R - 128 * x) + 15) & ~15, 0, 0);
+#pragma unroll
+                        for (int kk = 0; kk < DT / 16; ++kk) {
+                            const uint32_t off = (kk >> 2) * (128 * 128) + (kk & 3) * 32;
+                            mma_ss(tmem + sb * 128, sdesc_sw128(sbase + k_off + s * L::TILE + off, 16, 1024),
+                                   sdesc_sw128(sbase + x * L::TILE + off, 16, 1024), id, kk > 0);
+                        }
+                        // a group's barriers in its own turn: at most kBufs of its blocks are ahead of it
+                        const uint32_t m = dealt >> (8 * grp) & 3u;
+                        dealt = (dealt & ~(3u << (8 * grp))) | ((m + 1) & 3u) << (8 * grp);
+                        mma_commit(bar(L::B_SFULL + grp * kBufs + m));
+                    }
+                    if (!ok) break;
+                    mma_commit(bar(L::B_KEMPTY + s));
+                    ++kc;
+                }
+            }
+        } else if (warp >= 4) {
+            // ------------------------------------------------------------ sums
+            const int grp = (warp >> 2) - 1, key = tid & 127;
+            const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
+            const float c = a.g.scale * kLog2e;
+            const float2 c2 = make_float2(c, c);
+            for (int i = 0; i < count && ok; ++i, ++tc_) {
+                const int j0 = (first + i) * 128, j = j0 + key;
+                const bool sees = seen_tile(j0);
+                if (tc_ % kGroups != (uint32_t)grp) {
+                    if (sees) qc += nb;
+                    continue;
+                }
+                const int64_t at = (int64_t)bh * a.g.T + j;
+                const float base = a.mass_in && j < a.g.T ? a.mass_in[at] : 0.f;
+                const bool edge = j0 + 127 > ch.q_begin || j0 < ch.ctx_begin;
+                float sum = 0.f;
+                for (int x = 0; x < nb && ok && sees; ++x, ++qc, ++mine) {
+                    ok = mbar_wait_warp(bar(L::B_SFULL + grp * kBufs + mine % kBufs), (mine / kBufs) & 1, abort_flag, a.status,
+                                        a.wait_ns);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t sb = qc % kBufs, sa = tmem + lane_addr + sb * 128;
+                    const int cols = (min(128, R - 128 * x) + 15) & ~15;
+                    float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+                    for (int half = 0; half < cols; half += 64) {
+                        uint32_t r[4][16];
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+                            if (half + 16 * y < cols) tmem_ld16(sa + half + 16 * y, r[y]);
+                        tmem_ld_wait();
+                        if (half + 64 >= cols) {
+                            tc_fence_before();
+                            mbar_arrive(bar(L::B_SEMPTY + sb));          // the buffer has been read
+                        }
+                        const float* lse = s_lse + 128 * x + half;
+                        const int32_t* tok = s_tok + 128 * x + half;
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            if (half + 16 * y >= cols) break;
+                            if (!edge) {
+#pragma unroll
+                                for (int z = 0; z < 16; z += 4) {
+                                    const float4 l = *reinterpret_cast<const float4*>(lse + 16 * y + z);
+                                    const float2 e0 = ffma2(make_float2(__uint_as_float(r[y][z]), __uint_as_float(r[y][z + 1])), c2,
+                                                            make_float2(l.x, l.y));
+                                    const float2 e1 = ffma2(make_float2(__uint_as_float(r[y][z + 2]), __uint_as_float(r[y][z + 3])), c2,
+                                                            make_float2(l.z, l.w));
+                                    acc[0] = fadd2(acc[0], make_float2(ex2(e0.x), ex2(e0.y)));
+                                    acc[1] = fadd2(acc[1], make_float2(ex2(e1.x), ex2(e1.y)));
+                                }
+                            } else {
+#pragma unroll
+                                for (int z = 0; z < 16; ++z) {
+                                    const float e = fmaf(__uint_as_float(r[y][z]), c, lse[16 * y + z]);
+                                    const float p = j >= ch.ctx_begin && j <= tok[16 * y + z] ? ex2(e) : 0.f;
+                                    if (z & 1) acc[(z >> 1) & 1].y += p; else acc[(z >> 1) & 1].x += p;
+                                }
+                            }
+                        }
+                    }
+                    sum += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+                }
+                if (ok && j < a.g.T) a.mass_out[at] = base + sum;
+            }
+        }
+        __syncwarp();
+        tc_fence_before();
+        __syncthreads();                                // the head's queries have been read
+        tc_fence_after();
+        x0 += count;
+    }
+    // ---------------------------------------------------------------- teardown
+    if (warp == 1) {
+        __syncwarp();
+        if (*abort_flag) {
+            if (elect_one()) {
+                mma_commit(bar(L::B_DRAIN));
+                const uint64_t t0 = globaltimer();
+                while (!mbar_try_wait(bar(L::B_DRAIN), 0) && globaltimer() - t0 < a.wait_ns) {
+                }
+            }
+            __syncwarp();
+        }
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// Whether the window kernel takes these rows: one chunk of few rows, for which the work of
+// the tiles inside the chunk (all rows, without the causal half) does not matter.
+template <int DT>
+bool window(const MassArgs& a, const attn_chunk* chunks) {
+    if (a.n != 1) return false;
+    const int64_t w = chunks[0].q_end - chunks[0].q_begin;
+    return w * (a.g.H / a.g.Hkv) <= 128 * WinLayout<DT>::MAX_NB && 4 * w <= a.g.T;
+}
+
+template <int DT>
+cudaError_t launch_window(const MassArgs& a, const attn_chunk& ch, cudaStream_t s) {
+    using L = WinLayout<DT>;
+    CUtensorMap mk;
+    TcMaps mpkv{1, 2, 3};
+    if (!make_tile_map(&mk, a.k, a.g.kv(), mpkv, kBoxRows)) return cudaErrorInvalidValue;
+    const int nb = ((ch.q_end - ch.q_begin) * (a.g.H / a.g.Hkv) + 127) / 128, kst = L::key_stages(nb);
+    const size_t smem = L::bytes(nb, kst);
+    cudaError_t e = cudaFuncSetAttribute(key_mass_window_kernel<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    const int64_t total = (int64_t)a.g.B * a.g.Hkv * ((a.g.T + 127) / 128);
+    const int grid = (int)std::min<int64_t>(total, device_sm_count());
+    key_mass_window_kernel<DT><<<grid, kThreads, smem, s>>>(mk, a, mpkv, ch, nb, kst);
+    return counted(cudaGetLastError());
+}
+
 template <int DT>
 cudaError_t launch_d(const MassArgs& a, cudaStream_t s) {
     CUtensorMap mq, mk;
@@ -481,6 +734,14 @@ cudaError_t launch_d(const MassArgs& a, cudaStream_t s) {
 }
 
 }  // namespace
+
+bool key_mass_window(const MassArgs& a, const attn_chunk* chunks) {
+    return a.g.D > 128 ? window<256>(a, chunks) : a.g.D > 64 ? window<128>(a, chunks) : window<64>(a, chunks);
+}
+
+cudaError_t launch_key_mass_window(const MassArgs& a, const attn_chunk& ch, cudaStream_t s) {
+    return a.g.D > 128 ? launch_window<256>(a, ch, s) : a.g.D > 64 ? launch_window<128>(a, ch, s) : launch_window<64>(a, ch, s);
+}
 
 cudaError_t launch_key_mass(const MassArgs& a, cudaStream_t s) {
     return a.g.D > 128 ? launch_d<256>(a, s) : a.g.D > 64 ? launch_d<128>(a, s) : launch_d<64>(a, s);

@@ -93,6 +93,9 @@ cudaError_t launch_kv4_load(const Kv4RowsArgs& a, cudaStream_t s);     // kv4_ro
 cudaError_t launch_kv4_attend(const Kv4AttendArgs& a, cudaStream_t s); // kv4_attend.cu
 cudaError_t launch_kv4_evict(const Kv4EvictArgs& a, cudaStream_t s);   // kv4_evict.cu
 cudaError_t launch_key_mass(const MassArgs& a, cudaStream_t s);        // key_mass.cu
+// One chunk of few rows over many keys: whether these chunks (host) are that, and its kernel.
+bool key_mass_window(const MassArgs& a, const attn_chunk* chunks);
+cudaError_t launch_key_mass_window(const MassArgs& a, const attn_chunk& ch, cudaStream_t s);
 
 // attn_api.cpp's argument rules, for the entry points in kv4_api.cpp
 int shape_geom(const attn_shape* s, Geom* g);

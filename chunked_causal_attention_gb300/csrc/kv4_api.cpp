@@ -3,6 +3,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <new>
 #include <vector>
 
 #include "kv4.h"
@@ -247,20 +248,31 @@ int attn_key_mass(const void* q, const void* k, const float* lse, const attn_chu
     if ((st = check_mass(mass_in, mass_out, (size_t)a.g.B * a.g.Hkv * a.g.T))) return st;
     if ((st = check_ws(ws, ws_bytes, key_mass_bytes(a.g, chunks, n)))) return st;
     cudaStream_t s = (cudaStream_t)stream;
-    if (cudaMemsetAsync(ws, 0, kHeaderBytes, s) != cudaSuccess) return ATTN_E_CUDA;
     uint8_t* w = (uint8_t*)ws;
-    if (n && launch_upload(w + kHeaderBytes, chunks, (size_t)n * sizeof(attn_chunk), s) != cudaSuccess) return ATTN_E_CUDA;
     a.q = q; a.k = k; a.lse = lse; a.mass_in = mass_in; a.mass_out = mass_out;
-    const std::vector<MassItem> items = mass_items(a.g, chunks, n);
-    const size_t off = mass_items_offset(n);
-    if (launch_upload(w + off, items.data(), items.size() * sizeof(MassItem), s) != cudaSuccess) return ATTN_E_CUDA;
     a.chunks = (const attn_chunk*)(w + kHeaderBytes);
     a.n = n;
-    a.items = (const MassItem*)(w + off);
-    a.n_items = (int32_t)items.size();
+    a.items = (const MassItem*)(w + mass_items_offset(n));
+    a.n_items = 0;
     a.status = (uint32_t*)ws;
     a.counter = &((WsHeader*)ws)->counter[0];
     wait_settings(&a.wait_ns, &a.stall);
+    if (key_mass_window(a, chunks)) {
+        if (cudaMemsetAsync(ws, 0, kHeaderBytes, s) != cudaSuccess) return ATTN_E_CUDA;
+        return launched(launch_key_mass_window(a, chunks[0], s));
+    }
+    try {
+        // the zeroed header, the chunks and the items in one copy
+        const std::vector<MassItem> items = mass_items(a.g, chunks, n);
+        const size_t off = mass_items_offset(n), bytes = off + items.size() * sizeof(MassItem);
+        std::vector<uint8_t> lists(bytes, 0);
+        if (n) std::memcpy(lists.data() + kHeaderBytes, chunks, (size_t)n * sizeof(attn_chunk));
+        std::memcpy(lists.data() + off, items.data(), items.size() * sizeof(MassItem));
+        if (launch_upload(w, lists.data(), bytes, s) != cudaSuccess) return ATTN_E_CUDA;
+        a.n_items = (int32_t)items.size();
+    } catch (const std::bad_alloc&) {
+        return ATTN_E_CUDA;
+    }
     return launched(launch_key_mass(a, s));
 }
 

@@ -358,7 +358,8 @@ def check_mass(q, k, lse, chunks, got, scale, mass_in=None, packed=False):
 MASS_PLANS = {"whole": [(0, 700, 0, 0)], "cut": [(0, 300, 0, 0), (300, 301, 0, 0), (301, 700, 0, 128)],
               "window": [(683, 700, 0, 0)], "one row": [(699, 700, 0, 0)], "gap": [(0, 130, 0, 0), (500, 650, 0, 0)],
               "docs": [(0, 257, 0, 0), (257, 258, 257, 0), (258, 700, 258, 0)],
-              "late context": [(300, 500, 250, 0), (600, 700, 599, 0)], "none": []}
+              "late context": [(300, 500, 250, 0), (600, 700, 599, 0)], "late window": [(600, 640, 333, 0)],
+              "early window": [(128, 140, 0, 0)], "none": []}
 
 
 @pytest.mark.parametrize("plan", list(MASS_PLANS))
@@ -408,6 +409,23 @@ def test_key_mass_packed_streamed_and_empty_rows():
     check_mass(q, k, lse, chunks, m, 0.125, packed=True)
     lse[0, :, 50:90] = -math.inf
     check_mass(q, k, lse, chunks, cca.key_mass(q, k, lse, chunks, packed=True), 0.125, packed=True)
+
+
+@pytest.mark.parametrize("D,H,Hkv,w", [(128, 6, 3, 40), (128, 16, 2, 64), (64, 9, 3, 100), (256, 3, 3, 128), (80, 8, 1, 1),
+                                        (128, 4, 4, 129), (40, 8, 2, 17)])
+def test_key_mass_of_a_window(D, H, Hkv, w):
+    """Few rows over many key tiles: several tiles, and the ends of heads, in one block of the grid."""
+    rng = np.random.default_rng(D + w)
+    L = 19000 + w
+    q, k = 2 * bf16(rng, 1, H, L, D), bf16(rng, 1, Hkv, L, D)
+    chunks = [(L - w - 1, L - 1, 0, 0)]                        # the last key is seen by no row
+    _, lse = cca.forward(q, k, k, chunks)
+    lse[0, 0, L - 2] = -math.inf                               # a row that counts for nothing
+    got = cca.key_mass(q, k, lse, chunks)
+    check_mass(q, k, lse, chunks, got, D ** -0.5)
+    assert (got[..., -1] == 0).all() and torch.equal(got, cca.key_mass(q, k, lse, chunks))
+    m = torch.rand(1, Hkv, L, device="cuda")
+    check_mass(q, k, lse, chunks, cca.key_mass(q, k, lse, chunks, mass_in=m), D ** -0.5, mass_in=m)
 
 
 def test_key_mass_strided():
