@@ -139,6 +139,23 @@ __device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap* map, 
     }
 }
 
+// Weights of 64 columns that all see this thread's key, into four running sums.
+__device__ __forceinline__ void weigh64(const uint32_t (&r)[2][32], const float* lse, float2 c2, float2 (&acc)[2]) {
+    const float4* l4 = reinterpret_cast<const float4*>(lse);
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int y = 0; y < 8; ++y) {
+            const float4 l = l4[8 * x + y];
+            const float2 e0 =
+                ffma2(make_float2(__uint_as_float(r[x][4 * y]), __uint_as_float(r[x][4 * y + 1])), c2, make_float2(l.x, l.y));
+            const float2 e1 =
+                ffma2(make_float2(__uint_as_float(r[x][4 * y + 2]), __uint_as_float(r[x][4 * y + 3])), c2, make_float2(l.z, l.w));
+            acc[0] = fadd2(acc[0], make_float2(ex2(e0.x), ex2(e0.y)));
+            acc[1] = fadd2(acc[1], make_float2(ex2(e1.x), ex2(e1.y)));
+        }
+}
+
 template <int DT>
 __global__ void __launch_bounds__(kThreads, 1)
     key_mass_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk, const MassArgs a,
@@ -376,19 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mbar_arrive(bar(L::B_SEMPTY + sb));  // the buffer has been read
                     }
                     if (!edge) {
-                        const float4* l4 = reinterpret_cast<const float4*>(lse + half);
-#pragma unroll
-                        for (int x = 0; x < 2; ++x)
-#pragma unroll
-                            for (int y = 0; y < 8; ++y) {
-                                const float4 l = l4[8 * x + y];
-                                const float2 e0 = ffma2(make_float2(__uint_as_float(r[x][4 * y]), __uint_as_float(r[x][4 * y + 1])),
-                                                        c2, make_float2(l.x, l.y));
-                                const float2 e1 = ffma2(make_float2(__uint_as_float(r[x][4 * y + 2]), __uint_as_float(r[x][4 * y + 3])),
-                                                        c2, make_float2(l.z, l.w));
-                                acc[0] = fadd2(acc[0], make_float2(ex2(e0.x), ex2(e0.y)));
-                                acc[1] = fadd2(acc[1], make_float2(ex2(e1.x), ex2(e1.y)));
-                            }
+                        weigh64(r, lse + half, c2, acc);
                     } else if (half < n) {
                         const int from = lo - half, to = n - half;
 #pragma unroll
@@ -628,36 +633,36 @@ __global__ void __launch_bounds__(kThreads, 1)
                     float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll 1
                     for (int half = 0; half < cols; half += 64) {
-                        uint32_t r[4][16];
+                        const float* lse = s_lse + 128 * x + half;
+                        const int left = cols - half;                    // columns of this half
+                        uint32_t r[2][32];
+                        if (left >= 64) {
+                            tmem_ld32(sa + half, r[0]);
+                            tmem_ld32(sa + half + 32, r[1]);
+                        } else {
+                            // in sixteens: the columns past `cols` were never written
+                            uint32_t(&q16)[4][16] = reinterpret_cast<uint32_t(&)[4][16]>(r);
 #pragma unroll
-                        for (int y = 0; y < 4; ++y)
-                            if (half + 16 * y < cols) tmem_ld16(sa + half + 16 * y, r[y]);
+                            for (int y = 0; y < 4; ++y)
+                                if (16 * y < left) tmem_ld16(sa + half + 16 * y, q16[y]);
+                        }
                         tmem_ld_wait();
-                        if (half + 64 >= cols) {
+                        if (left <= 64) {
                             tc_fence_before();
                             mbar_arrive(bar(L::B_SEMPTY + sb));          // the buffer has been read
                         }
-                        const float* lse = s_lse + 128 * x + half;
-                        const int32_t* tok = s_tok + 128 * x + half;
+                        if (left >= 64 && !edge) {
+                            weigh64(r, lse, c2, acc);
+                        } else {
+                            const int32_t* tok = s_tok + 128 * x + half;
 #pragma unroll
-                        for (int y = 0; y < 4; ++y) {
-                            if (half + 16 * y >= cols) break;
-                            if (!edge) {
-#pragma unroll
-                                for (int z = 0; z < 16; z += 4) {
-                                    const float4 l = *reinterpret_cast<const float4*>(lse + 16 * y + z);
-                                    const float2 e0 = ffma2(make_float2(__uint_as_float(r[y][z]), __uint_as_float(r[y][z + 1])), c2,
-                                                            make_float2(l.x, l.y));
-                                    const float2 e1 = ffma2(make_float2(__uint_as_float(r[y][z + 2]), __uint_as_float(r[y][z + 3])), c2,
-                                                            make_float2(l.z, l.w));
-                                    acc[0] = fadd2(acc[0], make_float2(ex2(e0.x), ex2(e0.y)));
-                                    acc[1] = fadd2(acc[1], make_float2(ex2(e1.x), ex2(e1.y)));
-                                }
-                            } else {
+                            for (int y = 0; y < 4; ++y) {
+                                if (16 * y >= left) break;
 #pragma unroll
                                 for (int z = 0; z < 16; ++z) {
-                                    const float e = fmaf(__uint_as_float(r[y][z]), c, lse[16 * y + z]);
-                                    const float p = j >= ch.ctx_begin && j <= tok[16 * y + z] ? ex2(e) : 0.f;
+                                    const float e = fmaf(__uint_as_float(r[y >> 1][16 * (y & 1) + z]), c, lse[16 * y + z]);
+                                    const bool on = !edge || (j >= ch.ctx_begin && j <= tok[16 * y + z]);
+                                    const float p = on ? ex2(e) : 0.f;
                                     if (z & 1) acc[(z >> 1) & 1].y += p; else acc[(z >> 1) & 1].x += p;
                                 }
                             }
