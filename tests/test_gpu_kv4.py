@@ -428,6 +428,32 @@ def test_key_mass_of_a_window(D, H, Hkv, w):
     check_mass(q, k, lse, chunks, cca.key_mass(q, k, lse, chunks, mass_in=m), D ** -0.5, mass_in=m)
 
 
+@pytest.mark.parametrize("D,G", [(64, 1), (80, 2), (128, 1)])
+@pytest.mark.parametrize("chunks", [[(0, 1300, 0, 0)], [(0, 257, 0, 0), (257, 390, 257, 0), (390, 1300, 390, 0)],
+                                    [(0, 130, 0, 0), (600, 1290, 100, 0)], [(700, 1300, 128, 0)]])
+def test_key_mass_with_many_heads(D, G, chunks):
+    """Many heads and key tiles of few blocks: the groups that sum skip items in which they have none."""
+    rng = np.random.default_rng(D + G)
+    B, Hkv, L = 2, 64, 1300
+    g = torch.Generator(device="cuda")
+    g.manual_seed(D)
+    q = 2 * torch.randn(B, Hkv * G, L, D, device="cuda", generator=g).bfloat16()
+    k = torch.randn(B, Hkv, L, D, device="cuda", generator=g).bfloat16()
+    _, lse = cca.forward(q, k, k, chunks)
+    got = cca.key_mass(q, k, lse, chunks)
+    heads = [0, 1, 31, 63]
+    qs = [h * G + i for h in heads for i in range(G)]
+    check_mass(q[:, qs], k[:, heads], lse[:, qs], chunks, got[:, heads], D ** -0.5)
+    # the other heads by the sum of their weights: one a row
+    total = G * sum(b - a for a, b, _, _ in chunks)
+    assert (got.double().sum(-1) - total).abs().max() <= total * 1e-4
+    for _ in range(3):
+        assert torch.equal(got, cca.key_mass(q, k, lse, chunks))
+    m = torch.rand(B, Hkv, L, device="cuda")
+    out = cca.key_mass(q, k, lse, chunks, mass_in=m)
+    check_mass(q[:, qs], k[:, heads], lse[:, qs], chunks, out[:, heads], D ** -0.5, mass_in=m[:, heads])
+
+
 def test_key_mass_strided():
     """Token-major storage, 80 dims of a wider buffer, a batch view."""
     rng = np.random.default_rng(33)
