@@ -236,17 +236,39 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(DT, NT)) split_kernel(
     const int32_t n_tiles = (int32_t)(first_tile(blockIdx.x + 1, total, blocks) - t0);
     Cursor cur{0, 0, 0, 0, 0};
     {
+        // the sequence that holds tile t0: a scan over as many sequences as there are threads, until it is among them
         int64_t left = t0;
-        cur.n = slots_of(a, 0);
-        cur.nt = tiles_of<L::TILE>(cur.n);
-        while (left >= (int64_t)cur.nt * units) {       // t0 < total: ends at a sequence with tiles
-            left -= (int64_t)cur.nt * units;
-            ++cur.b;
-            cur.n = slots_of(a, cur.b);
-            cur.nt = tiles_of<L::TILE>(cur.n);
+        for (int base = 0;; base += kThreads) {         // t0 < total: there is one
+            const int32_t mine = base + tid < a.c.B ? tiles_of<L::TILE>(slots_of(a, base + tid)) : 0;
+            int64_t upto = (int64_t)mine * units;
+#pragma unroll
+            for (int m = 1; m < 32; m <<= 1) {
+                const int64_t y = __shfl_up_sync(0xffffffffu, upto, m);
+                if (lane >= m) upto += y;
+            }
+            if (lane == 31) scratch[warp] = upto;
+            __syncthreads();
+            int64_t chunk = 0;
+            for (int w = 0; w < kWarps; ++w) {
+                if (w < warp) upto += scratch[w];
+                chunk += scratch[w];
+            }
+            if (left < upto && left >= upto - (int64_t)mine * units) {
+                scratch[kWarps] = base + tid;
+                scratch[kWarps + 1] = left - (upto - (int64_t)mine * units);
+            }
+            __syncthreads();
+            if (left < chunk) break;
+            left -= chunk;
+            if (base + kThreads >= a.c.B) return;       // lens changed under the kernel: nothing is addressed
         }
-        cur.v = (int32_t)divide(left, cur.nt);
+        cur.b = (int32_t)scratch[kWarps];
+        left = scratch[kWarps + 1];
+        cur.n = slots_of(a, cur.b);
+        cur.nt = tiles_of<L::TILE>(cur.n);
+        cur.v = (int32_t)divide(left, max(cur.nt, 1));
         cur.t = (int32_t)(left - (int64_t)cur.v * cur.nt);
+        __syncthreads();                                // scratch is read
     }
 
     // ---- bulk copies of the tiles, in list order. Every warp follows the cursor; a stage is

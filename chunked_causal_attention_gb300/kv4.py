@@ -177,9 +177,10 @@ def kv4_evict(cache: KV4Cache, lens, mass, keep: int, recent: int, out: KV4Cache
     and those with the highest mass, moved to the front of `out` in their order.
     Returns (lens_out, slots): int32 [B] and the source slots int32 [B, Hkv, keep]."""
     import torch
-    if out.device != cache.device or lens.device != cache.device:
+    if out.device != cache.device or lens.device != cache.device or not 0 < keep <= out.cap or recent < 0:
         raise AttnError("kv4_evict", ATTN_E_INVAL)
-    slots = torch.empty((cache.B, cache.Hkv, max(int(keep), 0)), dtype=torch.int32, device=lens.device)
+    recent = min(int(recent), int(keep))
+    slots = torch.empty((cache.B, cache.Hkv, int(keep)), dtype=torch.int32, device=lens.device)
     if lens_out is None:
         lens_out = torch.empty_like(lens)
     if ws is None:

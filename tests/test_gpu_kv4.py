@@ -269,6 +269,78 @@ def test_attend_long_with_split_keys():
     check_attend(q, c, [n], o, lse, None, None, mo)
 
 
+def test_attend_more_sequences_than_threads():
+    """300 sequences, most of them empty: blocks find theirs by a scan over more than one group."""
+    rng = np.random.default_rng(19)
+    lens = [int(x) if x % 3 == 0 else 0 for x in rng.integers(0, 200, 300)]
+    lens[-1] = 208
+    c = random_cache(300, 1, 208, 64, 20)
+    q = bf16(rng, 300, 2, 1, 64)
+    o, lse = cca.kv4_attention(q, c, i32(lens))
+    check_attend(q, c, lens, o, lse)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.2, 1e-3])
+def test_attend_many_rows_and_scales(scale):
+    """A prompt chunk's worth of rows, more than there are slots, at scales other than 1/sqrt(D)."""
+    rng = np.random.default_rng(27)
+    c = random_cache(1, 2, 272, 80, 28)
+    q = bf16(rng, 1, 6, 300, 80)
+    mo = torch.zeros(1, 2, 272, device="cuda")
+    o, lse = cca.kv4_attention(q, c, i32([257]), scale=scale, mass_out=mo)
+    check_attend(q, c, [257], o, lse, scale, None, mo, kept_tail=0.0)
+
+
+def test_offsets_past_32_bits():
+    """Heads 70 million slots apart: byte offsets of the second head pass 2^32."""
+    apart, cap, D = 70_000_000 // 16 * 16, 512, 128
+    arrays = [torch.empty((1, 2, apart, n), dtype=torch.uint8, device="cuda")[:, :, :cap] for n in (64, 8, 64, 8)]
+    c = cca.KV4Cache(*arrays, D=D)
+    assert c.desc.sh * 64 > 1 << 32
+    rng = np.random.default_rng(29)
+    k, v = bf16(rng, 1, 2, cap, D), bf16(rng, 1, 2, cap, D)
+    cca.kv4_store(c, k, v, i32([0]))
+    kk, vv = cca.kv4_load(c, i32([0]), cap)
+    near = cca.kv4_cache(1, 2, cap, D)
+    cca.kv4_store(near, k, v, i32([0]))
+    nk, nv = cca.kv4_load(near, i32([0]), cap)
+    assert torch.equal(kk, nk) and torch.equal(vv, nv)
+    q = bf16(rng, 1, 8, 2, D)
+    for a, b in zip(cca.kv4_attention(q, c, i32([500])), cca.kv4_attention(q, near, i32([500]))):
+        assert torch.equal(a, b)
+    mass = torch.rand(1, 2, cap, device="cuda")
+    small = [cca.kv4_cache(1, 2, 64, D) for _ in range(2)]
+    for s, x in zip(small, (c, near)):
+        cca.kv4_evict(x, i32([500]), mass, 64, 8, s)
+    assert torch.equal(small[0].v_codes, small[1].v_codes) and torch.equal(small[0].k_scales, small[1].k_scales)
+
+
+@pytest.mark.parametrize("window", [False, True])
+def test_waits_that_run_out_are_reported(monkeypatch, window):
+    """With the copies held back (a test switch) every wait ends after its limit with ATTN_E_TIMEOUT in the
+    status word, and the next calls work."""
+    rng = np.random.default_rng(30)
+    c = random_cache(1, 1, 256, 64, 31)
+    q = bf16(rng, 1, 2, 1, 64)
+    ws = cca.kv4_workspace(c, q)
+    good, _ = cca.kv4_attention(q, c, i32([250]), ws=ws)
+    qq, k = bf16(rng, 1, 2, 700, 64), bf16(rng, 1, 1, 700, 64)
+    chunks = [(690, 700, 0, 0)] if window else [(0, 700, 0, 0)]
+    _, lse = cca.forward(qq, k, k, chunks)
+    mws = cca.key_mass_workspace(qq, k, chunks)
+    want = cca.key_mass(qq, k, lse, chunks, ws=mws)
+    monkeypatch.setenv("ATTN_TEST_STALL_PRODUCER", "1")
+    monkeypatch.setenv("ATTN_WAIT_LIMIT_MS", "200")
+    cca.kv4_attention(q, c, i32([250]), ws=ws)
+    assert cca.attn_status(ws) == 6
+    cca.key_mass(qq, k, lse, chunks, ws=mws)
+    assert cca.attn_status(mws) == 6
+    monkeypatch.delenv("ATTN_TEST_STALL_PRODUCER")
+    assert torch.equal(cca.kv4_attention(q, c, i32([250]), ws=ws)[0], good)
+    assert torch.equal(cca.key_mass(qq, k, lse, chunks, ws=mws), want)
+    assert cca.attn_status(ws) == 0 and cca.attn_status(mws) == 0
+
+
 def test_attend_strided_queries_and_repeat():
     """Token-major queries, a view of wider rows, scores of one sharp maximum; the same bits each time."""
     rng = np.random.default_rng(9)
