@@ -177,13 +177,22 @@ def kv4_evict(cache: KV4Cache, lens, mass, keep: int, recent: int, out: KV4Cache
     and those with the highest mass, moved to the front of `out` in their order.
     Returns (lens_out, slots): int32 [B] and the source slots int32 [B, Hkv, keep]."""
     import torch
-    if out.device != cache.device or lens.device != cache.device or not 0 < keep <= out.cap or recent < 0:
-        raise AttnError("kv4_evict", ATTN_E_INVAL)
-    recent = min(int(recent), int(keep))
+    fn = "kv4_evict"
+    if out.device != cache.device or not 0 < keep <= out.cap or recent < 0:
+        raise AttnError(fn, ATTN_E_INVAL)
+    if ws is None:
+        ws = kv4_workspace(cache)
+    cache._check(fn, lens, cache.B, mass, mass_out, lens_out, ws)
     slots = torch.empty((cache.B, cache.Hkv, int(keep)), dtype=torch.int32, device=lens.device)
     if lens_out is None:
         lens_out = torch.empty_like(lens)
-    if ws is None:
-        ws = kv4_workspace(cache)
-    _lib.attn_kv4_evict(cache.desc, lens, mass, keep, recent, out.desc, lens_out, mass_out, slots, ws, stream)
+    else:
+        cache._check(fn, lens_out, cache.B)
+    ld = _lib._mass_ld(fn, cache.desc, mass)
+    ld_out = 0 if mass_out is None else _lib._mass_ld(fn, cache.desc, mass_out)
+    with _lib._on(lens):
+        _lib._check("attn_kv4_evict", _lib.lib().attn_kv4_evict(
+            cache._ref, lens.data_ptr(), mass.data_ptr(), ld, keep, min(int(recent), int(keep)), out._ref,
+            lens_out.data_ptr(), _lib._ptr(mass_out), ld_out, slots.data_ptr(), ws.data_ptr(),
+            ws.numel() * ws.element_size(), _lib._stream_of(stream, lens)))
     return lens_out, slots
