@@ -125,6 +125,25 @@ __device__ __forceinline__ bool item_ok(const MassItem& it, const MassArgs& a) {
     return 0 <= it.j0 && it.j0 < it.j1 && it.j1 - it.j0 <= 128 && it.j1 <= a.g.T && 0 <= it.c_lo && it.c_hi <= a.n;
 }
 
+// The MMA thread's instructions are what a block waits for: alone in its warp it issues
+// one in about ten cycles, and a trace of it showed 390 cycles for eight MMAs whose
+// descriptors were built one by one. So a tile's descriptor is built once; a step of 16
+// dims adds to its low word (the address field: 14 bits of 16 bytes each, which the
+// shared memory's 228 KB never carry out of).
+struct TileDesc {
+    uint32_t lo, hi;
+    __device__ __forceinline__ explicit TileDesc(uint32_t saddr) {
+        const uint64_t d = sdesc_sw128(saddr, 16, 1024);
+        lo = (uint32_t)d;
+        hi = (uint32_t)(d >> 32);
+    }
+    __device__ __forceinline__ uint64_t at(uint32_t bytes) const {
+        uint64_t d;
+        asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo + (bytes >> 4)), "r"(hi));
+        return d;
+    }
+};
+
 // ROWS rows x DT dims: boxes of 64 dims x 64 rows, dims in strides of 128 rows.
 template <int DT>
 __device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap* map, uint32_t bar, const TcMaps& mp, int row,
@@ -293,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t ks = kc % L::KST;
                 ok = mbar_wait(bar(L::B_KFULL + ks), (kc / L::KST) & 1, abort_flag, a.status, a.wait_ns);
                 if (!ok) break;
-                const uint32_t k0 = sbase + L::K_OFF + ks * L::TILE;
+                const TileDesc k0(sbase + L::K_OFF + ks * L::TILE);
                 bool bad = false;
                 ok = walk_blocks(a, item, G, qc, 1, 0, bad, [&](uint32_t q, int, int, int, int rows) {
                     const uint32_t qs = q % L::QST, sb = q % kBufs;
@@ -301,13 +320,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         !mbar_wait(bar(L::B_SEMPTY + sb), ((q / kBufs) & 1) ^ 1, abort_flag, a.status, a.wait_ns))
                         return false;
                     tc_fence_after();
-                    const uint32_t q0 = sbase + L::Q_OFF + qs * L::TILE;
+                    const TileDesc q0(sbase + L::Q_OFF + qs * L::TILE);
                     // as many columns as the block has rows, in steps of 16
                     const uint32_t id = idesc_bf16(128, (rows + 15) & ~15, 0, 0);
 #pragma unroll
                     for (int kk = 0; kk < DT / 16; ++kk) {
                         const uint32_t off = (kk >> 2) * (128 * 128) + (kk & 3) * 32;
-                        mma_ss(tmem + sb * kRows, sdesc_sw128(k0 + off, 16, 1024), sdesc_sw128(q0 + off, 16, 1024), id, kk > 0);
+                        mma_ss(tmem + sb * kRows, k0.at(off), q0.at(off), id, kk > 0);
                     }
                     mma_commit(bar(L::B_QEMPTY + qs));
                     mma_commit(bar(L::B_SFULL + sb));
@@ -533,7 +552,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int64_t begin = blockIdx.x * total / gridDim.x, end = (blockIdx.x + 1) * total / gridDim.x;
     // whether any row sees a key of the tile, and whether all rows see all of its keys
     auto seen_tile = [&](int j0) { return j0 < ch.q_end && j0 + 128 > ch.ctx_begin; };
-    uint32_t kc = 0, qc = 0, tc_ = 0, dealt = 0, mine = 0;      // key tiles, blocks, tiles, blocks of each group, of this one
+    uint32_t ks = 0, kp = 0;                                    // stage of the next key tile, and its parity
+    uint32_t qc = 0, turn = 0, dealt = 0, mine = 0;             // blocks; the next tile's group; blocks of each group, of this one
+    auto next_stage = [&]() {
+        if (++ks == (uint32_t)kst) {
+            ks = 0;
+            kp ^= 1;
+        }
+    };
+    auto next_turn = [&]() { turn = turn + 1 == kGroups ? 0 : turn + 1; };
+    const TileDesc qd(sbase);
     bool ok = true;
     for (int64_t x0 = begin; x0 < end;) {
         const int bh = (int)(x0 / tiles), first = (int)(x0 - (int64_t)bh * tiles);
@@ -569,21 +597,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < count && ok; ++i) {
                     const int j0 = (first + i) * 128;
                     if (!seen_tile(j0)) continue;
-                    const uint32_t s = kc % kst;
-                    ok = mbar_wait(bar(L::B_KEMPTY + s), ((kc / kst) & 1) ^ 1, abort_flag, a.status, a.wait_ns);
+                    ok = mbar_wait(bar(L::B_KEMPTY + ks), kp ^ 1, abort_flag, a.status, a.wait_ns);
                     if (!ok) break;
-                    mbar_expect_tx(bar(L::B_KFULL + s), L::TILE);
-                    load_rows<DT>(sbase + k_off + s * L::TILE, &tmk, bar(L::B_KFULL + s), mpkv, j0, 2, hk, b);
-                    ++kc;
+                    mbar_expect_tx(bar(L::B_KFULL + ks), L::TILE);
+                    load_rows<DT>(sbase + k_off + ks * L::TILE, &tmk, bar(L::B_KFULL + ks), mpkv, j0, 2, hk, b);
+                    next_stage();
                 }
             }
         } else if (warp == 1) {
             // ------------------------------------------------------------ MMA issuer
             if (elect_one()) {
-                for (int i = 0; i < count && ok; ++i, ++tc_) {
+                for (int i = 0; i < count && ok; ++i, next_turn()) {
                     if (!seen_tile((first + i) * 128)) continue;
-                    const uint32_t s = kc % kst, grp = tc_ % kGroups;
-                    ok = mbar_wait(bar(L::B_KFULL + s), (kc / kst) & 1, abort_flag, a.status, a.wait_ns);
+                    const uint32_t grp = turn;
+                    ok = mbar_wait(bar(L::B_KFULL + ks), kp, abort_flag, a.status, a.wait_ns);
+                    const TileDesc kd(sbase + k_off + ks * L::TILE);
                     for (int x = 0; x < nb && ok; ++x, ++qc) {
                         const uint32_t sb = qc % kBufs;
                         ok = mbar_wait(bar(L::B_SEMPTY + sb), ((qc / kBufs) & 1) ^ 1, abort_flag, a.status, a.wait_ns);
@@ -593,8 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int kk = 0; kk < DT / 16; ++kk) {
                             const uint32_t off = (kk >> 2) * (128 * 128) + (kk & 3) * 32;
-                            mma_ss(tmem + sb * 128, sdesc_sw128(sbase + k_off + s * L::TILE + off, 16, 1024),
-                                   sdesc_sw128(sbase + x * L::TILE + off, 16, 1024), id, kk > 0);
+                            mma_ss(tmem + sb * 128, kd.at(off), qd.at(off + x * L::TILE), id, kk > 0);
                         }
                         // a group's barriers in its own turn: at most kBufs of its blocks are ahead of it
                         const uint32_t m = dealt >> (8 * grp) & 3u;
@@ -602,8 +629,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mma_commit(bar(L::B_SFULL + grp * kBufs + m));
                     }
                     if (!ok) break;
-                    mma_commit(bar(L::B_KEMPTY + s));
-                    ++kc;
+                    mma_commit(bar(L::B_KEMPTY + ks));
+                    next_stage();
                 }
             }
         } else if (warp >= 4) {
@@ -612,10 +639,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
             const float c = a.g.scale * kLog2e;
             const float2 c2 = make_float2(c, c);
-            for (int i = 0; i < count && ok; ++i, ++tc_) {
+            for (int i = 0; i < count && ok; ++i, next_turn()) {
                 const int j0 = (first + i) * 128, j = j0 + key;
                 const bool sees = seen_tile(j0);
-                if (tc_ % kGroups != (uint32_t)grp) {
+                if (turn != (uint32_t)grp) {
                     if (sees) qc += nb;
                     continue;
                 }
