@@ -20,6 +20,11 @@
 //   warp 3      adds up the groups' sums of a finished item, in order, and writes them
 // Per block 2 * 128 * 128 * D FLOP (512 cycles of an SM at D = 128) stand against
 // 128 * 128 exponentials (512 cycles at 32 a cycle): both pipes are needed whole.
+// Measured: 8192 tokens of 32 heads of 128 dims 245 us (1120 TFLOP/s, 1060 cycles a
+// block), 32768 tokens 3.23 ms (1360 TFLOP/s); both pipes are 53% busy. Copies without
+// the exponentials (195 us) and also without most products (154 to 179 us) show that the
+// hand-over of a block from pipe to pipe is what is left; three groups hide more of it
+// than two (266 us) and than four on fewer registers (299 us).
 //
 // Sums: 128 weights of a block in four fp32 chains, blocks with a compensated sum
 // (Kahan), so that a million rows lose no more than a block does.
@@ -494,8 +499,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 // an equal stretch of the (head, key tile) list; at the start of each head all threads
 // lay its queries out as TMA would (128-byte swizzle), with -lse log2 e and the token of
 // each row. A key tile is one group's: its rows' weights are summed by one thread in
-// order. The keys' bytes are the bound: 32 KB at D = 128 are 1390 cycles of an SM's share
-// of the memory rate, two blocks of products and exponentials 1024.
+// order. The keys' bytes are the floor: 32 KB at D = 128 are 1390 cycles of an SM's share
+// of the memory rate, two blocks of products and exponentials 1024. Measured: 64 rows of 4
+// heads over 128K keys of 8 key/value heads 85 us (3.2 TB/s, 2500 cycles a tile; 158 us with
+// the general kernel, which brings the queries from L2 again for every tile), one row 51 us
+// (5.2 TB/s). A trace shows the MMA thread busy all the time at 250 to 450 cycles a step
+// (wait, eight products, commit) and the groups waiting for it a third of theirs; a second
+// MMA thread for every other tile gained 2% and was not kept.
 template <int DT>
 struct WinLayout {
     static constexpr int TILE = 128 * DT * 2;

@@ -30,6 +30,12 @@
 // holds an eighth, and two slots' words are interleaved by two logical operations
 // into bytes that convert to (slot a, slot b) pairs.
 //
+// Measured (128 dims, 4 or 5 rows a head): 1M slots of 8 heads 225 us (5.4 TB/s, 79% of
+// the copy rate), 4 x 128K slots 118 us, 1000 slots 9.3 us. 279 instructions for 16 slots
+// of keys and values (128 of them conversions and multiplications) keep the issue slots
+// 56% and the ALU pipe 49% busy with four warps a scheduler; three blocks an SM are 4%
+// slower, five or more spill or wait, 16 slots a step 22% slower.
+//
 // Softmax weights are rounded to fp16 too, after a factor 2^11 and with a running
 // maximum that may lag by up to 2^4: weights stay below 2^15, and those under 2^-35
 // of the row's largest are flushed (1M of them would be 2^-15 of the sum). l is

