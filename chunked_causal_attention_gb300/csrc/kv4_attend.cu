@@ -796,6 +796,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Kv4AttendArg
     // every block waits for the kernel before, so that this one does not end ahead of it
     if (rt * unit_rows + (blockIdx.x - u * groups) * ROWS >= sp.R) {            // no row of the block is one
         grid_wait();
+        grid_go();
         return;
     }
     const int32_t n = slots_of(a, b);
@@ -809,6 +810,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Kv4AttendArg
         range[1] = nt ? block_of(first + nt - 1, total, blocks) : 0;
     }
     grid_wait();                                        // the split kernel's partials
+    grid_go();
     __syncthreads();
     const int c0 = range[0], c1 = range[1];
     const bool row = rr < sp.R, none = n - a.g.T + 1 + i <= 0;
@@ -912,6 +914,7 @@ __global__ void __launch_bounds__(kMassThreads) mass_kernel(const Kv4AttendArgs 
     const int j0 = (blockIdx.x - bh * chunks) * kMassThreads * kMassSlots + threadIdx.x;
     if (j0 - (int)threadIdx.x >= n) {
         grid_wait();
+        grid_go();
         return;
     }
     float sum[kMassSlots], base[kMassSlots];
@@ -922,6 +925,7 @@ __global__ void __launch_bounds__(kMassThreads) mass_kernel(const Kv4AttendArgs 
         base[x] = a.mass_in && j0 + x * kMassThreads < n ? a.mass_in[at + x * kMassThreads] : 0.f;
     }
     grid_wait();                                        // scores and sums
+    grid_go();
     for (int rt = 0; rt < sp.RT; ++rt) {
         __syncthreads();
         if (threadIdx.x < sp.pitch) {
