@@ -10,7 +10,7 @@ from __future__ import annotations
 
 from typing import Optional, Sequence
 
-from ._lib import (AttnError, EXPORTS, KV4_ATTEND, KV4_ATTEND_MASS, KV4_ROWS, PASS_BWD, PASS_BWD_CHUNK, PASS_FWD,
+from ._lib import (_alloc_on, AttnError, EXPORTS, KV4_ATTEND, KV4_ATTEND_MASS, KV4_ROWS, PASS_BWD, PASS_BWD_CHUNK, PASS_FWD,
                    PASS_MASS, PLAN_FLOPS, PLAN_FLOPS_RESPLIT_EDGES,
                    PLAN_UNIFORM, attn_bwd, attn_bwd_chunk, attn_bwd_dq, attn_bwd_prep, attn_bwd_tiles, attn_fwd,
                    attn_fwd_merge, attn_fwd_noalloc, attn_fwd_tiles, attn_key_mass, attn_kv4_attend, attn_kv4_cache,
@@ -128,10 +128,11 @@ def key_mass(q, k, lse, chunks: Sequence, scale: Optional[float] = None, packed:
     over the last rows alone give the weights as those rows see them."""
     import torch
     shape = shape_of(q, scale, packed, k)
-    if mass_out is None:
-        mass_out = torch.empty((shape.B, shape.Hkv or shape.H, shape.T), dtype=torch.float32, device=q.device)
-    if ws is None:
-        ws = workspace(shape, chunks, PASS_MASS, q.device)
+    with _alloc_on(stream, q.device):
+        if mass_out is None:
+            mass_out = torch.empty((shape.B, shape.Hkv or shape.H, shape.T), dtype=torch.float32, device=q.device)
+        if ws is None:
+            ws = workspace(shape, chunks, PASS_MASS, q.device)
     attn_key_mass(q, k, lse, chunks, shape, mass_in, mass_out, ws, stream)
     return mass_out
 

@@ -415,6 +415,15 @@ def _stream_of(stream, t) -> Optional[int]:
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
+def _alloc_on(stream, device):
+    """The given stream (None: as it is) as torch's current one, for what a call allocates: a workspace
+    zeroed and given back on another stream than its kernels' would be written while they run."""
+    if stream is None or device.type != "cuda":
+        return _STAY
+    import torch
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device) if isinstance(stream, int) else stream)
+
+
 def _same_device(fn: str, first, *others) -> None:
     """All tensors (None passes) on the device of the first, a GPU."""
     dev = first.device

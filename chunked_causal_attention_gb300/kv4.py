@@ -105,7 +105,8 @@ def kv4_store(cache: KV4Cache, k, v, pos, cu_seqlens=None, ws=None, stream=None)
     """Store rows: k, v bf16 [B, Hkv, T, D], row t of sequence b in slot pos[b] + t;
     with cu_seqlens (int32 [B + 1]) packed [T, Hkv, D], each sequence's tokens from pos[b] on."""
     if ws is None:
-        ws = kv4_workspace(cache)
+        with _lib._alloc_on(stream, cache.device):
+            ws = kv4_workspace(cache)
     _, ref = cache._shape(k, 1.0, cu_seqlens is not None)
     _rows_checks("kv4_store", cache, k, v, pos, cu_seqlens, ws)
     with _lib._on(k):
@@ -129,12 +130,13 @@ def kv4_load(cache: KV4Cache, pos, T: int, cu_seqlens=None, k=None, v=None, ws=N
     packed [T, Hkv, D]. k and v may be given (rows outside the cache stay as they were)."""
     import torch
     shape = (T, cache.Hkv, cache.D) if cu_seqlens is not None else (cache.B, cache.Hkv, T, cache.D)
-    if k is None:
-        k = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
-    if v is None:
-        v = torch.empty_like(k)
-    if ws is None:
-        ws = kv4_workspace(cache)
+    with _lib._alloc_on(stream, cache.device):
+        if k is None:
+            k = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
+        if v is None:
+            v = torch.empty_like(k)
+        if ws is None:
+            ws = kv4_workspace(cache)
     _, ref = cache._shape(k, 1.0, cu_seqlens is not None)
     _rows_checks("kv4_load", cache, k, v, pos, cu_seqlens, ws)
     if k.shape != shape:
@@ -154,16 +156,18 @@ def kv4_attention(q, cache: KV4Cache, lens, scale: Optional[float] = None, mass_
     import torch
     shape, ref = cache._shape(q, scale, False)
     if ws is None:
-        ws = kv4_workspace(cache, q, mass_out is not None)
+        with _lib._alloc_on(stream, cache.device):
+            ws = kv4_workspace(cache, q, mass_out is not None)
     cache._check("kv4_attention", lens, cache.B, q, ws, mass_in, mass_out)
     if q.dtype is not torch.bfloat16:
         raise AttnError("kv4_attention", ATTN_E_INVAL)
     ld = 0
     if mass_in is not None or mass_out is not None:
         ld = _lib._mass_ld("kv4_attention", cache.desc, mass_in, mass_out)
-    o = torch.empty_like(q) if q.is_contiguous() else \
-        torch.empty_strided(q.shape, q.stride(), dtype=q.dtype, device=q.device)
-    lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+    with _lib._alloc_on(stream, q.device):
+        o = torch.empty_like(q) if q.is_contiguous() else \
+            torch.empty_strided(q.shape, q.stride(), dtype=q.dtype, device=q.device)
+        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
     with _lib._on(q):
         _lib._check("attn_kv4_attend", _lib.lib().attn_kv4_attend(
             q.data_ptr(), ref, cache._ref, lens.data_ptr(), o.data_ptr(), lse.data_ptr(), _lib._ptr(mass_in),
@@ -181,13 +185,15 @@ def kv4_evict(cache: KV4Cache, lens, mass, keep: int, recent: int, out: KV4Cache
     if out.device != cache.device or not 0 < keep <= out.cap or recent < 0:
         raise AttnError(fn, ATTN_E_INVAL)
     if ws is None:
-        ws = kv4_workspace(cache)
+        with _lib._alloc_on(stream, cache.device):
+            ws = kv4_workspace(cache)
     cache._check(fn, lens, cache.B, mass, mass_out, lens_out, ws)
-    slots = torch.empty((cache.B, cache.Hkv, int(keep)), dtype=torch.int32, device=lens.device)
-    if lens_out is None:
-        lens_out = torch.empty_like(lens)
-    else:
+    if lens_out is not None:
         cache._check(fn, lens_out, cache.B)
+    with _lib._alloc_on(stream, lens.device):
+        slots = torch.empty((cache.B, cache.Hkv, int(keep)), dtype=torch.int32, device=lens.device)
+        if lens_out is None:
+            lens_out = torch.empty_like(lens)
     ld = _lib._mass_ld(fn, cache.desc, mass)
     ld_out = 0 if mass_out is None else _lib._mass_ld(fn, cache.desc, mass_out)
     with _lib._on(lens):

@@ -702,3 +702,42 @@ def test_calls_on_two_streams_and_wrong_sizes():
                 lambda: cca.kv4_evict(c, lens, torch.zeros(2, 2, 2048, device="cuda"), 16, 2, c)):
         with pytest.raises(cca.AttnError):
             bad()
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_a_given_stream_holds_what_a_call_allocates(raw, monkeypatch):
+    """With stream= alone, workspaces and outputs are allocated (and zeroed, and given back) on that stream."""
+    rng = np.random.default_rng(47)
+    c, d = random_cache(2, 2, 1024, 64, 48), cca.kv4_cache(2, 2, 256, 64, k_scale=0.5, v_scale=2.0)
+    q, lens = bf16(rng, 2, 4, 1, 64), i32([1000, 30])
+    mass = torch.rand(2, 2, 1024, device="cuda")
+    p, rows, zero = bf16(rng, 2, 4, 300, 64), bf16(rng, 2, 2, 9, 64), i32([0, 16])
+    chunks = [(0, 300, 0, 0)]
+    _, p_lse = cca.forward(p, p, p, chunks)
+    side = torch.cuda.Stream()
+    seen = []
+
+    def watched(f):
+        def g(*a, **kw):
+            seen.append(torch.cuda.current_stream().cuda_stream)
+            return f(*a, **kw)
+        return g
+
+    def calls(**kw):
+        cca.kv4_store(c, rows, rows, zero, **kw)
+        k, v = cca.kv4_load(c, zero, 9, **kw)
+        o, lse = cca.kv4_attention(q, c, lens, **kw)
+        n, slots = cca.kv4_evict(c, lens, mass, 200, 8, d, **kw)
+        return k, v, o, lse, n, slots, cca.key_mass(p, p, p_lse, chunks, **kw)
+
+    want = calls()
+    torch.cuda.synchronize()
+    monkeypatch.setattr(cca.kv4, "kv4_workspace", watched(cca.kv4.kv4_workspace))
+    monkeypatch.setattr(cca, "workspace", watched(cca.workspace))
+    here = torch.cuda.current_stream().cuda_stream
+    got = calls(stream=side.cuda_stream if raw else side)
+    assert torch.cuda.current_stream().cuda_stream == here
+    torch.cuda.synchronize()
+    assert seen == [side.cuda_stream] * 5
+    for x, y in zip(got, want):
+        assert torch.equal(x, y)
