@@ -56,7 +56,7 @@ struct Layout {
     static constexpr int LSE_OFF = Q_OFF + QST * TILE;            // [buffer][128] floats
     static constexpr int PART_OFF = LSE_OFF + kBufs * 128 * 4;   // [2][group][128] floats
     static constexpr int ITEM_OFF = PART_OFF + 2 * kGroups * 128 * 4;           // [2] items handed out
-    static constexpr int TAG_OFF = ITEM_OFF + 2 * 16;                            // [buffer] block whose lse it holds, plus 1
+    static constexpr int TAG_OFF = ITEM_OFF + 2 * 16;                            // [buffer] tag of the block whose lse it holds
     static constexpr int BAR_OFF = TAG_OFF + kBufs * 4;
     static constexpr int B_KFULL = 0, B_KEMPTY = B_KFULL + KST;
     static constexpr int B_QFULL = B_KEMPTY + KST, B_QEMPTY = B_QFULL + QST;
@@ -109,12 +109,18 @@ __device__ __forceinline__ bool seen(const MassArgs& a, const MassItem& it) {
     return false;
 }
 
-// Wait, for a whole warp, until *tag is `want`; bounded like an mbarrier wait.
+// The tag of block q's log-sum-exps in a buffer, the lowest bit set where a row of the
+// block has none (-inf). Such a row weighs nothing whatever its query holds, and
+// 2^(s c - inf) is 0 only while the score s is not NaN or +inf: blocks with one select.
+__device__ __forceinline__ uint32_t tag_of(uint32_t q, bool without) { return 2 * (q + 1) + (without ? 1u : 0u); }
+__device__ __forceinline__ bool same_block(uint32_t tag, uint32_t want) { return ((tag ^ want) & ~1u) == 0; }
+
+// Wait, for a whole warp, until *tag is the block's of `want`; bounded like an mbarrier wait.
 __device__ __noinline__ bool tag_wait(volatile uint32_t* tag, uint32_t want, volatile int* abort, uint32_t* status,
                                       uint64_t limit_ns) {
     const uint64_t t0 = globaltimer();
     bool ok = true;
-    while (ok && *tag != want) {
+    while (ok && !same_block(*tag, want)) {
         if (*abort) {
             ok = false;
         } else if (globaltimer() - t0 > limit_ns) {
@@ -370,7 +376,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float* dst = reinterpret_cast<float*>(sm + L::LSE_OFF) + sb * 128;
 #pragma unroll
                 for (int y = 0; y < 4; ++y) dst[32 * y + lane] = x[y];
-                if (lane == 0) s_tag[sb] = q + 1;
+                // x is -inf past the block's rows too; those are told apart by their number
+                bool none = false;
+#pragma unroll
+                for (int y = 0; y < 4; ++y) none |= 32 * y + lane < n && x[y] == -INFINITY;
+                none = __any_sync(0xffffffffu, none);
+                if (lane == 0) s_tag[sb] = tag_of(q, none);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(L::B_SFULL + sb));
                 return true;
@@ -398,12 +409,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // A parity tells neighbouring phases apart only, and a group that had no block for a while may
                 // come before the phase ahead of its own has ended: the buffer's tag names the block
                 // whose lse it holds, written once the block before it there has been summed.
-                if (__any_sync(0xffffffffu, s_tag[sb] != q + 1) && !tag_wait(s_tag + sb, q + 1, abort_flag, a.status, a.wait_ns)) return false;
+                uint32_t tag = s_tag[sb];
+                if (__any_sync(0xffffffffu, !same_block(tag, tag_of(q, false)))) {
+                    if (!tag_wait(s_tag + sb, tag_of(q, false), abort_flag, a.status, a.wait_ns)) return false;
+                    tag = s_tag[sb];                         // stays until this block has been summed
+                }
                 if (!mbar_wait_warp(bar(L::B_SFULL + sb), (q / kBufs) & 1, abort_flag, a.status, a.wait_ns)) return false;
                 tc_fence_after();
                 // this key is seen by the columns [lo, n)
                 const int lo = ctx <= j ? max(0, j - row0) : kRows;
-                const bool edge = n < kRows || row0 < item.j1 - 1 || ctx > item.j0;
+                const bool edge = n < kRows || row0 < item.j1 - 1 || ctx > item.j0 || (tag & 1u);
                 const uint32_t sa = tmem + lane_addr + sb * kRows;
                 float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll 1
@@ -425,8 +440,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int y = 0; y < 32; ++y) {
                                 const int col = 32 * x + y;
-                                const float e = fmaf(__uint_as_float(r[x][y]), c, lse[half + col]);
-                                const float p = col >= from && col < to ? ex2(e) : 0.f;
+                                const float l = lse[half + col], e = fmaf(__uint_as_float(r[x][y]), c, l);
+                                const float p = col >= from && col < to && l != -INFINITY ? ex2(e) : 0.f;
                                 if (y & 1) acc[(y >> 1) & 1].y += p; else acc[(y >> 1) & 1].x += p;
                             }
                     }
