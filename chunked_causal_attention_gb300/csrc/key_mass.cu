@@ -449,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive(bar(L::B_LEMPTY + sb));
                 const float part = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
                 const float y = __fsub_rn(part, err), t = __fadd_rn(sum, y);
-                err = __fsub_rn(__fsub_rn(t, sum), y);
+                err = t == INFINITY ? 0.f : __fsub_rn(__fsub_rn(t, sum), y);   // an infinite weight stays one: no inf - inf
                 sum = t;
                 return true;
             });

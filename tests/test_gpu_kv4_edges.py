@@ -1,5 +1,5 @@
 """GPU tests of the 4-bit cache and of the key mass where test_gpu_kv4.py has none: rows
-without a log-sum-exp whose queries are not finite. Tolerances are those derived there."""
+without a log-sum-exp whose queries are not finite, keys that are not. Tolerances are those derived there."""
 import math
 
 import numpy as np
@@ -54,3 +54,45 @@ def test_key_mass_after_a_forward_over_a_nan_query():
     _, lse = cca.forward(bad, k, k, chunks)
     assert lse[0, 0, 650] == -math.inf and int(lse.isfinite().sum()) == 2 * 900 - 1
     check_mass(q, k, lse, chunks, cca.key_mass(bad, k, lse, chunks), 128 ** -0.5)
+
+
+def log_sum_exps(q, k, chunks, scale):
+    """lse [B, H, T] of the chunks' rows in 64 bits, rounded once (zero elsewhere)."""
+    B, H, T, _ = q.shape
+    lse = torch.zeros(B, H, T, device="cuda")
+    for a, b, ctx, _ in chunks:
+        t = torch.arange(a, b, device="cuda")[:, None]
+        seen = torch.arange(ctx, b, device="cuda")[None, :] <= t
+        for h in range(H):
+            s = q[:, h, a:b].double() @ k[:, h * k.shape[1] // H, ctx:b].double().transpose(-1, -2) * scale
+            lse[:, h, a:b] = torch.logsumexp(s.masked_fill(~seen, -math.inf), -1)
+    return lse
+
+
+# rows of all heads of a group (w * H / Hkv): 200, 250 (a half of 64 columns ends in rows past the last), 15, 128, 300, 1
+WINDOWS = [(128, 4, 1, 50), (64, 10, 2, 50), (80, 3, 1, 5), (256, 2, 1, 64), (40, 6, 2, 100), (128, 2, 2, 1)]
+
+
+@pytest.mark.parametrize("D,H,Hkv,w", WINDOWS)
+@pytest.mark.parametrize("pieces", [2])
+def test_key_mass_of_keys_that_are_not_finite(D, H, Hkv, w, pieces):
+    """A key's infinity or NaN is its own: -inf scores weigh 0, +inf ones inf, NaN ones NaN, whichever kernel
+    the number of chunks picks, and the other keys' weights stay."""
+    rng = np.random.default_rng(3 * D + w)
+    L, scale = 3001, D ** -0.5
+    q, k = 2 * bf16(rng, 1, H, L, D), bf16(rng, 1, Hkv, L, D)
+    q[..., 0] = q[..., 0].abs() + 0.25
+    low, high, nan = [0, 5, 130, 1000, 2047, 2 * L // 3], [6, 131, 1001], [9, 1002]
+    w = max(w, pieces)
+    cut = L - w + w // 2
+    chunks = [(L - w, L, 0, 0)] if pieces == 1 else [(L - w, cut, 0, 0), (cut, L, 0, 0)]
+    lse = log_sum_exps(q, k, chunks, scale)
+    want = cca.key_mass(q, k, lse, chunks)
+    check_mass(q, k, lse, chunks, want, scale)
+    bad = k.clone()
+    bad[:, :, low, 0], bad[:, :, high, 0], bad[:, :, nan, D - 1] = -math.inf, math.inf, math.nan
+    got = cca.key_mass(q, bad, lse, chunks)
+    assert (got[..., low] == 0).all() and (got[..., high] == math.inf).all() and got[..., nan].isnan().all()
+    other = torch.ones(L, dtype=torch.bool)
+    other[low + high + nan] = False
+    assert torch.equal(got[..., other], want[..., other])
