@@ -531,7 +531,8 @@ struct WinLayout {
     static constexpr int B_DRAIN = B_SEMPTY + kBufs, NBAR = B_DRAIN + 1;
     static constexpr int BAR_BYTES = NBAR * 8 + 16;
     static int key_stages(int nb) { return std::min(MAX_KST, (212 * 1024 - nb * (TILE + 1024)) / TILE); }
-    static size_t bytes(int nb, int kst) { return (size_t)(nb + kst) * TILE + nb * 1024 + BAR_BYTES + 1024; }
+    // the tiles; -lse, token and flags (4 bytes of 32 rows each) of the rows; barriers; alignment
+    static size_t bytes(int nb, int kst) { return (size_t)(nb + kst) * TILE + nb * 1028 + BAR_BYTES + 1024 + 8; }
 };
 
 template <int DT>
@@ -544,9 +545,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t sbase = smem_u32(sm), k_off = nb * L::TILE;
     float* s_lse = reinterpret_cast<float*>(sm + (size_t)(nb + kst) * L::TILE);
     int32_t* s_tok = reinterpret_cast<int32_t*>(s_lse + nb * 128);
-    const uint32_t bar0 = smem_u32(s_tok + nb * 128);
+    // a byte for 32 rows, set where one of them weighs nothing
+    uint8_t* s_none = reinterpret_cast<uint8_t*>(s_tok + nb * 128);
+    uint8_t* s_bar = s_none + ((nb * 4 + 7) & ~7);
+    const uint32_t bar0 = smem_u32(s_bar);
     auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
-    uint8_t* misc = reinterpret_cast<uint8_t*>(s_tok + nb * 128) + L::NBAR * 8;
+    uint8_t* misc = s_bar + L::NBAR * 8;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 4);
     const int tid = threadIdx.x, warp = tid >> 5;
@@ -612,7 +616,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 l = l == -INFINITY ? l : -l * kLog2e;
             }
             s_lse[p] = l;
-            s_tok[p] = p < R ? t : -1;
+            // 2^(s c - inf) is 0 only while the score s is not NaN or +inf, which the zero queries of a row
+            // past the last make of a key that is not finite, and a row without a sum may be: no key is theirs
+            s_tok[p] = l == -INFINITY ? -1 : t;
+            const bool none = __any_sync(0xffffffffu, l == -INFINITY);
+            if ((tid & 31) == 0) s_none[p >> 5] = none;
         }
         fence_proxy_async_smem();
         __syncthreads();
@@ -664,6 +672,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
             const float c = a.g.scale * kLog2e;
             const float2 c2 = make_float2(c, c);
+            uint32_t without = 0;                       // a bit for 64 rows of the head, set where one weighs nothing
+            for (int y = 0; y < 2 * nb; ++y)
+                without |= (reinterpret_cast<const uint16_t*>(s_none)[y] ? 1u : 0u) << y;
             for (int i = 0; i < count && ok; ++i, next_turn()) {
                 const int j0 = (first + i) * 128, j = j0 + key;
                 const bool sees = seen_tile(j0);
@@ -703,7 +714,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tc_fence_before();
                             mbar_arrive(bar(L::B_SEMPTY + sb));          // the buffer has been read
                         }
-                        if (left >= 64 && !edge) {
+                        const bool pick = edge || (without >> (2 * x + half / 64) & 1u);
+                        if (left >= 64 && !pick) {
                             weigh64(r, lse, c2, acc);
                         } else {
                             const int32_t* tok = s_tok + 128 * x + half;
@@ -713,7 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                                 for (int z = 0; z < 16; ++z) {
                                     const float e = fmaf(__uint_as_float(r[y >> 1][16 * (y & 1) + z]), c, lse[16 * y + z]);
-                                    const bool on = !edge || (j >= ch.ctx_begin && j <= tok[16 * y + z]);
+                                    const bool on = !pick || (j >= ch.ctx_begin && j <= tok[16 * y + z]);
                                     const float p = on ? ex2(e) : 0.f;
                                     if (z & 1) acc[(z >> 1) & 1].y += p; else acc[(z >> 1) & 1].x += p;
                                 }

@@ -74,7 +74,22 @@ WINDOWS = [(128, 4, 1, 50), (64, 10, 2, 50), (80, 3, 1, 5), (256, 2, 1, 64), (40
 
 
 @pytest.mark.parametrize("D,H,Hkv,w", WINDOWS)
-@pytest.mark.parametrize("pieces", [2])
+def test_key_mass_of_a_window_with_rows_without_lse_that_are_not_finite(D, H, Hkv, w):
+    rng = np.random.default_rng(D + w)
+    L = 3001
+    q, k = 2 * bf16(rng, 2, H, L, D), bf16(rng, 2, Hkv, L, D)
+    chunks = [(L - w - 3, L - 3, 7, 0)]
+    lse = log_sum_exps(q, k, chunks, D ** -0.5)
+    rows = [L - 4 - i for i in range(0, w, 7)]
+    for i, t in enumerate(rows):
+        lse[:, i % H, t] = -math.inf
+    want = cca.key_mass(q, k, lse, chunks)
+    check_mass(q, k, lse, chunks, want, D ** -0.5)
+    assert torch.equal(cca.key_mass(unset_rows(q, rows), k, lse, chunks), want)
+
+
+@pytest.mark.parametrize("D,H,Hkv,w", WINDOWS)
+@pytest.mark.parametrize("pieces", [1, 2])
 def test_key_mass_of_keys_that_are_not_finite(D, H, Hkv, w, pieces):
     """A key's infinity or NaN is its own: -inf scores weigh 0, +inf ones inf, NaN ones NaN, whichever kernel
     the number of chunks picks, and the other keys' weights stay."""
