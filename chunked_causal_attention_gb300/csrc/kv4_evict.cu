@@ -309,7 +309,9 @@ cudaError_t launch_choose(const Kv4EvictArgs& a, cudaStream_t s) {
     const int tiles = (a.src.cap + kChunk - 1) / kChunk;
     const int smem = std::min((tiles + blocks - 1) / blocks * kChunk, kHeld) * 4;
     if (smem > 40 * 1024) {                      // 48 KB with the static part is what a block may have without asking
-        const cudaError_t e = cudaFuncSetAttribute(choose_kernel<THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        // always the most that any call takes: the limit is the function's, and a call of another thread may be
+        // between its own limit and its launch
+        const cudaError_t e = cudaFuncSetAttribute(choose_kernel<THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kHeld * 4);
         if (e != cudaSuccess) return e;
     }
     return launch_early(choose_kernel<THREADS>, dim3((unsigned)(BH * blocks)), THREADS, smem, blocks, s, a, (int32_t)blocks);

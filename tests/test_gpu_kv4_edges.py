@@ -1,6 +1,9 @@
 """GPU tests of the 4-bit cache and of the key mass where test_gpu_kv4.py has none: rows
-without a log-sum-exp whose queries are not finite, keys that are not. Tolerances are those derived there."""
+without a log-sum-exp whose queries are not finite, keys that are not, calls of several
+threads at once. Tolerances are those derived there."""
+import ctypes
 import math
+import threading
 
 import numpy as np
 import pytest
@@ -8,7 +11,7 @@ import torch
 
 import chunked_causal_attention_gb300 as cca
 
-from test_gpu_kv4 import MASS_PLANS, bf16, built, check_mass
+from test_gpu_kv4 import MASS_PLANS, bf16, built, check_mass, i32, random_cache
 
 pytestmark = pytest.mark.gpu
 
@@ -111,3 +114,45 @@ def test_key_mass_of_keys_that_are_not_finite(D, H, Hkv, w, pieces):
     other = torch.ones(L, dtype=torch.bool)
     other[low + high + nan] = False
     assert torch.equal(got[..., other], want[..., other])
+
+
+# ------------------------------------------------------------------ calls of several threads at once
+
+def at_once(*calls, times):
+    """Each call (of a stream's handle, returning a status) many times in a thread of its own, on a stream of its
+    own; the statuses that are not ATTN_OK."""
+    bad, start = [], threading.Barrier(len(calls))
+    torch.cuda.synchronize()
+
+    def work(call, stream):
+        start.wait()
+        for _ in range(times):
+            status = call(stream.cuda_stream)
+            if status:
+                bad.append(status)
+
+    threads = [threading.Thread(target=work, args=(c, torch.cuda.Stream())) for c in calls]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    return bad
+
+
+def test_evictions_of_two_threads():
+    """Caches of different capacity ask for different amounts of shared memory in the same kernel. The C calls
+    themselves, on short sequences, so that the threads are in them most of the time."""
+    calls, results, fn = [], [], cca.lib().attn_kv4_evict
+    for cap in (300000, 90000):
+        src, dst = random_cache(1, 1, cap, 8, cap), cca.kv4_cache(1, 1, 512, 8, k_scale=0.5, v_scale=2.0)
+        mass, lens, out = torch.rand(1, 1, cap, device="cuda"), i32([600]), i32([0])
+        slots, ws = torch.empty(1, 1, 500, dtype=torch.int32, device="cuda"), cca.kv4_workspace(src)
+        want = cca.kv4_evict(src, lens, mass, 500, 3, dst)[1]
+        args = (ctypes.byref(src.desc), lens.data_ptr(), mass.data_ptr(), cap, 500, 3, ctypes.byref(dst.desc),
+                out.data_ptr(), None, 0, slots.data_ptr(), ws.data_ptr(), ws.numel())
+        calls.append(lambda s, a=args: fn(*a, s))
+        results.append((slots, want, ws, src, dst, mass, lens, out))       # args holds addresses only
+    assert at_once(*calls, times=20000) == []
+    for slots, want, ws, *_ in results:
+        assert torch.equal(slots, want) and cca.attn_status(ws) == 0
