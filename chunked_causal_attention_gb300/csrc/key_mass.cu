@@ -532,6 +532,11 @@ struct WinLayout {
     static constexpr int BAR_BYTES = NBAR * 8 + 16;
     static int key_stages(int nb) { return std::min(MAX_KST, (212 * 1024 - nb * (TILE + 1024)) / TILE); }
     // the tiles; -lse, token and flags (4 bytes of 32 rows each) of the rows; barriers; alignment
+    static size_t most() {
+        size_t m = 0;
+        for (int nb = 1; nb <= MAX_NB; ++nb) m = std::max(m, bytes(nb, key_stages(nb)));
+        return m;
+    }
     static size_t bytes(int nb, int kst) { return (size_t)(nb + kst) * TILE + nb * 1028 + BAR_BYTES + 1024 + 8; }
 };
 
@@ -776,7 +781,9 @@ cudaError_t launch_window(const MassArgs& a, const attn_chunk& ch, cudaStream_t 
     if (!make_tile_map(&mk, a.k, a.g.kv(), mpkv, kBoxRows)) return cudaErrorInvalidValue;
     const int nb = ((ch.q_end - ch.q_begin) * (a.g.H / a.g.Hkv) + 127) / 128, kst = L::key_stages(nb);
     const size_t smem = L::bytes(nb, kst);
-    cudaError_t e = cudaFuncSetAttribute(key_mass_window_kernel<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // always the most that any call takes: the limit is the function's, and a call of another thread may be
+    // between its own limit and its launch
+    cudaError_t e = cudaFuncSetAttribute(key_mass_window_kernel<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::most());
     if (e != cudaSuccess) return e;
     const int64_t total = (int64_t)a.g.B * a.g.Hkv * ((a.g.T + 127) / 128);
     const int grid = (int)std::min<int64_t>(total, device_sm_count());

@@ -10,6 +10,7 @@ import pytest
 import torch
 
 import chunked_causal_attention_gb300 as cca
+from chunked_causal_attention_gb300 import _lib
 
 from test_gpu_kv4 import MASS_PLANS, bf16, built, check_mass, i32, random_cache
 
@@ -156,3 +157,23 @@ def test_evictions_of_two_threads():
     assert at_once(*calls, times=20000) == []
     for slots, want, ws, *_ in results:
         assert torch.equal(slots, want) and cca.attn_status(ws) == 0
+
+
+def test_window_masses_of_two_threads():
+    """Windows of different length ask for different amounts of shared memory in the same kernel."""
+    calls, results, fn = [], [], cca.lib().attn_key_mass
+    for w in (1, 250):
+        rng = np.random.default_rng(w)
+        q, k = bf16(rng, 1, 2, 1024, 64), bf16(rng, 1, 1, 1024, 64)
+        chunks = [(1024 - w, 1024, 0, 0)]
+        lse = log_sum_exps(q, k, chunks, 0.125)
+        ws, shape, out = cca.key_mass_workspace(q, k, chunks), cca.shape_of(q, None, False, k), torch.zeros(1, 1, 1024, device="cuda")
+        want = cca.key_mass(q, k, lse, chunks)
+        arr, n = _lib.chunk_array(chunks)
+        args = (q.data_ptr(), k.data_ptr(), lse.data_ptr(), arr, n, ctypes.byref(shape), None, out.data_ptr(),
+                ws.data_ptr(), ws.numel())
+        calls.append(lambda s, a=args: fn(*a, s))
+        results.append((out, want, ws, q, k, lse, shape))
+    assert at_once(*calls, times=20000) == []
+    for out, want, ws, *_ in results:
+        assert torch.equal(out, want) and cca.attn_status(ws) == 0
