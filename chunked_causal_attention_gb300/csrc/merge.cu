@@ -337,7 +337,10 @@ cudaError_t launch_fwd_merge(const MergeArgs& a, cudaStream_t s) {
     const size_t smem = (size_t)a.bulk_parts * RB * a.g.D * sizeof(float);   // up to 64 KB
     auto kern = a.g.D > 128 ? (np == 2 ? merge_kernel<2, 2> : merge_kernel<2, kBulkParts>)
                             : (np == 2 ? merge_kernel<1, 2> : merge_kernel<1, kBulkParts>);
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // always the most that any call of this instantiation takes: the limit is the function's, and a call of
+    // another thread may be between its own limit and its launch
+    const int most = np * RB * (a.g.D > 128 ? 256 : 128) * (int)sizeof(float);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e != cudaSuccess) return e;
     kern<<<(unsigned)a.total_work, 256, smem, s>>>(a);
     return counted(cudaGetLastError());

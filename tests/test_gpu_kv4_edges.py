@@ -177,3 +177,22 @@ def test_window_masses_of_two_threads():
     assert at_once(*calls, times=20000) == []
     for out, want, ws, *_ in results:
         assert torch.equal(out, want) and cca.attn_status(ws) == 0
+
+
+def test_merges_of_two_threads():
+    """Forwards with re-split chunks at 8 and 128 dims: the merge kernel is one, its shared memory is not."""
+    calls, results, fn = [], [], cca.lib().attn_fwd
+    for D in (8, 128):
+        q = bf16(np.random.default_rng(D), 1, 1, 2048, D)
+        chunks = [(0, 1920, 0, 0), (1920, 2048, 0, -4)]
+        shape, o, lse = cca.shape_of(q), torch.zeros_like(q), torch.zeros(1, 1, 2048, device="cuda")
+        ws = cca.workspace(shape, chunks, cca.PASS_FWD)
+        want = cca.forward(q, q, q, chunks)
+        arr, n = _lib.chunk_array(chunks)
+        args = (q.data_ptr(), q.data_ptr(), q.data_ptr(), arr, n, ctypes.byref(shape), o.data_ptr(), lse.data_ptr(),
+                ws.data_ptr(), ws.numel())
+        calls.append(lambda s, a=args: fn(*a, s))
+        results.append((o, lse, want, ws, q, shape))
+    assert at_once(*calls, times=20000) == []
+    for o, lse, want, ws, *_ in results:
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1]) and cca.attn_status(ws) == 0
