@@ -57,10 +57,12 @@ constexpr int kSlots = 16;                 // slots of a fragment; a warp's slic
 constexpr float kLag = 4.f;                // how far (log2) a score may pass the running maximum
 constexpr float kUp = 11.f;                // weights are held times 2^kUp
 constexpr int kMaxGrid = 1024;            // blocks of the split kernel
+constexpr int64_t kScores = 1 << 28;       // scores (mass) that a pass keeps, if it has more than one unit a head
 
 // What the launch derives from the shapes.
 struct Split {
-    int32_t R, RT;        // rows of a key/value head; units they make
+    int32_t R;            // rows of a key/value head
+    int32_t rt0, RT;      // of the units that they make, those of this pass: the first and how many
     int32_t pitch;        // fp32 scores kept of each slot (mass), a row group
     int64_t slot_floats;  // floats of a partial: 8 NT rows of D, then m and l of each
     float* lse2;          // [B H T] log2 of the rows' sums (mass)
@@ -326,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(DT, NT)) split_kernel(
             // ---- a unit begins: its queries
             fresh = false;
             hk = cur.v / sp.RT;
-            rt = cur.v - hk * sp.RT;
+            rt = sp.rt0 + cur.v - hk * sp.RT;
             __syncthreads();                            // the last unit's sO, sQ, sQS are read
             const int rows = min(L::ROWS, sp.R - rt * L::ROWS);
 #pragma unroll 1
@@ -790,7 +792,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Kv4AttendArg
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, part = warp % WPR;
     const int G = a.g.H / a.c.Hkv, units = a.c.Hkv * sp.RT, groups = unit_rows / ROWS;
     const int u = blockIdx.x / groups, r = (blockIdx.x - u * groups) * ROWS + warp / WPR;
-    const int b = u / units, v = u - b * units, hk = v / sp.RT, rt = v - hk * sp.RT;
+    const int b = u / units, v = u - b * units, hk = v / sp.RT, rt = sp.rt0 + v - hk * sp.RT;
     const int rr = rt * unit_rows + r;
     const int i = rr / G, h = hk * G + rr - i * G, D = a.c.D;
     // every block waits for the kernel before, so that this one does not end ahead of it
@@ -903,7 +905,8 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Kv4AttendArg
 
 // mass_out = mass_in + sum over the rows of 2^(s2 - lse2), from the scores that the
 // split kernel kept; a thread takes kMassSlots slots, kMassThreads apart, V scores of
-// a slot at a time.
+// a slot at a time. What it reads before its wait, the weights so far, the pass before may
+// have written: older than the split and merge kernels between.
 constexpr int kMassThreads = 256, kMassSlots = 4;
 template <int V>
 __global__ void __launch_bounds__(kMassThreads) mass_kernel(const Kv4AttendArgs a, const Split sp, int32_t unit_rows) {
@@ -930,7 +933,7 @@ __global__ void __launch_bounds__(kMassThreads) mass_kernel(const Kv4AttendArgs 
         __syncthreads();
         if (threadIdx.x < sp.pitch) {
             // rows that see nothing, and columns past the rows, weigh nothing
-            const int rr = rt * unit_rows + threadIdx.x;
+            const int rr = (sp.rt0 + rt) * unit_rows + threadIdx.x;
             float l2 = rr < sp.R ? sp.lse2[((int64_t)b * a.g.H + hk * G + rr % G) * a.g.T + rr / G] : INFINITY;
             s_lse[threadIdx.x] = l2 == -INFINITY ? INFINITY : l2;
         }
@@ -971,6 +974,7 @@ int dims_of(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
 
 struct Plan {
     int nt, tile, grid;
+    int units;                        // of 8 nt rows, of a key/value head; sp.RT of them a pass
     Split sp;
     int64_t parts, lse2, scores;      // floats
 };
@@ -980,8 +984,17 @@ Plan plan_of(const Kv4Geom& c, const Geom& g, bool mass) {
     const int64_t R = (int64_t)(g.H / c.Hkv) * g.T;
     p.nt = row_groups(c.D, R, (int64_t)c.B * c.Hkv * c.cap);
     p.sp.R = (int32_t)R;
-    p.sp.RT = (int32_t)((R + 8 * p.nt - 1) / (8 * p.nt));
+    p.units = (int32_t)((R + 8 * p.nt - 1) / (8 * p.nt));
+    p.sp.rt0 = 0;
+    p.sp.RT = p.units;
     p.sp.pitch = R <= 2 ? 2 : R <= 4 ? 4 : 8 * p.nt;
+    if (mass) {
+        // each unit goes over the cache by itself, so passes cost their launches only, against a pass's work on
+        // 1 GiB of scores (8 heads of 128K slots: 256 rows of each)
+        const int64_t most = std::max<int64_t>(1, kScores / ((int64_t)c.B * c.Hkv * c.cap * p.sp.pitch));
+        const int64_t passes = (p.units + most - 1) / most;
+        p.sp.RT = (int32_t)((p.units + passes - 1) / passes);
+    }
     p.sp.slot_floats = (int64_t)8 * p.nt * (c.D + 2);
     const int64_t units = (int64_t)c.B * c.Hkv * p.sp.RT;
     p.tile = tile_slots(dims_of(c.D), p.nt);
@@ -1024,23 +1037,30 @@ cudaError_t launch_kv4_attend(const Kv4AttendArgs& args, cudaStream_t s) {
     p.sp.lse2 = a.mass_out ? a.parts + p.parts : nullptr;
     p.sp.scores = a.mass_out ? a.parts + p.parts + p.lse2 : nullptr;
     wait_settings(&p.sp.wait_ns, &p.sp.stall);
-    cudaError_t e;
-    if (a.c.D <= 64) e = p.nt == 1 ? launch_dims<64, 1>(a, p, s) : launch_dims<64, 4>(a, p, s);
-    else if (a.c.D <= 128) e = p.nt == 1 ? launch_dims<128, 1>(a, p, s) : launch_dims<128, 4>(a, p, s);
-    else e = p.nt == 1 ? launch_dims<256, 1>(a, p, s) : launch_dims<256, 2>(a, p, s);
-    if (e != cudaSuccess) return e;
     const int unit_rows = 8 * p.nt;
-    const int64_t units = (int64_t)a.c.B * a.c.Hkv * p.sp.RT;
-    // eight warps a row while that leaves the SMs fewer than two blocks each
-    const bool few = units * std::min(unit_rows, p.sp.R) <= 2 * device_sm_count();
-    e = launch_early(few ? (p.tile == 128 ? merge_kernel<128, 8> : merge_kernel<64, 8>)
-                         : (p.tile == 128 ? merge_kernel<128, 1> : merge_kernel<64, 1>),
-                     dim3((unsigned)(units * unit_rows / (few ? 1 : kMergeWarps))), kMergeThreads, 0, 1, s, a, p.sp, unit_rows);
-    if (e != cudaSuccess || !a.mass_out) return e;
-    constexpr int per = kMassThreads * kMassSlots;
-    return launch_early(p.sp.pitch % 4 ? mass_kernel<2> : mass_kernel<4>,
-                        dim3((unsigned)((int64_t)((a.c.cap + per - 1) / per) * a.c.B * a.c.Hkv)), kMassThreads, 0, 1, s, a, p.sp,
-                        unit_rows);
+    for (int32_t RT = p.sp.RT; p.sp.rt0 < p.units; p.sp.rt0 += RT) {
+        p.sp.RT = std::min(RT, p.units - p.sp.rt0);
+        if (p.sp.rt0) a.mass_in = a.mass_out;
+        cudaError_t e;
+        if (a.c.D <= 64) e = p.nt == 1 ? launch_dims<64, 1>(a, p, s) : launch_dims<64, 4>(a, p, s);
+        else if (a.c.D <= 128) e = p.nt == 1 ? launch_dims<128, 1>(a, p, s) : launch_dims<128, 4>(a, p, s);
+        else e = p.nt == 1 ? launch_dims<256, 1>(a, p, s) : launch_dims<256, 2>(a, p, s);
+        if (e != cudaSuccess) return e;
+        const int64_t units = (int64_t)a.c.B * a.c.Hkv * p.sp.RT;
+        // eight warps a row while that leaves the SMs fewer than two blocks each
+        const bool few = units * std::min(unit_rows, p.sp.R) <= 2 * device_sm_count();
+        e = launch_early(few ? (p.tile == 128 ? merge_kernel<128, 8> : merge_kernel<64, 8>)
+                             : (p.tile == 128 ? merge_kernel<128, 1> : merge_kernel<64, 1>),
+                         dim3((unsigned)(units * unit_rows / (few ? 1 : kMergeWarps))), kMergeThreads, 0, 1, s, a, p.sp, unit_rows);
+        if (e != cudaSuccess) return e;
+        if (!a.mass_out) continue;
+        constexpr int per = kMassThreads * kMassSlots;
+        e = launch_early(p.sp.pitch % 4 ? mass_kernel<2> : mass_kernel<4>,
+                         dim3((unsigned)((int64_t)((a.c.cap + per - 1) / per) * a.c.B * a.c.Hkv)), kMassThreads, 0, 1, s, a, p.sp,
+                         unit_rows);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 }  // namespace attn

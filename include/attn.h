@@ -339,7 +339,10 @@ typedef struct {
  * attn_kv4_load, attn_kv4_evict; shape may be NULL), ATTN_KV4_ATTEND
  * (attn_kv4_attend without mass_out; shape is the queries') or
  * ATTN_KV4_ATTEND_MASS (with). A workspace that is large enough for one may
- * serve the others. */
+ * serve the others. With mass_out it holds fp32 scores: 4 B Hkv cap bytes for each
+ * of the H / Hkv * T rows of a key/value head (their number rounded up to 2, 4 or
+ * groups of 8, 16 or 32), at most 1 GiB, or one group's where that is more; calls of
+ * more rows take them in several passes. */
 #define ATTN_KV4_ROWS         0
 #define ATTN_KV4_ATTEND       1
 #define ATTN_KV4_ATTEND_MASS  2

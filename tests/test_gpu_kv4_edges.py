@@ -1,6 +1,6 @@
 """GPU tests of the 4-bit cache and of the key mass where test_gpu_kv4.py has none: rows
 without a log-sum-exp whose queries are not finite, keys that are not, calls of several
-threads at once. Tolerances are those derived there."""
+threads at once, weights of more rows than one pass takes. Tolerances are those derived there."""
 import ctypes
 import math
 import threading
@@ -12,7 +12,7 @@ import torch
 import chunked_causal_attention_gb300 as cca
 from chunked_causal_attention_gb300 import _lib
 
-from test_gpu_kv4 import MASS_PLANS, bf16, built, check_mass, i32, random_cache
+from test_gpu_kv4 import MASS_PLANS, bf16, built, check_attend, check_mass, i32, random_cache
 
 pytestmark = pytest.mark.gpu
 
@@ -196,3 +196,34 @@ def test_merges_of_two_threads():
     assert at_once(*calls, times=20000) == []
     for o, lse, want, ws, *_ in results:
         assert torch.equal(o, want[0]) and torch.equal(lse, want[1]) and cca.attn_status(ws) == 0
+
+
+# ------------------------------------------------------------------ attention of many rows
+
+@pytest.mark.parametrize("B,cap,H,T,D,lens", [
+    (1, 1 << 20, 2, 150, 8, [700]),                       # 10 groups of 32 rows in two passes
+    (2, 1 << 20, 3, 101, 40, [900, 77]),                  # 303 rows in three; the first rows of a sequence see nothing
+    (1, (1 << 20) - 16, 1, 300, 8, [513]),                # 38 groups of 8 rows in two
+    (1, 1 << 20, 1, 300, 136, [600])])                    # 19 groups of 16 rows in two
+def test_weights_of_more_rows_than_one_pass_takes(B, cap, H, T, D, lens):
+    rng = np.random.default_rng(D + T)
+    c = cca.kv4_cache(B, 1, cap, D, k_scale=0.5, v_scale=2.0)
+    near = random_cache(B, 1, 1024, D, T)
+    for a, b in zip((c.k_codes, c.k_scales, c.v_codes, c.v_scales), (near.k_codes, near.k_scales, near.v_codes, near.v_scales)):
+        a[:, :, :1024] = b
+    q = 2 * bf16(rng, B, H, T, D)
+    ws = cca.kv4_workspace(c, q, mass=True)
+    rows = -(-H * T // 8) * 8
+    assert ws.numel() < 4 * B * cap * rows                # the scores of all rows at once would be this
+    mi, mo = torch.rand(B, 1, cap, device="cuda"), torch.full((B, 1, cap), -3.0, device="cuda")
+    launches = cca.kernel_launches()
+    o, lse = cca.kv4_attention(q, c, i32(lens), mass_in=mi, mass_out=mo, ws=ws)
+    assert cca.kernel_launches() - launches >= 6
+    check_attend(q, c, lens, o, lse, None, mi, mo, kept_tail=-3.0)
+    m = mi.clone()
+    cca.kv4_attention(q, c, i32(lens), mass_in=m, mass_out=m, ws=ws)
+    for b, n in enumerate(lens):
+        assert torch.equal(m[b, :, :n], mo[b, :, :n]) and torch.equal(m[b, :, n:], mi[b, :, n:])
+    cca.kv4_attention(q, c, i32(lens), mass_out=mo, ws=ws)
+    check_attend(q, c, lens, o, lse, None, None, mo, kept_tail=-3.0)
+    assert cca.attn_status(ws) == 0

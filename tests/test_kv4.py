@@ -200,3 +200,14 @@ def test_wrappers_refuse_host_tensors_and_wrong_sizes():
         with pytest.raises(cca.AttnError) as e:
             fn()
         assert e.value.status == 1
+
+
+@pytest.mark.parametrize("cap,T,D", [(131072, 512, 128), (131072, 4096, 64), (262144, 64, 256), (1 << 20, 16, 128), (65536, 1 << 15, 128)])
+def test_workspace_of_weights_is_bounded(cap, T, D):
+    """Scores of all rows of a long call would take up to 550 GB; what is kept stays within 1 GiB or a group of rows."""
+    c = cache(B=1, Hkv=8, cap=cap, D=D)
+    s = cca.make_shape(1, 32, T, D, 32 * T * D, D, T * D, 0.125)
+    plain = cca.attn_kv4_workspace_size(c, s, cca.KV4_ATTEND)
+    group = 4 * 8 * cap * (32 if D <= 128 else 16)
+    lse = 4 * 32 * T + 256
+    assert cca.attn_kv4_workspace_size(c, s, cca.KV4_ATTEND_MASS) <= plain + lse + max(1 << 30, group)
