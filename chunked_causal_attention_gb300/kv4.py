@@ -6,7 +6,7 @@ and a cache is cut to a budget by the attention weight that its slots received.
     cache = cca.kv4_cache(B, Hkv, cap, D)
     cca.kv4_store(cache, k, v, pos)                      # a prompt's rows, or one row a sequence
     o, lse = cca.kv4_attention(q, cache, lens, mass_in=mass, mass_out=mass)
-    lens2, slots = cca.kv4_evict(cache, lens, mass, keep, recent, smaller, mass2)
+    lens2, slots = cca.kv4_evict(cache, lens, mass, keep, recent, smaller, mass2.zero_())
 
 pos and lens are int32 tensors on the GPU, so the calls can be captured into a
 graph and replayed. Torch provides memory and streams only.
@@ -152,7 +152,8 @@ def kv4_attention(q, cache: KV4Cache, lens, scale: Optional[float] = None, mass_
                   stream=None):
     """(o, lse) of the newest T tokens of each sequence, q bf16 [B, H, T, D], over the
     lens[b] slots in use (their own included). mass_out fp32 [B, Hkv, n]: each slot's
-    weight over the call's rows is added to mass_in (None: zeros; may be mass_out)."""
+    weight over the call's rows is added to mass_in (None: zeros; may be mass_out). The
+    entry of a slot that was appended since has to be 0 in mass_in."""
     import torch
     shape, ref = cache._shape(q, scale, False)
     if ws is None:
@@ -178,7 +179,9 @@ def kv4_attention(q, cache: KV4Cache, lens, scale: Optional[float] = None, mass_
 def kv4_evict(cache: KV4Cache, lens, mass, keep: int, recent: int, out: KV4Cache, mass_out=None, lens_out=None,
               ws=None, stream=None):
     """Cut each sequence to at most keep slots, per key/value head: its last `recent`
-    and those with the highest mass, moved to the front of `out` in their order.
+    and those with the highest mass, moved to the front of `out` in their order, their
+    masses to the front of mass_out. What lies behind them stays as it was: zero a
+    mass_out that was in use before, or the slots appended later start from its weights.
     Returns (lens_out, slots): int32 [B] and the source slots int32 [B, Hkv, keep]."""
     import torch
     fn = "kv4_evict"

@@ -381,7 +381,10 @@ int attn_kv4_load(const attn_kv4_cache* cache, const int32_t* pos, const int32_t
  * the call's queries and the heads of its key/value head is added,
  *   mass_out[b][hk][j] = mass_in[b][hk][j] + sum exp(scale * q_i . k_j - LSE_i)  for j < n,
  * with rows of mass_ld fp32 (mass_in NULL: zeros; it may equal mass_out and must
- * not overlap it otherwise); entries j >= n are left as they were. A length outside
+ * not overlap it otherwise); entries j >= n are left as they were. A slot that was
+ * appended since the last call counts too: its entry of mass_in has to be 0 before
+ * the first call that sees it, also where the buffer held another cache's weights.
+ * A length outside
  * [0, cap] (with mass_out: or above mass_ld) is reported (ATTN_E_BOUNDS) and taken
  * as the nearest in range. The products are made in fp16 with fp32 sums: cache
  * values and queries (scaled by a power of two) are exact there, softmax weights
@@ -396,7 +399,8 @@ int attn_kv4_attend(const void* q, const attn_shape* shape, const attn_kv4_cache
  * 0..m-1 of dst in their order, chosen for each key/value head on its own.
  *   lens_out[b] = m;  slots[b][h][i] = the source slot of row i, -1 for m <= i < keep
  *   mass_out[b][h][i] = mass[b][h][slots[b][h][i]]   (mass_out may be NULL)
- * Rows m and on of dst and mass_out are left as they were. mass: rows of mass_ld
+ * Rows m and on of dst and mass_out are left as they were: clear mass_out before the
+ * call if slots appended later are to be weighed in it. mass: rows of mass_ld
  * fp32; mass_out: rows of mass_out_ld >= keep; slots: int32 [B][Hkv][keep]
  * contiguous (fewer than 2^31). src and dst have the same B, Hkv, D and tensor scales, dst.cap >= keep >= 1,
  * 0 <= recent; src and dst, and mass and mass_out, must not overlap, and lens_out

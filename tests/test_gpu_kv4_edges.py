@@ -1,8 +1,11 @@
 """GPU tests of the 4-bit cache and of the key mass where test_gpu_kv4.py has none: rows
 without a log-sum-exp whose queries are not finite, keys that are not, calls of several
-threads at once, weights of more rows than one pass takes. Tolerances are those derived there."""
+threads at once, weights of more rows than one pass takes, buffers of weights used again.
+Tolerances are those derived there."""
 import ctypes
 import math
+import os
+import re
 import threading
 
 import numpy as np
@@ -12,7 +15,9 @@ import torch
 import chunked_causal_attention_gb300 as cca
 from chunked_causal_attention_gb300 import _lib
 
-from test_gpu_kv4 import MASS_PLANS, bf16, built, check_attend, check_mass, i32, random_cache
+from oracle import kv4 as K
+
+from test_gpu_kv4 import MASS_PLANS, bf16, built, cached, check_attend, check_mass, f64, i32, random_cache
 
 pytestmark = pytest.mark.gpu
 
@@ -226,4 +231,65 @@ def test_weights_of_more_rows_than_one_pass_takes(B, cap, H, T, D, lens):
         assert torch.equal(m[b, :, :n], mo[b, :, :n]) and torch.equal(m[b, :, n:], mi[b, :, n:])
     cca.kv4_attention(q, c, i32(lens), mass_out=mo, ws=ws)
     check_attend(q, c, lens, o, lse, None, None, mo, kept_tail=-3.0)
+    assert cca.attn_status(ws) == 0
+
+
+# ------------------------------------------------------------------ buffers of weights used again
+
+def test_the_serving_example_with_a_buffer_in_use_before():
+    """README's example as it stands, into a cache and weights that held something else: the token that it
+    appends starts from no weight."""
+    text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")).read()
+    example, = (b for b in re.findall(r"```python\n(.*?)```", text, re.S) if "kv4_evict(" in b)
+    rng = np.random.default_rng(51)
+    B, H, Hkv, D, L, keep = 1, 2, 1, 64, 5000, 4096
+    g = {"cca": cca, "B": B, "Hkv": Hkv, "D": D, "L": L, "cap": 5008, "T": 16, "pos": i32([0]), "lens": i32([L])}
+    g["q"], g["k"], g["v"] = 2 * bf16(rng, B, H, L, D), bf16(rng, B, Hkv, L, D), bf16(rng, B, Hkv, L, D)
+    g["chunks"] = cca.attn_plan(L, 2, cca.PLAN_FLOPS)
+    _, g["lse"] = cca.forward(g["q"], g["k"], g["v"], g["chunks"])
+    g["small"], g["mass2"] = random_cache(B, Hkv, 4112, D, 52, ts=(1.0, 1.0)), torch.full((B, Hkv, 4112), 9.0, device="cuda")
+    g["q1"], g["k1"], g["v1"] = bf16(rng, B, H, 1, D), bf16(rng, B, Hkv, 1, D), bf16(rng, B, Hkv, 1, D)
+    g["ws"] = cca.kv4_workspace(g["small"], g["q1"], mass=True)
+    exec(example, g)
+    assert g["lens2"].tolist() == [keep + 1] and cca.attn_status(g["ws"]) == 0
+    before = torch.zeros(B, Hkv, 4112, device="cuda")
+    before[..., :keep] = g["mass"].gather(2, g["slots"].long())
+    check_attend(g["q1"], g["small"], [keep + 1], g["o"], g["lse1"], None, before, g["mass2"])
+
+
+def test_two_caches_in_turn():
+    """Decoding and eviction over and over between two caches and two buffers of weights: every slot's weight
+    is that of its own token, and the slots are chosen by it."""
+    rng = np.random.default_rng(53)
+    B, H, Hkv, D, cap, keep, recent, steps = 2, 4, 2, 64, 128, 48, 8, 20
+    caches = [random_cache(B, Hkv, cap, D, 54 + i) for i in range(2)]
+    masses = [torch.full((B, Hkv, cap), 7.0 + i, device="cuda") for i in range(2)]
+    lens = i32([100, 30])
+    masses[0].copy_(torch.rand(B, Hkv, cap))
+    masses[0][0, :, 100:], masses[0][1, :, 30:] = 0, 0
+    true = f64(masses[0])
+    ws = cca.kv4_workspace(caches[0], bf16(rng, B, H, 1, D), mass=True)
+    for turn in range(4):
+        a, b = turn % 2, 1 - turn % 2
+        chosen = [[K.evict(masses[a][i, h].cpu().numpy(), int(lens[i]), keep, recent) for h in range(Hkv)] for i in range(B)]
+        lens, slots = cca.kv4_evict(caches[a], lens, masses[a], keep, recent, caches[b], masses[b].zero_(), ws=ws)
+        kept = np.zeros_like(true)
+        for i in range(B):
+            for h in range(Hkv):
+                m = len(chosen[i][h])
+                assert slots[i, h, :m].tolist() == chosen[i][h]
+                kept[i, h, :m] = true[i, h, chosen[i][h]]
+        true = kept
+        for _ in range(steps):
+            q, k, v = 2 * bf16(rng, B, H, 1, D), bf16(rng, B, Hkv, 1, D), bf16(rng, B, Hkv, 1, D)
+            cca.kv4_store(caches[b], k, v, lens, ws=ws)
+            lens += 1
+            cca.kv4_attention(q, caches[b], lens, mass_in=masses[b], mass_out=masses[b], ws=ws)
+            for i in range(B):
+                for h in range(Hkv):
+                    n = int(lens[i])
+                    kk, vv = cached(caches[b], i, h, n)
+                    true[i, h, :n] += K.attend(f64(q[i, 2 * h:2 * h + 2]), kk, vv, n, D ** -0.5)[2].sum((0, 1))
+            # scores below 64 here: a weight is off by 2 (D + 4) 2^-23 64 + 2^-13 of itself at most (test_gpu_kv4)
+            assert (np.abs(f64(masses[b]) - true) <= 2e-3 * true + 1e-30).all()
     assert cca.attn_status(ws) == 0
