@@ -39,9 +39,13 @@ int check_cache(const attn_kv4_cache* c, Kv4Geom* g) {
     if (c->D < 8 || c->D > 256 || c->D % 8) return ATTN_E_UNSUPPORTED;
     if (!tensor_scale_ok(c->k_scale) || !tensor_scale_ok(c->v_scale)) return ATTN_E_INVAL;
     if (c->sb <= 0 || c->sh <= 0) return ATTN_E_INVAL;
-    // rows of different sequences and heads are different rows
+    // rows of different sequences and heads are different rows: the heads of a sequence lie between two sequences,
+    // or the sequences of a head between two heads
+    if (c->sb > INT64_MAX / c->B / 4 || c->sh > INT64_MAX / c->Hkv / 4) return ATTN_E_INVAL;
     if (c->sh < c->cap && c->Hkv > 1) return ATTN_E_INVAL;
     if (c->sb < c->cap && c->B > 1) return ATTN_E_INVAL;
+    if (c->B > 1 && c->Hkv > 1 && c->sb < (c->Hkv - 1) * c->sh + c->cap && c->sh < (c->B - 1) * c->sb + c->cap)
+        return ATTN_E_INVAL;
     if (c->cap % 16 || c->sb % 16 || c->sh % 16) return ATTN_E_ALIGN;
     const void* p[] = {c->k_codes, c->k_scales, c->v_codes, c->v_scales};
     for (const void* x : p)

@@ -315,7 +315,9 @@ int attn_key_mass(const void* q, const void* k, const float* lse, const attn_chu
  * powers of two in [2^-64, 2^64], so every value has at most six significant bits
  * and is exact in bf16. A block that held a NaN or an infinity has scale NaN.
  * D: a multiple of 8 from 8 to 256. cap, sb and sh: multiples of 16; sb and sh
- * (in slots) allow a view of some sequences, heads or slots of a larger cache.
+ * (in slots) allow a view of some sequences, heads or slots of a larger cache, no
+ * two of whose rows are the same (ATTN_E_INVAL: the heads of a sequence lie between
+ * two sequences, or the other way round).
  * The arrays are 16-byte aligned. */
 typedef struct {
     int64_t B, Hkv, cap, D;

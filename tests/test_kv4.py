@@ -211,3 +211,26 @@ def test_workspace_of_weights_is_bounded(cap, T, D):
     group = 4 * 8 * cap * (32 if D <= 128 else 16)
     lse = 4 * 32 * T + 256
     assert cca.attn_kv4_workspace_size(c, s, cca.KV4_ATTEND_MASS) <= plain + lse + max(1 << 30, group)
+
+
+@pytest.mark.parametrize("B,Hkv,cap,sb,sh,ok", [
+    (2, 2, 64, 128, 64, True), (2, 2, 64, 64, 128, True), (3, 4, 32, 32, 96, True), (3, 4, 32, 128, 32, True),
+    (2, 3, 48, 640, 64, True), (2, 3, 48, 64, 640, True), (2, 1, 64, 64, 16, True), (1, 2, 64, 16, 64, True),
+    (2, 2, 64, 64, 64, False),                      # head 1 of sequence 0 is head 0 of sequence 1
+    (2, 2, 64, 112, 64, False), (3, 3, 32, 64, 32, False), (2, 4, 64, 128, 64, False), (4, 2, 64, 64, 128, False),
+    (2, 2, 64, 1 << 62, 64, False), (2, 2, 64, 64, 1 << 62, False)])
+def test_cache_rows_are_not_shared(B, Hkv, cap, sb, sh, ok):
+    """Two rows of a cache in the same place: a store would write both."""
+    rows = {b * sb + h * sh + t for b in range(B) for h in range(Hkv) for t in range(cap)}
+    assert not ok or len(rows) == B * Hkv * cap
+    c = cache(B=B, Hkv=Hkv, cap=cap, sb=sb, sh=sh)
+    n = ctypes.c_size_t(0)
+    assert cca.lib().attn_kv4_workspace_size(ctypes.byref(c), None, 0, ctypes.byref(n)) == (0 if ok else 1)
+
+
+def test_cache_object_refuses_shared_rows():
+    a = [torch.zeros(4 * 64, n, dtype=torch.uint8) for n in (32, 4, 32, 4)]
+    shared = [t.as_strided((2, 2, 64, n), (64 * n, 64 * n, n, 1)) for t, n in zip(a, (32, 4, 32, 4))]
+    with pytest.raises(cca.AttnError) as e:
+        cca.KV4Cache(*shared, D=64)
+    assert e.value.status == 1
