@@ -4,6 +4,7 @@
 #include <cmath>
 #include <cstring>
 #include <new>
+#include <numeric>
 #include <vector>
 
 #include "kv4.h"
@@ -13,6 +14,7 @@ using namespace attn;
 namespace {
 
 constexpr size_t kAlign = 256;
+constexpr int64_t kMaxLd = 1ll << 36;   // floats between two rows of weights; with 2^24 rows offsets stay below 2^63
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
@@ -72,21 +74,44 @@ size_t span_rows(const Kv4Geom& c) {
     return (size_t)(c.B - 1) * c.sb + (size_t)(c.Hkv - 1) * c.sh + c.cap;
 }
 
+// Whether stretches of na bytes at a and of nb bytes at b, each repeated at multiples of `period` bytes, never
+// meet: slots of one allocation taken as two caches lie between one another without overlapping.
+bool apart(const void* a, size_t na, const void* b, size_t nb, size_t period) {
+    if (!period) return false;
+    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+    const size_t d = y >= x ? (y - x) % period : (period - (x - y) % period) % period;
+    return d >= na && d + nb <= period;
+}
+
 bool overlap(const Kv4Geom& a, const Kv4Geom& b) {
     const size_t ra = span_rows(a), rb = span_rows(b);
-    struct Arr { const void* p; size_t n; };
-    const Arr x[] = {{a.kc, ra * a.cb}, {a.ks, ra * a.nb}, {a.vc, ra * a.cb}, {a.vs, ra * a.nb}};
-    const Arr y[] = {{b.kc, rb * b.cb}, {b.ks, rb * b.nb}, {b.vc, rb * b.cb}, {b.vs, rb * b.nb}};
+    // rows that divide the distances between all heads and sequences
+    int64_t g = 0;
+    for (const Kv4Geom* c : {&a, &b}) {
+        if (c->B > 1) g = std::gcd(g, c->sb);
+        if (c->Hkv > 1) g = std::gcd(g, c->sh);
+    }
+    struct Arr { const void* p; int32_t row; };
+    const Arr x[] = {{a.kc, a.cb}, {a.ks, a.nb}, {a.vc, a.cb}, {a.vs, a.nb}};
+    const Arr y[] = {{b.kc, b.cb}, {b.ks, b.nb}, {b.vc, b.cb}, {b.vs, b.nb}};
     for (const Arr& p : x)
         for (const Arr& q : y)
-            if (overlap(p.p, p.n, q.p, q.n)) return true;
+            if (overlap(p.p, ra * p.row, q.p, rb * q.row) &&
+                !(p.row == q.row && apart(p.p, (size_t)a.cap * p.row, q.p, (size_t)b.cap * q.row, (size_t)g * p.row)))
+                return true;
     return false;
 }
 
+// Rows of weights, a of na floats `lda` apart and b of nb floats `ldb` apart.
+bool mass_overlap(const float* a, int64_t na, int64_t lda, const float* b, int64_t nb, int64_t ldb, int64_t rows) {
+    return overlap(a, ((rows - 1) * lda + na) * 4, b, ((rows - 1) * ldb + nb) * 4) &&
+           !(rows > 1 && apart(a, na * 4, b, nb * 4, (size_t)std::gcd(lda, ldb) * 4));
+}
+
 // mass_in null, equal to mass_out, or apart from it.
-int check_mass(const float* in, const float* out, size_t floats) {
+int check_mass(const float* in, const float* out, int64_t floats, int64_t ld, int64_t rows) {
     if (!aligned(in, 16) || !aligned(out, 16)) return ATTN_E_ALIGN;
-    if (in && in != out && overlap(in, floats * 4, out, floats * 4)) return ATTN_E_INVAL;
+    if (in && in != out && mass_overlap(in, floats, ld, out, floats, ld, rows)) return ATTN_E_INVAL;
     return ATTN_OK;
 }
 
@@ -194,9 +219,9 @@ int attn_kv4_attend(const void* q, const attn_shape* shape, const attn_kv4_cache
     if (!q || !lens || !o || !lse) return ATTN_E_INVAL;
     if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 16) || !aligned(lens, 4)) return ATTN_E_ALIGN;
     if (mass_out) {
-        if (mass_ld <= 0) return ATTN_E_INVAL;
-        const size_t rows = (size_t)a.c.B * a.c.Hkv;
-        if ((st = check_mass(mass_in, mass_out, (rows - 1) * mass_ld + std::min<int64_t>(mass_ld, a.c.cap)))) return st;
+        if (mass_ld <= 0 || mass_ld > kMaxLd) return ATTN_E_INVAL;
+        if ((st = check_mass(mass_in, mass_out, std::min<int64_t>(mass_ld, a.c.cap), mass_ld, (int64_t)a.c.B * a.c.Hkv)))
+            return st;
     } else if (mass_in) {
         return ATTN_E_INVAL;
     }
@@ -221,15 +246,16 @@ int attn_kv4_evict(const attn_kv4_cache* src, const int32_t* lens, const float* 
     if (a.src.B != a.dst.B || a.src.Hkv != a.dst.Hkv || a.src.D != a.dst.D || a.src.k_scale != a.dst.k_scale ||
         a.src.v_scale != a.dst.v_scale)
         return ATTN_E_INVAL;
-    if (keep < 1 || keep > a.dst.cap || recent < 0 || mass_ld <= 0 || (mass_out && mass_out_ld < keep))
+    if (keep < 1 || keep > a.dst.cap || recent < 0 || mass_ld <= 0 || mass_ld > kMaxLd ||
+        (mass_out && (mass_out_ld < keep || mass_out_ld > kMaxLd)))
         return ATTN_E_INVAL;
     if (!aligned(mass, 16) || !aligned(mass_out, 16) || !aligned(slots, 4) || !aligned(lens, 4) || !aligned(lens_out, 4))
         return ATTN_E_ALIGN;
     if ((int64_t)a.src.B * a.src.Hkv * keep > INT32_MAX) return ATTN_E_INVAL;
     if (overlap(a.src, a.dst)) return ATTN_E_INVAL;
-    const size_t rows = (size_t)a.src.B * a.src.Hkv;
-    const size_t n_in = ((rows - 1) * mass_ld + std::min<int64_t>(mass_ld, a.src.cap)) * 4;
-    if (mass_out && overlap(mass, n_in, mass_out, ((rows - 1) * mass_out_ld + keep) * 4)) return ATTN_E_INVAL;
+    if (mass_out && mass_overlap(mass, std::min<int64_t>(mass_ld, a.src.cap), mass_ld, mass_out, keep, mass_out_ld,
+                                 (int64_t)a.src.B * a.src.Hkv))
+        return ATTN_E_INVAL;
     if ((st = check_ws(ws, ws_bytes, kHeaderBytes))) return st;
     a.lens = lens; a.lens_out = lens_out;
     a.mass = mass; a.mass_ld = mass_ld;
@@ -249,7 +275,7 @@ int attn_key_mass(const void* q, const void* k, const float* lse, const attn_chu
     if ((st = chunks_fwd_status(chunks, n, a.g.T))) return st;
     if (!q || !k || !lse || !mass_out) return ATTN_E_INVAL;
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(lse, 16)) return ATTN_E_ALIGN;
-    if ((st = check_mass(mass_in, mass_out, (size_t)a.g.B * a.g.Hkv * a.g.T))) return st;
+    if ((st = check_mass(mass_in, mass_out, (int64_t)a.g.B * a.g.Hkv * a.g.T, 0, 1))) return st;
     if ((st = check_ws(ws, ws_bytes, key_mass_bytes(a.g, chunks, n)))) return st;
     cudaStream_t s = (cudaStream_t)stream;
     uint8_t* w = (uint8_t*)ws;

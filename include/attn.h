@@ -405,8 +405,8 @@ int attn_kv4_attend(const void* q, const attn_shape* shape, const attn_kv4_cache
  * call if slots appended later are to be weighed in it. mass: rows of mass_ld
  * fp32; mass_out: rows of mass_out_ld >= keep; slots: int32 [B][Hkv][keep]
  * contiguous (fewer than 2^31). src and dst have the same B, Hkv, D and tensor scales, dst.cap >= keep >= 1,
- * 0 <= recent; src and dst, and mass and mass_out, must not overlap, and lens_out
- * may equal lens. Lengths out of range as in attn_kv4_attend. Errors as
+ * 0 <= recent; src and dst, and mass and mass_out, must not overlap (but may be slots
+ * of one allocation that lie between one another), and lens_out may equal lens. Lengths out of range as in attn_kv4_attend. Errors as
  * attn_kv4_store. */
 int attn_kv4_evict(const attn_kv4_cache* src, const int32_t* lens, const float* mass, int64_t mass_ld,
                    int32_t keep, int32_t recent, const attn_kv4_cache* dst, int32_t* lens_out,

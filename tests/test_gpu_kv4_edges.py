@@ -1,6 +1,7 @@
 """GPU tests of the 4-bit cache and of the key mass where test_gpu_kv4.py has none: rows
 without a log-sum-exp whose queries are not finite, keys that are not, calls of several
-threads at once, weights of more rows than one pass takes, buffers of weights used again.
+threads at once, weights of more rows than one pass takes, buffers of weights used again,
+caches within one allocation.
 Tolerances are those derived there."""
 import ctypes
 import math
@@ -293,3 +294,28 @@ def test_two_caches_in_turn():
             # scores below 64 here: a weight is off by 2 (D + 4) 2^-23 64 + 2^-13 of itself at most (test_gpu_kv4)
             assert (np.abs(f64(masses[b]) - true) <= 2e-3 * true + 1e-30).all()
     assert cca.attn_status(ws) == 0
+
+
+# ------------------------------------------------------------------ caches within one allocation
+
+def test_evict_within_one_allocation():
+    """From the front slots of a cache to slots behind them, heads between one another; and back."""
+    rng = np.random.default_rng(57)
+    B, Hkv, D, keep = 2, 3, 80, 100
+    big = random_cache(B, Hkv, 640, D, 58)
+    view = lambda a, b: cca.KV4Cache(*(t[:, :, a:b] for t in (big.k_codes, big.k_scales, big.v_codes, big.v_scales)), D=D,
+                                     k_scale=big.k_scale, v_scale=big.v_scale)
+    front, back, other = view(0, 512), view(512, 640), cca.kv4_cache(B, Hkv, 128, D, k_scale=0.5, v_scale=2.0)
+    before = [t.clone() for t in (front.k_codes, front.v_scales)]
+    mass, lens = torch.rand(B, Hkv, 512, device="cuda"), i32([512, 77])
+    want = cca.kv4_evict(front, lens, mass, keep, 9, other)
+    got = cca.kv4_evict(front, lens, mass, keep, 9, back)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    for b, n in enumerate(want[0].tolist()):
+        for x, y in ((back.k_codes, other.k_codes), (back.k_scales, other.k_scales), (back.v_codes, other.v_codes),
+                     (back.v_scales, other.v_scales)):
+            assert torch.equal(x[b, :, :n], y[b, :, :n])
+    assert torch.equal(front.k_codes, before[0]) and torch.equal(front.v_scales, before[1])
+    q = bf16(rng, B, 6, 1, D)
+    for x, y in zip(cca.kv4_attention(q, back, got[0]), cca.kv4_attention(q, other, want[0])):
+        assert torch.equal(x, y)

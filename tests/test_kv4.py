@@ -234,3 +234,37 @@ def test_cache_object_refuses_shared_rows():
     with pytest.raises(cca.AttnError) as e:
         cca.KV4Cache(*shared, D=64)
     assert e.value.status == 1
+
+
+def test_evict_within_one_allocation():
+    """Source and destination are slots of the same larger cache: between one another, or overlapping."""
+    L = cca.lib()
+
+    def call(a, b, mass=1 << 40, ld=256, mo=None, mld=0, B=2, Hkv=2, **kw):
+        view = lambda first, cap: cache(B=B, Hkv=Hkv, cap=cap, sb=Hkv * 256, sh=256,
+                                        ptrs=[(i << 24) + first * n for i, n in ((1, 32), (2, 4), (3, 32), (4, 4))])
+        # a missing workspace (4) is seen after the overlaps (1)
+        return L.attn_kv4_evict(ctypes.byref(view(*a)), FAKE, ctypes.c_void_p(mass), ld, 16, 4, ctypes.byref(view(*b)), FAKE,
+                                mo and ctypes.c_void_p(mo), mld, FAKE, None, 0, None)
+
+    for B, Hkv in ((2, 2), (1, 2), (2, 1), (1, 1)):
+        assert call((0, 128), (128, 128), B=B, Hkv=Hkv) == 4 and call((128, 64), (64, 64), B=B, Hkv=Hkv) == 4
+        assert call((0, 128), (112, 64), B=B, Hkv=Hkv) == 1 and call((0, 128), (0, 32), B=B, Hkv=Hkv) == 1
+        assert call((64, 64), (32, 48), B=B, Hkv=Hkv) == 1
+    assert call((0, 144), (240, 32)) == 1                  # its last slots are the next head's first
+    # rows of weights between one another: 128 in, 16 out, 256 apart
+    assert call((0, 128), (128, 128), mo=(1 << 40) + 4 * 128, mld=256) == 4
+    assert call((0, 128), (128, 128), mo=(1 << 40) - 4 * 128, mld=256) == 4
+    assert call((0, 128), (128, 128), mo=(1 << 40) + 4 * 124, mld=256) == 1
+    assert call((0, 128), (128, 128), mo=(1 << 40) + 4 * 128, mld=192) == 1      # not at the same distance
+    assert call((0, 128), (128, 128), ld=1 << 62) == 1
+
+
+def test_weights_of_a_call_between_one_another():
+    L, s, c = cca.lib(), shape(), cache(cap=64)
+    call = lambda mi, mo, ld: L.attn_kv4_attend(FAKE, ctypes.byref(s), ctypes.byref(c), FAKE, FAKE, FAKE, ctypes.c_void_p(mi),
+                                                ctypes.c_void_p(mo), ld, None, 0, None)
+    assert call(1 << 40, (1 << 40) + 256, 128) == 4 and call((1 << 40) + 256, 1 << 40, 128) == 4
+    assert call(1 << 40, 1 << 40, 128) == 4
+    assert call(1 << 40, (1 << 40) + 240, 128) == 1 and call(1 << 40, (1 << 40) + 272, 128) == 1
+    assert call(1 << 40, 1 << 41, 1 << 62) == 1
