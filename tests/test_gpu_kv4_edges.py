@@ -1,7 +1,8 @@
 """GPU tests of the 4-bit cache and of the key mass where test_gpu_kv4.py has none: rows
 without a log-sum-exp whose queries are not finite, keys that are not, calls of several
 threads at once, weights of more rows than one pass takes, buffers of weights used again,
-caches within one allocation.
+caches within one allocation, the kernels that large shapes pick, slots behind the last one
+that hold NaN, forked captures.
 Tolerances are those derived there."""
 import ctypes
 import math
@@ -18,7 +19,7 @@ from chunked_causal_attention_gb300 import _lib
 
 from oracle import kv4 as K
 
-from test_gpu_kv4 import MASS_PLANS, bf16, built, cached, check_attend, check_mass, f64, i32, random_cache
+from test_gpu_kv4 import MASSES, MASS_PLANS, bf16, built, cached, check_attend, check_mass, f64, i32, random_cache
 
 pytestmark = pytest.mark.gpu
 
@@ -206,6 +207,20 @@ def test_merges_of_two_threads():
 
 # ------------------------------------------------------------------ attention of many rows
 
+def mostly_empty_cache(B, Hkv, cap, D, used, seed):
+    """A cache whose first `used` slots are random and whose others hold NaN scales."""
+    c, near = cca.kv4_cache(B, Hkv, cap, D, k_scale=0.5, v_scale=2.0), random_cache(B, Hkv, used, D, seed)
+    for a, b in zip((c.k_codes, c.k_scales, c.v_codes, c.v_scales), (near.k_codes, near.k_scales, near.v_codes, near.v_scales)):
+        a.fill_(0x7F)
+        a[:, :, :used] = b
+    return c
+
+
+def nan_behind(c, lens):
+    for b, n in enumerate(lens):
+        c.k_scales[b, :, n:], c.v_scales[b, :, n:] = 0x7F, 0xFF
+
+
 @pytest.mark.parametrize("B,cap,H,T,D,lens", [
     (1, 1 << 20, 2, 150, 8, [700]),                       # 10 groups of 32 rows in two passes
     (2, 1 << 20, 3, 101, 40, [900, 77]),                  # 303 rows in three; the first rows of a sequence see nothing
@@ -213,10 +228,7 @@ def test_merges_of_two_threads():
     (1, 1 << 20, 1, 300, 136, [600])])                    # 19 groups of 16 rows in two
 def test_weights_of_more_rows_than_one_pass_takes(B, cap, H, T, D, lens):
     rng = np.random.default_rng(D + T)
-    c = cca.kv4_cache(B, 1, cap, D, k_scale=0.5, v_scale=2.0)
-    near = random_cache(B, 1, 1024, D, T)
-    for a, b in zip((c.k_codes, c.k_scales, c.v_codes, c.v_scales), (near.k_codes, near.k_scales, near.v_codes, near.v_scales)):
-        a[:, :, :1024] = b
+    c = mostly_empty_cache(B, 1, cap, D, 1024, T)
     q = 2 * bf16(rng, B, H, T, D)
     ws = cca.kv4_workspace(c, q, mass=True)
     rows = -(-H * T // 8) * 8
@@ -233,6 +245,115 @@ def test_weights_of_more_rows_than_one_pass_takes(B, cap, H, T, D, lens):
     cca.kv4_attention(q, c, i32(lens), mass_out=mo, ws=ws)
     check_attend(q, c, lens, o, lse, None, None, mo, kept_tail=-3.0)
     assert cca.attn_status(ws) == 0
+
+
+def groups_of_32_rows(c, q):
+    """Whether the call of these shapes runs on groups of 32 rows: the scores in its workspace say so."""
+    rows = q.shape[1] // c.Hkv * q.shape[2]
+    more = cca.kv4_workspace(c, q, mass=True).numel() - cca.kv4_workspace(c, q).numel()
+    return more >= 4 * c.B * c.Hkv * c.cap * 32 * -(-rows // 32)
+
+
+@pytest.mark.parametrize("D", [40, 64, 80, 128])
+@pytest.mark.parametrize("G,T", [(32, 1), (11, 3), (4, 16), (1, 40)])
+def test_attend_with_four_groups_of_rows(D, G, T):
+    """At least 32 rows a head and 2^20 slots: the kernels that take 32 rows at a time (33 and 40 rows: the last
+    group nearly empty)."""
+    B, Hkv, cap = 2, 2, 262144
+    lens = [6, 4999] if T > 1 else [0, 4999]
+    c = mostly_empty_cache(B, Hkv, cap, D, 5008, D + G)
+    nan_behind(c, lens)
+    q = 2 * bf16(np.random.default_rng(D + 7 * G + T), B, Hkv * G, T, D)
+    assert B * Hkv * cap >= 1 << 20 and G * T >= 32 and groups_of_32_rows(c, q)
+    ws = cca.kv4_workspace(c, q, mass=True)
+    o, lse = cca.kv4_attention(q, c, i32(lens), ws=ws)
+    check_attend(q, c, lens, o, lse)
+    mi, mo = torch.rand(B, Hkv, cap, device="cuda"), torch.full((B, Hkv, cap), -3.0, device="cuda")
+    o2, lse2 = cca.kv4_attention(q, c, i32(lens), mass_in=mi, mass_out=mo, ws=ws)
+    check_attend(q, c, lens, o2, lse2, None, mi, mo, kept_tail=-3.0)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2) and cca.attn_status(ws) == 0
+    for _ in range(3):
+        again = torch.full_like(mo, -3.0)
+        o2, lse2 = cca.kv4_attention(q, c, i32(lens), mass_in=mi, mass_out=again, ws=ws)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2) and torch.equal(mo, again)
+
+
+@pytest.mark.parametrize("D", [40, 64, 80, 128])
+@pytest.mark.parametrize("what", ["k", "v"])
+def test_attend_nan_rows_with_four_groups_of_rows(D, what):
+    """A NaN slot among those in use reaches the queries that see it and no other."""
+    T, n, cap = 20, 3150, 1 << 20
+    c = mostly_empty_cache(1, 1, cap, D, 3200, D)
+    blk = -(-D // 16) // 2
+    getattr(c, what + "_scales")[0, 0, n - 2, blk] = 0x7F          # seen by queries T-2 and T-1
+    q = bf16(np.random.default_rng(13), 1, 2, T, D)
+    assert groups_of_32_rows(c, q)
+    o, lse = cca.kv4_attention(q, c, i32([n]))
+    bad = o[0, :, T - 2:].isnan()
+    if what == "k":
+        assert bad.all() and lse[0, :, T - 2:].isnan().all()
+    else:
+        hit = torch.zeros(D, dtype=torch.bool, device="cuda")
+        hit[16 * blk:16 * blk + 16] = True
+        assert (bad == hit).all() and lse.isfinite().all()
+    assert o[0, :, :T - 2].isfinite().all() and lse[0, :, :T - 2].isfinite().all()
+
+
+@pytest.mark.parametrize("D", [64, 72, 128, 256])
+@pytest.mark.parametrize("n", [1, 15, 16, 17, 63, 64, 65, 127, 128, 129, 1000, 4095, 4096])
+def test_attend_lengths_with_nan_behind(D, n):
+    c = random_cache(1, 3, 4096, D, n)
+    nan_behind(c, [n])
+    q = 2 * bf16(np.random.default_rng(n), 1, 12, 2, D)
+    mo = torch.zeros(1, 3, 4096, device="cuda")
+    o, lse = cca.kv4_attention(q, c, i32([n]), mass_out=mo)
+    check_attend(q, c, [n], o, lse, None, None, mo, kept_tail=0.0)
+
+
+def test_attend_ragged_with_nan_behind():
+    rng = np.random.default_rng(61)
+    lens = [int(x) for x in rng.integers(0, 500, 70)]
+    c = random_cache(70, 2, 512, 128, 62)
+    nan_behind(c, lens)
+    q = bf16(rng, 70, 10, 3, 128)
+    o, lse = cca.kv4_attention(q, c, i32(lens))
+    check_attend(q, c, lens, o, lse)
+
+
+def test_attend_in_a_captured_fork():
+    """Two attentions on forked streams of one capture, joined by an eviction; replayed with other lengths."""
+    rng = np.random.default_rng(63)
+    B, Hkv, cap, D = 2, 2, 2048, 128
+    c, d = random_cache(B, Hkv, cap, D, 64), random_cache(B, Hkv, cap, D, 65)
+    small = cca.kv4_cache(B, Hkv, 256, D, k_scale=0.5, v_scale=2.0)
+    q, lens = [bf16(rng, B, 8, t, D) for t in (1, 5)], i32([2000, 300])
+    mass, kept, out = torch.rand(B, Hkv, cap, device="cuda"), torch.zeros(B, Hkv, 256, device="cuda"), i32([0, 0])
+    ws = [cca.kv4_workspace(c, q[0], mass=True), cca.kv4_workspace(d, q[1])]
+    torch.cuda.synchronize()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph):
+        here = torch.cuda.current_stream()
+        lens.add_(1)
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            o1, l1 = cca.kv4_attention(q[1], d, lens, ws=ws[1])
+        o0, l0 = cca.kv4_attention(q[0], c, lens, mass_in=mass, mass_out=mass, ws=ws[0])
+        here.wait_stream(side)
+        _, slots = cca.kv4_evict(c, lens, mass, 200, 8, small, kept, lens_out=out, ws=ws[0])
+        o2, l2 = cca.kv4_attention(q[0], small, out, ws=ws[0])
+    for start in ([2000, 300], [7, 2047], [0, 1]):
+        lens.copy_(i32(start))
+        m = mass.clone()
+        graph.replay()
+        n = i32([x + 1 for x in start])
+        e0, f0 = cca.kv4_attention(q[0], c, n, mass_in=m, mass_out=m)
+        e1, f1 = cca.kv4_attention(q[1], d, n)
+        small2, kept2 = cca.kv4_cache(B, Hkv, 256, D, k_scale=0.5, v_scale=2.0), torch.zeros_like(kept)
+        n2, s2 = cca.kv4_evict(c, n, m, 200, 8, small2, kept2)
+        e2, f2 = cca.kv4_attention(q[0], small2, n2)
+        for x, y in ((o0, e0), (l0, f0), (o1, e1), (l1, f1), (o2, e2), (l2, f2), (slots, s2), (mass, m), (out, n2)):
+            assert torch.equal(x, y)
+    assert cca.attn_status(ws[0]) == 0 and cca.attn_status(ws[1]) == 0
 
 
 # ------------------------------------------------------------------ buffers of weights used again
@@ -319,3 +440,57 @@ def test_evict_within_one_allocation():
     q = bf16(rng, B, 6, 1, D)
     for x, y in zip(cca.kv4_attention(q, back, got[0]), cca.kv4_attention(q, other, want[0])):
         assert torch.equal(x, y)
+
+
+# ------------------------------------------------------------------ eviction of many heads
+
+def many_heads(B, Hkv):
+    """As many heads as the eviction wants for one block of 512 threads a head."""
+    return B * Hkv >= 2 * torch.cuda.get_device_properties(0).multi_processor_count
+
+
+@pytest.mark.parametrize("kind", ["ties", "special"])
+@pytest.mark.parametrize("keep,recent", [(2040, 0), (2056, 65), (2048, 2048), (300, 1)])
+def test_evict_of_many_heads(kind, keep, recent):
+    rng = np.random.default_rng(keep + recent)
+    B, Hkv, cap, D = 48, 8, 4112, 64
+    assert many_heads(B, Hkv)
+    lens = [0, 1, keep, keep + 1, cap, 2047, 2048, 2049] + [int(x) for x in rng.integers(0, cap + 1, B - 8)]
+    src = random_cache(B, Hkv, cap, D, 67)
+    dst = cca.kv4_cache(B, Hkv, (keep + 15) // 16 * 16 + 16, D, k_scale=0.5, v_scale=2.0)
+    for t in (dst.k_codes, dst.k_scales, dst.v_codes, dst.v_scales):
+        t.fill_(0xCD)
+    mass = torch.tensor(MASSES[kind](rng, (B, Hkv, cap)), dtype=torch.float32).cuda()
+    mo, dl, ws = torch.full((B, Hkv, keep + 5), -7.0, device="cuda"), i32(lens), cca.kv4_workspace(src)
+    _, slots = cca.kv4_evict(src, dl, mass, keep, recent, dst, mo, lens_out=dl, ws=ws)
+    assert dl.tolist() == [min(n, keep) for n in lens] and cca.attn_status(ws) == 0
+    hm, got = mass.cpu().numpy(), slots.cpu().numpy()
+    for b, n in enumerate(lens):
+        m = min(n, keep)
+        for h in range(Hkv):
+            assert got[b, h].tolist() == K.evict(hm[b, h], n, keep, recent) + [-1] * (keep - m)
+        at = slots[b, :, :m, None].long()
+        for a, z in ((src.k_codes, dst.k_codes), (src.k_scales, dst.k_scales), (src.v_codes, dst.v_codes),
+                     (src.v_scales, dst.v_scales)):
+            assert torch.equal(z[b, :, :m], a[b].gather(1, at.expand(-1, -1, a.shape[-1]))) and (z[b, :, m:] == 0xCD).all()
+        assert torch.equal(mo[b, :, :m].view(torch.int32), mass[b].gather(1, at[..., 0]).view(torch.int32))
+        assert (mo[b, :, m:] == -7).all()
+
+
+@pytest.mark.parametrize("keep,recent", [(1000, 3), (32784, 0), (32790, 77)])
+def test_evict_of_many_long_heads(keep, recent):
+    """More slots than a block holds: the last ones' masses are read again for each pass."""
+    rng = np.random.default_rng(keep)
+    B, Hkv, cap, D = 48, 8, 32800 + 2048, 8
+    assert many_heads(B, Hkv)
+    lens = [cap, cap - 1, 32768, 32769, 5] + [int(x) for x in rng.integers(32000, cap + 1, B - 5)]
+    src, dst = random_cache(B, Hkv, cap, D, 69), cca.kv4_cache(B, Hkv, (keep + 15) // 16 * 16, D, k_scale=0.5, v_scale=2.0)
+    mass = torch.tensor(np.round(np.exp(rng.normal(size=(B, Hkv, cap))), 2), dtype=torch.float32).cuda()        # many ties
+    _, slots = cca.kv4_evict(src, i32(lens), mass, keep, recent, dst)
+    for b, n in enumerate(lens):
+        m, r = min(n, keep), min(recent, n, keep)
+        best = torch.sort(mass[b, :, :n - r], dim=-1, descending=True, stable=True).indices[:, :m - r]
+        last = torch.arange(n - r, n, device="cuda").expand(Hkv, -1)
+        assert torch.equal(slots[b, :, :m].long(), torch.cat((best.sort(-1).values, last), -1)) and (slots[b, :, m:] == -1).all()
+        if b < 2:
+            assert slots[b, 3, :m].tolist() == K.evict(mass[b, 3].cpu().numpy(), n, keep, recent)
