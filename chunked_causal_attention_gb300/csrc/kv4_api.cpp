@@ -115,6 +115,20 @@ int check_mass(const float* in, const float* out, int64_t floats, int64_t ld, in
     return ATTN_OK;
 }
 
+// Whether rows with these strides, of D elements each, lie apart: a call writes them, so no two may share memory.
+bool rows_apart(const Geom& g) {
+    struct Dim { int64_t stride, n; };
+    Dim d[] = {{g.sb, g.B}, {g.sh, g.H}, {g.st, g.T}};
+    std::sort(d, d + 3, [](const Dim& a, const Dim& b) { return a.stride < b.stride; });
+    __int128 extent = g.D;
+    for (const Dim& x : d) {
+        if (x.n == 1) continue;
+        if (x.stride < extent) return false;
+        extent += (__int128)x.stride * (x.n - 1);
+    }
+    return true;
+}
+
 int rows_common(const void* k, const void* v, const attn_shape* shape, const attn_kv4_cache* cache,
                 const int32_t* pos, const int32_t* cu, void* ws, size_t ws_bytes, cudaStream_t s, bool store) {
     Kv4RowsArgs a;
@@ -124,6 +138,7 @@ int rows_common(const void* k, const void* v, const attn_shape* shape, const att
     if ((st = shape_geom(shape, &g))) return st;
     if (!k || !v || !pos) return ATTN_E_INVAL;
     if (g.D != a.c.D || g.H != a.c.Hkv || g.B != (cu ? 1 : a.c.B)) return ATTN_E_INVAL;
+    if (!store && !rows_apart(g)) return ATTN_E_INVAL;
     a.rows = (int64_t)g.B * g.H * g.T;
     if (a.rows > INT32_MAX) return ATTN_E_INVAL;
     if (!aligned(k, 16) || !aligned(v, 16) || !aligned(pos, 4) || !aligned(cu, 4)) return ATTN_E_ALIGN;
@@ -141,6 +156,7 @@ int attend_geom(const attn_shape* shape, const Kv4Geom& c, Geom* g) {
     int st = shape_geom(shape, g);
     if (st) return st;
     if (g->D != c.D || g->B != c.B || g->H % c.Hkv) return ATTN_E_INVAL;
+    if (!rows_apart(*g)) return ATTN_E_INVAL;
     // the queries' rows are numbered in 31 bits
     if ((int64_t)g->B * g->H * g->T > INT32_MAX) return ATTN_E_INVAL;
     g->Hkv = c.Hkv;

@@ -367,7 +367,8 @@ int attn_kv4_store(const void* k, const void* v, const attn_shape* shape, const 
 
 /* The reverse of attn_kv4_store: the rows' values in bf16 (exact unless a value
  * leaves bf16's range). Rows that attn_kv4_store would skip are left as they were
- * (ATTN_E_BOUNDS). Errors as attn_kv4_store. */
+ * (ATTN_E_BOUNDS). Rows of k and v that share memory (strides under which they
+ * overlap) are ATTN_E_INVAL. Errors as attn_kv4_store. */
 int attn_kv4_load(const attn_kv4_cache* cache, const int32_t* pos, const int32_t* cu_seqlens,
                   const attn_shape* shape, void* k, void* v, void* ws, size_t ws_bytes, void* stream);
 
@@ -375,7 +376,7 @@ int attn_kv4_load(const attn_kv4_cache* cache, const int32_t* pos, const int32_t
  * rows stored before the call). q, o: bf16 with the shape's (query) strides,
  * shape B = cache B, H a multiple of cache Hkv (query head h reads key/value head
  * h / (H / Hkv); the shape's own Hkv fields are ignored), T = 1 for single-token
- * decoding, D = cache D. With n = lens[b] slots in use, query i sees
+ * decoding, D = cache D, no two rows in the same memory (o has the same strides). With n = lens[b] slots in use, query i sees
  * the slots j <= n - T + i:
  *   LSE_i = ln sum_j exp(scale * q_i . k_j),  O_i = sum_j exp(scale * q_i . k_j - LSE_i) v_j
  * A query that sees no slot (n - T + i < 0; n = 0) has O = 0 and LSE = -inf.

@@ -268,3 +268,17 @@ def test_weights_of_a_call_between_one_another():
     assert call(1 << 40, 1 << 40, 128) == 4
     assert call(1 << 40, (1 << 40) + 240, 128) == 1 and call(1 << 40, (1 << 40) + 272, 128) == 1
     assert call(1 << 40, 1 << 41, 1 << 62) == 1
+
+
+@pytest.mark.parametrize("B,H,T,sb,sh,st,ok", [
+    (2, 2, 3, 384, 192, 64, True), (2, 2, 3, 384, 64, 128, True), (2, 2, 3, 64, 128, 256, True), (2, 2, 3, 4096, 72, 160, True),
+    (2, 2, 1, 128, 64, 8, True), (2, 2, 3, 384, 192, 56, False), (2, 2, 3, 384, 64, 64, False), (2, 2, 3, 320, 192, 64, False),
+    (2, 2, 3, 256, 128, 64, False), (2, 2, 3, 1 << 62, 1 << 62, 1 << 62, False)])
+def test_rows_that_are_written_lie_apart(B, H, T, sb, sh, st, ok):
+    """Queries' strides are the outputs' too: windows that overlap would be written twice. Rows to store may overlap."""
+    s, c, L = cca.make_shape(B, H, T, 64, sb, st, sh, 0.125), cache(B=B, Hkv=H, cap=64), cca.lib()
+    # a missing workspace (4) is seen after the strides (1)
+    want = 4 if ok else 1
+    assert L.attn_kv4_attend(FAKE, ctypes.byref(s), ctypes.byref(c), FAKE, FAKE, FAKE, None, None, 0, None, 0, None) == want
+    assert L.attn_kv4_load(ctypes.byref(c), FAKE, None, ctypes.byref(s), FAKE, FAKE, None, 0, None) == want
+    assert L.attn_kv4_store(FAKE, FAKE, ctypes.byref(s), ctypes.byref(c), FAKE, None, None, 0, None) == 4
