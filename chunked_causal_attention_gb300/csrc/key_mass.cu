@@ -764,13 +764,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// Whether the window kernel takes these rows: one chunk of few rows, for which the work of
-// the tiles inside the chunk (all rows, without the causal half) does not matter.
+// Whether the window kernel takes these rows: one chunk whose rows of a group fit. It lays
+// them out first, 7 us for each 128 (above 128 dims 11), and then takes nb blocks a key
+// tile, where the general kernel takes a block of each head, 0.72 us each; a tile costs the
+// general kernel no less than 1.8 us and this one 0.95. So the tiles of an SM decide. Both
+// measured, general / window, us, at w rows, G heads a group, key/value heads x keys:
+//   128 dims, w 1,   G 4:  8 x 1K 12 / 9,  8 x 16K 27 / 13,  8 x 128K 157 / 52
+//             w 64,  G 4:  8 x 1K 12 / 25, 8 x 16K 27 / 31,  8 x 32K 45 / 38,  8 x 128K 158 / 86
+//             w 128, G 4:  8 x 1K 14 / 39, 8 x 16K 29 / 54,  8 x 128K 162 / 181
+//             w 128, G 1:  8 x 4K 10 / 17, 8 x 16K 20 / 21,  8 x 32K 31 / 25,  32 x 64K 192 / 101
+//             w 64,  G 8:  4 x 8K 16 / 41, 4 x 64K 72 / 72,  4 x 128K 134 / 113
+//   64 dims,  w 256, G 4:  8 x 1K 17 / 64, 8 x 128K 238 / 376
+//   256 dims, w 32,  G 4:  8 x 8K 20 / 21, 8 x 16K 31 / 25;  w 128, G 1: 32 x 8K 40 / 47, 32 x 16K 69 / 64
 template <int DT>
 bool window(const MassArgs& a, const attn_chunk* chunks) {
     if (a.n != 1) return false;
-    const int64_t w = chunks[0].q_end - chunks[0].q_begin;
-    return w * (a.g.H / a.g.Hkv) <= 128 * WinLayout<DT>::MAX_NB && 4 * w <= a.g.T;
+    const int64_t w = chunks[0].q_end - chunks[0].q_begin, G = a.g.H / a.g.Hkv, rows = w * G, nb = (rows + 127) / 128;
+    if (nb > WinLayout<DT>::MAX_NB) return false;
+    const int64_t tiles = (int64_t)a.g.B * a.g.Hkv * ((a.g.T + 127) / 128), sms = device_sm_count(), n = (tiles + sms - 1) / sms;
+    const int64_t blocks = G * ((w + 127) / 128);
+    // in tenths of a block: what is saved a tile, against the rows' layout and two blocks
+    return n * (std::max<int64_t>(10 * blocks, 25) - std::max<int64_t>(10 * nb, 13)) > (DT > 128 ? 150 : 100) * rows / 128 + 20;
 }
 
 template <int DT>

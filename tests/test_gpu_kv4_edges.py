@@ -19,7 +19,8 @@ from chunked_causal_attention_gb300 import _lib
 
 from oracle import kv4 as K
 
-from test_gpu_kv4 import MASSES, MASS_PLANS, bf16, built, cached, check_attend, check_mass, f64, i32, random_cache
+from test_gpu_kv4 import (MASSES, MASS_PLANS, SUM, bf16, built, cached, check_attend, check_mass, f64, i32, random_cache,
+                          score_error)
 
 pytestmark = pytest.mark.gpu
 
@@ -124,6 +125,100 @@ def test_key_mass_of_keys_that_are_not_finite(D, H, Hkv, w, pieces):
     assert torch.equal(got[..., other], want[..., other])
 
 
+# D, query and key/value heads, batch, rows, keys: long enough for the kernel of few rows over many keys
+LONG = [(128, 32, 8, 1, 1, 16384), (128, 8, 8, 1, 100, 40007), (64, 40, 8, 1, 50, 40000), (80, 24, 8, 1, 5, 16384),
+        (256, 16, 8, 2, 60, 20000), (40, 64, 8, 1, 60, 30001), (64, 8, 1, 3, 33, 120000), (128, 24, 3, 1, 40, 100001)]
+
+
+def window_call(*a, **kw):
+    """key_mass, as the kernel of few rows takes it: one launch, where the general one uploads its lists."""
+    launches = cca.kernel_launches()
+    out = cca.key_mass(*a, **kw)
+    assert cca.kernel_launches() - launches == 1
+    return out
+
+
+def check_rows(q, k, lse, chunk, got, scale, heads, mass_in=None):
+    """check_mass of one chunk for some key/value heads, with errors from the chunk's rows alone (all rows against
+    all keys of a long prompt would not fit)."""
+    a, b, ctx, _ = chunk
+    G = q.shape[1] // k.shape[1]
+    for i in range(q.shape[0]):
+        for hk in heads:
+            qs, ls, kh = f64(q[i, hk * G:hk * G + G]), f64(lse[i, hk * G:hk * G + G]), f64(k[i, hk])
+            ref, rows = K.key_mass(qs, kh, ls, [chunk], scale), ls[:, a:b]
+            e = score_error(qs[:, a:b].reshape(-1, qs.shape[-1]), kh[ctx:b], scale) + 2.0 ** -22 * np.abs(rows[np.isfinite(rows)]).max()
+            base = f64(mass_in[i, hk]) if mass_in is not None else 0.0
+            tol = (2 * e + SUM) * ref + 2.0 ** -22 * np.abs(base + ref) + 1e-35
+            assert (np.abs(f64(got[i, hk]) - base - ref) <= tol).all()
+
+
+@pytest.mark.parametrize("D,H,Hkv,B,w,T", LONG)
+def test_key_mass_of_few_rows_over_many_keys(D, H, Hkv, B, w, T):
+    rng = np.random.default_rng(D + w)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(T)
+    scale, heads = D ** -0.5, sorted({0, Hkv - 1})
+    q = 2 * torch.randn(B, H, T, D, device="cuda", generator=g).bfloat16()
+    k = torch.randn(B, Hkv, T, D, device="cuda", generator=g).bfloat16()
+    q[..., 0] = q[..., 0].abs() + 0.25
+    chunks = [(T - w - 3, T - 3, 300, 0)]                            # the first and last keys are seen by no row
+    lse = log_sum_exps(q, k, chunks, scale)
+    lse[:, 0, T - 4] = -math.inf                                     # a row that counts for nothing
+    ws = cca.key_mass_workspace(q, k, chunks)
+    want = window_call(q, k, lse, chunks, ws=ws)
+    check_rows(q, k, lse, chunks[0], want, scale, heads)
+    assert (want[..., :300] == 0).all() and (want[..., T - 3:] == 0).all()
+    m = torch.rand(B, Hkv, T, device="cuda")
+    start = m.clone()
+    window_call(q, k, lse, chunks, mass_in=m, mass_out=m, ws=ws)
+    check_rows(q, k, lse, chunks[0], m, scale, heads, mass_in=start)
+    for _ in range(3):
+        assert torch.equal(window_call(q, k, lse, chunks, ws=ws), want)
+    # rows without a log-sum-exp that hold anything
+    rows = [T - 4 - i for i in range(0, w, 7)]
+    for i, t in enumerate(rows):
+        lse[:, i % H, t] = -math.inf
+    some = window_call(q, k, lse, chunks, ws=ws)
+    assert torch.equal(window_call(unset_rows(q, rows), k, lse, chunks, ws=ws), some)
+    check_rows(q, k, lse, chunks[0], some, scale, heads)
+    # keys that are not finite
+    low, high, nan = [300, 305, 1000, T // 2], [306, 1001], [309, 1002]
+    bad = k.clone()
+    bad[:, :, low, 0], bad[:, :, high, 0], bad[:, :, nan, D - 1] = -math.inf, math.inf, math.nan
+    lse = log_sum_exps(q, k, chunks, scale)
+    want, got = (window_call(q, x, lse, chunks, ws=ws) for x in (k, bad))
+    assert (got[..., low] == 0).all() and (got[..., high] == math.inf).all() and got[..., nan].isnan().all()
+    other = torch.ones(T, dtype=torch.bool)
+    other[low + high + nan] = False
+    assert torch.equal(got[..., other], want[..., other]) and cca.attn_status(ws) == 0
+
+
+def test_waits_of_the_kernel_of_few_rows_run_out(monkeypatch):
+    rng = np.random.default_rng(71)
+    q, k, chunks = bf16(rng, 1, 32, 16384, 64), bf16(rng, 1, 8, 16384, 64), [(16380, 16384, 0, 0)]
+    lse, ws = log_sum_exps(q, k, chunks, 0.125), cca.key_mass_workspace(q, k, chunks)
+    want = window_call(q, k, lse, chunks, ws=ws)
+    monkeypatch.setenv("ATTN_TEST_STALL_PRODUCER", "1")
+    monkeypatch.setenv("ATTN_WAIT_LIMIT_MS", "200")
+    window_call(q, k, lse, chunks, ws=ws)
+    assert cca.attn_status(ws) == 6
+    monkeypatch.delenv("ATTN_TEST_STALL_PRODUCER")
+    assert torch.equal(window_call(q, k, lse, chunks, ws=ws), want) and cca.attn_status(ws) == 0
+
+
+@pytest.mark.parametrize("D,H,Hkv,w,T,one", [
+    (128, 32, 8, 1, 16384, True), (128, 32, 8, 64, 131072, True), (128, 32, 8, 64, 2048, False), (128, 32, 8, 128, 16384, False),
+    (64, 32, 8, 256, 16384, False), (128, 8, 8, 128, 2048, False), (128, 8, 8, 128, 65536, True), (256, 8, 8, 128, 2048, False)])
+def test_which_kernel_takes_a_window(D, H, Hkv, w, T, one):
+    """By the tiles of keys that an SM takes: below, the general kernel is up to five times as fast."""
+    q, k = torch.zeros(1, H, T, D, dtype=torch.bfloat16, device="cuda"), torch.zeros(1, Hkv, T, D, dtype=torch.bfloat16, device="cuda")
+    chunks, lse = [(T - w, T, 0, 0)], torch.zeros(1, H, T, device="cuda")
+    ws, launches = cca.key_mass_workspace(q, k, chunks), cca.kernel_launches()
+    cca.key_mass(q, k, lse, chunks, ws=ws)
+    assert (cca.kernel_launches() - launches == 1) == one
+
+
 # ------------------------------------------------------------------ calls of several threads at once
 
 def at_once(*calls, times):
@@ -169,13 +264,13 @@ def test_evictions_of_two_threads():
 def test_window_masses_of_two_threads():
     """Windows of different length ask for different amounts of shared memory in the same kernel."""
     calls, results, fn = [], [], cca.lib().attn_key_mass
-    for w in (1, 250):
+    for w in (1, 32):
         rng = np.random.default_rng(w)
-        q, k = bf16(rng, 1, 2, 1024, 64), bf16(rng, 1, 1, 1024, 64)
-        chunks = [(1024 - w, 1024, 0, 0)]
+        q, k = bf16(rng, 1, 64, 8192, 64), bf16(rng, 1, 8, 8192, 64)
+        chunks = [(8192 - w, 8192, 0, 0)]
         lse = log_sum_exps(q, k, chunks, 0.125)
-        ws, shape, out = cca.key_mass_workspace(q, k, chunks), cca.shape_of(q, None, False, k), torch.zeros(1, 1, 1024, device="cuda")
-        want = cca.key_mass(q, k, lse, chunks)
+        ws, shape, out = cca.key_mass_workspace(q, k, chunks), cca.shape_of(q, None, False, k), torch.zeros(1, 8, 8192, device="cuda")
+        want = window_call(q, k, lse, chunks, ws=ws)
         arr, n = _lib.chunk_array(chunks)
         args = (q.data_ptr(), k.data_ptr(), lse.data_ptr(), arr, n, ctypes.byref(shape), None, out.data_ptr(),
                 ws.data_ptr(), ws.numel())
