@@ -20,14 +20,18 @@
 //   warp 3      adds up the groups' sums of a finished item, in order, and writes them
 // Per block 2 * 128 * 128 * D FLOP (512 cycles of an SM at D = 128) stand against
 // 128 * 128 exponentials (512 cycles at 32 a cycle): both pipes are needed whole.
-// Measured: 8192 tokens of 32 heads of 128 dims 245 us (1120 TFLOP/s, 1060 cycles a
-// block), 32768 tokens 3.23 ms (1360 TFLOP/s); both pipes are 53% busy. Copies without
-// the exponentials (195 us) and also without most products (154 to 179 us) show that the
+// Measured, the kernel alone: 8192 tokens of 32 heads of 128 dims 245 to 260 us (1060 to
+// 1120 TFLOP/s, 1060 cycles a block; a call 260), 32768 tokens 3.3 to 3.4 ms (1290 to 1340
+// TFLOP/s); both pipes are 53% busy at 8192. Copies without the
+// exponentials (195 us) and also without most products (154 to 179 us) show that the
 // hand-over of a block from pipe to pipe is what is left; three groups hide more of it
 // than two (266 us) and than four on fewer registers (299 us).
 //
 // Sums: 128 weights of a block in four fp32 chains, blocks with a compensated sum
-// (Kahan), so that a million rows lose no more than a block does.
+// (Kahan), so that a million rows lose no more than a block does. (The kernel for few
+// rows has at most eight blocks a key and adds them plainly.) A weight's own error is
+// larger: scores are summed by the tensor core, 2^(s c - lse2) is one FMA and ex2.approx;
+// 7e-7 of the masses at 8192 tokens, where fp32 throughout has 2e-7.
 //
 // Every mbarrier wait is bounded (ATTN_E_TIMEOUT); items and chunks are checked
 // before use (ATTN_E_BOUNDS).
@@ -516,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // each row. A key tile is one group's: its rows' weights are summed by one thread in
 // order. The keys' bytes are the floor: 32 KB at D = 128 are 1390 cycles of an SM's share
 // of the memory rate, two blocks of products and exponentials 1024. Measured: 64 rows of 4
-// heads over 128K keys of 8 key/value heads 85 us (3.2 TB/s, 2500 cycles a tile; 158 us with
+// heads over 128K keys of 8 key/value heads 86 us (3.1 TB/s, 2500 cycles a tile; 158 us with
 // the general kernel, which brings the queries from L2 again for every tile), one row 51 us
 // (5.2 TB/s). A trace shows the MMA thread busy all the time at 250 to 450 cycles a step
 // (wait, eight products, commit) and the groups waiting for it a third of theirs; a second
