@@ -127,14 +127,18 @@ def _rows_checks(fn: str, cache: KV4Cache, k, v, pos, cu_seqlens, ws) -> None:
 
 def kv4_load(cache: KV4Cache, pos, T: int, cu_seqlens=None, k=None, v=None, ws=None, stream=None):
     """The values of T rows from slot pos[b] on, bf16 [B, Hkv, T, D]; with cu_seqlens
-    packed [T, Hkv, D]. k and v may be given (rows outside the cache stay as they were)."""
+    packed [T, Hkv, D]. k and v may be given (rows outside the cache stay as they were), views
+    of wider tensors too; one that is not given has the other's strides."""
     import torch
     shape = (T, cache.Hkv, cache.D) if cu_seqlens is not None else (cache.B, cache.Hkv, T, cache.D)
     with _lib._alloc_on(stream, cache.device):
-        if k is None:
-            k = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
-        if v is None:
-            v = torch.empty_like(k)
+        given = v if k is None else k
+        if given is None:
+            k, v = (torch.empty(shape, dtype=torch.bfloat16, device=cache.device) for _ in range(2))
+        elif k is None or v is None:
+            # one shape describes both, so the other has the strides of the one that is given
+            other = torch.empty_strided(given.shape, given.stride(), dtype=torch.bfloat16, device=cache.device)
+            k, v = (other, v) if k is None else (k, other)
         if ws is None:
             ws = kv4_workspace(cache)
     _, ref = cache._shape(k, 1.0, cu_seqlens is not None)
@@ -153,7 +157,8 @@ def kv4_attention(q, cache: KV4Cache, lens, scale: Optional[float] = None, mass_
     """(o, lse) of the newest T tokens of each sequence, q bf16 [B, H, T, D], over the
     lens[b] slots in use (their own included). mass_out fp32 [B, Hkv, n]: each slot's
     weight over the call's rows is added to mass_in (None: zeros; may be mass_out). The
-    entry of a slot that was appended since has to be 0 in mass_in."""
+    entry of a slot that was appended since has to be 0 in mass_in. o has q's strides, gaps
+    included: for a few rows of a long tensor pass a contiguous copy."""
     import torch
     shape, ref = cache._shape(q, scale, False)
     if ws is None:

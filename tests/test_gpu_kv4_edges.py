@@ -589,3 +589,19 @@ def test_evict_of_many_long_heads(keep, recent):
         assert torch.equal(slots[b, :, :m].long(), torch.cat((best.sort(-1).values, last), -1)) and (slots[b, :, m:] == -1).all()
         if b < 2:
             assert slots[b, 3, :m].tolist() == K.evict(mass[b, 3].cpu().numpy(), n, keep, recent)
+
+
+# ------------------------------------------------------------------ layouts
+
+@pytest.mark.parametrize("give", ["k", "v", "both", "neither"])
+def test_load_into_a_view(give):
+    """Rows into views of wider tensors, one of the two given or both."""
+    c, pos = random_cache(2, 3, 64, 80, 73), i32([0, 30])
+    wide = [torch.full((2, 20, 3, 128), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    k, v = (w.permute(0, 2, 1, 3)[..., :80] for w in wide)
+    want = cca.kv4_load(c, pos, 20)
+    got = cca.kv4_load(c, pos, 20, k=k if give in ("k", "both") else None, v=v if give in ("v", "both") else None)
+    for x, y in zip(got, want):
+        assert torch.equal(x, y) and (give == "neither" or x.stride() == k.stride())
+    for w in wide:
+        assert (w[..., 80:] == 7).all()
