@@ -605,3 +605,22 @@ def test_load_into_a_view(give):
         assert torch.equal(x, y) and (give == "neither" or x.stride() == k.stride())
     for w in wide:
         assert (w[..., 80:] == 7).all()
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_key_mass_of_few_rows_strided(packed):
+    """Token-major storage of wider rows, as a batch view and as packed tokens, in the kernel of few rows."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(75)
+    T, D, w, scale = 40010, 80, 20, 80 ** -0.5
+    q = torch.randn(3, T, 16, 128, device="cuda", generator=g).bfloat16()[1:, ..., :D]
+    k = torch.randn(3, T, 8, 96, device="cuda", generator=g).bfloat16()[1:, ..., :D]
+    chunks = [(T - w - 5, T - 5, 11, 0)]
+    qh, kh = (x.permute(0, 2, 1, 3) for x in (q, k))
+    lse = log_sum_exps(qh, kh, chunks, scale)
+    if packed:
+        got = torch.cat([window_call(q[b], k[b], lse[b:b + 1], chunks, packed=True) for b in range(2)])
+    else:
+        got = window_call(qh, kh, lse, chunks)
+    check_rows(qh, kh, lse, chunks[0], got, scale, [0, 7])
+    assert torch.equal(got, window_call(qh.contiguous(), kh.contiguous(), lse, chunks))
