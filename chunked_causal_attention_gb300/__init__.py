@@ -11,14 +11,17 @@ from __future__ import annotations
 from typing import Optional, Sequence
 
 from ._lib import (_alloc_on, AttnError, EXPORTS, KV4_ATTEND, KV4_ATTEND_MASS, KV4_ROWS, PASS_BWD, PASS_BWD_CHUNK, PASS_FWD,
-                   PASS_MASS, PLAN_FLOPS, PLAN_FLOPS_RESPLIT_EDGES,
+                   PAGED_ATTEND, PAGED_RESERVE, PAGED_STORE, PASS_MASS, PLAN_FLOPS, PLAN_FLOPS_RESPLIT_EDGES,
                    PLAN_UNIFORM, attn_bwd, attn_bwd_chunk, attn_bwd_dq, attn_bwd_prep, attn_bwd_tiles, attn_fwd,
                    attn_fwd_merge, attn_fwd_noalloc, attn_fwd_tiles, attn_key_mass, attn_kv4_attend, attn_kv4_cache,
-                   attn_kv4_evict, attn_kv4_load, attn_kv4_store, attn_kv4_workspace_size, attn_noalloc_status, attn_plan,
+                   attn_kv4_evict, attn_kv4_load, attn_kv4_store, attn_kv4_workspace_size, attn_noalloc_status, attn_paged_attend,
+                   attn_paged_cache, attn_paged_reserve, attn_paged_store, attn_paged_workspace_size, attn_plan,
                    attn_plan_infinipipe, attn_plan_multiplex, attn_plan_varlen, attn_shape, attn_status,
                    attn_workspace_size, lib, make_shape, shape_of, strerror, version,
                    kernel_launches)
 from .kv4 import KV4Cache, kv4_attention, kv4_cache, kv4_evict, kv4_load, kv4_store, kv4_workspace
+from .paged import (PagedCache, PagedTables, paged_attention, paged_cache, paged_reserve, paged_store, paged_tables,
+                    paged_workspace)
 
 __all__ = ["AttnError", "EXPORTS", "PLAN_UNIFORM", "PLAN_FLOPS", "PLAN_FLOPS_RESPLIT_EDGES", "attn_plan",
            "attn_plan_varlen", "attn_plan_infinipipe", "attn_plan_multiplex", "attn_workspace_size", "attn_fwd", "attn_fwd_tiles", "attn_fwd_merge", "attn_bwd",
@@ -28,7 +31,10 @@ __all__ = ["AttnError", "EXPORTS", "PLAN_UNIFORM", "PLAN_FLOPS", "PLAN_FLOPS_RES
            "PASS_FWD", "PASS_BWD", "PASS_BWD_CHUNK", "PASS_MASS", "plan_infinipipe",
            "attn_key_mass", "attn_kv4_cache", "attn_kv4_workspace_size", "attn_kv4_store", "attn_kv4_load",
            "attn_kv4_attend", "attn_kv4_evict", "KV4_ROWS", "KV4_ATTEND", "KV4_ATTEND_MASS", "KV4Cache", "kv4_cache",
-           "kv4_workspace", "kv4_store", "kv4_load", "kv4_attention", "kv4_evict", "key_mass", "key_mass_workspace", "lib", "strerror", "version",
+           "kv4_workspace", "kv4_store", "kv4_load", "kv4_attention", "kv4_evict",
+           "attn_paged_cache", "attn_paged_workspace_size", "attn_paged_reserve", "attn_paged_store", "attn_paged_attend",
+           "PAGED_STORE", "PAGED_RESERVE", "PAGED_ATTEND", "PagedCache", "PagedTables", "paged_cache", "paged_tables",
+           "paged_workspace", "paged_reserve", "paged_store", "paged_attention", "key_mass", "key_mass_workspace", "lib", "strerror", "version",
            "kernel_launches"]
 
 

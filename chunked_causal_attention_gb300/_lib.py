@@ -28,7 +28,8 @@ PLAN_FLOPS_RESPLIT_EDGES = 2
 EXPORTS = ("attn_plan", "attn_plan_varlen", "attn_plan_multiplex", "attn_plan_infinipipe", "attn_workspace_size", "attn_fwd", "attn_fwd_tiles",
            "attn_fwd_merge", "attn_bwd", "attn_bwd_prep", "attn_bwd_tiles", "attn_bwd_dq",
            "attn_bwd_chunk", "attn_key_mass", "attn_kv4_workspace_size", "attn_kv4_store", "attn_kv4_load",
-           "attn_kv4_attend", "attn_kv4_evict", "attn_fwd_noalloc", "attn_noalloc_status", "attn_status", "attn_strerror",
+           "attn_kv4_attend", "attn_kv4_evict", "attn_paged_workspace_size", "attn_paged_reserve", "attn_paged_store",
+           "attn_paged_attend", "attn_fwd_noalloc", "attn_noalloc_status", "attn_status", "attn_strerror",
            "attn_version", "attn_kernel_launches")
 
 # attn_workspace_size passes
@@ -41,6 +42,11 @@ PASS_MASS = 3
 KV4_ROWS = 0
 KV4_ATTEND = 1
 KV4_ATTEND_MASS = 2
+
+# attn_paged_workspace_size ops
+PAGED_STORE = 0
+PAGED_RESERVE = 1
+PAGED_ATTEND = 2
 
 # Size of the library-held scratch area of attn_fwd_noalloc (ATTN_NOALLOC_SCRATCH_BYTES).
 NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -71,6 +77,12 @@ class attn_kv4_cache(ctypes.Structure):
                 ("v_scales", ctypes.c_void_p), ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
 
 
+class attn_paged_cache(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_int64), ("Hkv", ctypes.c_int64), ("page", ctypes.c_int64), ("D", ctypes.c_int64),
+                ("sp", ctypes.c_int64), ("sh", ctypes.c_int64), ("st", ctypes.c_int64),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p)]
+
+
 _lib: Optional[ctypes.CDLL] = None
 
 _VP = ctypes.c_void_p
@@ -79,6 +91,7 @@ _I64 = ctypes.c_int64
 _CP = ctypes.POINTER(attn_chunk)
 _SP = ctypes.POINTER(attn_shape)
 _KP = ctypes.POINTER(attn_kv4_cache)
+_PP = ctypes.POINTER(attn_paged_cache)
 _SZ = ctypes.c_size_t
 _SIG = {
     "attn_plan": ([_I64, _I32, _I32, _CP, _I32, ctypes.POINTER(_I32)], ctypes.c_int),
@@ -105,6 +118,11 @@ _SIG = {
     "attn_kv4_load": ([_KP, _VP, _VP, _SP, _VP, _VP, _VP, _SZ, _VP], ctypes.c_int),
     "attn_kv4_attend": ([_VP, _SP, _KP, _VP, _VP, _VP, _VP, _VP, _I64, _VP, _SZ, _VP], ctypes.c_int),
     "attn_kv4_evict": ([_KP, _VP, _VP, _I64, _I32, _I32, _KP, _VP, _VP, _I64, _VP, _VP, _SZ, _VP], ctypes.c_int),
+    "attn_paged_workspace_size": ([_PP, _SP, _I64, _I32, ctypes.POINTER(_SZ)], ctypes.c_int),
+    "attn_paged_reserve": ([_VP, _VP, _I64, _I64, _I64, _VP, _VP, _VP, _I64, _I64, _VP, _VP, _VP, _VP, _I64, _VP, _SZ, _VP],
+                           ctypes.c_int),
+    "attn_paged_store": ([_VP, _VP, _SP, _PP, _VP, _VP, _SZ, _VP], ctypes.c_int),
+    "attn_paged_attend": ([_VP, _SP, _PP, _VP, _I64, _I64, _VP, _VP, _I64, _VP, _VP, _VP, _SZ, _VP], ctypes.c_int),
     "attn_fwd_noalloc": ([_VP, _VP, _VP, _CP, _I32, _SP, _VP, _VP, _VP], ctypes.c_int),
     "attn_noalloc_status": ([_VP], ctypes.c_int),
     "attn_status": ([_VP, _VP], ctypes.c_int),
@@ -515,6 +533,68 @@ def attn_kv4_evict(src: attn_kv4_cache, lens, mass, keep: int, recent: int, dst:
         _check(fn, lib().attn_kv4_evict(ctypes.byref(src), _ptr(lens), _ptr(mass), ld, keep, recent,
                                         ctypes.byref(dst), _ptr(lens_out), _ptr(mass_out), ld_out, _ptr(slots),
                                         _ptr(ws), ws.numel() * ws.element_size(), _stream_of(stream, lens)))
+
+
+# ------------------------------------------------------------------ paged cache
+
+def attn_paged_workspace_size(cache: Optional[attn_paged_cache], shape: Optional[attn_shape], B: int, op: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check("attn_paged_workspace_size", lib().attn_paged_workspace_size(
+        None if cache is None else ctypes.byref(cache), None if shape is None else ctypes.byref(shape), B, op,
+        ctypes.byref(out)))
+    return out.value
+
+
+def _table_ld(fn: str, table) -> int:
+    """Row distance of an int32 [B, max_pages] tensor whose rows are contiguous."""
+    import torch
+    if not (table.dim() == 2 and table.dtype == torch.int32 and (table.shape[1] == 1 or table.stride(1) == 1)):
+        raise AttnError(fn, ATTN_E_INVAL)
+    return table.stride(0) if table.shape[0] > 1 else table.shape[1]
+
+
+def attn_paged_reserve(add, lens, page: int, n_free, free_pages, table, lens_out, n_free_out, cu_seqlens, slots, ws,
+                       stream=None) -> None:
+    fn = "attn_paged_reserve"
+    _same_device(fn, table, add, lens, n_free, free_pages, lens_out, n_free_out, cu_seqlens, slots, ws)
+    ld = _table_ld(fn, table)
+    B = table.shape[0]
+    _expect_flat(fn, "int32", B, add, lens, lens_out)
+    _expect_flat(fn, "int32", 1, n_free, n_free_out)
+    _expect_flat(fn, "int32", B + 1, cu_seqlens)
+    _expect_flat(fn, "int32", free_pages.numel(), free_pages)
+    _expect_flat(fn, "int32", slots.numel(), slots)
+    with _on(table):
+        _check(fn, lib().attn_paged_reserve(
+            _ptr(add), _ptr(lens), B, page, free_pages.numel(), _ptr(n_free), _ptr(free_pages), _ptr(table), ld,
+            table.shape[1], _ptr(lens_out), _ptr(n_free_out), _ptr(cu_seqlens), _ptr(slots), slots.numel(), _ptr(ws),
+            ws.numel() * ws.element_size(), _stream_of(stream, table)))
+
+
+def attn_paged_store(k, v, shape, cache: attn_paged_cache, slots, ws, stream=None) -> None:
+    fn = "attn_paged_store"
+    _same_device(fn, k, v, slots, ws)
+    _expect(fn, shape, "q", k, v)
+    _expect_flat(fn, "int32", shape.T, slots)
+    with _on(k):
+        _check(fn, lib().attn_paged_store(k.data_ptr(), v.data_ptr(), ctypes.byref(shape), ctypes.byref(cache),
+                                          _ptr(slots), _ptr(ws), ws.numel() * ws.element_size(), _stream_of(stream, k)))
+
+
+def attn_paged_attend(q, shape, cache: attn_paged_cache, table, lens, cu_seqlens, o, lse, ws, stream=None) -> None:
+    fn = "attn_paged_attend"
+    _same_device(fn, q, table, lens, cu_seqlens, o, lse, ws)
+    _expect(fn, shape, "q", q, o)
+    _expect(fn, shape, "lse", lse)
+    ld = _table_ld(fn, table)
+    B = table.shape[0]
+    _expect_flat(fn, "int32", B, lens)
+    _expect_flat(fn, "int32", B + 1, cu_seqlens)
+    with _on(q):
+        _check(fn, lib().attn_paged_attend(
+            q.data_ptr(), ctypes.byref(shape), ctypes.byref(cache), _ptr(table), ld, table.shape[1], _ptr(lens),
+            _ptr(cu_seqlens), B, o.data_ptr(), lse.data_ptr(), _ptr(ws), ws.numel() * ws.element_size(),
+            _stream_of(stream, q)))
 
 
 def attn_fwd_noalloc(q, k, v, chunks, shape, o, lse, stream=None) -> None:

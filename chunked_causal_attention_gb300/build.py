@@ -21,7 +21,8 @@ LIB = os.path.join(PKG, "libattn.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["attn_plan.cpp", "attn_api.cpp", "tmap.cpp", "fwd_tc.cu", "bwd_tc.cu", "merge.cu", "bwd_aux.cu", "noalloc.cu",
-           "upload.cu", "bwd_wide.cu", "kv4_api.cpp", "kv4_rows.cu", "kv4_attend.cu", "kv4_evict.cu", "key_mass.cu"]
+           "upload.cu", "bwd_wide.cu", "kv4_api.cpp", "kv4_rows.cu", "kv4_attend.cu", "kv4_evict.cu", "key_mass.cu", "paged_api.cpp", "paged_rows.cu",
+           "paged_attend.cu"]
 
 
 def nvcc() -> str:

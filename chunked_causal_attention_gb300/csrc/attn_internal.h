@@ -19,7 +19,8 @@ constexpr size_t kHeaderBytes = 256;  // workspace header: status word, counters
 // Workspace header (first 256 bytes of every workspace).
 struct WsHeader {
     uint32_t status;      // first device-side error code (ATTN_E_*), 0 if none
-    uint32_t counter[3];  // work queues of the persistent kernels: [0] forward tiles, [1] backward tiles
+    uint32_t counter[3];  // work queues of the persistent kernels: [0] forward tiles, [1] backward tiles,
+                          // [2] paged attention (zero between calls)
 };
 
 // One forward work item: query rows [r0, r1) against keys [kv_lo, kv_hi)
@@ -181,8 +182,8 @@ struct TcMaps {
 
 // Rank-4 TMA map of a bf16 [B, T, H, D]-strided tensor: axis 0 is the head
 // dim, axes 1..3 are token/head/batch sorted by stride; box = 64 elements
-// (128 bytes, 128-byte swizzle) x box_rows tokens. Fills `mp`. False on failure.
-bool make_tile_map(CUtensorMap* m, const void* base, const Geom& g, TcMaps& mp, int box_rows = 128);
+// (128 bytes, 128-byte swizzle) x box_rows tokens x box_heads heads. Fills `mp`. False on failure.
+bool make_tile_map(CUtensorMap* m, const void* base, const Geom& g, TcMaps& mp, int box_rows = 128, int box_heads = 1);
 // Rank-3 TMA map of the fp32 dQ accumulator [B*H][rows][D]: box of 32 floats
 // (128 bytes, 128-byte swizzle) x 128 tokens, used for reduce-adds.
 bool make_dq_acc_map(CUtensorMap* m, float* dq_acc, const Geom& g, int32_t rows);

@@ -99,6 +99,9 @@ cudaError_t launch_key_mass_window(const MassArgs& a, const attn_chunk& ch, cuda
 
 // attn_api.cpp's argument rules, for the entry points in kv4_api.cpp
 int shape_geom(const attn_shape* s, Geom* g);
+// kv4_api.cpp: whether rows with these strides, of D elements each, lie apart: a call
+// that writes them may have no two in the same memory.
+bool rows_apart(const Geom& g);
 int chunks_fwd_status(const attn_chunk* c, int32_t n, int32_t T);
 
 }  // namespace attn

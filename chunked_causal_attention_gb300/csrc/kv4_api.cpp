@@ -115,20 +115,6 @@ int check_mass(const float* in, const float* out, int64_t floats, int64_t ld, in
     return ATTN_OK;
 }
 
-// Whether rows with these strides, of D elements each, lie apart: a call writes them, so no two may share memory.
-bool rows_apart(const Geom& g) {
-    struct Dim { int64_t stride, n; };
-    Dim d[] = {{g.sb, g.B}, {g.sh, g.H}, {g.st, g.T}};
-    std::sort(d, d + 3, [](const Dim& a, const Dim& b) { return a.stride < b.stride; });
-    __int128 extent = g.D;
-    for (const Dim& x : d) {
-        if (x.n == 1) continue;
-        if (x.stride < extent) return false;
-        extent += (__int128)x.stride * (x.n - 1);
-    }
-    return true;
-}
-
 int rows_common(const void* k, const void* v, const attn_shape* shape, const attn_kv4_cache* cache,
                 const int32_t* pos, const int32_t* cu, void* ws, size_t ws_bytes, cudaStream_t s, bool store) {
     Kv4RowsArgs a;
@@ -164,6 +150,20 @@ int attend_geom(const attn_shape* shape, const Kv4Geom& c, Geom* g) {
 }
 
 }  // namespace
+
+// Whether rows with these strides, of D elements each, lie apart: a call writes them, so no two may share memory.
+bool attn::rows_apart(const Geom& g) {
+    struct Dim { int64_t stride, n; };
+    Dim d[] = {{g.sb, g.B}, {g.sh, g.H}, {g.st, g.T}};
+    std::sort(d, d + 3, [](const Dim& a, const Dim& b) { return a.stride < b.stride; });
+    __int128 extent = g.D;
+    for (const Dim& x : d) {
+        if (x.n == 1) continue;
+        if (x.stride < extent) return false;
+        extent += (__int128)x.stride * (x.n - 1);
+    }
+    return true;
+}
 
 // Key tiles of attn_key_mass, those that the most rows see first. Chunks are sorted
 // by rows, so the ones that end after a tile's first key are a tail of the table; of

@@ -1,0 +1,985 @@
+// Attention of the newest tokens, one or a chunk of many a sequence, over the paged
+// cache, on the 5th-generation tensor cores (tcgen05 + TMEM + TMA).
+//
+//   s_rj = scale q_r . k_j,   O_r = sum_{j seen by r} 2^(s2_rj - m_r) v_j / l_r,   s2 = s log2 e
+//
+// Rows. The G = H / Hkv query heads that share a key/value head read the same slots, so
+// a tile of 128 rows is 128 / G tokens of all G heads (of up to 128 of them): a decode
+// step's rows are one tile a sequence and key/value head, and a chunk reads its keys
+// once for G heads. One TMA box brings the tile's queries, tokens by heads by 64 dims.
+//
+// Work. A unit is one row tile of one key/value head; it reads the slots up to its last
+// token. The lengths are on the device, so every block adds up the units' key tiles by
+// itself (one pass over the sequences and two block-wide sums) and derives the same
+// list: units of a sequence longer than C key tiles are cut into equal parts of at most
+// C, C the tiles of all units over kItemsPerSm times the SMs. The parts' (O, LSE) go to
+// the workspace and merge_kernel joins them in order. Items of one key/value head and
+// part follow each other in the list, so blocks that run together read the same keys
+// from L2; a block takes its first item by its number and the others from a queue.
+//
+// Roles of a block's warps: 0 takes items, looks up pages (32 boxes' page numbers at a
+// time, a lane each, one window ahead) and issues the TMA loads, a box for each page (or
+// part of one) and 64 dims; 1 issues the MMAs; 2 and 3 clear what no row may see in a
+// tile of V (below); 4 to 7 do the softmax, a row a thread, as in the forward.
+//
+// Masked slots. A masked score is replaced before the maximum, so K may hold anything
+// there. But weight 0 times a NaN or an infinity in V would reach the sum, so in tiles
+// that some row does not see whole, warps 2 and 3 zero the rows of V behind the last
+// slot, and replace values that are not finite in rows that only some tokens see; these
+// are added to the rows that do see them at the end. Pages behind the last one are
+// loaded from beyond the tensor map's edge: zeros.
+#include <algorithm>
+
+#include "kv4_device.cuh"
+#include "paged.h"
+#include "tc_common.cuh"
+
+namespace attn {
+namespace {
+
+using namespace tc;
+using kv4::grid_go;
+using kv4::grid_wait;
+using kv4::launch_early;
+
+constexpr int kThreads = 256;
+constexpr int kRuns = 128;                     // the sequences are taken in so many runs by the block-wide sums
+constexpr int kItemsPerSm = 4;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColS = 0;
+constexpr uint32_t kColO = 256;
+constexpr float kLag = 8.f;                    // how far (log2) a tile's maximum may pass the running one
+
+// What the launch derives from the shapes.
+struct Tiling {
+    int32_t heads, blocks;     // query heads of a row tile, and how many such tiles a key/value head's heads make
+    int32_t tok, few;          // tokens of a row tile, and of the small box that brings fewer
+    int32_t head_major;        // rows of a tile: head * tokens of the box + token, or token * heads + head
+    int32_t box;               // slots of a TMA box of K and V
+    int32_t part_rows;         // rows of a partial
+    int64_t part_floats;       // floats of a partial: rows of D, then their LSEs (base 2)
+    int64_t target;            // items that the whole work is cut into, about
+};
+
+__host__ __device__ constexpr int block_n(int d) { return d > 128 ? 64 : 128; }     // slots of a key tile
+__host__ __device__ constexpr int stages(int d) { return d > 128 ? 2 : d > 64 ? 3 : 6; }
+
+Tiling tiling(const PagedGeom& c, const Geom& g) {
+    Tiling t;
+    const int32_t G = g.H / c.Hkv;
+    t.heads = std::min(G, kTile);
+    t.blocks = (G - 1) / t.heads + 1;
+    t.tok = kTile / t.heads;
+    t.few = std::max(1, std::min(t.tok, 16 / t.heads));
+    t.head_major = 0;
+    t.box = std::min(c.page(), block_n(g.D));
+    t.part_rows = (int32_t)std::min<int64_t>(t.tok, g.T) * t.heads;
+    t.part_floats = ((int64_t)t.part_rows * (g.D + 1) + 31) / 32 * 32;
+    t.target = (int64_t)kItemsPerSm * device_sm_count();
+    return t;
+}
+
+// ------------------------------------------------------------------ the work list
+
+struct Seq {
+    int32_t q0, nq, n;         // first packed token, tokens, slots in use
+};
+
+__device__ __forceinline__ Seq seq_of(const PagedAttendArgs& a, int32_t b) {
+    Seq s;
+    int32_t hi;
+    if (a.cu) {
+        s.q0 = a.cu[b];
+        hi = a.cu[b + 1];
+        if (!(0 <= s.q0 && s.q0 <= hi && hi <= a.g.T)) {
+            set_error(a.status, ATTN_E_BOUNDS);
+            s.q0 = max(0, min(s.q0, a.g.T));
+            hi = max(s.q0, min(hi, a.g.T));
+        }
+    } else {
+        s.q0 = b * a.each;
+        hi = s.q0 + a.each;
+    }
+    s.nq = hi - s.q0;
+    const int32_t most = a.max_pages << a.c.shift;
+    s.n = a.lens[b];
+    if (s.n < 0 || s.n > most) {
+        set_error(a.status, ATTN_E_BOUNDS);
+        s.n = max(0, min(s.n, most));
+    }
+    return s;
+}
+
+__device__ __forceinline__ int32_t row_tiles_of(const Tiling& t, int32_t nq) { return nq > 0 ? (nq - 1) / t.tok + 1 : 0; }
+
+// Units of a sequence, and the key tiles of its longest.
+__device__ __forceinline__ int64_t units_of(const PagedAttendArgs& a, const Tiling& t, const Seq& s) {
+    return (int64_t)a.c.Hkv * t.blocks * row_tiles_of(t, s.nq);
+}
+template <int BN>
+__device__ __forceinline__ int32_t tiles_of(const Seq& s) { return max(1, (s.n + BN - 1) / BN); }
+
+__device__ __forceinline__ int32_t parts_of(int32_t tiles, int64_t C) {
+    return tiles > C ? (int32_t)((tiles + C - 1) / C) : 1;
+}
+
+// What a block knows of the list: where the runs' items and partials begin.
+struct List {
+    int32_t* items;            // shared memory, kRuns each
+    int32_t* parts;
+    int64_t C;
+    int32_t per;               // sequences of a run
+    int32_t n_items;
+};
+
+// Block-wide: sums over the sequences. scratch: 20 int64 in shared memory.
+template <int BN>
+__device__ __forceinline__ void make_list(const PagedAttendArgs& a, const Tiling& t, List& L, int64_t* scratch) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    L.per = (a.B + kRuns - 1) / kRuns;
+    const int32_t b0 = (int32_t)min((int64_t)tid * L.per, (int64_t)a.B);
+    const int32_t b1 = tid < kRuns ? (int32_t)min((int64_t)b0 + L.per, (int64_t)a.B) : b0;
+    int64_t units = 0, work = 0;
+    int32_t tiles = 0;
+    for (int32_t b = b0; b < b1; ++b) {
+        const Seq s = seq_of(a, b);
+        units = units_of(a, t, s);
+        tiles = tiles_of<BN>(s);
+        work += units * tiles;
+    }
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) work += __shfl_xor_sync(0xffffffffu, work, m);
+    if (lane == 0) scratch[warp] = work;
+    __syncthreads();
+    work = 0;
+    for (int w = 0; w < kRuns / 32; ++w) work += scratch[w];
+    L.C = max((int64_t)1, (work + t.target - 1) / t.target);
+    int64_t items = 0, cut = 0;
+    for (int32_t b = b0; b < b1; ++b) {
+        if (L.per > 1) {
+            const Seq s = seq_of(a, b);
+            units = units_of(a, t, s);
+            tiles = tiles_of<BN>(s);
+        }
+        const int32_t p = parts_of(tiles, L.C);
+        items += units * p;
+        if (p > 1) cut += units * p;
+    }
+    int64_t items_to = items, cut_to = cut;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, items_to, m), y = __shfl_up_sync(0xffffffffu, cut_to, m);
+        if (lane >= m) {
+            items_to += x;
+            cut_to += y;
+        }
+    }
+    if (lane == 31) {
+        scratch[4 + warp] = items_to;
+        scratch[12 + warp] = cut_to;
+    }
+    __syncthreads();
+    int64_t items_all = 0, cut_all = 0, items_before = 0, cut_before = 0;
+    for (int w = 0; w < kRuns / 32; ++w) {
+        if (w < warp) {
+            items_before += scratch[4 + w];
+            cut_before += scratch[12 + w];
+        }
+        items_all += scratch[4 + w];
+        cut_all += scratch[12 + w];
+    }
+    items_before += items_to - items;
+    cut_before += cut_to - cut;
+    // offsets that descend can give more items than there are tokens for: nothing is done then
+    const bool fits = items_all <= INT32_MAX && cut_all <= a.max_parts;
+    if (!fits) set_error(a.status, ATTN_E_BOUNDS);
+    L.n_items = fits ? (int32_t)items_all : 0;
+    if (tid < kRuns) {
+        L.items[tid] = fits ? (int32_t)items_before : 0;
+        L.parts[tid] = fits ? (int32_t)cut_before : 0;
+    }
+    if (blockIdx.x == 0) {
+        // for the merge kernel
+        for (int32_t b = b0; b < b1; ++b) {
+            if (L.per > 1) {
+                const Seq s = seq_of(a, b);
+                units = units_of(a, t, s);
+                tiles = tiles_of<BN>(s);
+            }
+            const int32_t p = fits ? parts_of(tiles, L.C) : 1;
+            a.cuts[b] = make_int2(p > 1 ? (int32_t)cut_before : 0, p);
+            if (p > 1) cut_before += units * p;
+        }
+    }
+    __syncthreads();
+}
+
+// An item as its consumers read it from shared memory.
+struct Item {
+    int32_t tiles;             // key tiles; -1: no more work
+    int32_t k0;                // first slot
+    int32_t tok0, toks;        // first packed token, tokens
+    int32_t head0, heads;      // first query head, heads
+    int32_t seen;              // slots that the first token sees
+    int32_t n;                 // slots in use
+    int32_t part;              // partial that it writes, -1: the output
+    int32_t box;               // tokens of the box that brought its queries
+    int32_t b, hk;
+};
+static_assert(sizeof(Item) == 48, "Item layout");
+
+// Item w of the list, by a whole warp; false if the lengths changed since the list was made.
+template <int BN>
+__device__ __forceinline__ bool find_item(const PagedAttendArgs& a, const Tiling& t, const List& L, int32_t w, Item& it) {
+    const int lane = threadIdx.x & 31;
+    int32_t r = -1;
+#pragma unroll
+    for (int i = 0; i < kRuns / 32; ++i) r += __popc(__ballot_sync(0xffffffffu, L.items[i * 32 + lane] <= w));
+    int64_t x = w - L.items[r], part0 = L.parts[r];
+    int32_t b = r * L.per;
+    if (L.per > 1) {
+        const int32_t end = (int32_t)min((int64_t)b + L.per, (int64_t)a.B);
+        bool found = false;
+        for (; b < end; b += 32) {
+            int64_t items = 0, cut = 0;
+            if (b + lane < end) {
+                const Seq s = seq_of(a, b + lane);
+                const int32_t p = parts_of(tiles_of<BN>(s), L.C);
+                items = units_of(a, t, s) * p;
+                cut = p > 1 ? items : 0;
+            }
+            int64_t items_to = items, cut_to = cut;
+#pragma unroll
+            for (int m = 1; m < 32; m <<= 1) {
+                const int64_t u = __shfl_up_sync(0xffffffffu, items_to, m), v = __shfl_up_sync(0xffffffffu, cut_to, m);
+                if (lane >= m) {
+                    items_to += u;
+                    cut_to += v;
+                }
+            }
+            const uint32_t past = __ballot_sync(0xffffffffu, items_to > x);
+            if (past) {
+                const int f = __ffs(past) - 1;
+                x -= __shfl_sync(0xffffffffu, items_to - items, f);
+                part0 += __shfl_sync(0xffffffffu, cut_to - cut, f);
+                b += f;
+                found = true;
+                break;
+            }
+            x -= __shfl_sync(0xffffffffu, items_to, 31);
+            part0 += __shfl_sync(0xffffffffu, cut_to, 31);
+        }
+        if (!found) return false;
+    }
+    if (b >= a.B) return false;
+    const Seq s = seq_of(a, b);
+    const int32_t parts = parts_of(tiles_of<BN>(s), L.C), row_tiles = row_tiles_of(t, s.nq);
+    if (x >= units_of(a, t, s) * parts || (parts > 1 && part0 + x >= a.max_parts)) return false;
+    // key/value head, block of heads, part, row tile: the tiles with the most slots first
+    const int32_t y = (int32_t)x / row_tiles, rt = row_tiles - 1 - ((int32_t)x - y * row_tiles);
+    const int32_t u = y / parts, p = y - u * parts, hk = u / t.blocks, hb = u - hk * t.blocks;
+    const int32_t G = a.g.H / a.c.Hkv, i0 = rt * t.tok;
+    it.tok0 = s.q0 + i0;
+    it.toks = min(t.tok, s.nq - i0);
+    it.head0 = hk * G + hb * t.heads;
+    it.heads = min(t.heads, G - hb * t.heads);
+    it.seen = s.n - s.nq + i0 + 1;
+    it.n = s.n;
+    const int32_t last = max(0, it.seen + it.toks - 1), tiles = (last + BN - 1) / BN;
+    const int32_t t0 = (int32_t)((int64_t)p * tiles / parts), t1 = (int32_t)((int64_t)(p + 1) * tiles / parts);
+    it.tiles = t1 - t0;
+    it.k0 = t0 * BN;
+    it.part = parts > 1 ? (int32_t)(part0 + x) : -1;
+    it.box = it.toks <= t.few ? t.few : t.tok;
+    it.b = b;
+    it.hk = hk;
+    return true;
+}
+
+// ------------------------------------------------------------------ the tile kernel
+
+template <int D>
+struct Layout {
+    static constexpr int BN = block_n(D), KVS = stages(D), CH = D / 64;
+    static constexpr int TILE_Q = kTile * D * 2;
+    static constexpr int TILE_KV = BN * D * 2;
+    static constexpr int Q_OFF = 0;
+    static constexpr int K_OFF = Q_OFF + TILE_Q;
+    static constexpr int V_OFF = K_OFF + KVS * TILE_KV;
+    static constexpr int BAR_OFF = V_OFF + KVS * TILE_KV;
+    static constexpr int B_QFULL = 0, B_QEMPTY = 1;
+    static constexpr int B_KFULL = 2, B_KEMPTY = B_KFULL + KVS;
+    static constexpr int B_VFULL = B_KEMPTY + KVS, B_VEMPTY = B_VFULL + KVS, B_VFIX = B_VEMPTY + KVS;
+    static constexpr int B_SFULL = B_VFIX + KVS;               // 2
+    static constexpr int B_PFULL = B_SFULL + 2;                // 2
+    static constexpr int B_ODONE = B_PFULL + 2;
+    static constexpr int B_OFREE = B_ODONE + 1;
+    static constexpr int B_OFULL = B_OFREE + 1;                // last product of an item complete
+    static constexpr int B_DRAIN = B_OFULL + 1;
+    static constexpr int B_RFULL = B_DRAIN + 1, B_REMPTY = B_RFULL + 2;   // items: 2 slots
+    static constexpr int NBAR = B_REMPTY + 2;
+    static constexpr int ITEM_OFF = BAR_OFF + (NBAR * 8 + 15) / 16 * 16;
+    static constexpr int LIST_OFF = ITEM_OFF + 2 * (int)sizeof(Item);
+    static constexpr int MISC_OFF = LIST_OFF + 2 * kRuns * 4;  // TMEM base, abort flag, 4 x item with values to add
+    static constexpr int SCRATCH_OFF = MISC_OFF + 32;
+    static constexpr int BYTES = SCRATCH_OFF + 20 * 8;
+    static constexpr size_t ALLOC = (size_t)BYTES + 1024;      // slack for 1024-byte alignment
+};
+
+// Values that are not finite among the eight bf16 of x, replaced by zeros; true if there were any.
+__device__ __forceinline__ bool only_finite(uint4& x) {
+    uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t e = w[i] & 0x7f807f80u;
+        if ((e & 0xffffu) == 0x7f80u) {
+            w[i] &= 0xffff0000u;
+            any = true;
+        }
+        if ((e >> 16) == 0x7f80u) {
+            w[i] &= 0x0000ffffu;
+            any = true;
+        }
+    }
+    return any;
+}
+
+// Page of the pool that holds slot j of an item's sequence, `pages` (none) behind the last or outside the pool.
+__device__ __forceinline__ int32_t page_of(const PagedAttendArgs& a, int32_t b, int32_t n, int64_t j) {
+    if (j >= n) return a.c.pages;
+    const int32_t id = a.table[(int64_t)b * a.table_ld + (j >> a.c.shift)];
+    if ((uint32_t)id < (uint32_t)a.c.pages) return id;
+    set_error(a.status, ATTN_E_BOUNDS);
+    return a.c.pages;
+}
+
+// Sum of V's values in dim d of slots [from, to) that are not finite: those that the products left
+// out, because other rows of the tile do not see them.
+__device__ __noinline__ float not_finite(const PagedAttendArgs& a, int32_t b, int32_t hk, int32_t n, int32_t from,
+                                         int32_t to, int d) {
+    float sum = 0.f;
+    for (int32_t j = from; j < to && d < a.g.D; ++j) {
+        const int32_t id = page_of(a, b, n, j);
+        if (id >= a.c.pages) continue;
+        const uint32_t v = static_cast<const uint16_t*>(a.c.v)[id * a.c.sp + hk * a.c.sh +
+                                                                (j & ((1 << a.c.shift) - 1)) * a.c.st + d];
+        if ((v & 0x7f80u) == 0x7f80u) sum += __uint_as_float(v << 16);
+    }
+    return sum;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    attend_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmq_few,
+                  const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
+                  const __grid_constant__ PagedAttendArgs a, const TcMaps mpq, const TcMaps mpkv,
+                  const __grid_constant__ Tiling t) {
+    using LY = Layout<D>;
+    constexpr int BN = LY::BN, KVS = LY::KVS, CH = LY::CH;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(sm);
+    const uint32_t bar0 = sbase + LY::BAR_OFF;
+    auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
+    Item* slot = reinterpret_cast<Item*>(sm + LY::ITEM_OFF);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + LY::MISC_OFF);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + LY::MISC_OFF + 4);
+    volatile uint32_t* to_add = reinterpret_cast<volatile uint32_t*>(sm + LY::MISC_OFF + 16);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (tid == 0) {
+        mbar_init(bar(LY::B_QFULL), 1);
+        mbar_init(bar(LY::B_QEMPTY), 1);
+        for (int s = 0; s < KVS; ++s) {
+            mbar_init(bar(LY::B_KFULL + s), 1);
+            mbar_init(bar(LY::B_KEMPTY + s), 1);
+            mbar_init(bar(LY::B_VFULL + s), 1);
+            mbar_init(bar(LY::B_VEMPTY + s), 1);
+            mbar_init(bar(LY::B_VFIX + s), 2);         // warps 2 and 3
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(bar(LY::B_SFULL + s), 1);
+            mbar_init(bar(LY::B_PFULL + s), 128);
+            mbar_init(bar(LY::B_RFULL + s), 1);
+            mbar_init(bar(LY::B_REMPTY + s), 7);       // MMA thread, warps 2 and 3, 4 softmax warps
+        }
+        mbar_init(bar(LY::B_ODONE), 1);
+        mbar_init(bar(LY::B_OFREE), 128);
+        mbar_init(bar(LY::B_OFULL), 1);
+        mbar_init(bar(LY::B_DRAIN), 1);
+        *abort_flag = 0;
+        for (int i = 0; i < 4; ++i) to_add[i] = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+        tmem_relinquish();
+    }
+    if (tid == 32) {
+        tma_prefetch_desc(&tmq);
+        tma_prefetch_desc(&tmq_few);
+        tma_prefetch_desc(&tmk);
+        tma_prefetch_desc(&tmv);
+    }
+    grid_wait();
+    grid_go();
+    List L{reinterpret_cast<int32_t*>(sm + LY::LIST_OFF), reinterpret_cast<int32_t*>(sm + LY::LIST_OFF) + kRuns, 1, 1, 0};
+    make_list<BN>(a, t, L, reinterpret_cast<int64_t*>(sm + LY::SCRATCH_OFF));
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    // the next item, for a consumer that is one thread or a warp (`one`: this lane arrives for it)
+    auto next_item = [&](uint32_t ic, Item& it, bool one) {
+        const uint32_t s = ic & 1;
+        if (!mbar_wait(bar(LY::B_RFULL + s), (ic >> 1) & 1, abort_flag, a.status, a.wait_ns)) return false;
+        const volatile int32_t* p = reinterpret_cast<const volatile int32_t*>(slot + s);
+        int32_t* to = reinterpret_cast<int32_t*>(&it);
+#pragma unroll
+        for (int i = 0; i < (int)(sizeof(Item) / 4); ++i) to[i] = p[i];
+        if (one) mbar_arrive(bar(LY::B_REMPTY + s));
+        return it.tiles >= 0 && !*abort_flag;
+    };
+    auto next_item_warp = [&](uint32_t ic, Item& it) {
+        const bool go = __all_sync(0xffffffffu, next_item(ic, it, false));
+        if (lane == 0) mbar_arrive(bar(LY::B_REMPTY + (ic & 1)));
+        return go;
+    };
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ items and loads
+        const int boxes = BN / t.box;                   // of a tile
+        const int window = 32 / boxes;                  // tiles whose pages the lanes hold
+        uint32_t kc = 0, ne = 0;
+        int32_t w = a.stall ? L.n_items : (int32_t)blockIdx.x;
+        bool ok = !a.stall;
+        for (uint32_t ic = 0; ok; ++ic) {
+            Item it{};
+            it.tiles = -1;
+            if (w < L.n_items && !find_item<BN>(a, t, L, w, it)) {
+                if (lane == 0) {
+                    set_error(a.status, ATTN_E_BOUNDS);
+                    *abort_flag = 1;
+                }
+                it.tiles = -1;
+            }
+            ok = mbar_wait_warp(bar(LY::B_REMPTY + (ic & 1)), ((ic >> 1) & 1) ^ 1, abort_flag, a.status, a.wait_ns);
+            if (!ok) break;
+            if (lane == 0) {
+                volatile int32_t* p = reinterpret_cast<volatile int32_t*>(slot + (ic & 1));
+                const int32_t* from = reinterpret_cast<const int32_t*>(&it);
+#pragma unroll
+                for (int i = 0; i < (int)(sizeof(Item) / 4); ++i) p[i] = from[i];
+                mbar_arrive(bar(LY::B_RFULL + (ic & 1)));
+            }
+            __syncwarp();
+            if (it.tiles < 0 || __any_sync(0xffffffffu, *abort_flag)) break;
+            if (it.tiles > 0) {
+                // page of box `lane` of the tiles from `first` on
+                auto pages_at = [&](int32_t first) {
+                    const int64_t j = (int64_t)it.k0 + (int64_t)first * BN + lane * t.box;
+                    return lane < window * boxes && first < it.tiles ? page_of(a, it.b, it.n, j) : a.c.pages;
+                };
+                int32_t ahead = pages_at(0), now = 0;
+                ok = mbar_wait_warp(bar(LY::B_QEMPTY), (ne & 1) ^ 1, abort_flag, a.status, a.wait_ns);
+                if (!ok) break;
+                const bool few = it.box == t.few && t.few < t.tok;
+                if (lane == 0) mbar_expect_tx(bar(LY::B_QFULL), (uint32_t)(it.box * t.heads * 128 * CH));
+                __syncwarp();
+                if (lane < CH) {
+                    const int c1 = mpq.pos_t == 1 ? it.tok0 : (mpq.pos_h == 1 ? it.head0 : 0);
+                    const int c2 = mpq.pos_t == 2 ? it.tok0 : (mpq.pos_h == 2 ? it.head0 : 0);
+                    const int c3 = mpq.pos_t == 3 ? it.tok0 : (mpq.pos_h == 3 ? it.head0 : 0);
+                    tma_load_4d(sbase + LY::Q_OFF + lane * (kTile * 128), few ? &tmq_few : &tmq, bar(LY::B_QFULL),
+                                lane * 64, c1, c2, c3);
+                }
+                ++ne;
+                // one lane a box: 64 dims of the slots of a page (or of a tile, if pages are longer)
+                const int bi = lane / CH, bc = lane - bi * CH;
+                const bool loads = lane < boxes * CH;
+                for (int32_t j = 0; j < it.tiles && ok; ++j) {
+                    const int32_t in = j % window;
+                    if (in == 0) {
+                        now = ahead;
+                        ahead = pages_at(j + window);
+                    }
+                    const int32_t id = __shfl_sync(0xffffffffu, now, (in * boxes + bi) & 31);
+                    const int32_t place = (it.k0 + j * BN + bi * t.box) & ((1 << a.c.shift) - 1);
+                    const int c1 = mpkv.pos_t == 1 ? place : (mpkv.pos_h == 1 ? it.hk : id);
+                    const int c2 = mpkv.pos_t == 2 ? place : (mpkv.pos_h == 2 ? it.hk : id);
+                    const int c3 = mpkv.pos_t == 3 ? place : (mpkv.pos_h == 3 ? it.hk : id);
+                    const uint32_t s = kc % KVS, turn = (kc / KVS) & 1;
+                    const uint32_t off = s * LY::TILE_KV + bc * (BN * 128) + bi * t.box * 128;
+                    ok = mbar_wait_warp(bar(LY::B_KEMPTY + s), turn ^ 1, abort_flag, a.status, a.wait_ns);
+                    if (!ok) break;
+                    if (lane == 0) mbar_expect_tx(bar(LY::B_KFULL + s), LY::TILE_KV);
+                    __syncwarp();
+                    if (loads) tma_load_4d(sbase + LY::K_OFF + off, &tmk, bar(LY::B_KFULL + s), bc * 64, c1, c2, c3);
+                    ok = mbar_wait_warp(bar(LY::B_VEMPTY + s), turn ^ 1, abort_flag, a.status, a.wait_ns);
+                    if (!ok) break;
+                    if (lane == 0) mbar_expect_tx(bar(LY::B_VFULL + s), LY::TILE_KV);
+                    __syncwarp();
+                    if (loads) tma_load_4d(sbase + LY::V_OFF + off, &tmv, bar(LY::B_VFULL + s), bc * 64, c1, c2, c3);
+                    ++kc;
+                }
+            }
+            // the item's last loads are out: claim the next one
+            if (lane == 0) w = (int32_t)min(atomicAdd(a.counter, 1u) + gridDim.x, (uint32_t)INT32_MAX);
+            w = __shfl_sync(0xffffffffu, w, 0);
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer
+        if (elect_one()) {
+            constexpr uint32_t id_s = idesc_bf16(128, BN, 0, 0);
+            constexpr uint32_t id_o = idesc_bf16(128, D, 0, 1);
+            uint32_t kc = 0, ne = 0, gt = 0;            // gt: tiles so far (S buffer, P, product)
+            Item it;
+            bool ok = true;
+            for (uint32_t ic = 0; ok; ++ic) {
+                if (!next_item(ic, it, true)) break;
+                if (it.tiles == 0) continue;
+                ok = mbar_wait(bar(LY::B_QFULL), ne & 1, abort_flag, a.status, a.wait_ns);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t q0 = sbase + LY::Q_OFF;
+                uint32_t vc = kc;
+                for (int j = 0; j <= it.tiles && ok; ++j) {
+                    if (j < it.tiles) {
+                        const uint32_t ks = kc % KVS;
+                        ok = mbar_wait(bar(LY::B_KFULL + ks), (kc / KVS) & 1, abort_flag, a.status, a.wait_ns);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t k0 = sbase + LY::K_OFF + ks * LY::TILE_KV;
+                        const uint32_t sb = tmem + kColS + ((gt + j) & 1) * BN;
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint32_t qoff = (kk >> 2) * (kTile * 128) + (kk & 3) * 32;
+                            const uint32_t koff = (kk >> 2) * (BN * 128) + (kk & 3) * 32;
+                            mma_ss(sb, sdesc_sw128(q0 + qoff, 16, 1024), sdesc_sw128(k0 + koff, 16, 1024), id_s, kk > 0);
+                        }
+                        mma_commit(bar(LY::B_KEMPTY + ks));
+                        mma_commit(bar(LY::B_SFULL + ((gt + j) & 1)));
+                        ++kc;
+                        if (j == it.tiles - 1) mma_commit(bar(LY::B_QEMPTY));
+                    }
+                    if (j >= 1) {
+                        const uint32_t x = gt + j - 1, pb = x & 1;
+                        if (j == 1) {
+                            ok = mbar_wait(bar(LY::B_OFREE), (ne & 1) ^ 1, abort_flag, a.status, a.wait_ns);
+                            if (!ok) break;
+                        }
+                        const uint32_t vs = vc % KVS;
+                        ok = mbar_wait(bar(LY::B_VFULL + vs), (vc / KVS) & 1, abort_flag, a.status, a.wait_ns) &&
+                             mbar_wait(bar(LY::B_VFIX + vs), (vc / KVS) & 1, abort_flag, a.status, a.wait_ns) &&
+                             mbar_wait(bar(LY::B_PFULL + pb), (x >> 1) & 1, abort_flag, a.status, a.wait_ns);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t v0 = sbase + LY::V_OFF + vs * LY::TILE_KV;
+                        const uint32_t pa = tmem + kColS + pb * BN;
+#pragma unroll
+                        for (int kk = 0; kk < BN / 16; ++kk)
+                            mma_ts(tmem + kColO, pa + kk * 8, sdesc_sw128(v0 + kk * 2048, BN * 128, 1024), id_o,
+                                   (j - 1 > 0 || kk > 0) ? 1u : 0u);
+                        mma_commit(bar(LY::B_VEMPTY + vs));
+                        mma_commit(bar(LY::B_ODONE));
+                        if (j == it.tiles) mma_commit(bar(LY::B_OFULL));
+                        ++vc;
+                    }
+                }
+                gt += it.tiles;
+                ++ne;
+            }
+        }
+    } else if (warp < 4) {
+        // ------------------------------------------------------------ what no row may see of V
+        Item it;
+        bool ok = true;
+        uint32_t vc = 0, ne = 0;
+        for (uint32_t ic = 0; ok; ++ic) {
+            if (!next_item_warp(ic, it)) break;
+            if (it.tiles == 0) continue;
+            for (int j = 0; j < it.tiles && ok; ++j, ++vc) {
+                const uint32_t vs = vc % KVS;
+                ok = mbar_wait_warp(bar(LY::B_VFULL + vs), (vc / KVS) & 1, abort_flag, a.status, a.wait_ns);
+                if (!ok) break;
+                const int32_t j0 = it.k0 + j * BN;
+                if (j0 + BN > it.seen) {
+                    const int r0 = max(0, it.seen - j0), rn = min(max(it.n - j0, 0), BN);   // rows [rn, BN) hold no slot in use
+                    uint8_t* v = sm + LY::V_OFF + vs * LY::TILE_KV;
+                    bool any = false;
+                    // 16-byte pieces of 64 dims of a row: eight lanes a row
+                    for (int x = (warp - 2) * 32 + lane; x < (BN - r0) * 8; x += 64) {
+                        const int r = r0 + (x >> 3);
+#pragma unroll
+                        for (int c = 0; c < CH; ++c) {
+                            uint4* p = reinterpret_cast<uint4*>(v + c * (BN * 128) + r * 128 + (x & 7) * 16);
+                            uint4 y = make_uint4(0, 0, 0, 0);
+                            bool put = r >= rn;
+                            if (!put) {
+                                y = *p;
+                                put = only_finite(y);
+                                any = any || put;
+                            }
+                            if (put) *p = y;
+                        }
+                    }
+                    if (any) to_add[ne & 3] = ne + 1;
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(LY::B_VFIX + vs));
+            }
+            ++ne;
+        }
+    } else {
+        // ------------------------------------------------------------ softmax / epilogue
+        const int row = tid - 128;                       // TMEM lane == tile row
+        const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
+        const float sl2 = a.g.scale * kLog2e;
+        uint32_t gt = 0, ne = 0;
+        bool ok = true;
+        Item it;
+        for (uint32_t ic = 0; ok; ++ic) {
+            if (!next_item_warp(ic, it)) break;
+            // this row's token and head
+            const int maj = t.head_major ? it.box : t.heads, hi = row / maj, lo = row - hi * maj;
+            const int ti = t.head_major ? lo : hi, gi = t.head_major ? hi : lo;
+            const bool live = ti < it.toks && gi < it.heads;
+            const bool warp_live = __any_sync(0xffffffffu, live);
+            const int32_t seen = it.seen + ti;           // slots [0, seen)
+            float m_run = -INFINITY, l_run = 0.f;
+            for (int j = 0; j < it.tiles && ok; ++j) {
+                const uint32_t x = gt + j, b = x & 1;
+                ok = mbar_wait_warp(bar(LY::B_SFULL + b), (x >> 1) & 1, abort_flag, a.status, a.wait_ns);
+                if (!ok) break;
+                if (!warp_live) {                        // rows that nobody reads
+                    mbar_arrive(bar(LY::B_PFULL + b));
+                    continue;
+                }
+                tc_fence_after();
+                constexpr int NC = BN / 32;
+                const uint32_t sa = tmem + lane_addr + kColS + b * BN;
+                uint32_t r[NC][32];
+#pragma unroll
+                for (int c = 0; c < NC; ++c) tmem_ld32(sa + c * 32, r[c]);
+                tmem_ld_wait();
+                const int j0 = it.k0 + j * BN;
+                float mt, mul = sl2;
+                if (j0 + BN > it.seen || !(sl2 > 0.f)) {
+                    // scaled before they are masked and compared, whatever the scale's sign
+                    const int lim = seen - j0;           // columns c < lim are seen
+                    mt = -INFINITY;
+                    mul = 1.f;
+#pragma unroll
+                    for (int c = 0; c < NC; ++c)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const float s = (c * 32 + i < lim) ? __uint_as_float(r[c][i]) * sl2 : -INFINITY;
+                            r[c][i] = __float_as_uint(s);
+                            mt = fmaxf(mt, s);
+                        }
+                } else {
+                    float hi4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int c = 0; c < NC; ++c)
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2)
+                            hi4[(c * 2 + (i >> 4)) & 3] =
+                                fmax3(hi4[(c * 2 + (i >> 4)) & 3], __uint_as_float(r[c][i]), __uint_as_float(r[c][i + 1]));
+                    mt = fmax3(fmaxf(hi4[0], hi4[1]), hi4[2], hi4[3]) * sl2;
+                }
+                bool rescale = false;
+                float alpha = 1.f;
+                if (mt > m_run + kLag) {
+                    if (m_run != -INFINITY) {
+                        rescale = true;
+                        alpha = ex2(m_run - mt);
+                    }
+                    m_run = mt;
+                }
+                const float base = m_run == -INFINITY ? 0.f : m_run;
+                const float2 mul2 = make_float2(mul, mul), nbase = make_float2(-base, -base);
+                float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                uint32_t p[NC / 2][32];
+#pragma unroll
+                for (int c = 0; c < NC; ++c)
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        const float2 e =
+                            ffma2(make_float2(__uint_as_float(r[c][i]), __uint_as_float(r[c][i + 1])), mul2, nbase);
+                        const float p0 = ex2(e.x), p1 = ex2(e.y);
+                        acc[(i >> 1) & 1] = fadd2(acc[(i >> 1) & 1], make_float2(p0, p1));
+                        p[c >> 1][(c & 1) * 16 + (i >> 1)] = pack_bf16(p0, p1);
+                    }
+                const float lsum = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+                l_run = rescale ? fmaf(l_run, alpha, lsum) : l_run + lsum;
+#pragma unroll
+                for (int c2 = 0; c2 < NC / 2; ++c2) tmem_st32(sa + 32 * c2, p[c2]);
+                if (__any_sync(0xffffffffu, rescale) && j > 0) {
+                    // O holds the sum over the item's earlier tiles once their products have completed
+                    ok = mbar_wait_warp(bar(LY::B_ODONE), (x - 1) & 1, abort_flag, a.status, a.wait_ns);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t oa = tmem + lane_addr + kColO;
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t o[32];
+                        tmem_ld32(oa + c * 32, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                        tmem_st32(oa + c * 32, o);
+                    }
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(bar(LY::B_PFULL + b));
+            }
+            if (!ok) break;
+            const int Dv = a.g.D, tok = it.tok0 + ti, h = it.head0 + gi;
+            const bool empty = it.tiles == 0;
+            bool add = false;
+            if (!empty) {
+                ok = mbar_wait_warp(bar(LY::B_OFULL), ne & 1, abort_flag, a.status, a.wait_ns);
+                if (!ok) break;
+                tc_fence_after();
+                add = to_add[ne & 3] == ne + 1;
+            }
+            // values to add: the slots of this item's tiles that not all of its rows see
+            const int32_t add0 = max(max(it.seen, 0), it.k0), add1 = min(seen, it.k0 + it.tiles * BN);
+            const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
+            const float lse2 = l_run == 0.f ? -INFINITY : m_run + lg2(l_run);
+            const uint32_t oa = tmem + lane_addr + kColO;
+            if (warp_live) {
+                __nv_bfloat16* dst = nullptr;
+                float* part = nullptr;
+                if (it.part < 0) {
+                    dst = reinterpret_cast<__nv_bfloat16*>(a.o) + (int64_t)tok * a.g.st + (int64_t)h * a.g.sh;
+                    if (live) a.lse[(int64_t)h * a.g.T + tok] = lse2 * kLn2;
+                } else {
+                    float* base = a.parts + it.part * t.part_floats;
+                    part = base + (int64_t)(ti * t.heads + gi) * Dv;
+                    if (live) base[(int64_t)t.part_rows * Dv + ti * t.heads + gi] = lse2;
+                }
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
+                    if (!empty) {
+                        tmem_ld32(oa + c * 32, o);
+                        tmem_ld_wait();
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = 0;
+                    }
+                    if (!live) continue;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
+                    if (add)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            o[i] = __float_as_uint(__uint_as_float(o[i]) +
+                                                   not_finite(a, it.b, it.hk, it.n, add0, add1, c * 32 + i));
+                    if (dst) {
+                        uint4* d4 = reinterpret_cast<uint4*>(dst + c * 32);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            if (c * 32 + i * 8 >= Dv) break;
+                            uint4 y;
+                            y.x = pack_bf16(__uint_as_float(o[8 * i + 0]), __uint_as_float(o[8 * i + 1]));
+                            y.y = pack_bf16(__uint_as_float(o[8 * i + 2]), __uint_as_float(o[8 * i + 3]));
+                            y.z = pack_bf16(__uint_as_float(o[8 * i + 4]), __uint_as_float(o[8 * i + 5]));
+                            y.w = pack_bf16(__uint_as_float(o[8 * i + 6]), __uint_as_float(o[8 * i + 7]));
+                            d4[i] = y;
+                        }
+                    } else {
+                        float4* d4 = reinterpret_cast<float4*>(part + c * 32);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (c * 32 + i * 4 < Dv)
+                                d4[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                                    __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+                    }
+                }
+            }
+            if (empty) continue;
+            tc_fence_before();
+            mbar_arrive(bar(LY::B_OFREE));
+            gt += it.tiles;
+            ++ne;
+        }
+    }
+    // ---------------------------------------------------------------- teardown
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) {
+        __syncwarp();
+        if (*abort_flag) {
+            // a wait gave up: let the MMAs already issued drain (bounded) before TMEM is released
+            if (elect_one()) {
+                mma_commit(bar(LY::B_DRAIN));
+                const uint64_t t0 = globaltimer();
+                while (!mbar_try_wait(bar(LY::B_DRAIN), 0) && globaltimer() - t0 < a.wait_ns) {
+                }
+            }
+            __syncwarp();
+        }
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// ------------------------------------------------------------------ parts of cut units, joined
+
+constexpr int kMergeWarps = 8;
+
+// WPR warps a row of the output: one where rows are many, the whole block where they are few.
+// Row r is head r % H of token r / H. Also leaves the work queue at zero for the next call.
+template <int WPR>
+__global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const PagedAttendArgs a, const Tiling t) {
+    constexpr int ROWS = kMergeWarps / WPR;
+    __shared__ float red[2][kMergeWarps];
+    __shared__ __align__(16) float sums[WPR == 1 ? 1 : kMergeWarps][WPR == 1 ? 4 : 256];
+    grid_wait();
+    grid_go();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % WPR;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.counter = 0;
+    const int64_t r = (int64_t)blockIdx.x * ROWS + warp / WPR;
+    if (r >= (int64_t)a.g.T * a.g.H) return;            // the same for the warps of a row
+    const int32_t tok = (int32_t)(r / a.g.H), h = (int32_t)(r - (int64_t)tok * a.g.H);
+    int32_t b, q0;
+    if (a.cu) {
+        // the last sequence that begins at or before the token, 32 at a time
+        int32_t lo = 0, hi = a.B;
+        while (hi - lo > 1) {
+            const int32_t step = (hi - lo + 31) / 32, at = lo + lane * step;
+            const bool before = at < hi && a.cu[at] <= tok;
+            const int32_t f = 31 - __clz(__ballot_sync(0xffffffffu, before) | 1u);
+            lo += f * step;
+            hi = min(hi, lo + step);
+        }
+        b = lo;
+        q0 = a.cu[b];
+        if (q0 < 0 || tok < q0 || tok >= a.cu[b + 1]) return;
+    } else {
+        b = tok / a.each;
+        q0 = b * a.each;
+    }
+    const int2 cut = a.cuts[b];
+    if (cut.y <= 1) return;
+    const int32_t nq = a.cu ? min(a.cu[b + 1], a.g.T) - q0 : a.each;
+    const int32_t row_tiles = row_tiles_of(t, nq), G = a.g.H / a.c.Hkv, hk = h / G, g = h - hk * G;
+    const int32_t hb = g / t.heads, i = tok - q0, rt = i / t.tok, row = (i - rt * t.tok) * t.heads + (g - hb * t.heads);
+    // part p of this row is partial first + p * row_tiles
+    const int64_t first = cut.x + ((int64_t)(hk * t.blocks + hb) * cut.y) * row_tiles + (row_tiles - 1 - rt);
+    if (first + (int64_t)(cut.y - 1) * row_tiles >= a.max_parts || row >= t.part_rows) {
+        if (lane == 0) set_error(a.status, ATTN_E_BOUNDS);   // offsets that overlap
+        return;
+    }
+    const float* base = a.parts + first * t.part_floats;
+    const int64_t step = (int64_t)row_tiles * t.part_floats;
+    const int32_t D = a.g.D;
+    const int64_t at_lse = (int64_t)t.part_rows * D + row;
+    float m = -INFINITY;
+    for (int32_t p = sub * 32 + lane; p < cut.y; p += 32 * WPR) m = fmaxf(m, base[p * step + at_lse]);
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+    if (WPR > 1) {
+        if (lane == 0) red[0][warp] = m;
+        __syncthreads();
+        for (int w = 0; w < kMergeWarps; ++w) m = fmaxf(m, red[0][w]);
+    }
+    const float from = m == -INFINITY ? 0.f : m;
+    // dims 4 lane .. 4 lane + 3, and 128 on where there are more than 128
+    float4 o[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+    float l = 0.f;
+    const float* mine = base + (int64_t)row * D + 4 * lane;
+#pragma unroll 4
+    for (int32_t p = sub; p < cut.y; p += WPR) {
+        const float w = ex2(base[p * step + at_lse] - from);
+        l += w;
+        if (w == 0.f) continue;                          // a part that sees nothing has no O either
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+            if (4 * lane + 128 * x < D) {
+                const float4 y = *reinterpret_cast<const float4*>(mine + p * step + 128 * x);
+                o[x].x = fmaf(w, y.x, o[x].x);
+                o[x].y = fmaf(w, y.y, o[x].y);
+                o[x].z = fmaf(w, y.z, o[x].z);
+                o[x].w = fmaf(w, y.w, o[x].w);
+            }
+    }
+    if (WPR > 1) {
+        if (lane == 0) red[1][warp] = l;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) *reinterpret_cast<float4*>(&sums[warp][4 * lane + 128 * x]) = o[x];
+        __syncthreads();
+        if (warp != 0) return;
+        for (int w = 1; w < kMergeWarps; ++w) {
+            l += red[1][w];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const float4 y = *reinterpret_cast<const float4*>(&sums[w][4 * lane + 128 * x]);
+                o[x].x += y.x;
+                o[x].y += y.y;
+                o[x].z += y.z;
+                o[x].w += y.w;
+            }
+        }
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(a.o) + (int64_t)tok * a.g.st + (int64_t)h * a.g.sh + 4 * lane;
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+        if (4 * lane + 128 * x < D)
+            *reinterpret_cast<uint2*>(dst + 128 * x) =
+                make_uint2(pack_bf16(o[x].x * inv, o[x].y * inv), pack_bf16(o[x].z * inv, o[x].w * inv));
+    if (lane == 0) a.lse[(int64_t)h * a.g.T + tok] = l == 0.f ? -INFINITY : (m + lg2(l)) * kLn2;
+}
+
+template <int D>
+cudaError_t launch_d(const PagedAttendArgs& a, cudaStream_t s) {
+    CUtensorMap mq, mq_few, mk, mv;
+    TcMaps mpq{1, 2, 3}, mpkv{1, 2, 3};
+    Tiling t = tiling(a.c, a.g);
+    const Geom kv = a.c.geom();
+    if (!make_tile_map(&mq, a.q, a.g, mpq, t.tok, t.heads) || !make_tile_map(&mq_few, a.q, a.g, mpq, t.few, t.heads) ||
+        !make_tile_map(&mk, a.c.k, kv, mpkv, t.box) || !make_tile_map(&mv, a.c.v, kv, mpkv, t.box))
+        return cudaErrorInvalidValue;
+    t.head_major = mpq.pos_t < mpq.pos_h;
+    static_assert(Layout<D>::ALLOC <= 232448, "shared memory of the paged attention's kernel");
+    cudaError_t e = cudaFuncSetAttribute(attend_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)Layout<D>::ALLOC);
+    if (e != cudaSuccess) return e;
+    e = launch_early(attend_kernel<D>, dim3(device_sm_count()), kThreads, Layout<D>::ALLOC, 1, s, mq, mq_few, mk, mv, a,
+                     mpq, mpkv, t);
+    if (e != cudaSuccess) return e;
+    const int64_t rows = (int64_t)a.g.T * a.g.H;
+    if (rows <= 8 * device_sm_count())
+        return launch_early(merge_kernel<kMergeWarps>, dim3((unsigned)rows), 32 * kMergeWarps, 0, 1, s, a, t);
+    return launch_early(merge_kernel<1>, dim3((unsigned)((rows + kMergeWarps - 1) / kMergeWarps)), 32 * kMergeWarps, 0, 1,
+                        s, a, t);
+}
+
+}  // namespace
+
+size_t paged_parts_bytes(const PagedGeom& c, const Geom& g, int32_t* max_parts) {
+    // a unit of n tiles that is cut has at most 2 n / C parts, so all have at most twice the target
+    const Tiling t = tiling(c, g);
+    *max_parts = (int32_t)(2 * t.target);
+    return (size_t)*max_parts * t.part_floats * sizeof(float);
+}
+
+bool paged_units_fit(const PagedGeom& c, const Geom& g, int64_t B) {
+    const Tiling t = tiling(c, g);
+    return ((int64_t)g.T / t.tok + B) * c.Hkv * t.blocks <= (1 << 30);
+}
+
+cudaError_t launch_paged_attend(const PagedAttendArgs& a, cudaStream_t s) {
+    // head dims run on tiles of 64, 128 or 256, as the forward's
+    if (a.g.D > 128) return launch_d<256>(a, s);
+    return a.g.D > 64 ? launch_d<128>(a, s) : launch_d<64>(a, s);
+}
+
+}  // namespace attn

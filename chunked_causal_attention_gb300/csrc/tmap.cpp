@@ -23,9 +23,9 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 }  // namespace
 
 // Rank-4 map of a [B, T, H, D]-strided tensor (axes 1..3 sorted by stride),
-// box = box_cols elements of the head dim x box_rows tokens, 128-byte swizzle.
+// box = box_cols elements of the head dim x box_rows tokens x box_heads heads, 128-byte swizzle.
 static bool make_map4(CUtensorMap* m, const void* base, const Geom& g, TcMaps& mp, CUtensorMapDataType dt,
-                      int elem_bytes, int box_cols, int box_rows) {
+                      int elem_bytes, int box_cols, int box_rows, int box_heads = 1) {
     auto enc = encode_fn();
     if (!enc) return false;
     struct Ax {
@@ -50,6 +50,7 @@ static bool make_map4(CUtensorMap* m, const void* base, const Geom& g, TcMaps& m
             box[i + 1] = (cuuint32_t)box_rows;
             mp.pos_t = i + 1;
         } else if (ax[i].which == 1) {
+            box[i + 1] = (cuuint32_t)box_heads;
             mp.pos_h = i + 1;
         } else {
             mp.pos_b = i + 1;
@@ -60,8 +61,8 @@ static bool make_map4(CUtensorMap* m, const void* base, const Geom& g, TcMaps& m
     return r == CUDA_SUCCESS;
 }
 
-bool make_tile_map(CUtensorMap* m, const void* base, const Geom& g, TcMaps& mp, int box_rows) {
-    return make_map4(m, base, g, mp, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, 64, box_rows);
+bool make_tile_map(CUtensorMap* m, const void* base, const Geom& g, TcMaps& mp, int box_rows, int box_heads) {
+    return make_map4(m, base, g, mp, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, 64, box_rows, box_heads);
 }
 
 bool make_kv_acc_map(CUtensorMap* m, float* acc, const Geom& gkv, TcMaps& mp) {

@@ -414,6 +414,100 @@ int attn_kv4_evict(const attn_kv4_cache* src, const int32_t* lens, const float* 
                    float* mass_out, int64_t mass_out_ld, int32_t* slots,
                    void* ws, size_t ws_bytes, void* stream);
 
+/* ---- key/value cache in pages --------------------------------------------- */
+
+/* A pool of pages of `page` slots each (a power of two from 16 to 1024), bf16, shared
+ * by all sequences: slot i of page p of key/value head h is the row of D elements at
+ *   p*sp + h*sh + i*st
+ * of k and of v (element strides, multiples of 8; no two rows share memory; base
+ * pointers 16-byte aligned). Slot j of sequence b is slot j % page of the page
+ * table[b*table_ld + j / page], and a slot's number in the pool is its page's number
+ * times `page` plus its place in the page; pages * page is below 2^31. */
+typedef struct {
+    int64_t pages, Hkv, page, D;
+    int64_t sp, sh, st;
+    void *k, *v;
+} attn_paged_cache;
+
+/* Conventions of the attn_paged_* calls
+ *   - Tokens are packed, [T, heads, D] (shape B = 1): sequence b's new tokens are those
+ *     from cu_seqlens[b] up to cu_seqlens[b + 1]; tokens behind the last sequence's are
+ *     padding, so that a captured graph serves batches of different sizes.
+ *   - add, lens, table, cu_seqlens, slots and n_free are device arrays of int32, read
+ *     when the call runs. Whatever they hold, nothing outside the given arrays is read
+ *     or written.
+ *   - ws: at least attn_paged_workspace_size() bytes, 256-byte aligned, its first 256
+ *     bytes zeroed by the caller once, before its first use. attn_status() reads and
+ *     clears the status word there, which the calls only set: ATTN_E_BOUNDS (a length,
+ *     offset, page or slot out of range), ATTN_E_CAPACITY (attn_paged_reserve: a
+ *     sequence was refused), ATTN_E_TIMEOUT. Calls that may overlap on the GPU take
+ *     different workspaces.
+ *   - Every call may be captured into a graph, and allocates nothing. */
+
+/* Workspace bytes of one attn_paged_* call: op ATTN_PAGED_STORE (shape may be NULL),
+ * ATTN_PAGED_RESERVE (cache and shape may be NULL) or ATTN_PAGED_ATTEND (shape is the
+ * queries') for B sequences. A workspace that is large enough for one may serve the
+ * others. */
+#define ATTN_PAGED_STORE    0
+#define ATTN_PAGED_RESERVE  1
+#define ATTN_PAGED_ATTEND   2
+int attn_paged_workspace_size(const attn_paged_cache* cache, const attn_shape* shape, int64_t B, int32_t op,
+                              size_t* bytes);
+
+/* Reserve slots for the next tokens of B sequences. With add[b] >= 0, sequence b gets
+ * add[b] slots behind the lens[b] that it uses; with add[b] < 0 it ends, its pages go
+ * back and lens_out[b] = 0 (its row of the table stays as it was). Free pages are a
+ * stack: free_pages[0 .. n_free - 1], of `pages` entries. In this order:
+ *   pages of ended sequences are put on the stack, sequence by sequence, page by page;
+ *   with held = ceil(lens / page) and need = ceil((lens + add) / page) - held, the
+ *   sequences are served in their order: page held + j of sequence b is the
+ *   (needs of the sequences before + j)-th from the top of the stack;
+ *   one whose need the rest of the stack does not cover is refused, and so are those
+ *   after it, but for the ones that need no page. One that would outgrow its table's
+ *   max_pages entries is refused on its own, and takes nothing (ATTN_E_CAPACITY).
+ *   lens_out[b] = lens[b] + add[b], or lens[b] if refused;
+ *   n_free_out = what is left on the stack;
+ *   cu_seqlens[b] = sum of max(add, 0) before b, for B + 1 entries, refused or not;
+ *   slots[t] = the slot's number in the pool, for token t of [0, T); -1 for the tokens
+ *   of refused sequences and those behind the last.
+ * Sequences whose tokens pass T are refused too and cu_seqlens ends at T; lengths
+ * outside [0, max_pages * page] are taken as the nearest; pages put back beyond the
+ * stack's end are dropped; a token whose page is outside the pool gets slot -1 (all
+ * ATTN_E_BOUNDS).
+ * lens_out may equal lens, and n_free_out n_free; otherwise no array that is written
+ * may overlap another (ATTN_E_INVAL). B * add, T: below 2^30. Errors: ATTN_E_INVAL
+ * (NULL pointers, sizes), ATTN_E_ALIGN, ATTN_E_WORKSPACE, ATTN_E_CUDA. */
+int attn_paged_reserve(const int32_t* add, const int32_t* lens, int64_t B, int64_t page, int64_t pages,
+                       const int32_t* n_free, int32_t* free_pages, int32_t* table, int64_t table_ld,
+                       int64_t max_pages, int32_t* lens_out, int32_t* n_free_out, int32_t* cu_seqlens,
+                       int32_t* slots, int64_t T, void* ws, size_t ws_bytes, void* stream);
+
+/* Store row t of k and v, bf16 [T, Hkv, D] with the shape's (query) strides, in slot
+ * slots[t]; a row with slot -1 is skipped, as is one with any other slot outside the
+ * pool (ATTN_E_BOUNDS). A slot that two rows name holds pieces of either. Errors:
+ * ATTN_E_INVAL (NULL pointers, sizes that do not fit each other, T * Hkv * D of 2^34
+ * or more), ATTN_E_ALIGN, ATTN_E_UNSUPPORTED, ATTN_E_WORKSPACE, ATTN_E_CUDA. */
+int attn_paged_store(const void* k, const void* v, const attn_shape* shape, const attn_paged_cache* cache,
+                     const int32_t* slots, void* ws, size_t ws_bytes, void* stream);
+
+/* Attention of the newest tokens of B sequences, one or a chunk of many each, over
+ * their pages (the tokens' own rows stored before the call). q, o: bf16 [T, H, D] with
+ * the shape's (query) strides, H a multiple of the cache's Hkv (query head h reads
+ * key/value head h / (H / Hkv)), o apart from q. cu_seqlens as above, or NULL: T / B
+ * tokens each. With n = lens[b] slots in use and n_q tokens, query i sees the slots
+ * j <= n - n_q + i:
+ *   LSE_i = ln sum_j exp(scale * q_i . k_j),  O_i = sum_j exp(scale * q_i . k_j - LSE_i) v_j
+ * A query that sees no slot has O = 0 and LSE = -inf. lse: fp32 [H][T] contiguous.
+ * Rows of padding are left as they were. Slots that a query does not see do not reach
+ * its output, whatever they hold. A length outside [0, max_pages * page] and offsets
+ * that leave [0, T] or descend are taken as the nearest in range, and a page outside
+ * the pool reads as zeros (all ATTN_E_BOUNDS). Softmax weights are rounded to bf16 for
+ * the product with V; sums are fp32, in an order that the lengths alone decide: the
+ * result does not change from run to run. Errors as attn_paged_store. */
+int attn_paged_attend(const void* q, const attn_shape* shape, const attn_paged_cache* cache, const int32_t* table,
+                      int64_t table_ld, int64_t max_pages, const int32_t* lens, const int32_t* cu_seqlens, int64_t B,
+                      void* o, float* lse, void* ws, size_t ws_bytes, void* stream);
+
 /* ---- forward without a caller-provided workspace ----------------------- */
 
 /* Bytes of the scratch area inside the library used by attn_fwd_noalloc. */
