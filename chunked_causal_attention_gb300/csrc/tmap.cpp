@@ -83,9 +83,13 @@ bool make_dq_acc_map(CUtensorMap* m, float* dq_acc, const Geom& g, int32_t rows)
 }
 
 int device_sm_count() {
+    // asked for several times a call; a device's count does not change
+    static std::atomic<int> known[64];
     int dev = 0, c = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 152;
+    if (dev >= 0 && dev < 64 && (c = known[dev].load(std::memory_order_relaxed)) > 0) return c;
     if (cudaDeviceGetAttribute(&c, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || c <= 0) return 152;
+    if (dev >= 0 && dev < 64) known[dev].store(c, std::memory_order_relaxed);
     return c;
 }
 

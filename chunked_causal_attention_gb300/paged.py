@@ -21,14 +21,32 @@ from . import _lib
 from ._lib import ATTN_E_INVAL, AttnError
 
 
-def _kept(shapes: dict, key, make):
-    """What make() gives, kept by key: a decode loop asks for the same at every step."""
-    got = shapes.get(key)
-    if got is None:
-        if len(shapes) >= 64:
-            shapes.clear()
-        got = shapes[key] = make()
-    return got
+class _Calls:
+    """What the calls on a handle's device ask for every time, looked up once: a decode step is
+    bound by the host's time, of which these lookups are the larger part."""
+
+    def __init__(self, device):
+        import torch
+        self.int32, self.bf16, self.fp32 = torch.int32, torch.bfloat16, torch.float32
+        self.empty, self.empty_like, self.empty_strided = torch.empty, torch.empty_like, torch.empty_strided
+        self.device = device
+        self.gpu = (device.index or 0) if device.type == "cuda" else -2      # no tensor's get_device()
+        self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+    def stream(self, stream, t):
+        """The given stream, or the current one of the device."""
+        if stream is None and self.raw_stream is not None:
+            return self.raw_stream(self.gpu)
+        return _lib._stream_of(stream, t)
+
+    def ints(self, t, numel: int) -> bool:
+        """A contiguous int32 tensor of numel elements on the device."""
+        return t.dtype is self.int32 and t.get_device() == self.gpu and t.numel() == numel and t.is_contiguous()
+
+    def table(self, t) -> bool:
+        """An int32 matrix on the device whose rows are contiguous."""
+        return (t.dtype is self.int32 and t.get_device() == self.gpu and t.dim() == 2
+                and (t.stride(1) == 1 or t.shape[1] == 1))
 
 
 class PagedCache:
@@ -51,15 +69,21 @@ class PagedCache:
         self.desc = _lib.attn_paged_cache(self.pages, self.Hkv, self.page, self.D, sp, sh, st, k.data_ptr(), v.data_ptr())
         _lib.attn_paged_workspace_size(self.desc, None, 1, _lib.PAGED_STORE)       # the library's own checks
         self._ref = ctypes.byref(self.desc)
+        self._calls = _Calls(self.device)
         self._shapes = {}
 
     def _shape(self, x, scale: Optional[float]):
-        def make():
+        """A reference to the attn_shape of a packed tensor, kept by sizes, strides and scale: a
+        decode loop asks for the same one at every step."""
+        key = (x.shape, x.stride(), scale)
+        got = self._shapes.get(key)
+        if got is None:
             if x.dim() != 3 or x.shape[-1] != self.D or x.stride(-1) != 1:
                 raise AttnError("attn_shape", ATTN_E_INVAL)
-            shape = _lib.shape_of(x, scale, True)
-            return shape, ctypes.byref(shape)
-        return _kept(self._shapes, (x.shape, x.stride(), scale), make)
+            if len(self._shapes) >= 64:
+                self._shapes.clear()
+            got = self._shapes[key] = ctypes.byref(_lib.shape_of(x, scale, True))
+        return got
 
 
 class PagedTables:
@@ -80,6 +104,7 @@ class PagedTables:
         _lib._expect_flat(fn, "int32", 1, n_free)
         if self.page < 16 or self.page > 1024 or self.page & (self.page - 1):
             raise AttnError(fn, ATTN_E_INVAL)
+        self._calls = _Calls(self.device)
 
 
 def paged_cache(pages: int, Hkv: int, page: int, D: int, device="cuda") -> PagedCache:
@@ -114,23 +139,6 @@ def paged_workspace(cache: Optional[PagedCache] = None, q=None, B: int = 1, tabl
     return ws
 
 
-def _on_device(fn: str, dev, *tensors) -> None:
-    """Tensors (None passes) on a GPU, dev."""
-    ok = dev.type == "cuda"
-    for t in tensors:
-        ok = ok and (t is None or t.device == dev)
-    if not ok:
-        raise AttnError(fn, ATTN_E_INVAL)
-
-
-def _ints(fn: str, numel: int, *tensors) -> None:
-    """Contiguous int32 tensors (None passes) of numel elements."""
-    import torch
-    for t in tensors:
-        if t is not None and not (t.dtype is torch.int32 and t.numel() == numel and t.is_contiguous()):
-            raise AttnError(fn, ATTN_E_INVAL)
-
-
 def paged_reserve(tables: PagedTables, add, T: int, lens_out=None, n_free_out=None, cu_seqlens=None, slots=None, ws=None,
                   stream=None):
     """Slots for the next tokens: add int32 [B], new tokens of each sequence (negative: it ends
@@ -138,50 +146,46 @@ def paged_reserve(tables: PagedTables, add, T: int, lens_out=None, n_free_out=No
     free pages too, unless lens_out or n_free_out take them. Returns (cu_seqlens, slots): int32
     [B + 1] offsets of the packed tokens and int32 [T] slots, -1 for padding and for sequences
     that found no pages (attn_status tells: ATTN_E_CAPACITY)."""
-    import torch
     fn = "paged_reserve"
-    dev = tables.device
-    with _lib._alloc_on(stream, dev):
+    c, B, table = tables._calls, tables.B, tables.table
+    with _lib._alloc_on(stream, c.device):
         if ws is None:
             ws = paged_workspace(tables=tables)
         if cu_seqlens is None:
-            cu_seqlens = torch.empty(tables.B + 1, dtype=torch.int32, device=dev)
+            cu_seqlens = c.empty(B + 1, dtype=c.int32, device=c.device)
         if slots is None:
-            slots = torch.empty(T, dtype=torch.int32, device=dev)
+            slots = c.empty(T, dtype=c.int32, device=c.device)
     lens_out = tables.lens if lens_out is None else lens_out
     n_free_out = tables.n_free if n_free_out is None else n_free_out
-    _on_device(fn, dev, add, lens_out, n_free_out, cu_seqlens, slots, ws)
-    _ints(fn, tables.B, add, lens_out)
-    _ints(fn, 1, n_free_out)
-    _ints(fn, tables.B + 1, cu_seqlens)
-    _ints(fn, T, slots)
-    with _lib._on(tables.table):
+    if not (c.ints(add, B) and c.ints(lens_out, B) and c.ints(n_free_out, 1) and c.ints(cu_seqlens, B + 1)
+            and c.ints(slots, T) and ws.get_device() == c.gpu):
+        raise AttnError(fn, ATTN_E_INVAL)
+    with _lib._on(table):
         _lib._check("attn_paged_reserve", _lib.lib().attn_paged_reserve(
-            add.data_ptr(), tables.lens.data_ptr(), tables.B, tables.page, tables.free.numel(), tables.n_free.data_ptr(),
-            tables.free.data_ptr(), tables.table.data_ptr(), tables.ld, tables.max_pages, lens_out.data_ptr(),
+            add.data_ptr(), tables.lens.data_ptr(), B, tables.page, tables.free.numel(), tables.n_free.data_ptr(),
+            tables.free.data_ptr(), table.data_ptr(), tables.ld, tables.max_pages, lens_out.data_ptr(),
             n_free_out.data_ptr(), cu_seqlens.data_ptr(), slots.data_ptr(), T, ws.data_ptr(),
-            ws.numel() * ws.element_size(), _lib._stream_of(stream, tables.table)))
+            ws.numel() * ws.element_size(), c.stream(stream, table)))
     return cu_seqlens, slots
 
 
 def paged_store(cache: PagedCache, k, v, slots, ws=None, stream=None) -> None:
     """Store the rows of k and v, bf16 packed [T, Hkv, D], in the slots (int32 [T]) that
     paged_reserve named; rows with slot -1 are skipped."""
-    import torch
     fn = "paged_store"
+    c = cache._calls
     if ws is None:
-        with _lib._alloc_on(stream, cache.device):
+        with _lib._alloc_on(stream, c.device):
             ws = paged_workspace(cache)
-    _, ref = cache._shape(k, 1.0)
-    _on_device(fn, cache.device, k, v, slots, ws)
-    _ints(fn, k.shape[0], slots)
-    if not (k.dtype is torch.bfloat16 and v.dtype is torch.bfloat16 and k.shape == v.shape
+    ref = cache._shape(k, 1.0)
+    if not (c.ints(slots, k.shape[0]) and k.dtype is c.bf16 and v.dtype is c.bf16 and k.get_device() == c.gpu
+            and v.get_device() == c.gpu and ws.get_device() == c.gpu and k.shape == v.shape
             and (k.stride() == v.stride() or _lib._same_rows(k, v))):
         raise AttnError(fn, ATTN_E_INVAL)
     with _lib._on(k):
         _lib._check("attn_paged_store", _lib.lib().attn_paged_store(
             k.data_ptr(), v.data_ptr(), ref, cache._ref, slots.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(),
-            _lib._stream_of(stream, k)))
+            c.stream(stream, k)))
 
 
 def paged_attention(q, cache: PagedCache, table, lens, cu_seqlens=None, scale: Optional[float] = None, o=None, lse=None,
@@ -191,29 +195,32 @@ def paged_attention(q, cache: PagedCache, table, lens, cu_seqlens=None, scale: O
     cu_seqlens (int32 [B + 1]) every sequence has T / B tokens. lse: fp32 [1, H, T]. o and lse
     may be given (o with q's strides); rows of padding stay as they were. o has q's strides,
     gaps included: for a slice of a wide tensor pass a contiguous copy."""
-    import torch
     fn = "paged_attention"
-    shape, ref = cache._shape(q, scale)
-    B = table.shape[0]
-    T, H = q.shape[0], q.shape[1]
-    with _lib._alloc_on(stream, cache.device):
+    c = cache._calls
+    ref = cache._shape(q, scale)
+    T, H, _ = q.shape
+    if not c.table(table):
+        raise AttnError(fn, ATTN_E_INVAL)
+    B, most = table.shape
+    if not (q.dtype is c.bf16 and q.get_device() == c.gpu and c.ints(lens, B)
+            and (cu_seqlens is None or c.ints(cu_seqlens, B + 1))
+            and (o is None or o.dtype is c.bf16 and o.get_device() == c.gpu and o.shape == q.shape
+                 and (o.stride() == q.stride() or _lib._same_rows(o, q)))
+            and (lse is None or lse.dtype is c.fp32 and lse.get_device() == c.gpu and lse.numel() == H * T
+                 and lse.is_contiguous())
+            and (ws is None or ws.get_device() == c.gpu)):
+        raise AttnError(fn, ATTN_E_INVAL)
+    with _lib._alloc_on(stream, c.device):
         if ws is None:
             ws = paged_workspace(cache, q, B)
         if o is None:
-            o = torch.empty_like(q) if q.is_contiguous() else \
-                torch.empty_strided(q.shape, q.stride(), dtype=q.dtype, device=q.device)
+            o = c.empty_like(q) if q.is_contiguous() else \
+                c.empty_strided(q.shape, q.stride(), dtype=c.bf16, device=c.device)
         if lse is None:
-            lse = torch.empty((1, H, T), dtype=torch.float32, device=q.device)
-    _on_device(fn, cache.device, q, table, lens, cu_seqlens, o, lse, ws)
-    _ints(fn, B, lens)
-    _ints(fn, B + 1, cu_seqlens)
-    ld = _lib._table_ld(fn, table)
-    if not (q.dtype is torch.bfloat16 and o.dtype is torch.bfloat16 and o.shape == q.shape
-            and (o.stride() == q.stride() or _lib._same_rows(o, q)) and lse.dtype is torch.float32
-            and lse.numel() == H * T and lse.is_contiguous()):
-        raise AttnError(fn, ATTN_E_INVAL)
+            lse = c.empty((1, H, T), dtype=c.fp32, device=c.device)
     with _lib._on(q):
         _lib._check("attn_paged_attend", _lib.lib().attn_paged_attend(
-            q.data_ptr(), ref, cache._ref, table.data_ptr(), ld, table.shape[1], lens.data_ptr(), _lib._ptr(cu_seqlens), B,
-            o.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), _lib._stream_of(stream, q)))
+            q.data_ptr(), ref, cache._ref, table.data_ptr(), table.stride(0) if B > 1 else most, most, lens.data_ptr(),
+            None if cu_seqlens is None else cu_seqlens.data_ptr(), B,
+            o.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), c.stream(stream, q)))
     return o, lse
