@@ -45,6 +45,7 @@ using kv4::launch_early;
 constexpr int kThreads = 256;
 constexpr int kRuns = 128;                     // the sequences are taken in so many runs by the block-wide sums
 constexpr int kItemsPerSm = 4;
+constexpr int kGatherPage = 32;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0;
 constexpr uint32_t kColO = 256;
@@ -345,6 +346,18 @@ __device__ __forceinline__ bool only_finite(uint4& x) {
     return any;
 }
 
+// 16 bytes of global memory to shared memory, or zeros, asynchronously.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)),
+                 "r"(there ? 16 : 0)
+                 : "memory");
+}
+// An arrival on `bar` when this thread's copies so far have landed.
+__device__ __forceinline__ void copy_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_all;\n" ::: "memory"); }
+
 // Page of the pool that holds slot j of an item's sequence, `pages` (none) behind the last or outside the pool.
 __device__ __forceinline__ int32_t page_of(const PagedAttendArgs& a, int32_t b, int32_t n, int64_t j) {
     if (j >= n) return a.c.pages;
@@ -369,7 +382,7 @@ __device__ __noinline__ float not_finite(const PagedAttendArgs& a, int32_t b, in
     return sum;
 }
 
-template <int D>
+template <int D, bool GATHER>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmq_few,
                   const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
@@ -394,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int s = 0; s < KVS; ++s) {
             mbar_init(bar(LY::B_KFULL + s), 1);
             mbar_init(bar(LY::B_KEMPTY + s), 1);
-            mbar_init(bar(LY::B_VFULL + s), 1);
+            mbar_init(bar(LY::B_VFULL + s), GATHER ? 64 : 1);       // every lane of warps 2 and 3
             mbar_init(bar(LY::B_VEMPTY + s), 1);
             mbar_init(bar(LY::B_VFIX + s), 2);         // warps 2 and 3
         }
@@ -448,10 +461,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         return go;
     };
 
+    const int boxes = BN / t.box;                       // of a tile
+    const int window = 32 / boxes;                      // tiles whose pages a warp's lanes hold
+    const int box_shift = 31 - __clz(t.box);
+    // page of box `lane` of an item's tiles from `first` on
+    auto pages_at = [&](const Item& it, int32_t first) {
+        const int64_t j = (int64_t)it.k0 + (int64_t)first * BN + lane * t.box;
+        return lane < window * boxes && first < it.tiles ? page_of(a, it.b, it.n, j) : a.c.pages;
+    };
+
     if (warp == 0) {
         // ------------------------------------------------------------ items and loads
-        const int boxes = BN / t.box;                   // of a tile
-        const int window = 32 / boxes;                  // tiles whose pages the lanes hold
         uint32_t kc = 0, ne = 0;
         int32_t w = a.stall ? L.n_items : (int32_t)blockIdx.x;
         bool ok = !a.stall;
@@ -477,12 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (it.tiles < 0 || __any_sync(0xffffffffu, *abort_flag)) break;
             if (it.tiles > 0) {
-                // page of box `lane` of the tiles from `first` on
-                auto pages_at = [&](int32_t first) {
-                    const int64_t j = (int64_t)it.k0 + (int64_t)first * BN + lane * t.box;
-                    return lane < window * boxes && first < it.tiles ? page_of(a, it.b, it.n, j) : a.c.pages;
-                };
-                int32_t ahead = pages_at(0), now = 0;
+                int32_t ahead = pages_at(it, 0), now = 0;
                 ok = mbar_wait_warp(bar(LY::B_QEMPTY), (ne & 1) ^ 1, abort_flag, a.status, a.wait_ns);
                 if (!ok) break;
                 const bool few = it.box == t.few && t.few < t.tok;
@@ -503,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int32_t in = j % window;
                     if (in == 0) {
                         now = ahead;
-                        ahead = pages_at(j + window);
+                        ahead = pages_at(it, j + window);
                     }
                     const int32_t id = __shfl_sync(0xffffffffu, now, (in * boxes + bi) & 31);
                     const int32_t place = (it.k0 + j * BN + bi * t.box) & ((1 << a.c.shift) - 1);
@@ -517,11 +532,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0) mbar_expect_tx(bar(LY::B_KFULL + s), LY::TILE_KV);
                     __syncwarp();
                     if (loads) tma_load_4d(sbase + LY::K_OFF + off, &tmk, bar(LY::B_KFULL + s), bc * 64, c1, c2, c3);
-                    ok = mbar_wait_warp(bar(LY::B_VEMPTY + s), turn ^ 1, abort_flag, a.status, a.wait_ns);
-                    if (!ok) break;
-                    if (lane == 0) mbar_expect_tx(bar(LY::B_VFULL + s), LY::TILE_KV);
-                    __syncwarp();
-                    if (loads) tma_load_4d(sbase + LY::V_OFF + off, &tmv, bar(LY::B_VFULL + s), bc * 64, c1, c2, c3);
+                    if (!GATHER) {
+                        ok = mbar_wait_warp(bar(LY::B_VEMPTY + s), turn ^ 1, abort_flag, a.status, a.wait_ns);
+                        if (!ok) break;
+                        if (lane == 0) mbar_expect_tx(bar(LY::B_VFULL + s), LY::TILE_KV);
+                        __syncwarp();
+                        if (loads) tma_load_4d(sbase + LY::V_OFF + off, &tmv, bar(LY::B_VFULL + s), bc * 64, c1, c2, c3);
+                    }
                     ++kc;
                 }
             }
@@ -572,9 +589,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         const uint32_t vs = vc % KVS;
                         ok = mbar_wait(bar(LY::B_VFULL + vs), (vc / KVS) & 1, abort_flag, a.status, a.wait_ns) &&
-                             mbar_wait(bar(LY::B_VFIX + vs), (vc / KVS) & 1, abort_flag, a.status, a.wait_ns) &&
+                             (GATHER ||
+                              mbar_wait(bar(LY::B_VFIX + vs), (vc / KVS) & 1, abort_flag, a.status, a.wait_ns)) &&
                              mbar_wait(bar(LY::B_PFULL + pb), (x >> 1) & 1, abort_flag, a.status, a.wait_ns);
                         if (!ok) break;
+                        if (GATHER) fence_proxy_async_smem();      // V came by copies of the generic proxy
                         tc_fence_after();
                         const uint32_t v0 = sbase + LY::V_OFF + vs * LY::TILE_KV;
                         const uint32_t pa = tmem + kColS + pb * BN;
@@ -592,6 +611,83 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++ne;
             }
         }
+    } else if (warp < 4 && GATHER) {
+        // ------------------------------------------------------------ V by 16-byte copies, half a tile each
+        constexpr int PIECES = D / 8, ROWS = 32 / PIECES, STEPS = 16 / ROWS;   // of a row; rows a step; steps of 16 rows
+        constexpr int BLOCKS = BN / 32;                  // of 16 rows, in a warp's half of a tile
+        const int piece = lane % PIECES, r_lane = lane / PIECES;
+        const bool in_row = piece * 8 < a.g.D;
+        // this lane's place in a tile: rows r_lane + ROWS i, whose low bits the swizzle mixes into the piece's
+        const uint32_t ring = sbase + LY::V_OFF + (piece >> 3) * (BN * 128) + r_lane * 128;
+        const uint32_t mixed = (uint32_t)((piece & 7) ^ r_lane);
+        const __nv_bfloat16* rows = static_cast<const __nv_bfloat16*>(a.c.v) + (in_row ? piece * 8 : 0);
+        const int64_t step = ROWS * a.c.st;
+        Item it;
+        bool ok = true;
+        uint32_t kc = 0, ne = 0;
+        for (uint32_t ic = 0; ok; ++ic) {
+            if (!next_item_warp(ic, it)) break;
+            if (it.tiles == 0) continue;
+            int32_t ahead = pages_at(it, 0), now = 0;
+            const __nv_bfloat16* head = rows + it.hk * a.c.sh;
+            for (int32_t j = 0; j < it.tiles; ++j) {
+                const int32_t in = j % window;
+                if (in == 0) {
+                    now = ahead;
+                    ahead = pages_at(it, j + window);
+                }
+                // the addresses first, while the stage may still be read
+                const int32_t j0 = it.k0 + j * BN + (warp - 2) * (BN / 2);   // this warp's half
+                const __nv_bfloat16* src[BLOCKS];
+                int32_t used[BLOCKS];                    // rows from this lane's first on that hold a slot in use
+#pragma unroll
+                for (int x = 0; x < BLOCKS; ++x) {
+                    const int32_t id = __shfl_sync(
+                        0xffffffffu, now, (in * boxes + (((warp - 2) * (BN / 2) + x * 16) >> box_shift)) & 31);
+                    const int32_t first = j0 + x * 16 + r_lane;
+                    const bool page = in_row && id < a.c.pages;
+                    src[x] = page ? head + id * a.c.sp + (first & ((1 << a.c.shift) - 1)) * a.c.st : rows;
+                    used[x] = page ? it.n - first : 0;
+                }
+                const uint32_t s = kc % KVS;
+                ok = mbar_wait_warp(bar(LY::B_VEMPTY + s), ((kc / KVS) & 1) ^ 1, abort_flag, a.status, a.wait_ns);
+                if (!ok) break;
+                const uint32_t dst = ring + s * LY::TILE_KV + (warp - 2) * (BN / 2) * 128;
+                const bool some = j0 + BN / 2 > it.seen && it.seen < it.n;   // some rows are not seen by all
+                if (!some) {
+#pragma unroll
+                    for (int x = 0; x < BLOCKS; ++x)
+#pragma unroll
+                        for (int i = 0; i < STEPS; ++i)
+                            copy16(dst + (x * 16 + i * ROWS) * 128 + ((mixed ^ ((i * ROWS) & 7)) << 4), src[x] + i * step,
+                                   i * ROWS < used[x]);
+                    copy_arrive(bar(LY::B_VFULL + s));
+                } else {
+                    bool any = false;
+#pragma unroll
+                    for (int x = 0; x < BLOCKS; ++x)
+#pragma unroll 1
+                        for (int i = 0; i < STEPS; ++i) {
+                            const uint32_t to = dst + (x * 16 + i * ROWS) * 128 + ((mixed ^ ((i * ROWS) & 7)) << 4);
+                            if (i * ROWS < used[x] && j0 + x * 16 + r_lane + i * ROWS >= it.seen) {
+                                uint4 y = *reinterpret_cast<const uint4*>(src[x] + i * step);
+                                any = only_finite(y) || any;
+                                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(to), "r"(y.x), "r"(y.y),
+                                             "r"(y.z), "r"(y.w)
+                                             : "memory");
+                            } else {
+                                copy16(to, i * ROWS < used[x] ? src[x] + i * step : rows, i * ROWS < used[x]);
+                            }
+                        }
+                    if (any) to_add[ne & 3] = ne + 1;
+                    copy_wait_all();                     // plain stores are among them, which copy_arrive does not follow
+                    mbar_arrive(bar(LY::B_VFULL + s));
+                }
+                ++kc;
+            }
+            ++ne;
+        }
+        copy_wait_all();
     } else if (warp < 4) {
         // ------------------------------------------------------------ what no row may see of V
         Item it;
@@ -938,7 +1034,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const PagedAtte
     if (lane == 0) a.lse[(int64_t)h * a.g.T + tok] = l == 0.f ? -INFINITY : (m + lg2(l)) * kLn2;
 }
 
-template <int D>
+template <int D, bool GATHER>
 cudaError_t launch_d(const PagedAttendArgs& a, cudaStream_t s) {
     CUtensorMap mq, mq_few, mk, mv;
     TcMaps mpq{1, 2, 3}, mpkv{1, 2, 3};
@@ -949,10 +1045,10 @@ cudaError_t launch_d(const PagedAttendArgs& a, cudaStream_t s) {
         return cudaErrorInvalidValue;
     t.head_major = mpq.pos_t < mpq.pos_h;
     static_assert(Layout<D>::ALLOC <= 232448, "shared memory of the paged attention's kernel");
-    cudaError_t e = cudaFuncSetAttribute(attend_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(attend_kernel<D, GATHER>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)Layout<D>::ALLOC);
     if (e != cudaSuccess) return e;
-    e = launch_early(attend_kernel<D>, dim3(device_sm_count()), kThreads, Layout<D>::ALLOC, 1, s, mq, mq_few, mk, mv, a,
+    e = launch_early(attend_kernel<D, GATHER>, dim3(device_sm_count()), kThreads, Layout<D>::ALLOC, 1, s, mq, mq_few, mk, mv, a,
                      mpq, mpkv, t);
     if (e != cudaSuccess) return e;
     const int64_t rows = (int64_t)a.g.T * a.g.H;
@@ -978,8 +1074,10 @@ bool paged_units_fit(const PagedGeom& c, const Geom& g, int64_t B) {
 
 cudaError_t launch_paged_attend(const PagedAttendArgs& a, cudaStream_t s) {
     // head dims run on tiles of 64, 128 or 256, as the forward's
-    if (a.g.D > 128) return launch_d<256>(a, s);
-    return a.g.D > 64 ? launch_d<128>(a, s) : launch_d<64>(a, s);
+    const bool gather = a.c.page() <= kGatherPage;
+    if (a.g.D > 128) return gather ? launch_d<256, true>(a, s) : launch_d<256, false>(a, s);
+    if (a.g.D > 64) return gather ? launch_d<128, true>(a, s) : launch_d<128, false>(a, s);
+    return gather ? launch_d<64, true>(a, s) : launch_d<64, false>(a, s);
 }
 
 }  // namespace attn
