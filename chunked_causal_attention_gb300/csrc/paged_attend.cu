@@ -43,8 +43,8 @@ using kv4::grid_wait;
 using kv4::launch_early;
 
 constexpr int kThreads = 256;
-constexpr int kRuns = 128;                     // the sequences are taken in so many runs by the block-wide sums
-constexpr int kItemsPerSm = 4;
+constexpr int kItemsPerSm = 6;                 // the smallest items are a sixth of an SM's work
+constexpr float kItemTiles = 3.f;              // what an item takes beside its key tiles, in those
 constexpr int kGatherPage = 32;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0;
@@ -54,12 +54,16 @@ constexpr float kLag = 8.f;                    // how far (log2) a tile's maximu
 // What the launch derives from the shapes.
 struct Tiling {
     int32_t heads, blocks;     // query heads of a row tile, and how many such tiles a key/value head's heads make
+    int32_t group;             // query heads of a key/value head
+    int32_t units;             // units of a row tile's tokens: key/value heads by blocks of heads
     int32_t tok, few;          // tokens of a row tile, and of the small box that brings fewer
+    FastDiv by_tok;
     int32_t head_major;        // rows of a tile: head * tokens of the box + token, or token * heads + head
     int32_t box;               // slots of a TMA box of K and V
     int32_t part_rows;         // rows of a partial
     int64_t part_floats;       // floats of a partial: rows of D, then their LSEs (base 2)
-    int64_t target;            // items that the whole work is cut into, about
+    int32_t sms;
+    float part_tiles;          // what a partial takes to write and read again, in key tiles
 };
 
 __host__ __device__ constexpr int block_n(int d) { return d > 128 ? 64 : 128; }     // slots of a key tile
@@ -70,13 +74,17 @@ Tiling tiling(const PagedGeom& c, const Geom& g) {
     const int32_t G = g.H / c.Hkv;
     t.heads = std::min(G, kTile);
     t.blocks = (G - 1) / t.heads + 1;
+    t.group = G;
+    t.units = c.Hkv * t.blocks;
     t.tok = kTile / t.heads;
+    t.by_tok = FastDiv::of((uint32_t)t.tok);
     t.few = std::max(1, std::min(t.tok, 16 / t.heads));
     t.head_major = 0;
     t.box = std::min(c.page(), block_n(g.D));
     t.part_rows = (int32_t)std::min<int64_t>(t.tok, g.T) * t.heads;
     t.part_floats = ((int64_t)t.part_rows * (g.D + 1) + 31) / 32 * 32;
-    t.target = (int64_t)kItemsPerSm * device_sm_count();
+    t.sms = device_sm_count();
+    t.part_tiles = 4.f * t.part_rows / kTile;
     return t;
 }
 
@@ -111,108 +119,124 @@ __device__ __forceinline__ Seq seq_of(const PagedAttendArgs& a, int32_t b) {
     return s;
 }
 
-__device__ __forceinline__ int32_t row_tiles_of(const Tiling& t, int32_t nq) { return nq > 0 ? (nq - 1) / t.tok + 1 : 0; }
+__device__ __forceinline__ int32_t row_tiles_of(const Tiling& t, int32_t nq) {
+    return nq > 0 ? (int32_t)t.by_tok.div((uint32_t)(nq - 1)) + 1 : 0;
+}
 
 // Units of a sequence, and the key tiles of its longest.
-__device__ __forceinline__ int64_t units_of(const PagedAttendArgs& a, const Tiling& t, const Seq& s) {
-    return (int64_t)a.c.Hkv * t.blocks * row_tiles_of(t, s.nq);
-}
+__device__ __forceinline__ int32_t units_of(const Tiling& t, const Seq& s) { return t.units * row_tiles_of(t, s.nq); }
 template <int BN>
 __device__ __forceinline__ int32_t tiles_of(const Seq& s) { return max(1, (s.n + BN - 1) / BN); }
 
-__device__ __forceinline__ int32_t parts_of(int32_t tiles, int64_t C) {
-    return tiles > C ? (int32_t)((tiles + C - 1) / C) : 1;
-}
+// n / d for whole numbers, where d is often one.
+__device__ __forceinline__ int32_t quotient(int32_t n, int32_t d) { return d == 1 ? n : (int32_t)((uint32_t)n / (uint32_t)d); }
 
-// What a block knows of the list: where the runs' items and partials begin.
+__device__ __forceinline__ int32_t parts_of(int32_t tiles, int32_t C) { return tiles > C ? (tiles - 1) / C + 1 : 1; }
+
+// The list as the lanes of a warp hold it: each a run of `per` sequences.
 struct List {
-    int32_t* items;            // shared memory, kRuns each
-    int32_t* parts;
-    int64_t C;
-    int32_t per;               // sequences of a run
+    int32_t items, parts;      // items and partials of the runs before
+    Seq seq;                   // the run's sequence, where it is one
+    int32_t per;
+    int32_t C;                 // most key tiles of an item
     int32_t n_items;
 };
 
-// Block-wide: sums over the sequences. scratch: 20 int64 in shared memory.
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
+    return x;
+}
+
+// Sizes of an item that are weighed against each other, in shares of an SM's work.
+constexpr int kTry = 8;
+__constant__ const float kShares[kTry] = {1.f / kItemsPerSm, 0.25f, 1.f / 3, 0.5f, 1.f, 1.25f, 1.5f, 2.f};
+
+// By one warp. `tell`: write a.cuts for the merge kernel.
 template <int BN>
-__device__ __forceinline__ void make_list(const PagedAttendArgs& a, const Tiling& t, List& L, int64_t* scratch) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    L.per = (a.B + kRuns - 1) / kRuns;
-    const int32_t b0 = (int32_t)min((int64_t)tid * L.per, (int64_t)a.B);
-    const int32_t b1 = tid < kRuns ? (int32_t)min((int64_t)b0 + L.per, (int64_t)a.B) : b0;
-    int64_t units = 0, work = 0;
-    int32_t tiles = 0;
+__device__ __forceinline__ List make_list(const PagedAttendArgs& a, const Tiling& t, bool tell) {
+    const int lane = threadIdx.x & 31;
+    List L;
+    L.per = (a.B + 31) / 32;
+    const int32_t b0 = (int32_t)min((int64_t)lane * L.per, (int64_t)a.B);
+    const int32_t b1 = (int32_t)min((int64_t)b0 + L.per, (int64_t)a.B);
+    float W = 0.f;
+    L.seq = Seq{0, 0, 0};
+#pragma unroll 4
     for (int32_t b = b0; b < b1; ++b) {
-        const Seq s = seq_of(a, b);
-        units = units_of(a, t, s);
-        tiles = tiles_of<BN>(s);
-        work += units * tiles;
+        L.seq = seq_of(a, b);
+        W += (float)units_of(t, L.seq) * (float)tiles_of<BN>(L.seq);
+    }
+    W = warp_sum(W);
+    // Of several sizes the one that is done first, in key tiles: by full rounds of the longest item, or as a queue
+    // hands items out, whichever is less. A lane takes one size and a quarter of the sequences.
+    const float sms = (float)t.sms;
+    const float size = fmaxf(1.f, ceilf(__fdividef(W, sms) * kShares[lane & (kTry - 1)]));
+    float n_items = 0.f, n_parts = 0.f, most = 0.f;
+    for (int32_t base = 0; base < a.B; base += 32) {
+        const Seq s = L.per == 1 ? L.seq : base + lane < a.B ? seq_of(a, base + lane) : Seq{0, 0, 0};
+        const float units = (float)units_of(t, s), tiles = (float)tiles_of<BN>(s);
+#pragma unroll 1
+        for (int i = 0; i < min(32, a.B - base); i += 32 / kTry) {
+            const float u = __shfl_sync(0xffffffffu, units, i + lane / kTry), n = __shfl_sync(0xffffffffu, tiles, i + lane / kTry);
+            const float p = ceilf(__fdividef(n, size));
+            n_items += u * p;
+            if (p > 1.f) n_parts += u * p;
+            if (u > 0.f) most = fmaxf(most, ceilf(__fdividef(n, p)));
+        }
     }
 #pragma unroll
-    for (int m = 16; m > 0; m >>= 1) work += __shfl_xor_sync(0xffffffffu, work, m);
-    if (lane == 0) scratch[warp] = work;
-    __syncthreads();
-    work = 0;
-    for (int w = 0; w < kRuns / 32; ++w) work += scratch[w];
-    L.C = max((int64_t)1, (work + t.target - 1) / t.target);
-    int64_t items = 0, cut = 0;
-    for (int32_t b = b0; b < b1; ++b) {
-        if (L.per > 1) {
-            const Seq s = seq_of(a, b);
-            units = units_of(a, t, s);
-            tiles = tiles_of<BN>(s);
-        }
-        const int32_t p = parts_of(tiles, L.C);
-        items += units * p;
-        if (p > 1) cut += units * p;
+    for (int m = kTry; m < 32; m <<= 1) {
+        n_items += __shfl_xor_sync(0xffffffffu, n_items, m);
+        n_parts += __shfl_xor_sync(0xffffffffu, n_parts, m);
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, m));
     }
-    int64_t items_to = items, cut_to = cut;
+    const float rounds = ceilf(__fdividef(n_items, sms)) * (most + kItemTiles);
+    const float queue = __fdividef(W + n_items * kItemTiles, sms) + most;
+    float time = fminf(rounds, queue) + __fdividef(n_parts, sms) * t.part_tiles, C = size;
+#pragma unroll
+    for (int m = 1; m < kTry; m <<= 1) {
+        const float time2 = __shfl_xor_sync(0xffffffffu, time, m), C2 = __shfl_xor_sync(0xffffffffu, C, m);
+        if (time2 < time || (time2 == time && C2 < C)) {
+            time = time2;
+            C = C2;
+        }
+    }
+    L.C = (int32_t)fminf(C, 1073741824.f);
+    int32_t items = 0, parts = 0;
+    float about = 0.f;                                   // their sum, where it does not fit an integer
+    for (int32_t b = b0; b < b1; ++b) {
+        if (L.per > 1) L.seq = seq_of(a, b);
+        const int32_t p = parts_of(tiles_of<BN>(L.seq), L.C), n = units_of(t, L.seq);
+        items += n * p;
+        if (p > 1) parts += n * p;
+        about += (float)n * (float)p;
+    }
+    int32_t items_to = items, parts_to = parts;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
-        const int64_t x = __shfl_up_sync(0xffffffffu, items_to, m), y = __shfl_up_sync(0xffffffffu, cut_to, m);
+        const int32_t x = __shfl_up_sync(0xffffffffu, items_to, m), y = __shfl_up_sync(0xffffffffu, parts_to, m);
         if (lane >= m) {
             items_to += x;
-            cut_to += y;
+            parts_to += y;
         }
     }
-    if (lane == 31) {
-        scratch[4 + warp] = items_to;
-        scratch[12 + warp] = cut_to;
-    }
-    __syncthreads();
-    int64_t items_all = 0, cut_all = 0, items_before = 0, cut_before = 0;
-    for (int w = 0; w < kRuns / 32; ++w) {
-        if (w < warp) {
-            items_before += scratch[4 + w];
-            cut_before += scratch[12 + w];
-        }
-        items_all += scratch[4 + w];
-        cut_all += scratch[12 + w];
-    }
-    items_before += items_to - items;
-    cut_before += cut_to - cut;
     // offsets that descend can give more items than there are tokens for: nothing is done then
-    const bool fits = items_all <= INT32_MAX && cut_all <= a.max_parts;
+    const bool fits = warp_sum(about) < 1073741824.f && __shfl_sync(0xffffffffu, parts_to, 31) <= a.max_parts;
     if (!fits) set_error(a.status, ATTN_E_BOUNDS);
-    L.n_items = fits ? (int32_t)items_all : 0;
-    if (tid < kRuns) {
-        L.items[tid] = fits ? (int32_t)items_before : 0;
-        L.parts[tid] = fits ? (int32_t)cut_before : 0;
-    }
-    if (blockIdx.x == 0) {
-        // for the merge kernel
+    L.n_items = fits ? __shfl_sync(0xffffffffu, items_to, 31) : 0;
+    L.items = fits ? items_to - items : 0;
+    L.parts = fits ? parts_to - parts : 0;
+    if (tell) {
+        int32_t before = parts_to - parts;
         for (int32_t b = b0; b < b1; ++b) {
-            if (L.per > 1) {
-                const Seq s = seq_of(a, b);
-                units = units_of(a, t, s);
-                tiles = tiles_of<BN>(s);
-            }
-            const int32_t p = fits ? parts_of(tiles, L.C) : 1;
-            a.cuts[b] = make_int2(p > 1 ? (int32_t)cut_before : 0, p);
-            if (p > 1) cut_before += units * p;
+            if (L.per > 1) L.seq = seq_of(a, b);
+            const int32_t p = fits ? parts_of(tiles_of<BN>(L.seq), L.C) : 1;
+            a.cuts[b] = make_int2(p > 1 ? before : 0, p);
+            if (p > 1) before += units_of(t, L.seq) * p;
         }
     }
-    __syncthreads();
+    return L;
 }
 
 // An item as its consumers read it from shared memory.
@@ -233,26 +257,26 @@ static_assert(sizeof(Item) == 48, "Item layout");
 template <int BN>
 __device__ __forceinline__ bool find_item(const PagedAttendArgs& a, const Tiling& t, const List& L, int32_t w, Item& it) {
     const int lane = threadIdx.x & 31;
-    int32_t r = -1;
-#pragma unroll
-    for (int i = 0; i < kRuns / 32; ++i) r += __popc(__ballot_sync(0xffffffffu, L.items[i * 32 + lane] <= w));
-    int64_t x = w - L.items[r], part0 = L.parts[r];
+    const int32_t r = __popc(__ballot_sync(0xffffffffu, L.items <= w)) - 1;
+    int32_t x = w - __shfl_sync(0xffffffffu, L.items, r), part0 = __shfl_sync(0xffffffffu, L.parts, r);
     int32_t b = r * L.per;
+    Seq s{__shfl_sync(0xffffffffu, L.seq.q0, r), __shfl_sync(0xffffffffu, L.seq.nq, r), __shfl_sync(0xffffffffu, L.seq.n, r)};
     if (L.per > 1) {
         const int32_t end = (int32_t)min((int64_t)b + L.per, (int64_t)a.B);
         bool found = false;
         for (; b < end; b += 32) {
-            int64_t items = 0, cut = 0;
+            int32_t items = 0, cut = 0;
+            s = Seq{0, 0, 0};
             if (b + lane < end) {
-                const Seq s = seq_of(a, b + lane);
+                s = seq_of(a, b + lane);
                 const int32_t p = parts_of(tiles_of<BN>(s), L.C);
-                items = units_of(a, t, s) * p;
+                items = units_of(t, s) * p;
                 cut = p > 1 ? items : 0;
             }
-            int64_t items_to = items, cut_to = cut;
+            int32_t items_to = items, cut_to = cut;
 #pragma unroll
             for (int m = 1; m < 32; m <<= 1) {
-                const int64_t u = __shfl_up_sync(0xffffffffu, items_to, m), v = __shfl_up_sync(0xffffffffu, cut_to, m);
+                const int32_t u = __shfl_up_sync(0xffffffffu, items_to, m), v = __shfl_up_sync(0xffffffffu, cut_to, m);
                 if (lane >= m) {
                     items_to += u;
                     cut_to += v;
@@ -263,6 +287,7 @@ __device__ __forceinline__ bool find_item(const PagedAttendArgs& a, const Tiling
                 const int f = __ffs(past) - 1;
                 x -= __shfl_sync(0xffffffffu, items_to - items, f);
                 part0 += __shfl_sync(0xffffffffu, cut_to - cut, f);
+                s = Seq{__shfl_sync(0xffffffffu, s.q0, f), __shfl_sync(0xffffffffu, s.nq, f), __shfl_sync(0xffffffffu, s.n, f)};
                 b += f;
                 found = true;
                 break;
@@ -273,13 +298,12 @@ __device__ __forceinline__ bool find_item(const PagedAttendArgs& a, const Tiling
         if (!found) return false;
     }
     if (b >= a.B) return false;
-    const Seq s = seq_of(a, b);
     const int32_t parts = parts_of(tiles_of<BN>(s), L.C), row_tiles = row_tiles_of(t, s.nq);
-    if (x >= units_of(a, t, s) * parts || (parts > 1 && part0 + x >= a.max_parts)) return false;
+    if (x < 0 || quotient(x, parts) >= units_of(t, s) || (parts > 1 && part0 + x >= a.max_parts)) return false;
     // key/value head, block of heads, part, row tile: the tiles with the most slots first
-    const int32_t y = (int32_t)x / row_tiles, rt = row_tiles - 1 - ((int32_t)x - y * row_tiles);
-    const int32_t u = y / parts, p = y - u * parts, hk = u / t.blocks, hb = u - hk * t.blocks;
-    const int32_t G = a.g.H / a.c.Hkv, i0 = rt * t.tok;
+    const int32_t y = quotient(x, row_tiles), rt = row_tiles - 1 - (x - y * row_tiles);
+    const int32_t u = quotient(y, parts), p = y - u * parts, hk = quotient(u, t.blocks), hb = u - hk * t.blocks;
+    const int32_t G = t.group, i0 = rt * t.tok;
     it.tok0 = s.q0 + i0;
     it.toks = min(t.tok, s.nq - i0);
     it.head0 = hk * G + hb * t.heads;
@@ -287,10 +311,11 @@ __device__ __forceinline__ bool find_item(const PagedAttendArgs& a, const Tiling
     it.seen = s.n - s.nq + i0 + 1;
     it.n = s.n;
     const int32_t last = max(0, it.seen + it.toks - 1), tiles = (last + BN - 1) / BN;
-    const int32_t t0 = (int32_t)((int64_t)p * tiles / parts), t1 = (int32_t)((int64_t)(p + 1) * tiles / parts);
-    it.tiles = t1 - t0;
-    it.k0 = t0 * BN;
-    it.part = parts > 1 ? (int32_t)(part0 + x) : -1;
+    // tiles in equal parts, the first ones with one more where they do not divide
+    const int32_t each = quotient(tiles, parts), more = tiles - each * parts;
+    it.tiles = each + (p < more ? 1 : 0);
+    it.k0 = (p * each + min(p, more)) * BN;
+    it.part = parts > 1 ? part0 + x : -1;
     it.box = it.toks <= t.few ? t.few : t.tok;
     it.b = b;
     it.hk = hk;
@@ -320,10 +345,8 @@ struct Layout {
     static constexpr int B_RFULL = B_DRAIN + 1, B_REMPTY = B_RFULL + 2;   // items: 2 slots
     static constexpr int NBAR = B_REMPTY + 2;
     static constexpr int ITEM_OFF = BAR_OFF + (NBAR * 8 + 15) / 16 * 16;
-    static constexpr int LIST_OFF = ITEM_OFF + 2 * (int)sizeof(Item);
-    static constexpr int MISC_OFF = LIST_OFF + 2 * kRuns * 4;  // TMEM base, abort flag, 4 x item with values to add
-    static constexpr int SCRATCH_OFF = MISC_OFF + 32;
-    static constexpr int BYTES = SCRATCH_OFF + 20 * 8;
+    static constexpr int MISC_OFF = ITEM_OFF + 2 * (int)sizeof(Item);   // TMEM base, abort flag, 4 x item with values to add
+    static constexpr int BYTES = MISC_OFF + 32;
     static constexpr size_t ALLOC = (size_t)BYTES + 1024;      // slack for 1024-byte alignment
 };
 
@@ -358,12 +381,15 @@ __device__ __forceinline__ void copy_arrive(uint32_t bar) {
 }
 __device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_all;\n" ::: "memory"); }
 
-// Page of the pool that holds slot j of an item's sequence, `pages` (none) behind the last or outside the pool.
-__device__ __forceinline__ int32_t page_of(const PagedAttendArgs& a, int32_t b, int32_t n, int64_t j) {
-    if (j >= n) return a.c.pages;
-    const int32_t id = a.table[(int64_t)b * a.table_ld + (j >> a.c.shift)];
-    if ((uint32_t)id < (uint32_t)a.c.pages) return id;
-    set_error(a.status, ATTN_E_BOUNDS);
+// What the table holds for slot j of an item's sequence, kNone behind the last.
+constexpr int32_t kNone = INT32_MIN;
+__device__ __forceinline__ int32_t entry_of(const PagedAttendArgs& a, int32_t b, int32_t n, int64_t j) {
+    return j < n ? max(a.table[(int64_t)b * a.table_ld + (j >> a.c.shift)], -1) : kNone;
+}
+// The page that it names; `pages`, which holds nothing, for none and for one outside the pool.
+__device__ __forceinline__ int32_t page_of(const PagedAttendArgs& a, int32_t entry) {
+    if ((uint32_t)entry < (uint32_t)a.c.pages) return entry;
+    if (entry != kNone) set_error(a.status, ATTN_E_BOUNDS);
     return a.c.pages;
 }
 
@@ -373,7 +399,7 @@ __device__ __noinline__ float not_finite(const PagedAttendArgs& a, int32_t b, in
                                          int32_t to, int d) {
     float sum = 0.f;
     for (int32_t j = from; j < to && d < a.g.D; ++j) {
-        const int32_t id = page_of(a, b, n, j);
+        const int32_t id = page_of(a, entry_of(a, b, n, j));
         if (id >= a.c.pages) continue;
         const uint32_t v = static_cast<const uint16_t*>(a.c.v)[id * a.c.sp + hk * a.c.sh +
                                                                 (j & ((1 << a.c.shift) - 1)) * a.c.st + d];
@@ -435,13 +461,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch_desc(&tmk);
         tma_prefetch_desc(&tmv);
     }
-    grid_wait();
-    grid_go();
-    List L{reinterpret_cast<int32_t*>(sm + LY::LIST_OFF), reinterpret_cast<int32_t*>(sm + LY::LIST_OFF) + kRuns, 1, 1, 0};
-    make_list<BN>(a, t, L, reinterpret_cast<int64_t*>(sm + LY::SCRATCH_OFF));
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    grid_wait();
+    grid_go();
     const uint32_t tmem = *tmem_slot;
 
     // the next item, for a consumer that is one thread or a warp (`one`: this lane arrives for it)
@@ -464,14 +488,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int boxes = BN / t.box;                       // of a tile
     const int window = 32 / boxes;                      // tiles whose pages a warp's lanes hold
     const int box_shift = 31 - __clz(t.box);
-    // page of box `lane` of an item's tiles from `first` on
+    // table entry of box `lane` of an item's tiles from `first` on
     auto pages_at = [&](const Item& it, int32_t first) {
         const int64_t j = (int64_t)it.k0 + (int64_t)first * BN + lane * t.box;
-        return lane < window * boxes && first < it.tiles ? page_of(a, it.b, it.n, j) : a.c.pages;
+        return lane < window * boxes && first < it.tiles ? entry_of(a, it.b, it.n, j) : kNone;
     };
 
     if (warp == 0) {
         // ------------------------------------------------------------ items and loads
+        const List L = make_list<BN>(a, t, blockIdx.x == 0);
         uint32_t kc = 0, ne = 0;
         int32_t w = a.stall ? L.n_items : (int32_t)blockIdx.x;
         bool ok = !a.stall;
@@ -517,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int32_t j = 0; j < it.tiles && ok; ++j) {
                     const int32_t in = j % window;
                     if (in == 0) {
-                        now = ahead;
+                        now = page_of(a, ahead);
                         ahead = pages_at(it, j + window);
                     }
                     const int32_t id = __shfl_sync(0xffffffffu, now, (in * boxes + bi) & 31);
@@ -633,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int32_t j = 0; j < it.tiles; ++j) {
                 const int32_t in = j % window;
                 if (in == 0) {
-                    now = ahead;
+                    now = page_of(a, ahead);
                     ahead = pages_at(it, j + window);
                 }
                 // the addresses first, while the stage may still be read
@@ -762,30 +787,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int c = 0; c < NC; ++c) tmem_ld32(sa + c * 32, r[c]);
                 tmem_ld_wait();
                 const int j0 = it.k0 + j * BN;
-                float mt, mul = sl2;
+                float mul = sl2;
                 if (j0 + BN > it.seen || !(sl2 > 0.f)) {
                     // scaled before they are masked and compared, whatever the scale's sign
                     const int lim = seen - j0;           // columns c < lim are seen
-                    mt = -INFINITY;
                     mul = 1.f;
 #pragma unroll
                     for (int c = 0; c < NC; ++c)
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const float s = (c * 32 + i < lim) ? __uint_as_float(r[c][i]) * sl2 : -INFINITY;
-                            r[c][i] = __float_as_uint(s);
-                            mt = fmaxf(mt, s);
-                        }
-                } else {
-                    float hi4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (int c = 0; c < NC; ++c)
-#pragma unroll
-                        for (int i = 0; i < 32; i += 2)
-                            hi4[(c * 2 + (i >> 4)) & 3] =
-                                fmax3(hi4[(c * 2 + (i >> 4)) & 3], __uint_as_float(r[c][i]), __uint_as_float(r[c][i + 1]));
-                    mt = fmax3(fmaxf(hi4[0], hi4[1]), hi4[2], hi4[3]) * sl2;
+                        for (int i = 0; i < 32; ++i)
+                            r[c][i] = __float_as_uint((c * 32 + i < lim) ? __uint_as_float(r[c][i]) * sl2 : -INFINITY);
                 }
+                float hi4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int c = 0; c < NC; ++c)
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2)
+                        hi4[(c * 2 + (i >> 4)) & 3] =
+                            fmax3(hi4[(c * 2 + (i >> 4)) & 3], __uint_as_float(r[c][i]), __uint_as_float(r[c][i + 1]));
+                const float mt = fmax3(fmaxf(hi4[0], hi4[1]), hi4[2], hi4[3]) * mul;
                 bool rescale = false;
                 float alpha = 1.f;
                 if (mt > m_run + kLag) {
@@ -849,53 +869,68 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float lse2 = l_run == 0.f ? -INFINITY : m_run + lg2(l_run);
             const uint32_t oa = tmem + lane_addr + kColO;
             if (warp_live) {
-                __nv_bfloat16* dst = nullptr;
-                float* part = nullptr;
-                if (it.part < 0) {
-                    dst = reinterpret_cast<__nv_bfloat16*>(a.o) + (int64_t)tok * a.g.st + (int64_t)h * a.g.sh;
-                    if (live) a.lse[(int64_t)h * a.g.T + tok] = lse2 * kLn2;
-                } else {
-                    float* base = a.parts + it.part * t.part_floats;
-                    part = base + (int64_t)(ti * t.heads + gi) * Dv;
-                    if (live) base[(int64_t)t.part_rows * Dv + ti * t.heads + gi] = lse2;
+                __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(a.o) + (int64_t)tok * a.g.st + (int64_t)h * a.g.sh;
+                const int at = ti * t.heads + gi;
+                float* base = a.parts + it.part * t.part_floats;
+                float* part = base + (int64_t)at * Dv;
+                if (live) {
+                    if (it.part < 0)
+                        a.lse[(int64_t)h * a.g.T + tok] = lse2 * kLn2;
+                    else
+                        base[(int64_t)t.part_rows * Dv + at] = lse2;
                 }
+                // as much of O at a time as the scores took registers
+                constexpr int AT_ONCE = BN / 32;
 #pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
-                    uint32_t o[32];
-                    if (!empty) {
-                        tmem_ld32(oa + c * 32, o);
-                        tmem_ld_wait();
-                    } else {
+                for (int c0 = 0; c0 < D / 32; c0 += AT_ONCE) {
+                    uint32_t o[AT_ONCE][32];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = 0;
+                    for (int c = 0; c < AT_ONCE; ++c) {
+                        if (c0 + c >= D / 32) break;
+                        if (!empty) {
+                            tmem_ld32(oa + (c0 + c) * 32, o[c]);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[c][i] = 0;
+                        }
                     }
+                    tmem_ld_wait();
                     if (!live) continue;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
-                    if (add)
+                    for (int c = 0; c < AT_ONCE; ++c) {
+                        const int d0 = (c0 + c) * 32;
+                        if (d0 >= D) break;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            o[i] = __float_as_uint(__uint_as_float(o[i]) +
-                                                   not_finite(a, it.b, it.hk, it.n, add0, add1, c * 32 + i));
-                    if (dst) {
-                        uint4* d4 = reinterpret_cast<uint4*>(dst + c * 32);
+                        for (int i = 0; i < 32; ++i) o[c][i] = __float_as_uint(__uint_as_float(o[c][i]) * inv);
+                        if (it.part < 0) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            if (c * 32 + i * 8 >= Dv) break;
-                            uint4 y;
-                            y.x = pack_bf16(__uint_as_float(o[8 * i + 0]), __uint_as_float(o[8 * i + 1]));
-                            y.y = pack_bf16(__uint_as_float(o[8 * i + 2]), __uint_as_float(o[8 * i + 3]));
-                            y.z = pack_bf16(__uint_as_float(o[8 * i + 4]), __uint_as_float(o[8 * i + 5]));
-                            y.w = pack_bf16(__uint_as_float(o[8 * i + 6]), __uint_as_float(o[8 * i + 7]));
-                            d4[i] = y;
+                            for (int i = 0; i < 32; i += 8) {
+                                if (d0 + i >= Dv) break;
+                                const uint32_t* x = &o[c][i];
+                                *reinterpret_cast<uint4*>(dst + d0 + i) =
+                                    make_uint4(pack_bf16(__uint_as_float(x[0]), __uint_as_float(x[1])),
+                                               pack_bf16(__uint_as_float(x[2]), __uint_as_float(x[3])),
+                                               pack_bf16(__uint_as_float(x[4]), __uint_as_float(x[5])),
+                                               pack_bf16(__uint_as_float(x[6]), __uint_as_float(x[7])));
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 32; i += 4)
+                                if (d0 + i < Dv)
+                                    *reinterpret_cast<uint4*>(part + d0 + i) =
+                                        make_uint4(o[c][i], o[c][i + 1], o[c][i + 2], o[c][i + 3]);
                         }
-                    } else {
-                        float4* d4 = reinterpret_cast<float4*>(part + c * 32);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            if (c * 32 + i * 4 < Dv)
-                                d4[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
-                                                    __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+                    }
+                }
+                if (add && live) {
+#pragma unroll 1
+                    for (int d = 0; d < Dv; ++d) {
+                        const float x = not_finite(a, it.b, it.hk, it.n, add0, add1, d);
+                        if (x == 0.f) continue;
+                        if (it.part < 0)
+                            dst[d] = __float2bfloat16(__bfloat162float(dst[d]) + x);
+                        else
+                            part[d] += x;
                     }
                 }
             }
@@ -937,36 +972,37 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const PagedAtte
     constexpr int ROWS = kMergeWarps / WPR;
     __shared__ float red[2][kMergeWarps];
     __shared__ __align__(16) float sums[WPR == 1 ? 1 : kMergeWarps][WPR == 1 ? 4 : 256];
-    grid_wait();
-    grid_go();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % WPR;
-    if (blockIdx.x == 0 && threadIdx.x == 0) *a.counter = 0;
     const int64_t r = (int64_t)blockIdx.x * ROWS + warp / WPR;
-    if (r >= (int64_t)a.g.T * a.g.H) return;            // the same for the warps of a row
-    const int32_t tok = (int32_t)(r / a.g.H), h = (int32_t)(r - (int64_t)tok * a.g.H);
-    int32_t b, q0;
+    // the row's sequence: offsets are older than the kernel before this one
+    bool there = r < (int64_t)a.g.T * a.g.H;              // the same for the warps of a row
+    const int32_t tok = there ? (int32_t)(r / a.g.H) : 0, h = (int32_t)(r - (int64_t)tok * a.g.H);
+    int32_t b = 0, q0 = 0, nq = a.each;
     if (a.cu) {
         // the last sequence that begins at or before the token, 32 at a time
-        int32_t lo = 0, hi = a.B;
-        while (hi - lo > 1) {
-            const int32_t step = (hi - lo + 31) / 32, at = lo + lane * step;
+        int32_t hi = a.B;
+        while (hi - b > 1) {
+            const int32_t step = (hi - b + 31) / 32, at = b + lane * step;
             const bool before = at < hi && a.cu[at] <= tok;
             const int32_t f = 31 - __clz(__ballot_sync(0xffffffffu, before) | 1u);
-            lo += f * step;
-            hi = min(hi, lo + step);
+            b += f * step;
+            hi = min(hi, b + step);
         }
-        b = lo;
         q0 = a.cu[b];
-        if (q0 < 0 || tok < q0 || tok >= a.cu[b + 1]) return;
+        nq = min(a.cu[b + 1], a.g.T) - q0;
+        there = there && q0 >= 0 && tok >= q0 && tok - q0 < nq;
     } else {
-        b = tok / a.each;
+        b = min(tok / a.each, a.B - 1);
         q0 = b * a.each;
     }
+    grid_wait();
+    grid_go();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.counter = 0;
+    if (!there) return;
     const int2 cut = a.cuts[b];
     if (cut.y <= 1) return;
-    const int32_t nq = a.cu ? min(a.cu[b + 1], a.g.T) - q0 : a.each;
-    const int32_t row_tiles = row_tiles_of(t, nq), G = a.g.H / a.c.Hkv, hk = h / G, g = h - hk * G;
-    const int32_t hb = g / t.heads, i = tok - q0, rt = i / t.tok, row = (i - rt * t.tok) * t.heads + (g - hb * t.heads);
+    const int32_t row_tiles = row_tiles_of(t, nq), hk = h / t.group, g = h - hk * t.group;
+    const int32_t hb = g / t.heads, i = tok - q0, rt = (int32_t)t.by_tok.div((uint32_t)i), row = (i - rt * t.tok) * t.heads + (g - hb * t.heads);
     // part p of this row is partial first + p * row_tiles
     const int64_t first = cut.x + ((int64_t)(hk * t.blocks + hb) * cut.y) * row_tiles + (row_tiles - 1 - rt);
     if (first + (int64_t)(cut.y - 1) * row_tiles >= a.max_parts || row >= t.part_rows) {
@@ -995,7 +1031,6 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const PagedAtte
     for (int32_t p = sub; p < cut.y; p += WPR) {
         const float w = ex2(base[p * step + at_lse] - from);
         l += w;
-        if (w == 0.f) continue;                          // a part that sees nothing has no O either
 #pragma unroll
         for (int x = 0; x < 2; ++x)
             if (4 * lane + 128 * x < D) {
@@ -1061,9 +1096,10 @@ cudaError_t launch_d(const PagedAttendArgs& a, cudaStream_t s) {
 }  // namespace
 
 size_t paged_parts_bytes(const PagedGeom& c, const Geom& g, int32_t* max_parts) {
-    // a unit of n tiles that is cut has at most 2 n / C parts, so all have at most twice the target
+    // a unit of n tiles that is cut has at most 2 n / C parts, and C is at least the work of an SM / kItemsPerSm,
+    // up to a rounding of fp32
     const Tiling t = tiling(c, g);
-    *max_parts = (int32_t)(2 * t.target);
+    *max_parts = (2 * kItemsPerSm + 1) * t.sms;
     return (size_t)*max_parts * t.part_floats * sizeof(float);
 }
 
