@@ -135,7 +135,8 @@ __device__ __forceinline__ int32_t parts_of(int32_t tiles, int32_t C) { return t
 
 // The list as the lanes of a warp hold it: each a run of `per` sequences.
 struct List {
-    int32_t items, parts;      // items and partials of the runs before
+    int32_t first, items;      // the run's first item, and how many it has
+    int32_t parts;             // partials of the runs before
     Seq seq;                   // the run's sequence, where it is one
     int32_t per;
     int32_t C;                 // most key tiles of an item
@@ -205,27 +206,34 @@ __device__ __forceinline__ List make_list(const PagedAttendArgs& a, const Tiling
     L.C = (int32_t)fminf(C, 1073741824.f);
     int32_t items = 0, parts = 0;
     float about = 0.f;                                   // their sum, where it does not fit an integer
+    bool chunk = false;                                  // several row tiles: its items go first
     for (int32_t b = b0; b < b1; ++b) {
         if (L.per > 1) L.seq = seq_of(a, b);
         const int32_t p = parts_of(tiles_of<BN>(L.seq), L.C), n = units_of(t, L.seq);
         items += n * p;
         if (p > 1) parts += n * p;
         about += (float)n * (float)p;
+        chunk = chunk || L.seq.nq > t.tok;
     }
-    int32_t items_to = items, parts_to = parts;
+    int32_t items_to = items, parts_to = parts, chunk_to = chunk ? items : 0;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
         const int32_t x = __shfl_up_sync(0xffffffffu, items_to, m), y = __shfl_up_sync(0xffffffffu, parts_to, m);
+        const int32_t z = __shfl_up_sync(0xffffffffu, chunk_to, m);
         if (lane >= m) {
             items_to += x;
             parts_to += y;
+            chunk_to += z;
         }
     }
+    const int32_t items_all = __shfl_sync(0xffffffffu, items_to, 31), parts_all = __shfl_sync(0xffffffffu, parts_to, 31);
+    const int32_t chunk_all = __shfl_sync(0xffffffffu, chunk_to, 31);
     // offsets that descend can give more items than there are tokens for: nothing is done then
-    const bool fits = warp_sum(about) < 1073741824.f && __shfl_sync(0xffffffffu, parts_to, 31) <= a.max_parts;
+    const bool fits = warp_sum(about) < 1073741824.f && parts_all <= a.max_parts;
     if (!fits) set_error(a.status, ATTN_E_BOUNDS);
-    L.n_items = fits ? __shfl_sync(0xffffffffu, items_to, 31) : 0;
-    L.items = fits ? items_to - items : 0;
+    L.n_items = fits ? items_all : 0;
+    L.first = (chunk ? chunk_to : chunk_all + items_to - chunk_to) - items;
+    L.items = items;
     L.parts = fits ? parts_to - parts : 0;
     if (tell) {
         int32_t before = parts_to - parts;
@@ -257,8 +265,10 @@ static_assert(sizeof(Item) == 48, "Item layout");
 template <int BN>
 __device__ __forceinline__ bool find_item(const PagedAttendArgs& a, const Tiling& t, const List& L, int32_t w, Item& it) {
     const int lane = threadIdx.x & 31;
-    const int32_t r = __popc(__ballot_sync(0xffffffffu, L.items <= w)) - 1;
-    int32_t x = w - __shfl_sync(0xffffffffu, L.items, r), part0 = __shfl_sync(0xffffffffu, L.parts, r);
+    const uint32_t here = __ballot_sync(0xffffffffu, w >= L.first && w - L.first < L.items);
+    if (!here) return false;
+    const int32_t r = __ffs(here) - 1;
+    int32_t x = w - __shfl_sync(0xffffffffu, L.first, r), part0 = __shfl_sync(0xffffffffu, L.parts, r);
     int32_t b = r * L.per;
     Seq s{__shfl_sync(0xffffffffu, L.seq.q0, r), __shfl_sync(0xffffffffu, L.seq.nq, r), __shfl_sync(0xffffffffu, L.seq.n, r)};
     if (L.per > 1) {
