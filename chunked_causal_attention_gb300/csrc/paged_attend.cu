@@ -46,6 +46,7 @@ constexpr int kThreads = 256;
 constexpr int kItemsPerSm = 6;                 // the smallest items are a sixth of an SM's work
 constexpr float kItemTiles = 3.f;              // what an item takes beside its key tiles, in those
 constexpr int kGatherPage = 32;
+constexpr int kLookAhead = 4;                  // tiles left to load when the next item is looked up
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0;
 constexpr uint32_t kColO = 256;
@@ -507,19 +508,32 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) {
         // ------------------------------------------------------------ items and loads
         const List L = make_list<BN>(a, t, blockIdx.x == 0);
-        uint32_t kc = 0, ne = 0;
-        int32_t w = a.stall ? L.n_items : (int32_t)blockIdx.x;
-        bool ok = !a.stall;
-        for (uint32_t ic = 0; ok; ++ic) {
-            Item it{};
+        // item w of the list and its first table entries
+        auto look_up = [&](int32_t w, Item& it, int32_t& entries) {
             it.tiles = -1;
-            if (w < L.n_items && !find_item<BN>(a, t, L, w, it)) {
+            entries = kNone;
+            if (w >= L.n_items) return;
+            if (find_item<BN>(a, t, L, w, it)) {
+                entries = pages_at(it, 0);
+            } else {
+                it.tiles = -1;
                 if (lane == 0) {
                     set_error(a.status, ATTN_E_BOUNDS);
                     *abort_flag = 1;
                 }
-                it.tiles = -1;
             }
+        };
+        auto claim = [&]() {
+            int32_t w = 0;
+            if (lane == 0) w = (int32_t)min(atomicAdd(a.counter, 1u) + gridDim.x, (uint32_t)INT32_MAX);
+            return __shfl_sync(0xffffffffu, w, 0);
+        };
+        uint32_t kc = 0, ne = 0;
+        Item it{}, next{};
+        int32_t ahead = kNone, ahead_next = kNone;
+        bool ok = !a.stall;
+        if (ok) look_up((int32_t)blockIdx.x, it, ahead);
+        for (uint32_t ic = 0; ok; ++ic) {
             ok = mbar_wait_warp(bar(LY::B_REMPTY + (ic & 1)), ((ic >> 1) & 1) ^ 1, abort_flag, a.status, a.wait_ns);
             if (!ok) break;
             if (lane == 0) {
@@ -532,7 +546,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (it.tiles < 0 || __any_sync(0xffffffffu, *abort_flag)) break;
             if (it.tiles > 0) {
-                int32_t ahead = pages_at(it, 0), now = 0;
                 ok = mbar_wait_warp(bar(LY::B_QEMPTY), (ne & 1) ^ 1, abort_flag, a.status, a.wait_ns);
                 if (!ok) break;
                 const bool few = it.box == t.few && t.few < t.tok;
@@ -549,6 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // one lane a box: 64 dims of the slots of a page (or of a tile, if pages are longer)
                 const int bi = lane / CH, bc = lane - bi * CH;
                 const bool loads = lane < boxes * CH;
+                int32_t now = 0;
                 for (int32_t j = 0; j < it.tiles && ok; ++j) {
                     const int32_t in = j % window;
                     if (in == 0) {
@@ -575,11 +589,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (loads) tma_load_4d(sbase + LY::V_OFF + off, &tmv, bar(LY::B_VFULL + s), bc * 64, c1, c2, c3);
                     }
                     ++kc;
+                    // the next item is looked up a few tiles before this one's last: that takes as long as they do
+                    if (j == max(0, it.tiles - kLookAhead)) look_up(claim(), next, ahead_next);
                 }
+                if (!ok) break;
+            } else {
+                look_up(claim(), next, ahead_next);
             }
-            // the item's last loads are out: claim the next one
-            if (lane == 0) w = (int32_t)min(atomicAdd(a.counter, 1u) + gridDim.x, (uint32_t)INT32_MAX);
-            w = __shfl_sync(0xffffffffu, w, 0);
+            it = next;
+            ahead = ahead_next;
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
@@ -975,28 +993,28 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 constexpr int kMergeWarps = 8;
 
-// WPR warps a row of the output: one where rows are many, the whole block where they are few.
+// LPR lanes a row of the output: a quarter of a warp where rows are many, the whole block where they are few (2048
+// tokens of 32 heads in two parts 752 us with a quarter, 763 with a warp; 40 rows of 32 heads in four parts 18.3 and 16.1).
 // Row r is head r % H of token r / H. Also leaves the work queue at zero for the next call.
-template <int WPR>
+template <int LPR>
 __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const PagedAttendArgs a, const Tiling t) {
-    constexpr int ROWS = kMergeWarps / WPR;
+    constexpr int ROWS = 32 * kMergeWarps / LPR;
+    constexpr bool BLOCK = ROWS == 1;                    // the block's warps take parts in turn
+    constexpr int LANES = BLOCK ? 32 : LPR;              // over a row's dims
+    constexpr int VECS = 256 / 4 / LANES;                // float4 of a row that a lane holds
     __shared__ float red[2][kMergeWarps];
-    __shared__ __align__(16) float sums[WPR == 1 ? 1 : kMergeWarps][WPR == 1 ? 4 : 256];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % WPR;
-    const int64_t r = (int64_t)blockIdx.x * ROWS + warp / WPR;
+    __shared__ __align__(16) float sums[BLOCK ? kMergeWarps : 1][BLOCK ? 256 : 4];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x % LANES, sub = BLOCK ? warp : 0, subs = BLOCK ? kMergeWarps : 1;
+    const uint32_t group = LANES == 32 ? 0xffffffffu : ((1u << (LANES % 32)) - 1) << (threadIdx.x & 31 & ~(LANES - 1));
+    const int64_t r = (int64_t)blockIdx.x * ROWS + threadIdx.x / LPR;
     // the row's sequence: offsets are older than the kernel before this one
-    bool there = r < (int64_t)a.g.T * a.g.H;              // the same for the warps of a row
-    const int32_t tok = there ? (int32_t)(r / a.g.H) : 0, h = (int32_t)(r - (int64_t)tok * a.g.H);
+    bool there = r < (int64_t)a.g.T * a.g.H;             // the same for the lanes of a row
+    const int32_t tok = there ? (int32_t)((uint32_t)r / (uint32_t)a.g.H) : 0, h = (int32_t)(r - (int64_t)tok * a.g.H);
     int32_t b = 0, q0 = 0, nq = a.each;
     if (a.cu) {
-        // the last sequence that begins at or before the token, 32 at a time
-        int32_t hi = a.B;
-        while (hi - b > 1) {
-            const int32_t step = (hi - b + 31) / 32, at = b + lane * step;
-            const bool before = at < hi && a.cu[at] <= tok;
-            const int32_t f = 31 - __clz(__ballot_sync(0xffffffffu, before) | 1u);
-            b += f * step;
-            hi = min(hi, b + step);
+        for (int32_t hi = a.B; hi - b > 1;) {            // the last sequence that begins at or before the token
+            const int32_t mid = (b + hi) >> 1;
+            if (a.cu[mid] <= tok) b = mid; else hi = mid;
         }
         q0 = a.cu[b];
         nq = min(a.cu[b + 1], a.g.T) - q0;
@@ -1012,7 +1030,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const PagedAtte
     const int2 cut = a.cuts[b];
     if (cut.y <= 1) return;
     const int32_t row_tiles = row_tiles_of(t, nq), hk = h / t.group, g = h - hk * t.group;
-    const int32_t hb = g / t.heads, i = tok - q0, rt = (int32_t)t.by_tok.div((uint32_t)i), row = (i - rt * t.tok) * t.heads + (g - hb * t.heads);
+    const int32_t hb = g / t.heads, i = tok - q0, rt = (int32_t)t.by_tok.div((uint32_t)i);
+    const int32_t row = (i - rt * t.tok) * t.heads + (g - hb * t.heads);
     // part p of this row is partial first + p * row_tiles
     const int64_t first = cut.x + ((int64_t)(hk * t.blocks + hb) * cut.y) * row_tiles + (row_tiles - 1 - rt);
     if (first + (int64_t)(cut.y - 1) * row_tiles >= a.max_parts || row >= t.part_rows) {
@@ -1022,46 +1041,48 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const PagedAtte
     const float* base = a.parts + first * t.part_floats;
     const int64_t step = (int64_t)row_tiles * t.part_floats;
     const int32_t D = a.g.D;
-    const int64_t at_lse = (int64_t)t.part_rows * D + row;
+    const float* lses = base + (int64_t)t.part_rows * D + row;
     float m = -INFINITY;
-    for (int32_t p = sub * 32 + lane; p < cut.y; p += 32 * WPR) m = fmaxf(m, base[p * step + at_lse]);
+    for (int32_t p = sub * LANES + lane; p < cut.y; p += LANES * subs) m = fmaxf(m, lses[p * step]);
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-    if (WPR > 1) {
+    for (int x = LANES / 2; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(group, m, x));
+    if (BLOCK) {
         if (lane == 0) red[0][warp] = m;
         __syncthreads();
         for (int w = 0; w < kMergeWarps; ++w) m = fmaxf(m, red[0][w]);
     }
     const float from = m == -INFINITY ? 0.f : m;
-    // dims 4 lane .. 4 lane + 3, and 128 on where there are more than 128
-    float4 o[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+    // dims 4 lane .. 4 lane + 3, and 4 LANES on, as far as there are any
+    float4 o[VECS];
+#pragma unroll
+    for (int x = 0; x < VECS; ++x) o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
     float l = 0.f;
     const float* mine = base + (int64_t)row * D + 4 * lane;
-#pragma unroll 4
-    for (int32_t p = sub; p < cut.y; p += WPR) {
-        const float w = ex2(base[p * step + at_lse] - from);
+#pragma unroll 2
+    for (int32_t p = sub; p < cut.y; p += subs) {
+        const float w = ex2(lses[p * step] - from);
         l += w;
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
-            if (4 * lane + 128 * x < D) {
-                const float4 y = *reinterpret_cast<const float4*>(mine + p * step + 128 * x);
+        for (int x = 0; x < VECS; ++x)
+            if (4 * (lane + LANES * x) < D) {
+                const float4 y = *reinterpret_cast<const float4*>(mine + p * step + 4 * LANES * x);
                 o[x].x = fmaf(w, y.x, o[x].x);
                 o[x].y = fmaf(w, y.y, o[x].y);
                 o[x].z = fmaf(w, y.z, o[x].z);
                 o[x].w = fmaf(w, y.w, o[x].w);
             }
     }
-    if (WPR > 1) {
+    if (BLOCK) {
         if (lane == 0) red[1][warp] = l;
 #pragma unroll
-        for (int x = 0; x < 2; ++x) *reinterpret_cast<float4*>(&sums[warp][4 * lane + 128 * x]) = o[x];
+        for (int x = 0; x < VECS; ++x) *reinterpret_cast<float4*>(&sums[warp][4 * (lane + LANES * x)]) = o[x];
         __syncthreads();
         if (warp != 0) return;
         for (int w = 1; w < kMergeWarps; ++w) {
             l += red[1][w];
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const float4 y = *reinterpret_cast<const float4*>(&sums[w][4 * lane + 128 * x]);
+            for (int x = 0; x < VECS; ++x) {
+                const float4 y = *reinterpret_cast<const float4*>(&sums[w][4 * (lane + LANES * x)]);
                 o[x].x += y.x;
                 o[x].y += y.y;
                 o[x].z += y.z;
@@ -1072,9 +1093,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const PagedAtte
     const float inv = l == 0.f ? 0.f : 1.f / l;
     __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(a.o) + (int64_t)tok * a.g.st + (int64_t)h * a.g.sh + 4 * lane;
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
-        if (4 * lane + 128 * x < D)
-            *reinterpret_cast<uint2*>(dst + 128 * x) =
+    for (int x = 0; x < VECS; ++x)
+        if (4 * (lane + LANES * x) < D)
+            *reinterpret_cast<uint2*>(dst + 4 * LANES * x) =
                 make_uint2(pack_bf16(o[x].x * inv, o[x].y * inv), pack_bf16(o[x].z * inv, o[x].w * inv));
     if (lane == 0) a.lse[(int64_t)h * a.g.T + tok] = l == 0.f ? -INFINITY : (m + lg2(l)) * kLn2;
 }
@@ -1097,10 +1118,13 @@ cudaError_t launch_d(const PagedAttendArgs& a, cudaStream_t s) {
                      mpq, mpkv, t);
     if (e != cudaSuccess) return e;
     const int64_t rows = (int64_t)a.g.T * a.g.H;
-    if (rows <= 8 * device_sm_count())
-        return launch_early(merge_kernel<kMergeWarps>, dim3((unsigned)rows), 32 * kMergeWarps, 0, 1, s, a, t);
-    return launch_early(merge_kernel<1>, dim3((unsigned)((rows + kMergeWarps - 1) / kMergeWarps)), 32 * kMergeWarps, 0, 1,
-                        s, a, t);
+    constexpr int kBlock = 32 * kMergeWarps;
+    auto merge = [&](auto kernel, int lanes) {
+        const int64_t per = kBlock / lanes;
+        return launch_early(kernel, dim3((unsigned)((rows + per - 1) / per)), kBlock, 0, 1, s, a, t);
+    };
+    if (rows <= 8 * t.sms) return merge(merge_kernel<kBlock>, kBlock);
+    return rows <= 64 * t.sms ? merge(merge_kernel<32>, 32) : merge(merge_kernel<8>, 8);
 }
 
 }  // namespace
