@@ -361,23 +361,28 @@ struct Layout {
     static constexpr size_t ALLOC = (size_t)BYTES + 1024;      // slack for 1024-byte alignment
 };
 
-// Values that are not finite among the eight bf16 of x, replaced by zeros; true if there were any.
-__device__ __forceinline__ bool only_finite(uint4& x) {
-    uint32_t* w = reinterpret_cast<uint32_t*>(&x);
-    bool any = false;
+// Whether any of the eight bf16 of x is not finite: x - x is zero or NaN.
+__device__ __forceinline__ bool not_finite8(const uint4& x) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    uint32_t any = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t e = w[i] & 0x7f807f80u;
-        if ((e & 0xffffu) == 0x7f80u) {
-            w[i] &= 0xffff0000u;
-            any = true;
-        }
-        if ((e >> 16) == 0x7f80u) {
-            w[i] &= 0x0000ffffu;
-            any = true;
-        }
+        const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162*>(&w[i]);
+        const __nv_bfloat162 d = __hsub2(v, v);
+        any |= *reinterpret_cast<const uint32_t*>(&d);
     }
-    return any;
+    return any != 0;
+}
+
+// Those replaced by zeros.
+__device__ __noinline__ uint4 only_finite(uint4 x) {
+    uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if ((w[i] & 0x7f80u) == 0x7f80u) w[i] &= 0xffff0000u;
+        if ((w[i] & 0x7f800000u) == 0x7f800000u) w[i] &= 0x0000ffffu;
+    }
+    return x;
 }
 
 // 16 bytes of global memory to shared memory, or zeros, asynchronously.
@@ -717,23 +722,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                     copy_arrive(bar(LY::B_VFULL + s));
                 } else {
                     bool any = false;
-#pragma unroll
-                    for (int x = 0; x < BLOCKS; ++x)
 #pragma unroll 1
-                        for (int i = 0; i < STEPS; ++i) {
-                            const uint32_t to = dst + (x * 16 + i * ROWS) * 128 + ((mixed ^ ((i * ROWS) & 7)) << 4);
-                            if (i * ROWS < used[x] && j0 + x * 16 + r_lane + i * ROWS >= it.seen) {
-                                uint4 y = *reinterpret_cast<const uint4*>(src[x] + i * step);
-                                any = only_finite(y) || any;
-                                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(to), "r"(y.x), "r"(y.y),
-                                             "r"(y.z), "r"(y.w)
-                                             : "memory");
-                            } else {
-                                copy16(to, i * ROWS < used[x] ? src[x] + i * step : rows, i * ROWS < used[x]);
+                    for (int x = 0; x < BLOCKS; ++x) {
+                        const int32_t all = it.seen - (j0 + x * 16 + r_lane);      // rows before it are seen by all
+                        const __nv_bfloat16* from = src[0];
+                        int32_t rows_used = used[0];
+#pragma unroll
+                        for (int y = 1; y < BLOCKS; ++y)
+                            if (x == y) {
+                                from = src[y];
+                                rows_used = used[y];
                             }
+                        uint4 v[STEPS];
+#pragma unroll
+                        for (int i = 0; i < STEPS; ++i)
+                            v[i] = i * ROWS < rows_used ? *reinterpret_cast<const uint4*>(from + i * step) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                        for (int i = 0; i < STEPS; ++i) {
+                            if (i * ROWS >= all && not_finite8(v[i])) {
+                                v[i] = only_finite(v[i]);
+                                any = true;
+                            }
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(
+                                             dst + (x * 16 + i * ROWS) * 128 + ((mixed ^ ((i * ROWS) & 7)) << 4)),
+                                         "r"(v[i].x), "r"(v[i].y), "r"(v[i].z), "r"(v[i].w)
+                                         : "memory");
                         }
+                    }
                     if (any) to_add[ne & 3] = ne + 1;
-                    copy_wait_all();                     // plain stores are among them, which copy_arrive does not follow
                     mbar_arrive(bar(LY::B_VFULL + s));
                 }
                 ++kc;
@@ -758,21 +774,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int r0 = max(0, it.seen - j0), rn = min(max(it.n - j0, 0), BN);   // rows [rn, BN) hold no slot in use
                     uint8_t* v = sm + LY::V_OFF + vs * LY::TILE_KV;
                     bool any = false;
-                    // 16-byte pieces of 64 dims of a row: eight lanes a row
-                    for (int x = (warp - 2) * 32 + lane; x < (BN - r0) * 8; x += 64) {
-                        const int r = r0 + (x >> 3);
+                    // 16-byte pieces of 64 dims of a row: eight lanes a row, four rows a warp, eight steps in flight
+                    constexpr int AT_ONCE = 8 / CH;
+#pragma unroll 1
+                    for (int y = r0 + (warp - 2) * 4 + (lane >> 3); y < BN; y += 8 * AT_ONCE) {
+                        uint4 x[AT_ONCE][CH];
 #pragma unroll
-                        for (int c = 0; c < CH; ++c) {
-                            uint4* p = reinterpret_cast<uint4*>(v + c * (BN * 128) + r * 128 + (x & 7) * 16);
-                            uint4 y = make_uint4(0, 0, 0, 0);
-                            bool put = r >= rn;
-                            if (!put) {
-                                y = *p;
-                                put = only_finite(y);
-                                any = any || put;
+                        for (int i = 0; i < AT_ONCE; ++i)
+#pragma unroll
+                            for (int c = 0; c < CH; ++c)
+                                if (y + 8 * i < rn)
+                                    x[i][c] = *reinterpret_cast<const uint4*>(v + c * (BN * 128) + (y + 8 * i) * 128 + (lane & 7) * 16);
+#pragma unroll
+                        for (int i = 0; i < AT_ONCE; ++i)
+#pragma unroll
+                            for (int c = 0; c < CH; ++c) {
+                                uint4* p = reinterpret_cast<uint4*>(v + c * (BN * 128) + (y + 8 * i) * 128 + (lane & 7) * 16);
+                                if (y + 8 * i < rn) {
+                                    if (not_finite8(x[i][c])) {
+                                        *p = only_finite(x[i][c]);
+                                        any = true;
+                                    }
+                                } else if (y + 8 * i < BN) {
+                                    *p = make_uint4(0, 0, 0, 0);
+                                }
                             }
-                            if (put) *p = y;
-                        }
                     }
                     if (any) to_add[ne & 3] = ne + 1;
                     fence_proxy_async_smem();
@@ -943,10 +969,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                         } else {
 #pragma unroll
-                            for (int i = 0; i < 32; i += 4)
+                            for (int i = 0; i < 32; i += 8)
                                 if (d0 + i < Dv)
-                                    *reinterpret_cast<uint4*>(part + d0 + i) =
-                                        make_uint4(o[c][i], o[c][i + 1], o[c][i + 2], o[c][i + 3]);
+                                    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(
+                                                     part + d0 + i),
+                                                 "r"(o[c][i]), "r"(o[c][i + 1]), "r"(o[c][i + 2]), "r"(o[c][i + 3]),
+                                                 "r"(o[c][i + 4]), "r"(o[c][i + 5]), "r"(o[c][i + 6]), "r"(o[c][i + 7])
+                                                 : "memory");
                         }
                     }
                 }
