@@ -43,8 +43,9 @@ using kv4::grid_wait;
 using kv4::launch_early;
 
 constexpr int kThreads = 256;
-constexpr int kItemsPerSm = 6;                 // the smallest items are a sixth of an SM's work
+constexpr int kItemsPerSm = 8;                 // the smallest items are an eighth of an SM's work
 constexpr float kItemTiles = 3.f;              // what an item takes beside its key tiles, in those
+constexpr float kRowTiles = 1.f / 16;          // what a row of a partial takes to write and read again
 constexpr int kGatherPage = 32;
 constexpr int kLookAhead = 4;                  // tiles left to load when the next item is looked up
 constexpr uint32_t kTmemCols = 512;
@@ -64,7 +65,6 @@ struct Tiling {
     int32_t part_rows;         // rows of a partial
     int64_t part_floats;       // floats of a partial: rows of D, then their LSEs (base 2)
     int32_t sms;
-    float part_tiles;          // what a partial takes to write and read again, in key tiles
 };
 
 __host__ __device__ constexpr int block_n(int d) { return d > 128 ? 64 : 128; }     // slots of a key tile
@@ -85,7 +85,6 @@ Tiling tiling(const PagedGeom& c, const Geom& g) {
     t.part_rows = (int32_t)std::min<int64_t>(t.tok, g.T) * t.heads;
     t.part_floats = ((int64_t)t.part_rows * (g.D + 1) + 31) / 32 * 32;
     t.sms = device_sm_count();
-    t.part_tiles = 4.f * t.part_rows / kTile;
     return t;
 }
 
@@ -152,7 +151,7 @@ __device__ __forceinline__ float warp_sum(float x) {
 
 // Sizes of an item that are weighed against each other, in shares of an SM's work.
 constexpr int kTry = 8;
-__constant__ const float kShares[kTry] = {1.f / kItemsPerSm, 0.25f, 1.f / 3, 0.5f, 1.f, 1.25f, 1.5f, 2.f};
+__constant__ const float kShares[kTry] = {1.f / kItemsPerSm, 0.2f, 1.f / 3, 0.5f, 1.f, 1.25f, 1.5f, 2.f};
 
 // By one warp. `tell`: write a.cuts for the merge kernel.
 template <int BN>
@@ -174,28 +173,30 @@ __device__ __forceinline__ List make_list(const PagedAttendArgs& a, const Tiling
     // hands items out, whichever is less. A lane takes one size and a quarter of the sequences.
     const float sms = (float)t.sms;
     const float size = fmaxf(1.f, ceilf(__fdividef(W, sms) * kShares[lane & (kTry - 1)]));
-    float n_items = 0.f, n_parts = 0.f, most = 0.f;
+    float n_items = 0.f, extra = 0.f, most = 0.f;
     for (int32_t base = 0; base < a.B; base += 32) {
         const Seq s = L.per == 1 ? L.seq : base + lane < a.B ? seq_of(a, base + lane) : Seq{0, 0, 0};
         const float units = (float)units_of(t, s), tiles = (float)tiles_of<BN>(s);
+        const float rows = (float)(min(s.nq, t.tok) * t.heads) * kRowTiles;
 #pragma unroll 1
         for (int i = 0; i < min(32, a.B - base); i += 32 / kTry) {
             const float u = __shfl_sync(0xffffffffu, units, i + lane / kTry), n = __shfl_sync(0xffffffffu, tiles, i + lane / kTry);
             const float p = ceilf(__fdividef(n, size));
             n_items += u * p;
-            if (p > 1.f) n_parts += u * p;
+            const float each = __shfl_sync(0xffffffffu, rows, i + lane / kTry);
+            if (p > 1.f) extra += u * p * each;
             if (u > 0.f) most = fmaxf(most, ceilf(__fdividef(n, p)));
         }
     }
 #pragma unroll
     for (int m = kTry; m < 32; m <<= 1) {
         n_items += __shfl_xor_sync(0xffffffffu, n_items, m);
-        n_parts += __shfl_xor_sync(0xffffffffu, n_parts, m);
+        extra += __shfl_xor_sync(0xffffffffu, extra, m);
         most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, m));
     }
     const float rounds = ceilf(__fdividef(n_items, sms)) * (most + kItemTiles);
     const float queue = __fdividef(W + n_items * kItemTiles, sms) + most;
-    float time = fminf(rounds, queue) + __fdividef(n_parts, sms) * t.part_tiles, C = size;
+    float time = fminf(rounds, queue) + __fdividef(extra, sms), C = size;
 #pragma unroll
     for (int m = 1; m < kTry; m <<= 1) {
         const float time2 = __shfl_xor_sync(0xffffffffu, time, m), C2 = __shfl_xor_sync(0xffffffffu, C, m);

@@ -32,12 +32,24 @@ class _Calls:
         self.device = device
         self.gpu = (device.index or 0) if device.type == "cuda" else -2      # no tensor's get_device()
         self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        self.current = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
     def stream(self, stream, t):
         """The given stream, or the current one of the device."""
         if stream is None and self.raw_stream is not None:
             return self.raw_stream(self.gpu)
         return _lib._stream_of(stream, t)
+
+    def run(self, name: str, t, *args) -> None:
+        """The library's entry point of that name, on the device (t's)."""
+        fn = getattr(_lib._lib or _lib.lib(), name)
+        if self.current() == self.gpu:
+            st = fn(*args)
+        else:
+            with _lib._on(t):
+                st = fn(*args)
+        if st:
+            raise AttnError(name, st)
 
     def ints(self, t, numel: int) -> bool:
         """A contiguous int32 tensor of numel elements on the device."""
@@ -148,24 +160,23 @@ def paged_reserve(tables: PagedTables, add, T: int, lens_out=None, n_free_out=No
     that found no pages (attn_status tells: ATTN_E_CAPACITY)."""
     fn = "paged_reserve"
     c, B, table = tables._calls, tables.B, tables.table
-    with _lib._alloc_on(stream, c.device):
-        if ws is None:
-            ws = paged_workspace(tables=tables)
-        if cu_seqlens is None:
-            cu_seqlens = c.empty(B + 1, dtype=c.int32, device=c.device)
-        if slots is None:
-            slots = c.empty(T, dtype=c.int32, device=c.device)
+    if ws is None or cu_seqlens is None or slots is None:
+        with _lib._alloc_on(stream, c.device):
+            if ws is None:
+                ws = paged_workspace(tables=tables)
+            if cu_seqlens is None:
+                cu_seqlens = c.empty(B + 1, dtype=c.int32, device=c.device)
+            if slots is None:
+                slots = c.empty(T, dtype=c.int32, device=c.device)
     lens_out = tables.lens if lens_out is None else lens_out
     n_free_out = tables.n_free if n_free_out is None else n_free_out
     if not (c.ints(add, B) and c.ints(lens_out, B) and c.ints(n_free_out, 1) and c.ints(cu_seqlens, B + 1)
             and c.ints(slots, T) and ws.get_device() == c.gpu):
         raise AttnError(fn, ATTN_E_INVAL)
-    with _lib._on(table):
-        _lib._check("attn_paged_reserve", _lib.lib().attn_paged_reserve(
-            add.data_ptr(), tables.lens.data_ptr(), B, tables.page, tables.free.numel(), tables.n_free.data_ptr(),
-            tables.free.data_ptr(), table.data_ptr(), tables.ld, tables.max_pages, lens_out.data_ptr(),
-            n_free_out.data_ptr(), cu_seqlens.data_ptr(), slots.data_ptr(), T, ws.data_ptr(),
-            ws.numel() * ws.element_size(), c.stream(stream, table)))
+    c.run("attn_paged_reserve", table, add.data_ptr(), tables.lens.data_ptr(), B, tables.page, tables.free.numel(),
+          tables.n_free.data_ptr(), tables.free.data_ptr(), table.data_ptr(), tables.ld, tables.max_pages,
+          lens_out.data_ptr(), n_free_out.data_ptr(), cu_seqlens.data_ptr(), slots.data_ptr(), T, ws.data_ptr(),
+          ws.nbytes, c.stream(stream, table))
     return cu_seqlens, slots
 
 
@@ -182,10 +193,8 @@ def paged_store(cache: PagedCache, k, v, slots, ws=None, stream=None) -> None:
             and v.get_device() == c.gpu and ws.get_device() == c.gpu and k.shape == v.shape
             and (k.stride() == v.stride() or _lib._same_rows(k, v))):
         raise AttnError(fn, ATTN_E_INVAL)
-    with _lib._on(k):
-        _lib._check("attn_paged_store", _lib.lib().attn_paged_store(
-            k.data_ptr(), v.data_ptr(), ref, cache._ref, slots.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(),
-            c.stream(stream, k)))
+    c.run("attn_paged_store", k, k.data_ptr(), v.data_ptr(), ref, cache._ref, slots.data_ptr(), ws.data_ptr(), ws.nbytes,
+          c.stream(stream, k))
 
 
 def paged_attention(q, cache: PagedCache, table, lens, cu_seqlens=None, scale: Optional[float] = None, o=None, lse=None,
@@ -218,9 +227,7 @@ def paged_attention(q, cache: PagedCache, table, lens, cu_seqlens=None, scale: O
                 c.empty_strided(q.shape, q.stride(), dtype=c.bf16, device=c.device)
         if lse is None:
             lse = c.empty((1, H, T), dtype=c.fp32, device=c.device)
-    with _lib._on(q):
-        _lib._check("attn_paged_attend", _lib.lib().attn_paged_attend(
-            q.data_ptr(), ref, cache._ref, table.data_ptr(), table.stride(0) if B > 1 else most, most, lens.data_ptr(),
-            None if cu_seqlens is None else cu_seqlens.data_ptr(), B,
-            o.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), c.stream(stream, q)))
+    c.run("attn_paged_attend", q, q.data_ptr(), ref, cache._ref, table.data_ptr(), table.stride(0) if B > 1 else most, most,
+          lens.data_ptr(), None if cu_seqlens is None else cu_seqlens.data_ptr(), B, o.data_ptr(), lse.data_ptr(),
+          ws.data_ptr(), ws.nbytes, c.stream(stream, q))
     return o, lse
