@@ -206,35 +206,35 @@ __device__ __forceinline__ List make_list(const PagedAttendArgs& a, const Tiling
         }
     }
     L.C = (int32_t)fminf(C, 1073741824.f);
-    int32_t items = 0, parts = 0;
+    int32_t items = 0, parts = 0, longest = 0;
     float about = 0.f;                                   // their sum, where it does not fit an integer
-    bool chunk = false;                                  // several row tiles: its items go first
     for (int32_t b = b0; b < b1; ++b) {
         if (L.per > 1) L.seq = seq_of(a, b);
-        const int32_t p = parts_of(tiles_of<BN>(L.seq), L.C), n = units_of(t, L.seq);
+        const int32_t tiles = tiles_of<BN>(L.seq), p = parts_of(tiles, L.C), n = units_of(t, L.seq);
         items += n * p;
         if (p > 1) parts += n * p;
         about += (float)n * (float)p;
-        chunk = chunk || L.seq.nq > t.tok;
+        longest = max(longest, (tiles - 1) / p + 1);
     }
-    int32_t items_to = items, parts_to = parts, chunk_to = chunk ? items : 0;
+    int32_t parts_to = parts;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
-        const int32_t x = __shfl_up_sync(0xffffffffu, items_to, m), y = __shfl_up_sync(0xffffffffu, parts_to, m);
-        const int32_t z = __shfl_up_sync(0xffffffffu, chunk_to, m);
-        if (lane >= m) {
-            items_to += x;
-            parts_to += y;
-            chunk_to += z;
-        }
+        const int32_t y = __shfl_up_sync(0xffffffffu, parts_to, m);
+        if (lane >= m) parts_to += y;
     }
-    const int32_t items_all = __shfl_sync(0xffffffffu, items_to, 31), parts_all = __shfl_sync(0xffffffffu, parts_to, 31);
-    const int32_t chunk_all = __shfl_sync(0xffffffffu, chunk_to, 31);
+    // the runs with the longest items go first, so that the last ones to end are short
+    L.first = 0;
+    int32_t items_all = 0;
+    for (int i = 0; i < min(32, a.B); ++i) {
+        const int32_t other = __shfl_sync(0xffffffffu, longest, i), n = __shfl_sync(0xffffffffu, items, i);
+        if (other > longest || (other == longest && i < lane)) L.first += n;
+        items_all += n;
+    }
+    const int32_t parts_all = __shfl_sync(0xffffffffu, parts_to, 31);
     // offsets that descend can give more items than there are tokens for: nothing is done then
     const bool fits = warp_sum(about) < 1073741824.f && parts_all <= a.max_parts;
     if (!fits) set_error(a.status, ATTN_E_BOUNDS);
     L.n_items = fits ? items_all : 0;
-    L.first = (chunk ? chunk_to : chunk_all + items_to - chunk_to) - items;
     L.items = items;
     L.parts = fits ? parts_to - parts : 0;
     if (tell) {
