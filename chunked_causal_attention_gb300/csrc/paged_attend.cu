@@ -1026,14 +1026,15 @@ constexpr int kMergeWarps = 8;
 // LPR lanes a row of the output: a quarter of a warp where rows are many, the whole block where they are few (2048
 // tokens of 32 heads in two parts 752 us with a quarter, 763 with a warp; 40 rows of 32 heads in four parts 18.3 and 16.1).
 // Row r is head r % H of token r / H. Also leaves the work queue at zero for the next call.
-template <int LPR>
+template <int LPR, int DT>
 __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const PagedAttendArgs a, const Tiling t) {
     constexpr int ROWS = 32 * kMergeWarps / LPR;
     constexpr bool BLOCK = ROWS == 1;                    // the block's warps take parts in turn
     constexpr int LANES = BLOCK ? 32 : LPR;              // over a row's dims
-    constexpr int VECS = 256 / 4 / LANES;                // float4 of a row that a lane holds
+    constexpr int VECS = DT / 4 / LANES;                 // float4 of a row that a lane holds
+    constexpr int AT_ONCE = VECS > 4 ? 2 : 4;            // parts whose loads are in flight together
     __shared__ float red[2][kMergeWarps];
-    __shared__ __align__(16) float sums[BLOCK ? kMergeWarps : 1][BLOCK ? 256 : 4];
+    __shared__ __align__(16) float sums[BLOCK ? kMergeWarps : 1][BLOCK ? DT : 4];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x % LANES, sub = BLOCK ? warp : 0, subs = BLOCK ? kMergeWarps : 1;
     const uint32_t group = LANES == 32 ? 0xffffffffu : ((1u << (LANES % 32)) - 1) << (threadIdx.x & 31 & ~(LANES - 1));
     const int64_t r = (int64_t)blockIdx.x * ROWS + threadIdx.x / LPR;
@@ -1072,52 +1073,68 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const PagedAtte
     const int64_t step = (int64_t)row_tiles * t.part_floats;
     const int32_t D = a.g.D;
     const float* lses = base + (int64_t)t.part_rows * D + row;
-    float m = -INFINITY;
-    for (int32_t p = sub * LANES + lane; p < cut.y; p += LANES * subs) m = fmaxf(m, lses[p * step]);
-#pragma unroll
-    for (int x = LANES / 2; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(group, m, x));
-    if (BLOCK) {
-        if (lane == 0) red[0][warp] = m;
-        __syncthreads();
-        for (int w = 0; w < kMergeWarps; ++w) m = fmaxf(m, red[0][w]);
-    }
-    const float from = m == -INFINITY ? 0.f : m;
+    // one pass with a running maximum; a few parts at a time, all of their loads before the first use
+    float m = -INFINITY, l = 0.f;
     // dims 4 lane .. 4 lane + 3, and 4 LANES on, as far as there are any
     float4 o[VECS];
 #pragma unroll
     for (int x = 0; x < VECS; ++x) o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
     const float* mine = base + (int64_t)row * D + 4 * lane;
-#pragma unroll 2
-    for (int32_t p = sub; p < cut.y; p += subs) {
-        const float w = ex2(lses[p * step] - from);
-        l += w;
+    auto add = [](float4& to, float w, const float4& y) {
+        to.x = fmaf(w, y.x, to.x);
+        to.y = fmaf(w, y.y, to.y);
+        to.z = fmaf(w, y.z, to.z);
+        to.w = fmaf(w, y.w, to.w);
+    };
+    auto rescale = [&](float to) {                       // to a maximum of at least m; m is -inf before the first part
+        const float f = m == to ? 1.f : ex2(m - to);
+        l *= f;
 #pragma unroll
-        for (int x = 0; x < VECS; ++x)
-            if (4 * (lane + LANES * x) < D) {
-                const float4 y = *reinterpret_cast<const float4*>(mine + p * step + 4 * LANES * x);
-                o[x].x = fmaf(w, y.x, o[x].x);
-                o[x].y = fmaf(w, y.y, o[x].y);
-                o[x].z = fmaf(w, y.z, o[x].z);
-                o[x].w = fmaf(w, y.w, o[x].w);
-            }
+        for (int x = 0; x < VECS; ++x) o[x] = make_float4(o[x].x * f, o[x].y * f, o[x].z * f, o[x].w * f);
+        m = to;
+    };
+    for (int32_t p0 = sub; p0 < cut.y; p0 += AT_ONCE * subs) {
+        float lse[AT_ONCE];
+        float4 y[AT_ONCE][VECS];
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; ++i) {
+            const int32_t p = p0 + i * subs;
+            lse[i] = p < cut.y ? lses[p * step] : -INFINITY;
+#pragma unroll
+            for (int x = 0; x < VECS; ++x)
+                y[i][x] = p < cut.y && 4 * (lane + LANES * x) < D
+                              ? *reinterpret_cast<const float4*>(mine + p * step + 4 * LANES * x)
+                              : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        float top = m;
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; ++i) top = fmaxf(top, lse[i]);
+        rescale(top);
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; ++i) {
+            const float w = ex2(lse[i] - (m == -INFINITY ? 0.f : m));
+            l += w;
+#pragma unroll
+            for (int x = 0; x < VECS; ++x) add(o[x], w, y[i][x]);
+        }
     }
     if (BLOCK) {
-        if (lane == 0) red[1][warp] = l;
+        if (lane == 0) {
+            red[0][warp] = m;
+            red[1][warp] = l;
+        }
 #pragma unroll
         for (int x = 0; x < VECS; ++x) *reinterpret_cast<float4*>(&sums[warp][4 * (lane + LANES * x)]) = o[x];
         __syncthreads();
         if (warp != 0) return;
+        float top = m;
+        for (int w = 1; w < kMergeWarps; ++w) top = fmaxf(top, red[0][w]);
+        rescale(top);
         for (int w = 1; w < kMergeWarps; ++w) {
-            l += red[1][w];
+            const float f = ex2(red[0][w] - (m == -INFINITY ? 0.f : m));
+            l = fmaf(f, red[1][w], l);
 #pragma unroll
-            for (int x = 0; x < VECS; ++x) {
-                const float4 y = *reinterpret_cast<const float4*>(&sums[w][4 * (lane + LANES * x)]);
-                o[x].x += y.x;
-                o[x].y += y.y;
-                o[x].z += y.z;
-                o[x].w += y.w;
-            }
+            for (int x = 0; x < VECS; ++x) add(o[x], f, *reinterpret_cast<const float4*>(&sums[w][4 * (lane + LANES * x)]));
         }
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -1148,13 +1165,13 @@ cudaError_t launch_d(const PagedAttendArgs& a, cudaStream_t s) {
                      mpq, mpkv, t);
     if (e != cudaSuccess) return e;
     const int64_t rows = (int64_t)a.g.T * a.g.H;
-    constexpr int kBlock = 32 * kMergeWarps;
+    constexpr int kBlock = 32 * kMergeWarps, DT = D < 128 ? 128 : D;
     auto merge = [&](auto kernel, int lanes) {
         const int64_t per = kBlock / lanes;
         return launch_early(kernel, dim3((unsigned)((rows + per - 1) / per)), kBlock, 0, 1, s, a, t);
     };
-    if (rows <= 8 * t.sms) return merge(merge_kernel<kBlock>, kBlock);
-    return rows <= 64 * t.sms ? merge(merge_kernel<32>, 32) : merge(merge_kernel<8>, 8);
+    if (rows <= 8 * t.sms) return merge(merge_kernel<kBlock, DT>, kBlock);
+    return rows <= 64 * t.sms ? merge(merge_kernel<32, DT>, 32) : merge(merge_kernel<8, DT>, 8);
 }
 
 }  // namespace
