@@ -24,6 +24,8 @@ int launched(cudaError_t e) { return e == cudaSuccess ? ATTN_OK : ATTN_E_CUDA; }
 // Most slots of a sequence: a tile more is still an int32.
 constexpr int64_t kMaxSlots = INT32_MAX - 4096;
 
+constexpr int64_t kMaxSeqs = 1 << 20;
+
 // log2 of a page's slots, -1 if they are no power of two from 16 to 1024.
 int page_shift(int64_t page) {
     for (int s = 4; s <= 10; ++s)
@@ -67,7 +69,7 @@ int packed_geom(const attn_shape* shape, const PagedGeom& c, Geom* g) {
 int attend_geom(const attn_shape* shape, const PagedGeom& c, int64_t B, Geom* g) {
     int st = packed_geom(shape, c, g);
     if (st) return st;
-    if (B <= 0 || B > INT32_MAX / 2 || g->H % c.Hkv || !rows_apart(*g)) return ATTN_E_INVAL;
+    if (B <= 0 || B > kMaxSeqs || g->H % c.Hkv || !rows_apart(*g)) return ATTN_E_INVAL;
     g->Hkv = c.Hkv;
     return (int64_t)g->H * g->T <= INT32_MAX && paged_units_fit(c, *g, B) ? ATTN_OK : ATTN_E_INVAL;
 }
@@ -86,7 +88,7 @@ int attn_paged_workspace_size(const attn_paged_cache* cache, const attn_shape* s
                               size_t* bytes) {
     if (!bytes) return ATTN_E_INVAL;
     if (op == ATTN_PAGED_RESERVE) {
-        if (B <= 0 || B > INT32_MAX / 2) return ATTN_E_INVAL;
+        if (B <= 0 || B > kMaxSeqs) return ATTN_E_INVAL;
         *bytes = reserve_bytes(B);
         return ATTN_OK;
     }
@@ -112,7 +114,7 @@ int attn_paged_reserve(const int32_t* add, const int32_t* lens, int64_t B, int64
                        int32_t* slots, int64_t T, void* ws, size_t ws_bytes, void* stream) {
     PagedReserveArgs a;
     a.shift = page_shift(page);
-    if (a.shift < 0 || B <= 0 || B > INT32_MAX / 2 || T <= 0 || T > INT32_MAX / 2) return ATTN_E_INVAL;
+    if (a.shift < 0 || B <= 0 || B > kMaxSeqs || T <= 0 || T > INT32_MAX / 2) return ATTN_E_INVAL;
     if (pages <= 0 || pages > INT32_MAX / page || max_pages <= 0 || max_pages > kMaxSlots / page) return ATTN_E_INVAL;
     if (table_ld < max_pages || table_ld > INT64_MAX / 8 / B) return ATTN_E_INVAL;
     const void* p[] = {add, lens, n_free, free_pages, table, lens_out, n_free_out, cu_seqlens, slots};

@@ -7,10 +7,13 @@
 // by bisection of the offsets and its slot from the table, or from the stack for a new
 // page, whose first token writes it into the table. A decode step's few tokens are
 // taken by the block itself, so that the call is one launch: it is bound by latency
-// (reads of add and lens, three block-wide steps, reads of table or stack).
+// (reads of add and lens, three block-wide steps, reads of table or stack). Measured: one
+// token for each of 64 sequences 3.8 us, 40007 tokens of 512 sequences 8.8 us, 131072
+// tokens of 8 sequences 5.1 us.
 //
 // Store. A copy: a thread moves 16-byte pieces of keys and values, four of each in
-// flight; bound by memory.
+// flight; bound by memory. Measured: 16384 rows of 32 heads of 128 dims 80.7 us (6.65
+// TB/s, 98% of the copy rate), 64 rows of 8 heads 2.6 us.
 #include <algorithm>
 
 #include "kv4_device.cuh"
@@ -27,7 +30,9 @@ using kv4::launch_early;
 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanSeqs = 1024;          // sequences whose records the first kernel keeps in shared memory
-constexpr int kInlineTokens = 4096;      // calls of at most so many tokens are one launch
+// Calls of at most so many tokens are one launch: 64 sequences' 4096 tokens 6.0 us and 5.5 by two, 1024 3.8 and 5.5,
+// 8192 8.8 and 5.7; a second launch is 2 us of the host's time.
+constexpr int kInlineTokens = 4096;
 constexpr int kSlotThreads = 256;
 
 // Slot of packed token t, -1 if it has none. cu: where the sequences begin, ascending.

@@ -442,12 +442,14 @@ typedef struct {
  *     offset, page or slot out of range), ATTN_E_CAPACITY (attn_paged_reserve: a
  *     sequence was refused), ATTN_E_TIMEOUT. Calls that may overlap on the GPU take
  *     different workspaces.
+ *   - B is at most 2^20, a sequence has fewer than 2^31 - 2^12 slots.
  *   - Every call may be captured into a graph, and allocates nothing. */
 
 /* Workspace bytes of one attn_paged_* call: op ATTN_PAGED_STORE (shape may be NULL),
  * ATTN_PAGED_RESERVE (cache and shape may be NULL) or ATTN_PAGED_ATTEND (shape is the
  * queries') for B sequences. A workspace that is large enough for one may serve the
- * others. */
+ * others. Attention keeps at most 17 partials of 128 rows for each SM (171 MB at 128
+ * dims; fewer rows where T tokens of H / Hkv heads are fewer). */
 #define ATTN_PAGED_STORE    0
 #define ATTN_PAGED_RESERVE  1
 #define ATTN_PAGED_ATTEND   2
@@ -475,8 +477,8 @@ int attn_paged_workspace_size(const attn_paged_cache* cache, const attn_shape* s
  * stack's end are dropped; a token whose page is outside the pool gets slot -1 (all
  * ATTN_E_BOUNDS).
  * lens_out may equal lens, and n_free_out n_free; otherwise no array that is written
- * may overlap another (ATTN_E_INVAL). B * add, T: below 2^30. Errors: ATTN_E_INVAL
- * (NULL pointers, sizes), ATTN_E_ALIGN, ATTN_E_WORKSPACE, ATTN_E_CUDA. */
+ * may overlap another (ATTN_E_INVAL). T is below 2^30. Errors: ATTN_E_INVAL (NULL
+ * pointers, sizes), ATTN_E_ALIGN, ATTN_E_WORKSPACE, ATTN_E_CUDA. */
 int attn_paged_reserve(const int32_t* add, const int32_t* lens, int64_t B, int64_t page, int64_t pages,
                        const int32_t* n_free, int32_t* free_pages, int32_t* table, int64_t table_ld,
                        int64_t max_pages, int32_t* lens_out, int32_t* n_free_out, int32_t* cu_seqlens,

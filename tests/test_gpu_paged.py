@@ -224,13 +224,14 @@ def test_strided_queries():
         assert torch.equal(o, want_o) and torch.equal(lse, want_l)
 
 
-def test_values_that_are_not_finite():
+@pytest.mark.parametrize("page,D", [(16, 64), (128, 64), (32, 128), (64, 128), (16, 256), (256, 256)])
+def test_values_that_are_not_finite(page, D):
     # NaN and infinity in V reach the rows that see their slot and no other
-    b = Batch([700], [300], 4, 2, 64, 16, seed=7)
+    b = Batch([700], [300], 4, 2, D, page, seed=7)
     clean_o, clean_l = b.run()
     slots = [(410, 3, math.inf), (450, 60, math.nan), (600, 5, -math.inf), (699, 0, math.nan), (100, 9, math.inf)]
     for j, d, x in slots:
-        b.v[b.table[0, j // 16], 1, j % 16, d] = x
+        b.v[b.table[0, j // page], 1, j % page, d] = x
     o, lse = b.run()
     assert torch.equal(lse, clean_l)
     want = f64(clean_o)
@@ -252,6 +253,45 @@ def test_keys_that_are_not_finite():
     o, lse = b.run()
     assert torch.equal(o[:150], clean_o[:150]) and torch.equal(lse[..., :150], clean_l[..., :150])
     assert o[150:].isnan().all() and lse[..., 150:].isnan().all()
+
+
+@pytest.mark.parametrize("page", [16, 64])
+def test_values_that_are_not_finite_in_every_edge_tile(page):
+    # one head to a key/value head: 128 tokens a tile, every one of which hides the ones after it
+    b = Batch([400, 130], [390, 130], 2, 2, 128, page, seed=17)
+    clean_o, clean_l = b.run()
+    for j in (129, 200, 399):
+        b.v[b.table[0, j // page], 0, j % page, 7] = math.nan
+    o, lse = b.run()
+    want = f64(clean_o)
+    want[129 - 10:390, 0, 7] = math.nan
+    assert np.array_equal(f64(o), want, equal_nan=True) and torch.equal(lse, clean_l)
+
+
+def test_tables_with_gaps_and_calls_on_other_streams():
+    b = Batch([3000, 65, 200], [40, 65, 1], 8, 2, 128, 16, seed=18)
+    want = b.run()
+    wide = torch.full((3, b.table.shape[1] + 13), 1 << 30, dtype=torch.int32, device="cuda")
+    wide[:, :b.table.shape[1]] = i32(b.table)
+    table, lens, cu = wide[:, :b.table.shape[1]], i32(b.lens), i32(b.cu)
+    ws = cca.paged_workspace(b.cache, b.q, 3)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for stream in (s, s.cuda_stream):
+        o, lse = cca.paged_attention(b.q, b.cache, table, lens, cu, ws=ws, stream=stream)
+        s.synchronize()
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    with torch.cuda.stream(s):
+        o, lse = cca.paged_attention(b.q, b.cache, table, lens, cu)
+    s.synchronize()
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1]) and cca.attn_status(ws) == 0
+
+
+def test_shared_pages():
+    # two sequences with the same first pages
+    b = Batch([96, 130], [3, 5], 4, 2, 64, 16, seed=19)
+    b.table[1, :4] = b.table[0, :4]
+    b.check()
 
 
 def test_same_result_every_time():

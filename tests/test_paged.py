@@ -184,3 +184,12 @@ def test_oracle_reserve_table_full():
 def test_oracle_rows():
     pool = np.arange(4 * 1 * 2 * 1).reshape(4, 1, 2, 1)
     assert P.rows(pool, [3, 0, 2], 3, 0, 2)[:, 0].tolist() == [6, 7, 0]
+
+
+def test_most_sequences():
+    most = 1 << 20
+    assert cca.attn_paged_workspace_size(None, None, most, cca.PAGED_RESERVE) >= 20 * most
+    for op, args in ((cca.PAGED_RESERVE, (None, None)), (cca.PAGED_ATTEND, (cache(), shape()))):
+        with pytest.raises(cca.AttnError) as e:
+            cca.attn_paged_workspace_size(*args, most + 1, op)
+        assert e.value.status == 1
