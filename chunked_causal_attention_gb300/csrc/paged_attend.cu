@@ -79,6 +79,7 @@ struct Tiling {
     int32_t units;             // units of a row tile's tokens: key/value heads by blocks of heads
     int32_t tok, few;          // tokens of a row tile, and of the small box that brings fewer
     FastDiv by_tok;
+    int32_t wide;              // rows of O may be stored 32 bytes at a time
     int32_t head_major;        // rows of a tile: head * tokens of the box + token, or token * heads + head
     int32_t box;               // slots of a TMA box of K and V
     int32_t part_rows;         // rows of a partial
@@ -99,7 +100,7 @@ Tiling tiling(const PagedGeom& c, const Geom& g) {
     t.tok = kTile / t.heads;
     t.by_tok = FastDiv::of((uint32_t)t.tok);
     t.few = std::max(1, std::min(t.tok, 16 / t.heads));
-    t.head_major = 0;
+    t.wide = t.head_major = 0;
     t.box = std::min(c.page(), block_n(g.D));
     t.part_rows = (int32_t)std::min<int64_t>(t.tok, g.T) * t.heads;
     t.part_floats = ((int64_t)t.part_rows * (g.D + 1) + 31) / 32 * 32;
@@ -403,6 +404,13 @@ __device__ __noinline__ uint4 only_finite(uint4 x) {
         if ((w[i] & 0x7f800000u) == 0x7f800000u) w[i] &= 0x0000ffffu;
     }
     return x;
+}
+
+// 32 bytes to global memory, 32-byte aligned: a whole sector of a row that one lane writes.
+__device__ __forceinline__ void store32(void* to, const uint32_t* x) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(to), "r"(x[0]), "r"(x[1]), "r"(x[2]),
+                 "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                 : "memory");
 }
 
 // 16 bytes of global memory to shared memory, or zeros, asynchronously.
@@ -977,25 +985,27 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int i = 0; i < 32; ++i) o[c][i] = __float_as_uint(__uint_as_float(o[c][i]) * inv);
                         if (it.part < 0) {
+                            uint32_t y[16];
 #pragma unroll
-                            for (int i = 0; i < 32; i += 8) {
-                                if (d0 + i >= Dv) break;
-                                const uint32_t* x = &o[c][i];
-                                *reinterpret_cast<uint4*>(dst + d0 + i) =
-                                    make_uint4(pack_bf16(__uint_as_float(x[0]), __uint_as_float(x[1])),
-                                               pack_bf16(__uint_as_float(x[2]), __uint_as_float(x[3])),
-                                               pack_bf16(__uint_as_float(x[4]), __uint_as_float(x[5])),
-                                               pack_bf16(__uint_as_float(x[6]), __uint_as_float(x[7])));
+                            for (int i = 0; i < 16; ++i)
+                                y[i] = pack_bf16(__uint_as_float(o[c][2 * i]), __uint_as_float(o[c][2 * i + 1]));
+#pragma unroll
+                            for (int i = 0; i < 16; i += 8) {
+                                if (d0 + 2 * i >= Dv) break;
+                                if (t.wide) {
+                                    store32(dst + d0 + 2 * i, y + i);
+                                } else {
+                                    *reinterpret_cast<uint4*>(dst + d0 + 2 * i) = make_uint4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+                                    if (d0 + 2 * i + 8 < Dv)
+                                        *reinterpret_cast<uint4*>(dst + d0 + 2 * i + 8) =
+                                            make_uint4(y[i + 4], y[i + 5], y[i + 6], y[i + 7]);
+                                }
                             }
                         } else {
 #pragma unroll
                             for (int i = 0; i < 32; i += 8)
                                 if (d0 + i < Dv)
-                                    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(
-                                                     part + d0 + i),
-                                                 "r"(o[c][i]), "r"(o[c][i + 1]), "r"(o[c][i + 2]), "r"(o[c][i + 3]),
-                                                 "r"(o[c][i + 4]), "r"(o[c][i + 5]), "r"(o[c][i + 6]), "r"(o[c][i + 7])
-                                                 : "memory");
+                                    store32(part + d0 + i, &o[c][i]);
                         }
                     }
                 }
@@ -1176,6 +1186,7 @@ cudaError_t launch_d(const PagedAttendArgs& a, cudaStream_t s) {
         !make_tile_map(&mk, a.c.k, kv, mpkv, t.box) || !make_tile_map(&mv, a.c.v, kv, mpkv, t.box))
         return cudaErrorInvalidValue;
     t.head_major = mpq.pos_t < mpq.pos_h;
+    t.wide = ((uintptr_t)a.o | (uintptr_t)(2 * a.g.st) | (uintptr_t)(2 * a.g.sh) | (uintptr_t)(2 * a.g.D)) % 32 == 0;
     static_assert(Layout<D>::ALLOC <= 232448, "shared memory of the paged attention's kernel");
     cudaError_t e = cudaFuncSetAttribute(attend_kernel<D, GATHER>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)Layout<D>::ALLOC);
