@@ -60,7 +60,7 @@ struct PagedAttendArgs {
     int32_t B, each;          // sequences; cu null: tokens of each
     uint32_t* status;
     uint32_t* counter;        // work queue, zero between calls
-    int2* cuts;               // workspace, B of them: first partial and parts of a sequence that is cut
+    int4* cuts;               // workspace, B of them: a sequence's first partial, parts of a cut unit, units left whole
     float* parts;             // workspace: partials
     int32_t max_parts;        // how many it holds
     uint64_t wait_ns; int32_t stall;

@@ -74,7 +74,7 @@ int attend_geom(const attn_shape* shape, const PagedGeom& c, int64_t B, Geom* g)
     return (int64_t)g->H * g->T <= INT32_MAX && paged_units_fit(c, *g, B) ? ATTN_OK : ATTN_E_INVAL;
 }
 
-size_t cuts_bytes(int64_t B) { return round_up((size_t)B * sizeof(int2), kAlign); }
+size_t cuts_bytes(int64_t B) { return round_up((size_t)B * sizeof(int4), kAlign); }
 
 size_t seqs_bytes(int64_t B) { return round_up((size_t)B * sizeof(PagedSeq), kAlign); }
 
@@ -190,7 +190,7 @@ int attn_paged_attend(const void* q, const attn_shape* shape, const attn_paged_c
     a.B = (int32_t)B; a.each = (int32_t)(a.g.T / B);
     a.status = &((WsHeader*)ws)->status;
     a.counter = &((WsHeader*)ws)->counter[2];
-    a.cuts = (int2*)((uint8_t*)ws + kHeaderBytes);
+    a.cuts = (int4*)((uint8_t*)ws + kHeaderBytes);
     a.parts = (float*)((uint8_t*)ws + kHeaderBytes + cuts_bytes(B));
     wait_settings(&a.wait_ns, &a.stall);
     return launched(launch_paged_attend(a, (cudaStream_t)stream));

@@ -160,6 +160,7 @@ struct List {
     Seq seq;                   // the run's sequence, where it is one
     int32_t per;
     int32_t C;                 // most key tiles of an item
+    int32_t whole, tail;       // one sequence's rounds: units left whole, parts of the others; tail 0: all are cut by C
     int32_t n_items;
 };
 
@@ -226,6 +227,33 @@ __device__ __forceinline__ List make_list(const PagedAttendArgs& a, const Tiling
         }
     }
     L.C = (int32_t)fminf(C, 1073741824.f);
+    // One sequence's units are about equal: as many as make full rounds may stay whole, and those of the last round
+    // be cut into a few parts (a lane each number), which leaves fewer partials to write and join.
+    L.whole = L.tail = 0;
+    const int32_t alone = units_of(t, L.seq);
+    const uint32_t have = __ballot_sync(0xffffffffu, alone > 0);
+    const int32_t at = max(0, __ffs(have) - 1), units = __shfl_sync(0xffffffffu, alone, at), left = units % t.sms;
+    if (L.per == 1 && __popc(have) == 1 && units > t.sms && left > 0) {
+        const int32_t tiles = __shfl_sync(0xffffffffu, tiles_of<BN>(L.seq), at);
+        const float n = (float)tiles, p = (float)min((lane & (kTry - 1)) + 1, tiles), cut = (float)left * p;
+        float rounds2 = (float)(units / t.sms) * (n + kItemTiles) +
+                        ceilf(__fdividef(cut, sms)) * (ceilf(__fdividef(n, p)) + kItemTiles);
+        if (p > 1.f) rounds2 += __fdividef(cut * (float)kTile * kRowTiles, sms);
+        int32_t best = (int32_t)p;
+#pragma unroll
+        for (int m = 1; m < kTry; m <<= 1) {
+            const float other = __shfl_xor_sync(0xffffffffu, rounds2, m);
+            const int32_t best2 = __shfl_xor_sync(0xffffffffu, best, m);
+            if (other < rounds2 || (other == rounds2 && best2 < best)) {
+                rounds2 = other;
+                best = best2;
+            }
+        }
+        if (rounds2 < time) {
+            L.whole = units - left;
+            L.tail = best;
+        }
+    }
     int32_t items = 0, parts = 0, longest = 0;
     float about = 0.f;                                   // their sum, where it does not fit an integer
     for (int32_t b = b0; b < b1; ++b) {
@@ -235,6 +263,11 @@ __device__ __forceinline__ List make_list(const PagedAttendArgs& a, const Tiling
         if (p > 1) parts += n * p;
         about += (float)n * (float)p;
         longest = max(longest, (tiles - 1) / p + 1);
+    }
+    if (L.tail && items) {
+        items = L.whole + (alone - L.whole) * L.tail;
+        parts = L.tail > 1 ? items - L.whole : 0;
+        about = (float)items;
     }
     int32_t parts_to = parts;
 #pragma unroll
@@ -261,8 +294,8 @@ __device__ __forceinline__ List make_list(const PagedAttendArgs& a, const Tiling
         int32_t before = parts_to - parts;
         for (int32_t b = b0; b < b1; ++b) {
             if (L.per > 1) L.seq = seq_of(a, b);
-            const int32_t p = fits ? parts_of(tiles_of<BN>(L.seq), L.C) : 1;
-            a.cuts[b] = make_int2(p > 1 ? before : 0, p);
+            const int32_t p = !fits ? 1 : L.tail ? L.tail : parts_of(tiles_of<BN>(L.seq), L.C);
+            a.cuts[b] = make_int4(p > 1 ? before : 0, p, L.whole, 0);
             if (p > 1) before += units_of(t, L.seq) * p;
         }
     }
@@ -289,10 +322,10 @@ __device__ __forceinline__ bool find_item(const PagedAttendArgs& a, const Tiling
     const int lane = threadIdx.x & 31;
     const uint32_t here = __ballot_sync(0xffffffffu, w >= L.first && w - L.first < L.items);
     if (!here) return false;
-    const int32_t r = __ffs(here) - 1;
-    int32_t x = w - __shfl_sync(0xffffffffu, L.first, r), part0 = __shfl_sync(0xffffffffu, L.parts, r);
-    int32_t b = r * L.per;
-    Seq s{__shfl_sync(0xffffffffu, L.seq.q0, r), __shfl_sync(0xffffffffu, L.seq.nq, r), __shfl_sync(0xffffffffu, L.seq.n, r)};
+    const int32_t run = __ffs(here) - 1;
+    int32_t x = w - __shfl_sync(0xffffffffu, L.first, run), part0 = __shfl_sync(0xffffffffu, L.parts, run);
+    int32_t b = run * L.per;
+    Seq s{__shfl_sync(0xffffffffu, L.seq.q0, run), __shfl_sync(0xffffffffu, L.seq.nq, run), __shfl_sync(0xffffffffu, L.seq.n, run)};
     if (L.per > 1) {
         const int32_t end = (int32_t)min((int64_t)b + L.per, (int64_t)a.B);
         bool found = false;
@@ -330,11 +363,29 @@ __device__ __forceinline__ bool find_item(const PagedAttendArgs& a, const Tiling
         if (!found) return false;
     }
     if (b >= a.B) return false;
-    const int32_t parts = parts_of(tiles_of<BN>(s), L.C), row_tiles = row_tiles_of(t, s.nq);
-    if (x < 0 || quotient(x, parts) >= units_of(t, s) || (parts > 1 && part0 + x >= a.max_parts)) return false;
-    // key/value head, block of heads, part, row tile: the tiles with the most slots first
-    const int32_t y = quotient(x, row_tiles), rt = row_tiles - 1 - (x - y * row_tiles);
-    const int32_t u = quotient(y, parts), p = y - u * parts, hk = quotient(u, t.blocks), hb = u - hk * t.blocks;
+    const int32_t row_tiles = row_tiles_of(t, s.nq), units = units_of(t, s);
+    if (x < 0 || units == 0) return false;
+    int32_t parts, p, u, r;                              // u: key/value head and block of heads; r: row tile, the last first
+    if (L.tail) {
+        const bool whole = x < L.whole;
+        const int32_t y = x - L.whole, left = units - L.whole;
+        if (left <= 0) return false;
+        p = whole ? 0 : y / left;
+        const int32_t unit = whole ? x : L.whole + y - p * left;
+        parts = whole ? 1 : L.tail;
+        u = unit / row_tiles;
+        r = unit - u * row_tiles;
+        if (!whole) x = y;
+    } else {
+        // head, part, row tile: blocks that run together read the same part
+        parts = parts_of(tiles_of<BN>(s), L.C);
+        const int32_t y = quotient(x, row_tiles);
+        r = x - y * row_tiles;
+        u = quotient(y, parts);
+        p = y - u * parts;
+    }
+    if (u >= t.units || p >= parts || (parts > 1 && part0 + x >= a.max_parts)) return false;
+    const int32_t rt = row_tiles - 1 - r, hk = quotient(u, t.blocks), hb = u - hk * t.blocks;
     const int32_t G = t.group, i0 = rt * t.tok;
     it.tok0 = s.q0 + i0;
     it.toks = min(t.tok, s.nq - i0);
@@ -1087,19 +1138,21 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const PagedAtte
     grid_go();
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.counter = 0;
     if (!there) return;
-    const int2 cut = a.cuts[b];
+    const int4 cut = a.cuts[b];
     if (cut.y <= 1) return;
     const int32_t row_tiles = row_tiles_of(t, nq), hk = h / t.group, g = h - hk * t.group;
     const int32_t hb = g / t.heads, i = tok - q0, rt = (int32_t)t.by_tok.div((uint32_t)i);
     const int32_t row = (i - rt * t.tok) * t.heads + (g - hb * t.heads);
-    // part p of this row is partial first + p * row_tiles
-    const int64_t first = cut.x + ((int64_t)(hk * t.blocks + hb) * cut.y) * row_tiles + (row_tiles - 1 - rt);
-    if (first + (int64_t)(cut.y - 1) * row_tiles >= a.max_parts || row >= t.part_rows) {
+    // part p of this row is partial first + p * apart; units in front of cut.z are whole
+    const int32_t unit = (hk * t.blocks + hb) * row_tiles + (row_tiles - 1 - rt), apart = cut.z ? t.units * row_tiles - cut.z : row_tiles;
+    if (unit < cut.z) return;
+    const int64_t first = cut.x + (cut.z ? unit - cut.z : (int64_t)(hk * t.blocks + hb) * cut.y * row_tiles + (row_tiles - 1 - rt));
+    if (first + (int64_t)(cut.y - 1) * apart >= a.max_parts || row >= t.part_rows) {
         if (lane == 0) set_error(a.status, ATTN_E_BOUNDS);   // offsets that overlap
         return;
     }
     const float* base = a.parts + first * t.part_floats;
-    const int64_t step = (int64_t)row_tiles * t.part_floats;
+    const int64_t step = (int64_t)apart * t.part_floats;
     const int32_t D = a.g.D;
     const float* lses = base + (int64_t)t.part_rows * D + row;
     // one pass with a running maximum; a few parts at a time, all of their loads before the first use

@@ -174,6 +174,17 @@ def test_attention_random(seed):
           str(rng.choice(["heads", "slots", "both", "gaps", "outer"])), seed=seed, pad=int(rng.integers(0, 50))).check()
 
 
+@pytest.mark.parametrize("lens,nq,H,Hkv,D,page", [
+    ([900], [700], 32, 32, 64, 64),                     # 192 units: more than there are SMs
+    ([5, 1200, 70], [0, 1100, 0], 24, 24, 128, 16),     # among sequences without tokens
+    ([2000], [1300], 64, 16, 64, 32),
+    ([700], [700], 30, 30, 256, 128),
+    ([40], [40], 200, 200, 8, 16),                      # one key tile each
+])
+def test_one_sequence_of_many_units(lens, nq, H, Hkv, D, page):
+    Batch(lens, nq, H, Hkv, D, page, seed=H).check()
+
+
 def test_queries_that_see_nothing():
     # more new tokens than slots in use: the first ones see none
     b = Batch([3, 0, 200], [10, 4, 250], 4, 2, 64, 16)
