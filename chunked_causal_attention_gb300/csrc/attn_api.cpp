@@ -536,7 +536,7 @@ const char* attn_strerror(int st) {
         case ATTN_E_CUDA: return "CUDA runtime call or kernel launch failed";
         case ATTN_E_TIMEOUT: return "device wait gave up (bounded wait timed out)";
         case ATTN_E_BOUNDS: return "device index check failed";
-        case ATTN_E_CAPACITY: return "plan output array too small";
+        case ATTN_E_CAPACITY: return "plan output array too small, or too few free pages";
         default: return "unknown status";
     }
 }

@@ -81,7 +81,7 @@ extern "C" {
 #define ATTN_E_CUDA         5  /* a CUDA runtime call or kernel launch failed  */
 #define ATTN_E_TIMEOUT      6  /* device: a bounded wait gave up               */
 #define ATTN_E_BOUNDS       7  /* device: an index check failed                */
-#define ATTN_E_CAPACITY     8  /* output array of attn_plan* too small          */
+#define ATTN_E_CAPACITY     8  /* output array of attn_plan* too small; device: too few pages */
 
 /* ---- plan modes (SPPO §3.2, §4) ---------------------------------------- */
 #define ATTN_PLAN_UNIFORM              0  /* length-based: equal 128-multiples  */
@@ -477,7 +477,7 @@ int attn_paged_workspace_size(const attn_paged_cache* cache, const attn_shape* s
  * stack's end are dropped; a token whose page is outside the pool gets slot -1 (all
  * ATTN_E_BOUNDS).
  * lens_out may equal lens, and n_free_out n_free; otherwise no array that is written
- * may overlap another (ATTN_E_INVAL). T is below 2^30. Errors: ATTN_E_INVAL (NULL
+ * may overlap another, the gaps between the table's rows included (ATTN_E_INVAL). T is below 2^30. Errors: ATTN_E_INVAL (NULL
  * pointers, sizes), ATTN_E_ALIGN, ATTN_E_WORKSPACE, ATTN_E_CUDA. */
 int attn_paged_reserve(const int32_t* add, const int32_t* lens, int64_t B, int64_t page, int64_t pages,
                        const int32_t* n_free, int32_t* free_pages, int32_t* table, int64_t table_ld,
@@ -551,8 +551,8 @@ int attn_noalloc_status(void* stream);
 /* ---- status ------------------------------------------------------------ */
 
 /* Synchronises `stream`, then reads and clears the device error word in the
- * workspace header: ATTN_OK, ATTN_E_TIMEOUT or ATTN_E_BOUNDS (or ATTN_E_CUDA
- * if the read itself fails). The word lives in the first 256 bytes of the
+ * workspace header: ATTN_OK, ATTN_E_TIMEOUT, ATTN_E_BOUNDS or, after
+ * attn_paged_reserve, ATTN_E_CAPACITY (or ATTN_E_CUDA if the read itself fails). The word lives in the first 256 bytes of the
  * workspace; attn_fwd / attn_fwd_tiles / attn_bwd / attn_bwd_prep / attn_bwd_chunk clear it
  * when they start, and a workspace no such call has used must be zeroed by
  * the caller before its status is read. */
