@@ -43,7 +43,7 @@
 //
 // Measured: one token over 1M slots of 8 heads 587 us (7.3 TB/s), of 48 sequences of 13K
 // slots on average over pages of 16 385 us (6.8 TB/s), over 1000 slots 12.8 us; 2048
-// tokens over 32K slots, 32 heads in groups of 4, 750 us (1420 TFLOP/s).
+// tokens over 32K slots, 32 heads in groups of 4, 722 us (1475 TFLOP/s).
 #include <algorithm>
 
 #include "kv4_device.cuh"
