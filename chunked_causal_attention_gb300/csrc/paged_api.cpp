@@ -125,14 +125,15 @@ int attn_paged_reserve(const int32_t* add, const int32_t* lens, int64_t B, int64
     // what is written lies apart from all the rest; lens_out may be lens and n_free_out n_free
     struct Range { const void* p; size_t n; bool out; };
     const size_t w = sizeof(int32_t), nt = ((size_t)(B - 1) * table_ld + max_pages) * w;
-    const Range r[] = {{add, B * w, false}, {lens, B * w, false}, {n_free, w, false}, {free_pages, pages * w, true},
-                       {table, nt, true}, {lens_out, B * w, true}, {n_free_out, w, true}, {cu_seqlens, (B + 1) * w, true},
-                       {slots, T * w, true}};
-    for (const Range& x : r)
-        for (const Range& y : r)
-            if (&x != &y && x.out && overlap(x.p, x.n, y.p, y.n) &&
-                !(x.p == y.p && (x.p == lens || x.p == n_free) && (!y.out || y.p == x.p) && x.n == y.n))
-                return ATTN_E_INVAL;
+    enum { ADD, LENS, N_FREE, FREE, TABLE, LENS_OUT, N_FREE_OUT, CU, SLOTS, RANGES };
+    const Range r[RANGES] = {{add, B * w, false}, {lens, B * w, false}, {n_free, w, false}, {free_pages, pages * w, true},
+                             {table, nt, true}, {lens_out, B * w, true}, {n_free_out, w, true},
+                             {cu_seqlens, (B + 1) * w, true}, {slots, T * w, true}};
+    for (int i = 0; i < RANGES; ++i)
+        for (int j = 0; j < i; ++j) {
+            const bool in_place = r[i].p == r[j].p && ((i == LENS_OUT && j == LENS) || (i == N_FREE_OUT && j == N_FREE));
+            if ((r[i].out || r[j].out) && !in_place && overlap(r[i].p, r[i].n, r[j].p, r[j].n)) return ATTN_E_INVAL;
+        }
     int st = check_ws(ws, ws_bytes, reserve_bytes(B));
     if (st) return st;
     a.add = add; a.lens = lens; a.n_free = n_free;

@@ -123,6 +123,11 @@ def test_reserve_refuses():
     assert call(slots=at["add"]) == 1 and call(cu=at["lens"]) == 1 and call(lens_out=at["lens"] + 4) == 1
     assert call(table=at["free"]) == 1 and call(n_free_out=at["free"]) == 1 and call(lens_out=at["add"]) == 1
     assert call(n_free_out=at["lens"]) == 1 and call(lens_out=at["lens"], slots=at["lens"]) == 1
+    one = dict(B=1, T=1, ld=1, most=1, pages=1)             # arrays of the same size
+    for name in names[3:]:
+        for other in names:
+            if name != other and (name, other) not in (("lens_out", "lens"), ("n_free_out", "n_free")):
+                assert call(**one, **{name: at[other]}) == 1, (name, other)
     assert cca.kernel_launches() == launches
 
 
