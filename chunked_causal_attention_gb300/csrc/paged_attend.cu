@@ -42,7 +42,7 @@
 // loaded from beyond the tensor map's edge: zeros.
 //
 // Measured: one token over 1M slots of 8 heads 587 us (7.3 TB/s), of 48 sequences of 13K
-// slots on average over pages of 16 385 us (6.8 TB/s), over 1000 slots 12.8 us; 2048
+// slots on average over pages of 16 385 us (6.8 TB/s), over 1000 slots 12.4 us; 2048
 // tokens over 32K slots, 32 heads in groups of 4, 722 us (1475 TFLOP/s).
 #include <algorithm>
 
@@ -174,22 +174,10 @@ __device__ __forceinline__ float warp_sum(float x) {
 constexpr int kTry = 8;
 __constant__ const float kShares[kTry] = {1.f / kItemsPerSm, 0.2f, 1.f / 3, 0.5f, 1.f, 1.25f, 1.5f, 2.f};
 
-// By one warp. `tell`: write a.cuts for the merge kernel.
+// How to cut W key tiles of work, by a warp: sets C, whole and tail.
 template <int BN>
-__device__ __forceinline__ List make_list(const PagedAttendArgs& a, const Tiling& t, bool tell) {
+__device__ __forceinline__ void weigh(const PagedAttendArgs& a, const Tiling& t, float W, List& L) {
     const int lane = threadIdx.x & 31;
-    List L;
-    L.per = (a.B + 31) / 32;
-    const int32_t b0 = (int32_t)min((int64_t)lane * L.per, (int64_t)a.B);
-    const int32_t b1 = (int32_t)min((int64_t)b0 + L.per, (int64_t)a.B);
-    float W = 0.f;
-    L.seq = Seq{0, 0, 0};
-#pragma unroll 4
-    for (int32_t b = b0; b < b1; ++b) {
-        L.seq = seq_of(a, b);
-        W += (float)units_of(t, L.seq) * (float)tiles_of<BN>(L.seq);
-    }
-    W = warp_sum(W);
     // Of several sizes the one that is done first, in key tiles: by full rounds of the longest item, or as a queue
     // hands items out, whichever is less. A lane takes one size and a quarter of the sequences.
     const float sms = (float)t.sms;
@@ -229,7 +217,6 @@ __device__ __forceinline__ List make_list(const PagedAttendArgs& a, const Tiling
     L.C = (int32_t)fminf(C, 1073741824.f);
     // One sequence's units are about equal: as many as make full rounds may stay whole, and those of the last round
     // be cut into a few parts (a lane each number), which leaves fewer partials to write and join.
-    L.whole = L.tail = 0;
     const int32_t alone = units_of(t, L.seq);
     const uint32_t have = __ballot_sync(0xffffffffu, alone > 0);
     const int32_t at = max(0, __ffs(have) - 1), units = __shfl_sync(0xffffffffu, alone, at), left = units % t.sms;
@@ -254,6 +241,27 @@ __device__ __forceinline__ List make_list(const PagedAttendArgs& a, const Tiling
             L.tail = best;
         }
     }
+}
+
+// By one warp. `tell`: write a.cuts for the merge kernel.
+template <int BN>
+__device__ __forceinline__ List make_list(const PagedAttendArgs& a, const Tiling& t, bool tell) {
+    const int lane = threadIdx.x & 31;
+    List L;
+    L.per = (a.B + 31) / 32;
+    const int32_t b0 = (int32_t)min((int64_t)lane * L.per, (int64_t)a.B);
+    const int32_t b1 = (int32_t)min((int64_t)b0 + L.per, (int64_t)a.B);
+    float W = 0.f;
+    L.seq = Seq{0, 0, 0};
+#pragma unroll 4
+    for (int32_t b = b0; b < b1; ++b) {
+        L.seq = seq_of(a, b);
+        W += (float)units_of(t, L.seq) * (float)tiles_of<BN>(L.seq);
+    }
+    W = warp_sum(W);
+    L.C = 1;
+    L.whole = L.tail = 0;
+    if (W > (float)t.sms) weigh<BN>(a, t, W, L);          // less work is cut into single tiles
     int32_t items = 0, parts = 0, longest = 0;
     float about = 0.f;                                   // their sum, where it does not fit an integer
     for (int32_t b = b0; b < b1; ++b) {
@@ -265,7 +273,7 @@ __device__ __forceinline__ List make_list(const PagedAttendArgs& a, const Tiling
         longest = max(longest, (tiles - 1) / p + 1);
     }
     if (L.tail && items) {
-        items = L.whole + (alone - L.whole) * L.tail;
+        items = L.whole + (units_of(t, L.seq) - L.whole) * L.tail;
         parts = L.tail > 1 ? items - L.whole : 0;
         about = (float)items;
     }
