@@ -537,6 +537,27 @@ def test_reserve_reports_bad_integers():
     assert cca.attn_status(ws) == 7 and cu.tolist() == [0, 5, 5] and slots.tolist() == [-1] * 5 and int(t.n_free) == 3
 
 
+def test_reserve_and_store_on_another_stream():
+    rng = np.random.default_rng(30)
+    k, v = bf16(rng, 50, 2, 64), bf16(rng, 50, 2, 64)
+    add = i32([30, 20])
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    want = None
+    for stream in (None, s, s.cuda_stream):
+        cache, tables = cca.paged_cache(9, 2, 16, 64), cca.paged_tables(2, 4, 9, 16)
+        torch.cuda.synchronize()
+        for _ in range(2):                           # 60 slots of one sequence, 40 of the other, by calls that allocate
+            cu, slots = cca.paged_reserve(tables, add, 50, stream=stream)
+            cca.paged_store(cache, k, v, slots, stream=stream)
+        torch.cuda.synchronize()
+        got = [x.clone() for x in (cache.k, cache.v, tables.table, tables.lens, tables.n_free, cu, slots)]
+        assert want is None or all(torch.equal(a, b) for a, b in zip(got, want))
+        want = got
+    assert tables.lens.tolist() == [60, 40] and tables.n_free.tolist() == [2]
+    assert tables.table.tolist() == [[0, 1, 4, 5], [2, 3, 6, -1]]
+
+
 # ------------------------------------------------------------------ a run of them together
 
 @pytest.mark.parametrize("graph", [False, True])
