@@ -413,6 +413,72 @@ __device__ __forceinline__ bool find_item(const PagedAttendArgs& a, const Tiling
     return true;
 }
 
+// ------------------------------------------------------------------ parts of a row, joined
+
+// O = sum_p 2^(L_p - m) O_p / sum_p 2^(L_p - m), L_p the part's log-sum-exp in base 2: in one pass with a running
+// maximum, a few parts at a time, all of their loads before the first use. LANES lanes hold a row, each VECS pieces
+// of four dims, 4 LANES dims apart.
+template <int VECS, int LANES>
+struct Joined {
+    static constexpr int AT_ONCE = VECS > 4 ? 2 : 4;
+    float m, l;
+    float4 o[VECS];
+    __device__ __forceinline__ void add(int x, float w, const float4& y) {
+        o[x] = make_float4(fmaf(w, y.x, o[x].x), fmaf(w, y.y, o[x].y), fmaf(w, y.z, o[x].z), fmaf(w, y.w, o[x].w));
+    }
+    __device__ __forceinline__ float weight(float lse) const { return ex2(lse - (m == -INFINITY ? 0.f : m)); }
+    __device__ __forceinline__ void rescale(float to) {  // to a maximum of at least m
+        const float f = m == to ? 1.f : ex2(m - to);
+        l *= f;
+#pragma unroll
+        for (int x = 0; x < VECS; ++x) o[x] = make_float4(o[x].x * f, o[x].y * f, o[x].z * f, o[x].w * f);
+        m = to;
+    }
+    // Parts p = from, from + by, .. below n; mine: this lane's first piece of part 0, lses: the row's sum of part 0.
+    // The loads go past L1, which may hold what an earlier item left there.
+    __device__ __forceinline__ void parts(const float* mine, const float* lses, int64_t step, int from, int by, int n, int lane,
+                                          int D) {
+        m = -INFINITY;
+        l = 0.f;
+#pragma unroll
+        for (int x = 0; x < VECS; ++x) o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int32_t p0 = from; p0 < n; p0 += AT_ONCE * by) {
+            float lse[AT_ONCE];
+            float4 y[AT_ONCE][VECS];
+#pragma unroll
+            for (int i = 0; i < AT_ONCE; ++i) {
+                const int32_t p = p0 + i * by;
+                lse[i] = p < n ? __ldcg(lses + p * step) : -INFINITY;
+#pragma unroll
+                for (int x = 0; x < VECS; ++x)
+                    y[i][x] = p < n && 4 * (lane + LANES * x) < D
+                                  ? __ldcg(reinterpret_cast<const float4*>(mine + p * step + 4 * LANES * x))
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            float top = m;
+#pragma unroll
+            for (int i = 0; i < AT_ONCE; ++i) top = fmaxf(top, lse[i]);
+            rescale(top);
+#pragma unroll
+            for (int i = 0; i < AT_ONCE; ++i) {
+                const float w = weight(lse[i]);
+                l += w;
+#pragma unroll
+                for (int x = 0; x < VECS; ++x) add(x, w, y[i][x]);
+            }
+        }
+    }
+    __device__ __forceinline__ void write(__nv_bfloat16* dst, float* lse, int lane, int D) const {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+        for (int x = 0; x < VECS; ++x)
+            if (4 * (lane + LANES * x) < D)
+                *reinterpret_cast<uint2*>(dst + 4 * LANES * x) =
+                    make_uint2(pack_bf16(o[x].x * inv, o[x].y * inv), pack_bf16(o[x].z * inv, o[x].w * inv));
+        if (lane == 0) *lse = l == 0.f ? -INFINITY : (m + lg2(l)) * kLn2;
+    }
+};
+
 // ------------------------------------------------------------------ the tile kernel
 
 template <int D>
@@ -1120,7 +1186,6 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const PagedAtte
     constexpr bool BLOCK = ROWS == 1;                    // the block's warps take parts in turn
     constexpr int LANES = BLOCK ? 32 : LPR;              // over a row's dims
     constexpr int VECS = DT / 4 / LANES;                 // float4 of a row that a lane holds
-    constexpr int AT_ONCE = VECS > 4 ? 2 : 4;            // parts whose loads are in flight together
     __shared__ float red[2][kMergeWarps];
     __shared__ __align__(16) float sums[BLOCK ? kMergeWarps : 1][BLOCK ? DT : 4];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x % LANES, sub = BLOCK ? warp : 0, subs = BLOCK ? kMergeWarps : 1;
@@ -1163,78 +1228,29 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const PagedAtte
     const int64_t step = (int64_t)apart * t.part_floats;
     const int32_t D = a.g.D;
     const float* lses = base + (int64_t)t.part_rows * D + row;
-    // one pass with a running maximum; a few parts at a time, all of their loads before the first use
-    float m = -INFINITY, l = 0.f;
-    // dims 4 lane .. 4 lane + 3, and 4 LANES on, as far as there are any
-    float4 o[VECS];
-#pragma unroll
-    for (int x = 0; x < VECS; ++x) o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-    const float* mine = base + (int64_t)row * D + 4 * lane;
-    auto add = [](float4& to, float w, const float4& y) {
-        to.x = fmaf(w, y.x, to.x);
-        to.y = fmaf(w, y.y, to.y);
-        to.z = fmaf(w, y.z, to.z);
-        to.w = fmaf(w, y.w, to.w);
-    };
-    auto rescale = [&](float to) {                       // to a maximum of at least m; m is -inf before the first part
-        const float f = m == to ? 1.f : ex2(m - to);
-        l *= f;
-#pragma unroll
-        for (int x = 0; x < VECS; ++x) o[x] = make_float4(o[x].x * f, o[x].y * f, o[x].z * f, o[x].w * f);
-        m = to;
-    };
-    for (int32_t p0 = sub; p0 < cut.y; p0 += AT_ONCE * subs) {
-        float lse[AT_ONCE];
-        float4 y[AT_ONCE][VECS];
-#pragma unroll
-        for (int i = 0; i < AT_ONCE; ++i) {
-            const int32_t p = p0 + i * subs;
-            lse[i] = p < cut.y ? lses[p * step] : -INFINITY;
-#pragma unroll
-            for (int x = 0; x < VECS; ++x)
-                y[i][x] = p < cut.y && 4 * (lane + LANES * x) < D
-                              ? *reinterpret_cast<const float4*>(mine + p * step + 4 * LANES * x)
-                              : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-        float top = m;
-#pragma unroll
-        for (int i = 0; i < AT_ONCE; ++i) top = fmaxf(top, lse[i]);
-        rescale(top);
-#pragma unroll
-        for (int i = 0; i < AT_ONCE; ++i) {
-            const float w = ex2(lse[i] - (m == -INFINITY ? 0.f : m));
-            l += w;
-#pragma unroll
-            for (int x = 0; x < VECS; ++x) add(o[x], w, y[i][x]);
-        }
-    }
+    Joined<VECS, LANES> j;
+    j.parts(base + (int64_t)row * D + 4 * lane, lses, step, sub, subs, cut.y, lane, D);
     if (BLOCK) {
         if (lane == 0) {
-            red[0][warp] = m;
-            red[1][warp] = l;
+            red[0][warp] = j.m;
+            red[1][warp] = j.l;
         }
 #pragma unroll
-        for (int x = 0; x < VECS; ++x) *reinterpret_cast<float4*>(&sums[warp][4 * (lane + LANES * x)]) = o[x];
+        for (int x = 0; x < VECS; ++x) *reinterpret_cast<float4*>(&sums[warp][4 * (lane + LANES * x)]) = j.o[x];
         __syncthreads();
         if (warp != 0) return;
-        float top = m;
+        float top = j.m;
         for (int w = 1; w < kMergeWarps; ++w) top = fmaxf(top, red[0][w]);
-        rescale(top);
+        j.rescale(top);
         for (int w = 1; w < kMergeWarps; ++w) {
-            const float f = ex2(red[0][w] - (m == -INFINITY ? 0.f : m));
-            l = fmaf(f, red[1][w], l);
+            const float f = j.weight(red[0][w]);
+            j.l = fmaf(f, red[1][w], j.l);
 #pragma unroll
-            for (int x = 0; x < VECS; ++x) add(o[x], f, *reinterpret_cast<const float4*>(&sums[w][4 * (lane + LANES * x)]));
+            for (int x = 0; x < VECS; ++x) j.add(x, f, *reinterpret_cast<const float4*>(&sums[w][4 * (lane + LANES * x)]));
         }
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(a.o) + (int64_t)tok * a.g.st + (int64_t)h * a.g.sh + 4 * lane;
-#pragma unroll
-    for (int x = 0; x < VECS; ++x)
-        if (4 * (lane + LANES * x) < D)
-            *reinterpret_cast<uint2*>(dst + 4 * LANES * x) =
-                make_uint2(pack_bf16(o[x].x * inv, o[x].y * inv), pack_bf16(o[x].z * inv, o[x].w * inv));
-    if (lane == 0) a.lse[(int64_t)h * a.g.T + tok] = l == 0.f ? -INFINITY : (m + lg2(l)) * kLn2;
+    j.write(reinterpret_cast<__nv_bfloat16*>(a.o) + (int64_t)tok * a.g.st + (int64_t)h * a.g.sh + 4 * lane,
+            a.lse + (int64_t)h * a.g.T + tok, lane, D);
 }
 
 template <int D, bool GATHER>
