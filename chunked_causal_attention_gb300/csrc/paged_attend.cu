@@ -435,7 +435,6 @@ struct Joined {
         m = to;
     }
     // Parts p = from, from + by, .. below n; mine: this lane's first piece of part 0, lses: the row's sum of part 0.
-    // The loads go past L1, which may hold what an earlier item left there.
     __device__ __forceinline__ void parts(const float* mine, const float* lses, int64_t step, int from, int by, int n, int lane,
                                           int D) {
         m = -INFINITY;
@@ -448,11 +447,11 @@ struct Joined {
 #pragma unroll
             for (int i = 0; i < AT_ONCE; ++i) {
                 const int32_t p = p0 + i * by;
-                lse[i] = p < n ? __ldcg(lses + p * step) : -INFINITY;
+                lse[i] = p < n ? lses[p * step] : -INFINITY;
 #pragma unroll
                 for (int x = 0; x < VECS; ++x)
                     y[i][x] = p < n && 4 * (lane + LANES * x) < D
-                                  ? __ldcg(reinterpret_cast<const float4*>(mine + p * step + 4 * LANES * x))
+                                  ? *reinterpret_cast<const float4*>(mine + p * step + 4 * LANES * x)
                                   : make_float4(0.f, 0.f, 0.f, 0.f);
             }
             float top = m;
