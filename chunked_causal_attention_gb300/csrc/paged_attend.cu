@@ -32,7 +32,8 @@
 // pages of 16 slots make 32 boxes a key tile, 1.5 us. There (GATHER) warps 2 and 3 bring
 // V by 16-byte copies, one half of a tile each, and TMA brings K alone. 2048 tokens over
 // 32K slots of 8 heads, 128 dims: pages of 16 1408 -> 924 us, of 32 959 -> 867; of 64 and
-// more 757 by TMA, 940 with the copies.
+// more 757 by TMA, 940 with the copies. 256 dims, 4 heads: 1343 -> 864 and 1027 -> 757; 64
+// dims: 898 -> 676 and 667 -> 675.
 //
 // Masked slots. A masked score is replaced before the maximum, so K may hold anything
 // there. But weight 0 times a NaN or an infinity in V would reach the sum, so in tiles
