@@ -60,7 +60,9 @@ struct PagedAttendArgs {
     int32_t B, each;          // sequences; cu null: tokens of each
     uint32_t* status;
     uint32_t* counter;        // work queue, zero between calls
-    int4* cuts;               // workspace, B of them: a sequence's first partial, parts of a cut unit, units left whole
+    int4* cuts;               // workspace, B of them: a sequence's first partial, parts of a cut unit, units left whole,
+                              // whether `offsets` stand for cu
+    int32_t* offsets;         // workspace, B + 1 of them: cu put in order, where it is not
     float* parts;             // workspace: partials
     int32_t max_parts;        // how many it holds
     uint64_t wait_ns; int32_t stall;

@@ -74,7 +74,9 @@ int attend_geom(const attn_shape* shape, const PagedGeom& c, int64_t B, Geom* g)
     return (int64_t)g->H * g->T <= INT32_MAX && paged_units_fit(c, *g, B) ? ATTN_OK : ATTN_E_INVAL;
 }
 
+// What the tile kernel of attention notes of its sequences: cuts, and offsets put in order.
 size_t cuts_bytes(int64_t B) { return round_up((size_t)B * sizeof(int4), kAlign); }
+size_t notes_bytes(int64_t B) { return cuts_bytes(B) + round_up((size_t)(B + 1) * sizeof(int32_t), kAlign); }
 
 size_t seqs_bytes(int64_t B) { return round_up((size_t)B * sizeof(PagedSeq), kAlign); }
 
@@ -101,7 +103,7 @@ int attn_paged_workspace_size(const attn_paged_cache* cache, const attn_shape* s
         Geom g;
         if ((st = attend_geom(shape, c, B, &g))) return st;
         int32_t n;
-        *bytes = kHeaderBytes + cuts_bytes(B) + round_up(paged_parts_bytes(c, g, &n), kAlign);
+        *bytes = kHeaderBytes + notes_bytes(B) + round_up(paged_parts_bytes(c, g, &n), kAlign);
     } else {
         return ATTN_E_INVAL;
     }
@@ -184,7 +186,7 @@ int attn_paged_attend(const void* q, const attn_shape* shape, const attn_paged_c
         return ATTN_E_ALIGN;
     if (overlap(q, span(a.g), o, span(a.g))) return ATTN_E_INVAL;
     size_t parts = paged_parts_bytes(a.c, a.g, &a.max_parts);
-    if ((st = check_ws(ws, ws_bytes, kHeaderBytes + cuts_bytes(B) + round_up(parts, kAlign)))) return st;
+    if ((st = check_ws(ws, ws_bytes, kHeaderBytes + notes_bytes(B) + round_up(parts, kAlign)))) return st;
     a.q = q; a.o = o; a.lse = lse;
     a.table = table; a.table_ld = table_ld; a.max_pages = (int32_t)max_pages;
     a.lens = lens; a.cu = cu_seqlens;
@@ -192,7 +194,8 @@ int attn_paged_attend(const void* q, const attn_shape* shape, const attn_paged_c
     a.status = &((WsHeader*)ws)->status;
     a.counter = &((WsHeader*)ws)->counter[2];
     a.cuts = (int4*)((uint8_t*)ws + kHeaderBytes);
-    a.parts = (float*)((uint8_t*)ws + kHeaderBytes + cuts_bytes(B));
+    a.offsets = (int32_t*)((uint8_t*)ws + kHeaderBytes + cuts_bytes(B));
+    a.parts = (float*)((uint8_t*)ws + kHeaderBytes + notes_bytes(B));
     wait_settings(&a.wait_ns, &a.stall);
     return launched(launch_paged_attend(a, (cudaStream_t)stream));
 }

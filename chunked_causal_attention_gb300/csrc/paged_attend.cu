@@ -120,14 +120,34 @@ struct Seq {
     int32_t q0, nq, n;         // first packed token, tokens, slots in use
 };
 
-__device__ __forceinline__ Seq seq_of(const PagedAttendArgs& a, int32_t b) {
+// Offsets that leave [0, T] or descend, each as the nearest one in [the one before it, T]: sequences have no token in
+// common then. By one warp of every block, all of which write the same to the workspace.
+__device__ __noinline__ const int32_t* offsets_in_order(const PagedAttendArgs& a) {
+    const int lane = threadIdx.x & 31;
+    int32_t from = 0;
+    for (int32_t base = 0; base <= a.B; base += 32) {
+        int32_t x = base + lane <= a.B ? max(from, min(a.cu[base + lane], a.g.T)) : from;
+        for (int m = 1; m < 32; m <<= 1) {
+            const int32_t y = __shfl_up_sync(0xffffffffu, x, m);
+            if (lane >= m) x = max(x, y);
+        }
+        if (base + lane <= a.B) a.offsets[base + lane] = x;
+        from = __shfl_sync(0xffffffffu, x, 31);
+    }
+    __syncwarp();
+    return a.offsets;
+}
+
+// Sequence b by the offsets cu; sets `bad` where they are not in order.
+__device__ __forceinline__ Seq seq_of(const PagedAttendArgs& a, const int32_t* cu, int32_t b, bool& bad) {
     Seq s;
     int32_t hi;
-    if (a.cu) {
-        s.q0 = a.cu[b];
-        hi = a.cu[b + 1];
+    if (cu) {
+        s.q0 = cu[b];
+        hi = cu[b + 1];
         if (!(0 <= s.q0 && s.q0 <= hi && hi <= a.g.T)) {
             set_error(a.status, ATTN_E_BOUNDS);
+            bad = true;
             s.q0 = max(0, min(s.q0, a.g.T));
             hi = max(s.q0, min(hi, a.g.T));
         }
@@ -164,6 +184,7 @@ struct List {
     int32_t first, items;      // the run's first item, and how many it has
     int32_t parts;             // partials of the runs before
     Seq seq;                   // the run's sequence, where it is one
+    const int32_t* cu;         // offsets in order: the caller's, or what was made of them
     int32_t per;
     int32_t C;                 // most key tiles of an item
     int32_t whole, tail;       // one sequence's rounds: units left whole, parts of the others; tail 0: all are cut by C
@@ -189,8 +210,9 @@ __device__ __forceinline__ void weigh(const PagedAttendArgs& a, const Tiling& t,
     const float sms = (float)t.sms;
     const float size = fmaxf(1.f, ceilf(__fdividef(W, sms) * kShares[lane & (kTry - 1)]));
     float n_items = 0.f, extra = 0.f, most = 0.f;
+    bool bad;
     for (int32_t base = 0; base < a.B; base += 32) {
-        const Seq s = L.per == 1 ? L.seq : base + lane < a.B ? seq_of(a, base + lane) : Seq{0, 0, 0};
+        const Seq s = L.per == 1 ? L.seq : base + lane < a.B ? seq_of(a, L.cu, base + lane, bad) : Seq{0, 0, 0};
         const float units = (float)units_of(t, s), tiles = (float)tiles_of<BN>(s);
         const float rows = (float)(min(s.nq, t.tok) * t.heads) * kRowTiles;
 #pragma unroll 1
@@ -257,31 +279,36 @@ __device__ __forceinline__ List make_list(const PagedAttendArgs& a, const Tiling
     L.per = (a.B + 31) / 32;
     const int32_t b0 = (int32_t)min((int64_t)lane * L.per, (int64_t)a.B);
     const int32_t b1 = (int32_t)min((int64_t)b0 + L.per, (int64_t)a.B);
-    float W = 0.f;
-    L.seq = Seq{0, 0, 0};
+    float W;
+    L.cu = a.cu;
+    while (true) {
+        bool bad = false;
+        W = 0.f;
+        L.seq = Seq{0, 0, 0};
 #pragma unroll 4
-    for (int32_t b = b0; b < b1; ++b) {
-        L.seq = seq_of(a, b);
-        W += (float)units_of(t, L.seq) * (float)tiles_of<BN>(L.seq);
+        for (int32_t b = b0; b < b1; ++b) {
+            L.seq = seq_of(a, L.cu, b, bad);
+            W += (float)units_of(t, L.seq) * (float)tiles_of<BN>(L.seq);
+        }
+        if (L.cu != a.cu || !__any_sync(0xffffffffu, bad)) break;
+        L.cu = offsets_in_order(a);                      // and once more
     }
     W = warp_sum(W);
     L.C = 1;
     L.whole = L.tail = 0;
     if (W > (float)t.sms) weigh<BN>(a, t, W, L);          // less work is cut into single tiles
     int32_t items = 0, parts = 0, longest = 0;
-    float about = 0.f;                                   // their sum, where it does not fit an integer
+    bool bad;
     for (int32_t b = b0; b < b1; ++b) {
-        if (L.per > 1) L.seq = seq_of(a, b);
+        if (L.per > 1) L.seq = seq_of(a, L.cu, b, bad);
         const int32_t tiles = tiles_of<BN>(L.seq), p = parts_of(tiles, L.C), n = units_of(t, L.seq);
         items += n * p;
         if (p > 1) parts += n * p;
-        about += (float)n * (float)p;
         longest = max(longest, (tiles - 1) / p + 1);
     }
     if (L.tail && items) {
         items = L.whole + (units_of(t, L.seq) - L.whole) * L.tail;
         parts = L.tail > 1 ? items - L.whole : 0;
-        about = (float)items;
     }
     int32_t parts_to = parts;
 #pragma unroll
@@ -298,8 +325,8 @@ __device__ __forceinline__ List make_list(const PagedAttendArgs& a, const Tiling
         items_all += n;
     }
     const int32_t parts_all = __shfl_sync(0xffffffffu, parts_to, 31);
-    // offsets that descend can give more items than there are tokens for: nothing is done then
-    const bool fits = warp_sum(about) < 1073741824.f && parts_all <= a.max_parts;
+    // a list of more parts than the workspace holds is not worked off
+    const bool fits = parts_all <= a.max_parts;
     if (!fits) set_error(a.status, ATTN_E_BOUNDS);
     L.n_items = fits ? items_all : 0;
     L.items = items;
@@ -307,9 +334,9 @@ __device__ __forceinline__ List make_list(const PagedAttendArgs& a, const Tiling
     if (tell) {
         int32_t before = parts_to - parts;
         for (int32_t b = b0; b < b1; ++b) {
-            if (L.per > 1) L.seq = seq_of(a, b);
+            if (L.per > 1) L.seq = seq_of(a, L.cu, b, bad);
             const int32_t p = !fits ? 1 : L.tail ? L.tail : parts_of(tiles_of<BN>(L.seq), L.C);
-            a.cuts[b] = make_int4(p > 1 ? before : 0, p, L.whole, 0);
+            a.cuts[b] = make_int4(p > 1 ? before : 0, p, L.whole, L.cu != a.cu);
             if (p > 1) before += units_of(t, L.seq) * p;
         }
     }
@@ -347,7 +374,8 @@ __device__ __forceinline__ bool find_item(const PagedAttendArgs& a, const Tiling
             int32_t items = 0, cut = 0;
             s = Seq{0, 0, 0};
             if (b + lane < end) {
-                s = seq_of(a, b + lane);
+                bool bad;
+                s = seq_of(a, L.cu, b + lane, bad);
                 const int32_t p = parts_of(tiles_of<BN>(s), L.C);
                 items = units_of(t, s) * p;
                 cut = p > 1 ? items : 0;
@@ -1184,6 +1212,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 constexpr int kMergeWarps = 8;
 
+// The last sequence that begins at or before the token.
+__device__ __forceinline__ int32_t sequence_at(const int32_t* cu, int32_t B, int32_t tok) {
+    int32_t b = 0;
+    for (int32_t hi = B; hi - b > 1;) {
+        const int32_t mid = (b + hi) >> 1;
+        if (cu[mid] <= tok) b = mid; else hi = mid;
+    }
+    return b;
+}
+
+// By the offsets that the kernel before put in order; out of line, which keeps the join's registers free.
+__device__ __noinline__ int32_t sequence_taken(const PagedAttendArgs& a, int32_t tok) { return sequence_at(a.offsets, a.B, tok); }
+
 // LPR lanes a row of the output: a quarter of a warp where rows are many, the whole block where they are few (2048
 // tokens of 32 heads in two parts 752 us with a quarter, 763 with a warp; 40 rows of 32 heads in four parts 18.3 and 16.1).
 // Row r is head r % H of token r / H. Also leaves the work queue at zero for the next call.
@@ -1198,29 +1239,32 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const PagedAtte
     const int warp = threadIdx.x >> 5, lane = threadIdx.x % LANES, sub = BLOCK ? warp : 0, subs = BLOCK ? kMergeWarps : 1;
     const uint32_t group = LANES == 32 ? 0xffffffffu : ((1u << (LANES % 32)) - 1) << (threadIdx.x & 31 & ~(LANES - 1));
     const int64_t r = (int64_t)blockIdx.x * ROWS + threadIdx.x / LPR;
-    // the row's sequence: offsets are older than the kernel before this one
-    bool there = r < (int64_t)a.g.T * a.g.H;             // the same for the lanes of a row
+    // the row's sequence, tokens [q0, to): offsets are older than the kernel before this one
+    const bool there = r < (int64_t)a.g.T * a.g.H;       // the same for the lanes of a row
     const int32_t tok = there ? (int32_t)((uint32_t)r / (uint32_t)a.g.H) : 0, h = (int32_t)(r - (int64_t)tok * a.g.H);
-    int32_t b = 0, q0 = 0, nq = a.each;
+    int32_t b, q0, to;
     if (a.cu) {
-        for (int32_t hi = a.B; hi - b > 1;) {            // the last sequence that begins at or before the token
-            const int32_t mid = (b + hi) >> 1;
-            if (a.cu[mid] <= tok) b = mid; else hi = mid;
-        }
+        b = sequence_at(a.cu, a.B, tok);
         q0 = a.cu[b];
-        nq = min(a.cu[b + 1], a.g.T) - q0;
-        there = there && q0 >= 0 && tok >= q0 && tok - q0 < nq;
+        to = a.cu[b + 1];
     } else {
         b = min(tok / a.each, a.B - 1);
         q0 = b * a.each;
+        to = q0 + a.each;
     }
     grid_wait();
     grid_go();
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.counter = 0;
     if (!there) return;
-    const int4 cut = a.cuts[b];
-    if (cut.y <= 1) return;
-    const int32_t row_tiles = row_tiles_of(t, nq), hk = h / t.group, g = h - hk * t.group;
+    int4 cut = a.cuts[b];
+    if (cut.w) {                                         // offsets out of order: as the kernel before took them
+        b = sequence_taken(a, tok);
+        q0 = a.offsets[b];
+        to = a.offsets[b + 1];
+        cut = a.cuts[b];
+    }
+    if (cut.y <= 1 || tok < q0 || tok >= to) return;
+    const int32_t row_tiles = row_tiles_of(t, to - q0), hk = h / t.group, g = h - hk * t.group;
     const int32_t hb = g / t.heads, i = tok - q0, rt = (int32_t)t.by_tok.div((uint32_t)i);
     const int32_t row = (i - rt * t.tok) * t.heads + (g - hb * t.heads);
     // part p of this row is partial first + p * apart; units in front of cut.z are whole
@@ -1228,7 +1272,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const PagedAtte
     if (unit < cut.z) return;
     const int64_t first = cut.x + (cut.z ? unit - cut.z : (int64_t)(hk * t.blocks + hb) * cut.y * row_tiles + (row_tiles - 1 - rt));
     if (first + (int64_t)(cut.y - 1) * apart >= a.max_parts || row >= t.part_rows) {
-        if (lane == 0) set_error(a.status, ATTN_E_BOUNDS);   // offsets that overlap
+        if (lane == 0) set_error(a.status, ATTN_E_BOUNDS);
         return;
     }
     const float* base = a.parts + first * t.part_floats;

@@ -501,9 +501,9 @@ int attn_paged_store(const void* k, const void* v, const attn_shape* shape, cons
  *   LSE_i = ln sum_j exp(scale * q_i . k_j),  O_i = sum_j exp(scale * q_i . k_j - LSE_i) v_j
  * A query that sees no slot has O = 0 and LSE = -inf. lse: fp32 [H][T] contiguous.
  * Rows of padding are left as they were. Slots that a query does not see do not reach
- * its output, whatever they hold. A length outside [0, max_pages * page] and offsets
- * that leave [0, T] or descend are taken as the nearest in range, and a page outside
- * the pool reads as zeros (all ATTN_E_BOUNDS). Softmax weights are rounded to bf16 for
+ * its output, whatever they hold. A length outside [0, max_pages * page] is taken as
+ * the nearest in range, an offset outside [the one before it, T] (the first: [0, T])
+ * likewise, and a page outside the pool reads as zeros (all ATTN_E_BOUNDS). Softmax weights are rounded to bf16 for
  * the product with V; sums are fp32, in an order that the lengths alone decide: the
  * result does not change from run to run. Errors as attn_paged_store. */
 int attn_paged_attend(const void* q, const attn_shape* shape, const attn_paged_cache* cache, const int32_t* table,

@@ -1,0 +1,68 @@
+"""The paged cache's calls at their edges: offsets out of order, calls as their documents allow them.
+Outputs are compared with those of a call that has to make the same ones, bit for bit."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import chunked_causal_attention_gb300 as cca
+from test_gpu_paged import Batch, bf16, built, i32      # noqa: F401 (built: the fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ offsets that leave [0, T] or descend
+
+def nearest(cu, T):
+    """Each offset the nearest one in [the one before it, T]."""
+    return np.maximum.accumulate(np.clip(np.asarray(cu, dtype=np.int64), 0, T))
+
+
+def check_offsets(b, cu):
+    """Rows of a call with these offsets are those of a call with the nearest ones, the others are left alone."""
+    ws = cca.paged_workspace(b.cache, b.q, len(b.lens))
+    good = nearest(cu, b.T)
+    outs = []
+    for x, status in ((good, 0), (cu, 7)):
+        o, lse = torch.full_like(b.q, 7.0), torch.full((1, b.H, b.T), 7.0, device="cuda")
+        cca.paged_attention(b.q, b.cache, i32(b.table), i32(b.lens), i32(x), o=o, lse=lse, ws=ws)
+        assert cca.attn_status(ws) == status
+        outs.append((o, lse))
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+    for o, lse in outs:
+        for rows in (slice(0, good[0]), slice(good[-1], b.T)):
+            assert (o[rows] == 7.0).all() and (lse[..., rows] == 7.0).all()
+        assert not (o[good[0]:good[-1]] == 7.0).all(-1).any()
+
+
+@pytest.mark.parametrize("cu", [[-4, 20, 21], [0, 20, 1 << 30], [-2 ** 31, 20, 2 ** 31 - 1], [0, -1, 21]])
+def test_offsets_outside(cu):
+    check_offsets(Batch([300, 40], [20, 1], 4, 2, 64, 16), cu)
+
+
+@pytest.mark.parametrize("cu", [[0, 20, 5], [21, 0, 21], [9, 3, 2]])
+def test_offsets_that_descend(cu):
+    check_offsets(Batch([300, 40], [20, 1], 4, 2, 64, 16), cu)
+
+
+@pytest.mark.parametrize("cu", [[0, 50, 20, 22, 30], [10, 0, 60, 30, 1000], [-5, 30, 30, 10, 40], [60, 61, 5, 9, 61]])
+@pytest.mark.parametrize("page", [16, 128])
+def test_offsets_that_descend_past_others(cu, page):
+    check_offsets(Batch([2000, 129, 700, 64], [50, 1, 5, 4], 8, 2, 128, page, seed=40), cu)
+
+
+@pytest.mark.parametrize("B", [40, 1200, 3000])
+def test_offsets_at_random(B):
+    # more sequences than a warp has lanes, and more in a lane's run
+    rng = np.random.default_rng(B)
+    lens = [int(x) for x in rng.integers(1, 200, B)]
+    lens[B // 3] = 4000
+    b = Batch(lens, [1] * B, 4, 2, 64, 16, seed=B, pad=37)
+    cu = b.cu.copy()
+    at = rng.choice(B + 1, 6, replace=False)
+    cu[at] = rng.integers(-50, b.T + 50, 6)
+    cu[0] = -3
+    check_offsets(b, cu)
+    check_offsets(b, np.concatenate([[-2 ** 31], rng.integers(-2 ** 31, 2 ** 31 - 1, B)]))
+    check_offsets(b, np.sort(rng.integers(-40, b.T + 40, B + 1))[::-1].copy())
