@@ -87,6 +87,7 @@ class PagedCache:
     def _shape(self, x, scale: Optional[float]):
         """A reference to the attn_shape of a packed tensor, kept by sizes, strides and scale: a
         decode loop asks for the same one at every step."""
+        scale = None if scale is None else float(scale)      # a tensor's value, which may change, not the tensor
         key = (x.shape, x.stride(), scale)
         got = self._shapes.get(key)
         if got is None:

@@ -198,3 +198,11 @@ def test_most_sequences():
         with pytest.raises(cca.AttnError) as e:
             cca.attn_paged_workspace_size(*args, most + 1, op)
         assert e.value.status == 1
+
+
+def test_scale_of_a_tensor_is_read_every_time():
+    c, q, scale = cca.paged_cache(4, 2, 16, 64, device="cpu"), torch.zeros(3, 4, 64, dtype=torch.bfloat16), torch.tensor(0.5)
+    assert c._shape(q, scale)._obj.scale == 0.5
+    scale.fill_(0.25)
+    assert c._shape(q, scale)._obj.scale == 0.25
+    assert c._shape(q, np.array(2.0))._obj.scale == 2.0 and c._shape(q, None)._obj.scale == 0.125
