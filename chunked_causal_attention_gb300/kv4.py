@@ -59,6 +59,7 @@ class KV4Cache:
     def _shape(self, x, scale: Optional[float], packed: bool):
         """The attn_shape of a tensor and a reference to it, kept by sizes, strides and scale: a
         decode loop asks for the same one at every step."""
+        scale = None if scale is None else float(scale)      # a tensor's value, which may change, not the tensor
         key = (x.shape, x.stride(), scale, packed)
         got = self._shapes.get(key)
         if got is None:

@@ -282,3 +282,11 @@ def test_rows_that_are_written_lie_apart(B, H, T, sb, sh, st, ok):
     assert L.attn_kv4_attend(FAKE, ctypes.byref(s), ctypes.byref(c), FAKE, FAKE, FAKE, None, None, 0, None, 0, None) == want
     assert L.attn_kv4_load(ctypes.byref(c), FAKE, None, ctypes.byref(s), FAKE, FAKE, None, 0, None) == want
     assert L.attn_kv4_store(FAKE, FAKE, ctypes.byref(s), ctypes.byref(c), FAKE, None, None, 0, None) == 4
+
+
+def test_scale_of_a_tensor_is_read_every_time():
+    c, q, scale = cca.kv4_cache(1, 2, 16, 64, device="cpu"), torch.zeros(1, 4, 3, 64, dtype=torch.bfloat16), torch.tensor(0.5)
+    assert c._shape(q, scale, False)[0].scale == 0.5
+    scale.fill_(0.25)
+    assert c._shape(q, scale, False)[0].scale == 0.25
+    assert c._shape(q, np.array(2.0), False)[0].scale == 2.0 and c._shape(q, None, False)[0].scale == 0.125
