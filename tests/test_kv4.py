@@ -289,4 +289,4 @@ def test_scale_of_a_tensor_is_read_every_time():
     assert c._shape(q, scale, False)[0].scale == 0.5
     scale.fill_(0.25)
     assert c._shape(q, scale, False)[0].scale == 0.25
-    assert c._shape(q, np.array(2.0), False)[0].scale == 2.0 and c._shape(q, None, False)[0].scale == 0.125
+    assert c._shape(q, torch.tensor(2), False)[0].scale == 2.0 and c._shape(q, None, False)[0].scale == 0.125
