@@ -66,3 +66,16 @@ def test_offsets_at_random(B):
     check_offsets(b, cu)
     check_offsets(b, np.concatenate([[-2 ** 31], rng.integers(-2 ** 31, 2 ** 31 - 1, B)]))
     check_offsets(b, np.sort(rng.integers(-40, b.T + 40, B + 1))[::-1].copy())
+
+
+# ------------------------------------------------------------------ many sequences
+
+def test_tens_of_thousands_of_sequences():
+    # runs of hundreds of sequences a lane: every block goes on in a run where it found its item before
+    B = 20000
+    rng = np.random.default_rng(50)
+    lens = [int(x) for x in rng.integers(0, 30, B)]
+    nq = [int(x) for x in rng.integers(0, 2, B)]
+    for b, n, q in ((3, 3000, 9), (B // 2, 9000, 200), (B - 1, 700, 1)):
+        lens[b], nq[b] = n, q
+    Batch(lens, nq, 2, 1, 64, 16, seed=50).check()
