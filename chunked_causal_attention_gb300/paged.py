@@ -156,7 +156,9 @@ def paged_reserve(tables: PagedTables, add, T: int, lens_out=None, n_free_out=No
                   stream=None):
     """Slots for the next tokens: add int32 [B], new tokens of each sequence (negative: it ends
     and its pages become free). Extends the table in place, and the lengths and the number of
-    free pages too, unless lens_out or n_free_out take them. Returns (cu_seqlens, slots): int32
+    free pages too, unless lens_out or n_free_out take them. A page that is in use has to be in one
+    sequence's row only: the ends of two would put it on the stack twice (attn.h has what to do
+    where sequences share pages). Returns (cu_seqlens, slots): int32
     [B + 1] offsets of the packed tokens and int32 [T] slots, -1 for padding and for sequences
     that found no pages (attn_status tells: ATTN_E_CAPACITY)."""
     fn = "paged_reserve"
@@ -183,7 +185,8 @@ def paged_reserve(tables: PagedTables, add, T: int, lens_out=None, n_free_out=No
 
 def paged_store(cache: PagedCache, k, v, slots, ws=None, stream=None) -> None:
     """Store the rows of k and v, bf16 packed [T, Hkv, D], in the slots (int32 [T]) that
-    paged_reserve named; rows with slot -1 are skipped."""
+    paged_reserve named; rows with slot -1 are skipped. k and v may be views of the pool, of a
+    page that is copied, as long as no slot is both read and written."""
     fn = "paged_store"
     c = cache._calls
     if ws is None:

@@ -476,9 +476,16 @@ int attn_paged_workspace_size(const attn_paged_cache* cache, const attn_shape* s
  * outside [0, max_pages * page] are taken as the nearest; pages put back beyond the
  * stack's end are dropped; a token whose page is outside the pool gets slot -1 (all
  * ATTN_E_BOUNDS).
+ * Every page has to be in one place, in use in one row of the table or on the stack: it
+ * keeps no count of a page's owners. A page in use in two rows goes onto the stack with
+ * each of them, after which two sequences get it and write over each other's rows; that
+ * is not found out. A caller whose sequences share pages ends them without this call:
+ * it sets their lengths to 0 and puts a page on the stack when its last owner ends, and
+ * gives a sequence that goes on in a shared page a copy of it first (attn_paged_store).
  * lens_out may equal lens, and n_free_out n_free; otherwise no array that is written
- * may overlap another, the gaps between the table's rows included (ATTN_E_INVAL). T is below 2^30. Errors: ATTN_E_INVAL (NULL
- * pointers, sizes), ATTN_E_ALIGN, ATTN_E_WORKSPACE, ATTN_E_CUDA. */
+ * may overlap another, the gaps between the table's rows included (ATTN_E_INVAL). T is
+ * below 2^30. Errors: ATTN_E_INVAL (NULL pointers, sizes), ATTN_E_ALIGN,
+ * ATTN_E_WORKSPACE, ATTN_E_CUDA. */
 int attn_paged_reserve(const int32_t* add, const int32_t* lens, int64_t B, int64_t page, int64_t pages,
                        const int32_t* n_free, int32_t* free_pages, int32_t* table, int64_t table_ld,
                        int64_t max_pages, int32_t* lens_out, int32_t* n_free_out, int32_t* cu_seqlens,
@@ -486,14 +493,17 @@ int attn_paged_reserve(const int32_t* add, const int32_t* lens, int64_t B, int64
 
 /* Store row t of k and v, bf16 [T, Hkv, D] with the shape's (query) strides, in slot
  * slots[t]; a row with slot -1 is skipped, as is one with any other slot outside the
- * pool (ATTN_E_BOUNDS). A slot that two rows name holds pieces of either. Errors:
+ * pool (ATTN_E_BOUNDS). A slot that two rows name holds pieces of either. Rows may be
+ * slots of the pool itself, a page that is copied, say; what the call reads from a slot
+ * that it also writes are pieces of the old row or of the new one. Errors:
  * ATTN_E_INVAL (NULL pointers, sizes that do not fit each other, T * Hkv * D of 2^34
  * or more), ATTN_E_ALIGN, ATTN_E_UNSUPPORTED, ATTN_E_WORKSPACE, ATTN_E_CUDA. */
 int attn_paged_store(const void* k, const void* v, const attn_shape* shape, const attn_paged_cache* cache,
                      const int32_t* slots, void* ws, size_t ws_bytes, void* stream);
 
 /* Attention of the newest tokens of B sequences, one or a chunk of many each, over
- * their pages (the tokens' own rows stored before the call). q, o: bf16 [T, H, D] with
+ * their pages (the tokens' own rows stored before the call; sequences may have pages in
+ * common). q, o: bf16 [T, H, D] with
  * the shape's (query) strides, H a multiple of the cache's Hkv (query head h reads
  * key/value head h / (H / Hkv)), o apart from q. cu_seqlens as above, or NULL: T / B
  * tokens each. With n = lens[b] slots in use and n_q tokens, query i sees the slots

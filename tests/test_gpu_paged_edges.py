@@ -79,3 +79,29 @@ def test_tens_of_thousands_of_sequences():
     for b, n, q in ((3, 3000, 9), (B // 2, 9000, 200), (B - 1, 700, 1)):
         lens[b], nq[b] = n, q
     Batch(lens, nq, 2, 1, 64, 16, seed=50).check()
+
+
+# ------------------------------------------------------------------ pages of several sequences
+
+def test_a_shared_page_is_copied_before_it_is_written():
+    """Two sequences begin with the same pages; the second one's last page, half full, is stored in a page of its own
+    before both go on. Rows of the pool are the call's rows, and no slot is both read and written."""
+    page, Hkv, D = 16, 2, 64
+    b = Batch([40, 40], [1, 1], 4, Hkv, D, page, seed=61, extra=3)
+    b.table[1, :2] = b.table[0, :2]                  # two full pages of both, eight slots of the third
+    own = int(b.table[1, 2])
+    for pool in (b.k, b.v):
+        pool[own] = math.nan
+    at = int(b.table[0, 2])
+    rows = [pool[at].transpose(0, 1) for pool in (b.k, b.v)]      # [page, Hkv, D], views of the pool
+    slots = [own * page + i if i < 8 else -1 for i in range(page)]
+    ws = cca.paged_workspace(b.cache, b.q, 2)
+    cca.paged_store(b.cache, *rows, i32(slots), ws=ws)
+    new = [bf16(np.random.default_rng(62 + i), 2, Hkv, D) for i in range(2)]
+    cca.paged_store(b.cache, *new, i32([at * page + 8, own * page + 8]), ws=ws)
+    assert cca.attn_status(ws) == 0
+    for pool, n in zip((b.k, b.v), new):
+        assert torch.equal(pool[own, :, :8], pool[at, :, :8])
+        assert torch.equal(pool[at, :, 8], n[0]) and torch.equal(pool[own, :, 8], n[1])
+    b.lens = [41, 41]
+    b.check()
