@@ -81,6 +81,51 @@ def test_tens_of_thousands_of_sequences():
     Batch(lens, nq, 2, 1, 64, 16, seed=50).check()
 
 
+# ------------------------------------------------------------------ the calls with every array given
+
+def test_calls_with_every_array_given():
+    """attn_paged_reserve, attn_paged_store and attn_paged_attend do what the handles' calls do."""
+    rng = np.random.default_rng(60)
+    B, H, Hkv, D, page, pages, most, T = 3, 8, 2, 64, 16, 40, 20, 120
+    q, k, v = (bf16(rng, T, n, D) for n in (H, Hkv, Hkv))
+    cache, tables = cca.paged_cache(pages, Hkv, page, D), cca.paged_tables(B, most, pages, page)
+    other, t = cca.paged_cache(pages, Hkv, page, D), cca.paged_tables(B, most, pages, page)
+    ws = cca.paged_workspace(cache, q, B, tables)
+    shape, rows = cca.shape_of(q, None, True), cca.shape_of(k, 1.0, True)
+    for plan in ([70, 0, 45], [1, 30, -1], [1, 1, 90]):
+        add = i32(plan)
+        cu, slots = cca.paged_reserve(tables, add, T, ws=ws)
+        cca.paged_store(cache, k, v, slots, ws=ws)
+        want = cca.paged_attention(q, cache, tables.table, tables.lens, cu, ws=ws)
+        cu2, slots2 = torch.empty_like(cu), torch.empty_like(slots)
+        o, lse = torch.empty_like(q), torch.empty((1, H, T), device="cuda")
+        cca.attn_paged_reserve(add, t.lens, page, t.n_free, t.free, t.table, t.lens, t.n_free, cu2, slots2, ws)
+        cca.attn_paged_store(k, v, rows, other.desc, slots2, ws)
+        cca.attn_paged_attend(q, shape, other.desc, t.table, t.lens, cu2, o, lse, ws)
+        assert cca.attn_status(ws) == 0
+        n = sum(max(x, 0) for x in plan)
+        for a, b in ((cu, cu2), (slots, slots2), (tables.table, t.table), (tables.lens, t.lens), (tables.free, t.free),
+                     (tables.n_free, t.n_free), (cache.k, other.k), (cache.v, other.v), (want[0][:n], o[:n]),
+                     (want[1][..., :n], lse[..., :n])):
+            assert torch.equal(a, b)
+    # T / B tokens of each without offsets
+    cca.attn_paged_attend(q, shape, other.desc, t.table, t.lens, None, o, lse, ws)
+    want = cca.paged_attention(q, cache, tables.table, tables.lens, ws=ws)
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1]) and cca.attn_status(ws) == 0
+    # what they refuse before the library is called
+    for call in (lambda: cca.attn_paged_reserve(add, t.lens[:2], page, t.n_free, t.free, t.table, t.lens, t.n_free, cu2, slots2, ws),
+                 lambda: cca.attn_paged_reserve(add.cpu(), t.lens, page, t.n_free, t.free, t.table, t.lens, t.n_free, cu2, slots2, ws),
+                 lambda: cca.attn_paged_reserve(add, t.lens, page, t.n_free, t.free, t.table.T, t.lens, t.n_free, cu2, slots2, ws),
+                 lambda: cca.attn_paged_store(k, v[:, :, ::2], rows, other.desc, slots2, ws),
+                 lambda: cca.attn_paged_store(k, v, rows, other.desc, slots2[1:], ws),
+                 lambda: cca.attn_paged_attend(q, shape, other.desc, t.table, t.lens, cu2, o.float(), lse, ws),
+                 lambda: cca.attn_paged_attend(q, shape, other.desc, t.table, t.lens, cu2[1:], o, lse, ws),
+                 lambda: cca.attn_paged_attend(q, shape, other.desc, t.table.long(), t.lens, cu2, o, lse, ws)):
+        with pytest.raises(cca.AttnError) as e:
+            call()
+        assert e.value.status == 1
+
+
 # ------------------------------------------------------------------ pages of several sequences
 
 def test_a_shared_page_is_copied_before_it_is_written():
