@@ -1252,7 +1252,6 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const PagedAtte
     __shared__ float red[2][kMergeWarps];
     __shared__ __align__(16) float sums[BLOCK ? kMergeWarps : 1][BLOCK ? DT : 4];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x % LANES, sub = BLOCK ? warp : 0, subs = BLOCK ? kMergeWarps : 1;
-    const uint32_t group = LANES == 32 ? 0xffffffffu : ((1u << (LANES % 32)) - 1) << (threadIdx.x & 31 & ~(LANES - 1));
     const int64_t r = (int64_t)blockIdx.x * ROWS + threadIdx.x / LPR;
     // the row's sequence, tokens [q0, to): offsets are older than the kernel before this one
     const bool there = r < (int64_t)a.g.T * a.g.H;       // the same for the lanes of a row
