@@ -4,8 +4,13 @@
 //   s_rj = scale q_r . k_j,   O_r = sum_{j seen by r} 2^(s2_rj - m_r) v_j / l_r,   s2 = s log2 e
 //
 // Bounds. A decode step reads every key and value once, 4 n Hkv D bytes, and is bound by
-// memory; a chunk of many tokens does 4 D operations a (row, slot) pair and is bound by
-// the tensor cores (at the board's power limit, as the forward).
+// memory. A chunk of many tokens does 4 D operations a (row, slot) pair, but its pace is
+// that of the one softmax warpgroup's loop (scores out of TMEM, weights back into it, the
+// hand-over to the next product): 2048 tokens over 32K slots take an SM 0.74 us a key tile
+// at 64 dims, where the products are 0.28 us, and 0.84 at 128 dims, where they are 0.57;
+// the tensor pipe is busy 36% and 67% of the time. Repeated for seconds, 128 dims reach the board's
+// power limit as well (704 -> 754 us at a median of 1800 MHz); 64 dims do not (619 -> 621,
+// 2070 MHz).
 //
 // Rows. The G = H / Hkv query heads that share a key/value head read the same slots, so
 // a tile of 128 rows is 128 / G tokens of all G heads (of up to 128 of them): a decode
@@ -31,9 +36,10 @@
 // Small pages. A TMA copy takes about 45 ns of the unit's time however small its box is:
 // pages of 16 slots make 32 boxes a key tile, 1.5 us. There (GATHER) warps 2 and 3 bring
 // V by 16-byte copies, one half of a tile each, and TMA brings K alone. 2048 tokens over
-// 32K slots of 8 heads, 128 dims: pages of 16 1408 -> 924 us, of 32 959 -> 867; of 64 and
-// more 757 by TMA, 940 with the copies. 256 dims, 4 heads: 1343 -> 864 and 1027 -> 757; 64
-// dims: 898 -> 676 and 667 -> 675.
+// 32K slots, by TMA and with the copies: 128 dims, pages of 16 1337 and 857 us, of 32 888
+// and 770, of 64 707 and 772; 64 dims 888 and 673, 659 and 669, 618 and 669; 256 dims, 4
+// heads: 1339 and 858, 1021 and 745, 913 and 739 (where pages of 64, which have 32 boxes of
+// K and V a tile as well, would be better off with the copies).
 //
 // Masked slots. A masked score is replaced before the maximum, so K may hold anything
 // there. But weight 0 times a NaN or an infinity in V would reach the sum, so in tiles
@@ -43,8 +49,9 @@
 // loaded from beyond the tensor map's edge: zeros.
 //
 // Measured: one token over 1M slots of 8 heads 587 us (7.3 TB/s), of 48 sequences of 13K
-// slots on average over pages of 16 390 us (6.7 TB/s), over 1000 slots 12.4 us; 2048
-// tokens over 32K slots, 32 heads in groups of 4, 722 us (1475 TFLOP/s).
+// slots on average over pages of 16 390 us (6.7 TB/s), of 512 sequences of 1300 slots 467 us
+// (5.9 TB/s), over 1000 slots 12.5 us; 2048 tokens over 32K slots, 32 heads in groups of 4,
+// 684 to 725 us (1470 to 1560 TFLOP/s).
 #include <algorithm>
 
 #include "kv4_device.cuh"
@@ -203,7 +210,10 @@ __device__ __forceinline__ float warp_sum(float x) {
     return x;
 }
 
-// Sizes of an item that are weighed against each other, in shares of an SM's work.
+// Sizes of an item that are weighed against each other, in shares of an SM's work. With one alone, of the whole work: five
+// tokens of 8 sequences 17.8 us against 17.1 and single tokens of 20 sequences 198 against 187.5, but of 48 381 against 390
+// and the mixed batch 110 against 114; of an eighth: 28.1, 189, 390, 139, chunks of four prompts 225 against 193. With four
+// (1/8, 1/3, 1, 2): 17.6 and 189, the others within 1%.
 constexpr int kTry = 8;
 __constant__ const float kShares[kTry] = {1.f / kItemsPerSm, 0.2f, 1.f / 3, 0.5f, 1.f, 1.25f, 1.5f, 2.f};
 
@@ -1240,9 +1250,10 @@ __device__ __forceinline__ int32_t sequence_at(const int32_t* cu, int32_t B, int
 // By the offsets that the kernel before put in order; out of line, which keeps the join's registers free.
 __device__ __noinline__ int32_t sequence_taken(const PagedAttendArgs& a, int32_t tok) { return sequence_at(a.offsets, a.B, tok); }
 
-// LPR lanes a row of the output: a quarter of a warp where rows are many, the whole block where they are few (2048
-// tokens of 32 heads in two parts 752 us with a quarter, 763 with a warp; 40 rows of 32 heads in four parts 18.3 and 16.1).
-// Row r is head r % H of token r / H. Also leaves the work queue at zero for the next call.
+// LPR lanes a row of the output: the whole block up to 8 rows an SM, a warp up to 64, a quarter of a warp beyond. Chunks of
+// 32 heads over 32K slots, by block, warp and quarter: 32 rows 34.0, 37.7 and 50.4 us, 640 rows 36.8, 39.8 and 55.0, 1216
+// rows (8 an SM) 45.2, 44.1 and 51.0, 2432 rows 58.7, 54.5 and 59.2; 9728 rows (64 an SM) 185, 163 and 167, 19456 rows 228,
+// 210.5 and 209, chunks of four prompts (97K rows and more) 309, 202 and 192. Row r is head r % H of token r / H. Also leaves the work queue at zero for the next call.
 template <int LPR, int DT>
 __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const PagedAttendArgs a, const Tiling t) {
     constexpr int ROWS = 32 * kMergeWarps / LPR;
