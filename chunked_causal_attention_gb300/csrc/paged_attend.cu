@@ -49,7 +49,7 @@
 // loaded from beyond the tensor map's edge: zeros.
 //
 // Measured: one token over 1M slots of 8 heads 587 us (7.3 TB/s), of 48 sequences of 13K
-// slots on average over pages of 16 390 us (6.7 TB/s), of 512 sequences of 1300 slots 467 us
+// slots on average over pages of 16 390 us (6.7 TB/s), of 512 sequences of 1300 slots 470 us
 // (5.9 TB/s), over 1000 slots 12.5 us; 2048 tokens over 32K slots, 32 heads in groups of 4,
 // 684 to 725 us (1470 to 1560 TFLOP/s).
 #include <algorithm>
