@@ -492,6 +492,7 @@ struct Joined {
         m = to;
     }
     // Parts p = from, from + by, .. below n; mine: this lane's first piece of part 0, lses: the row's sum of part 0.
+    // Plain loads: the parts are the kernel before's, visible since grid_wait.
     __device__ __forceinline__ void parts(const float* mine, const float* lses, int64_t step, int from, int by, int n, int lane,
                                           int D) {
         m = -INFINITY;
